@@ -9,6 +9,9 @@ calls raise.
 Names follow the C ABI: ``dsmem_hist``, ``dsmem_hist_ex``,
 ``dsmem_hist_global_atomic``, ``dsmem_hist_host``, ``dsmem_hist_plan``,
 ``dsmem_hist_plan_ex``, ``dsmem_hist_plan_for_device``, ``dsmem_hist_release``.
+The expert-layer operators (``dsmem_route``, ``dsmem_group``,
+``dsmem_grouped_matmul``, ``dsmem_combine``, ``dsmem_grad_clip`` and their
+gradients) are in ``experts`` and exported here too.
 """
 from __future__ import annotations
 
@@ -114,6 +117,8 @@ EXPORTS = (
     "dsmem_hist_plan", "dsmem_hist_plan_ex", "dsmem_hist_plan_for_device", "dsmem_hist_strerror",
     "dsmem_hist_last_error", "dsmem_hist_release", "dsmem_hist_device_status",
     "dsmem_hist_version",
+    "dsmem_route", "dsmem_route_backward", "dsmem_group", "dsmem_grouped_matmul",
+    "dsmem_grouped_matmul_wgrad", "dsmem_combine", "dsmem_combine_backward", "dsmem_grad_clip",
 )
 
 _lib = None
@@ -448,3 +453,8 @@ def dsmem_hist_version() -> int:
 
 def strerror(code: int) -> str:
     return lib().dsmem_hist_strerror(code).decode()
+
+
+from .experts import (  # noqa: E402
+    dsmem_combine, dsmem_combine_backward, dsmem_grad_clip, dsmem_group, dsmem_grouped_matmul,
+    dsmem_grouped_matmul_wgrad, dsmem_route, dsmem_route_backward)

@@ -16,9 +16,11 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libdsmemhist.so")
 
 SOURCES = ["cluster_hist.cu", "cluster_ship.cu", "static_scratch.cu", "microbench.cu", "planner.cpp",
-           "api.cpp"]
-HEADERS = [os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "ptx.cuh"),
-           os.path.join(CSRC, "helper_split.h"), os.path.join(INCLUDE, "dsmem_hist.h")]
+           "api.cpp", "experts_api.cpp", "expert_route.cu", "expert_product.cu", "expert_combine.cu",
+           "grad_clip.cu"]
+HEADERS = [os.path.join(CSRC, name) for name in ("internal.h", "ptx.cuh", "helper_split.h", "experts.h",
+                                                 "dtypes.cuh")] + \
+          [os.path.join(INCLUDE, name) for name in ("dsmem_hist.h", "dsmem_experts.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-Wall,-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]

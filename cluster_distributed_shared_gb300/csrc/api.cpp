@@ -19,6 +19,7 @@
 #include <cuda_runtime_api.h>
 
 #include "dsmem_hist.h"
+#include "experts.h"
 #include "helper_split.h"
 #include "internal.h"
 
@@ -268,8 +269,14 @@ void use_hot_bin(dsmem_hist_plan_t* plan, int32_t chosen, const SlotRef& r) {
 // Reports (once) a bounded wait that gave up in an earlier launch on this
 // stream, as seen from the host without synchronising.
 int take_pending_timeout(uint32_t* h) {
-  if (!h || *reinterpret_cast<volatile uint32_t*>(h) == 0u) return DSMEM_HIST_OK;
+  if (!h) return DSMEM_HIST_OK;
+  const uint32_t word = *reinterpret_cast<volatile uint32_t*>(h);
+  if (word == 0u) return DSMEM_HIST_OK;
   *reinterpret_cast<volatile uint32_t*>(h) = 0u;
+  if (word == kStatusProduct)
+    return fail(DSMEM_HIST_ETIMEOUT,
+                "an earlier grouped product on this stream had a bounded wait give up, so its output "
+                "was wrong; this call enqueued nothing (call again)");
   return fail(DSMEM_HIST_ETIMEOUT,
               "an earlier ship-kernel launch on this stream had a bounded inbox wait give up, so "
               "its histogram was wrong; this call enqueued nothing (call again)");
@@ -854,6 +861,48 @@ int run_with_fixed_scratch(const int32_t* keys, int64_t n, int32_t num_bins, uin
 }
 
 int record_error(int code, const char* what) { return fail(code, "%s", what); }
+
+int fail_with(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return fail(code, "%s", buf);
+}
+int fail_with_cuda(cudaError_t e, const char* what) { return fail_cuda(e, what); }
+
+int begin_call(cudaStream_t stream, CallContext* out) {
+  std::lock_guard<std::mutex> g(g_mutex);
+  DeviceState* st = nullptr;
+  SlotRef sr;
+  int rc = device_state(&st);
+  if (rc) return rc;
+  if (st->dev.cc_major != 10)
+    return fail(DSMEM_HIST_EUNSUPPORTED, "the expert-layer kernels are built for sm_103a");
+  if ((rc = stream_slot(st, stream, true, &sr))) return rc;
+  if ((rc = take_pending_timeout(sr.h_status))) return rc;
+  if ((rc = ensure_pool(st))) return rc;
+  out->status = sr.d_status;
+  out->pool = st->pool;
+  out->sm_count = st->dev.sm_count;
+  return DSMEM_HIST_OK;
+}
+
+int pool_alloc(const CallContext& ctx, void** out, size_t bytes, cudaStream_t stream) {
+  if (injected_alloc_failure())
+    return fail(DSMEM_HIST_ENOMEM, "scratch pool: %lld bytes: allocation failure injected by "
+                "DSMEM_HIST_TEST_FAIL_ALLOC", static_cast<long long>(bytes));
+  const cudaError_t e = cudaMallocFromPoolAsync(out, bytes, ctx.pool, stream);
+  if (e == cudaSuccess) return DSMEM_HIST_OK;
+  cudaGetLastError();
+  return fail(DSMEM_HIST_ENOMEM, "scratch pool: %lld bytes: %s", static_cast<long long>(bytes),
+              cudaGetErrorString(e));
+}
+int pool_free(void* p, cudaStream_t stream) {
+  const cudaError_t e = cudaFreeAsync(p, stream);
+  return e == cudaSuccess ? DSMEM_HIST_OK : fail_cuda(e, "cudaFreeAsync");
+}
 
 namespace {
 

@@ -1,0 +1,360 @@
+// Routing: the choice of each token's experts with its gradient, and the
+// stable grouping of keys that puts rows in expert order.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dtypes.cuh"
+#include "experts.h"
+#include "ptx.cuh"
+
+namespace dsmh {
+namespace {
+
+using namespace ptx;
+
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kRouteWarps = 4;
+
+// Floats as unsigned integers of the same order; 0 for what is masked (-inf
+// and NaN).  Adding zero makes -0 equal to +0.
+__device__ __forceinline__ uint32_t rank_key(float v) {
+  if (!(v > -INFINITY)) return 0u;
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float rank_value(uint32_t key) {
+  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+// exp(v - top), the unnormalised softmax of an unmasked logit.  With top at
+// +inf it is the limit: 1 for the entries at +inf, 0 for the others.
+__device__ __forceinline__ float raised(float v, float top) {
+  return top < INFINITY ? expf(v - top) : (v == top ? 1.0f : 0.0f);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+  return v;
+}
+
+// One warp per token, the row in registers: lane l holds logits l, l + 32, ..
+// Each of the top_k picks is a warp maximum over rank keys, then a warp
+// minimum over the indexes that hold it, so equal logits go to the lowest
+// index.  Softmax statistics are 32-bit.
+template <typename T, int R>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
+  const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+  if (token >= a.tokens) return;
+  const int lane = threadIdx.x & 31;
+  const T* row = static_cast<const T*>(a.logits) + token * a.row_stride;
+  uint32_t key[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int e = r * 32 + lane;
+    key[r] = e < a.experts ? rank_key(to_float(row[e])) : 0u;
+  }
+  uint32_t best = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) best = max(best, key[r]);
+  const uint32_t top_key = __reduce_max_sync(kFull, best);
+  const float top = rank_value(top_key);
+  float all = 0.0f;
+  if (!a.renormalize) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (key[r]) all += raised(rank_value(key[r]), top);
+    all = warp_sum(all);
+  }
+  int my_id = -1;
+  float mine = 0.0f;
+  for (int j = 0; j < a.top_k; ++j) {
+    best = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) best = max(best, key[r]);
+    const uint32_t m = __reduce_max_sync(kFull, best);
+    if (m == 0u) break;
+    uint32_t first = 0xffffffffu;
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r)
+      if (key[r] == m) first = r * 32 + lane;
+    const uint32_t id = __reduce_min_sync(kFull, first);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (static_cast<uint32_t>(r * 32 + lane) == id) key[r] = 0u;
+    if (lane == j) {
+      my_id = static_cast<int>(id);
+      mine = raised(rank_value(m), top);
+    }
+  }
+  if (a.renormalize) all = warp_sum(mine);
+  if (lane < a.top_k) {
+    a.ids[token * a.top_k + lane] = my_id;
+    a.weights[token * a.top_k + lane] = my_id >= 0 ? mine / all : 0.0f;
+  }
+}
+
+// The gradient, one warp per token.  With w the weights, g their gradient and
+// s = sum_j w_j g_j:  renormalised, d logit[ids_j] = w_j (g_j - s) and 0
+// elsewhere; else d logit[e] = [e = ids_j] w_j g_j - p_e s with the softmax p
+// taken again from the row.
+template <typename T, int R>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteArgs a) {
+  const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+  if (token >= a.tokens) return;
+  const int lane = threadIdx.x & 31;
+  int my_id = -1;
+  float w = 0.0f, wg = 0.0f;
+  if (lane < a.top_k) {
+    my_id = a.ids[token * a.top_k + lane];
+    if (my_id >= 0) {
+      w = a.weights[token * a.top_k + lane];
+      wg = w * a.grad_weights[token * a.top_k + lane];
+    }
+  }
+  const float s = warp_sum(wg);
+  const float mine = a.renormalize ? wg - w * s : wg;
+  float grad[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) grad[r] = 0.0f;
+  if (!a.renormalize) {
+    const T* row = static_cast<const T*>(a.logits) + token * a.row_stride;
+    float v[R];
+    float top = -INFINITY, all = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int e = r * 32 + lane;
+      v[r] = e < a.experts ? to_float(row[e]) : -INFINITY;
+      if (v[r] > top) top = v[r];
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      grad[r] = v[r] > -INFINITY ? raised(v[r], top) : 0.0f;
+      all += grad[r];
+    }
+    all = warp_sum(all);
+    const float scale = all > 0.0f ? -s / all : 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) grad[r] *= scale;
+  }
+  for (int j = 0; j < a.top_k; ++j) {
+    const int id = __shfl_sync(kFull, my_id, j);
+    const float g = __shfl_sync(kFull, mine, j);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r * 32 + lane == id) grad[r] += g;
+  }
+  T* out = static_cast<T*>(a.grad_logits) + token * a.experts;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (r * 32 + lane < a.experts) out[r * 32 + lane] = from_float<T>(grad[r]);
+}
+
+template <typename T>
+cudaError_t launch_route_t(const RouteArgs& a, bool backward, cudaStream_t stream) {
+  const int64_t blocks = (a.tokens + kRouteWarps - 1) / kRouteWarps;
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kRouteWarps * 32);
+#define DSMH_ROUTE(R)                                                  \
+  if (a.experts <= 32 * R) {                                           \
+    if (backward)                                                      \
+      route_backward_kernel<T, R><<<grid, block, 0, stream>>>(a);      \
+    else                                                               \
+      route_kernel<T, R><<<grid, block, 0, stream>>>(a);               \
+    return cudaGetLastError();                                         \
+  }
+  DSMH_ROUTE(2)
+  DSMH_ROUTE(8)
+  DSMH_ROUTE(32)
+#undef DSMH_ROUTE
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t dispatch_route(const RouteArgs& a, bool backward, cudaStream_t stream) {
+  if (a.dtype == DSMEM_F32) return launch_route_t<float>(a, backward, stream);
+  if (a.dtype == DSMEM_F16) return launch_route_t<__half>(a, backward, stream);
+  return launch_route_t<__nv_bfloat16>(a, backward, stream);
+}
+
+// Grouping: a counting sort by one cluster of P CTAs of W warps.  Every warp
+// owns a contiguous run of keys and a row of counters in its CTA's shared
+// memory, one per group.
+//   1. Each warp counts its keys into its row.
+//   2. Per group, the rows of a CTA become exclusive prefixes over its warps
+//      and the CTA's total; the totals of the cluster's CTAs are read through
+//      distributed shared memory, so every CTA knows what precedes it in the
+//      group and how large the group is; a scan over the groups gives the
+//      offsets.  Each row then holds where its warp's next key of a group goes.
+//   3. Each warp goes over its keys again, 32 at a time: lanes with equal
+//      keys are found by one ballot per key bit, take consecutive places in
+//      lane order and move the counter on.
+// Order is by warp, step and lane, that is by index: the sort is stable and
+// needs no atomics whose order could matter (the counts of step 1 commute).
+struct GroupArgs {
+  const int32_t* keys;
+  int64_t n;
+  int groups, warps, bits;
+  int shared_totals;  // one warp in one CTA: its row is the CTA's totals as well
+  int32_t* offsets;
+  int32_t* order;
+  int32_t* position;
+};
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(1024) group_kernel(GroupArgs a) {
+  extern __shared__ uint32_t smem[];  // rows [warps][groups], totals [groups], scan [32]
+  const uint32_t rank = cluster_ctarank(), P = cluster_nctarank();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t G = static_cast<uint32_t>(a.groups);
+  uint32_t* total = smem + (a.shared_totals ? 0 : static_cast<size_t>(a.warps) * G);
+  uint32_t* scan = total + G;
+  uint32_t* mine = smem + static_cast<size_t>(warp) * G;
+  for (uint32_t i = threadIdx.x; i < a.warps * G; i += blockDim.x) smem[i] = 0;
+  __syncthreads();
+
+  // Each warp's run of keys, a multiple of 32 long.
+  const int64_t parts = static_cast<int64_t>(P) * a.warps;
+  const int64_t run = ((a.n + parts - 1) / parts + 31) / 32 * 32;
+  int64_t begin = (static_cast<int64_t>(rank) * a.warps + warp) * run;
+  int64_t end = begin + run;
+  if (begin > a.n) begin = a.n;
+  if (end > a.n) end = a.n;
+
+  for (int64_t i = begin + lane; i < end; i += 32) {
+    const uint32_t key = static_cast<uint32_t>(a.keys[i]);
+    if (key < G) atomicAdd(mine + key, 1u);
+  }
+  __syncthreads();
+  for (uint32_t g = threadIdx.x; g < G && !a.shared_totals; g += blockDim.x) {
+    uint32_t sum = 0;
+    for (int w = 0; w < a.warps; ++w) {
+      const uint32_t c = smem[static_cast<size_t>(w) * G + g];
+      smem[static_cast<size_t>(w) * G + g] = sum;
+      sum += c;
+    }
+    total[g] = sum;
+  }
+  cluster_barrier();
+  // Scan over the groups, blockDim.x at a time, carrying the sum so far.
+  uint32_t carry = 0;
+  for (uint32_t g0 = 0; g0 < G; g0 += blockDim.x) {
+    const uint32_t g = g0 + threadIdx.x;
+    uint32_t before = 0, size = 0;
+    if (g < G) {
+      const uint32_t addr = smem_u32(total + g);
+      for (uint32_t r = 0; r < P; ++r) {
+        const uint32_t c = ld_cluster_u32(map_rank(addr, r));
+        if (r < rank) before += c;
+        size += c;
+      }
+    }
+    uint32_t incl = size;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t up = __shfl_up_sync(kFull, incl, d);
+      if (lane >= d) incl += up;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    uint32_t ahead = carry, block = 0;
+    for (int w = 0; w < a.warps; ++w) {
+      const uint32_t c = scan[w];
+      if (w < warp) ahead += c;
+      block += c;
+    }
+    const uint32_t offset = ahead + incl - size;
+    if (g < G) {
+      if (a.shared_totals) {
+        smem[g] = offset;
+      } else {
+        for (int w = 0; w < a.warps; ++w) smem[static_cast<size_t>(w) * G + g] += offset + before;
+      }
+      if (rank == 0) a.offsets[g] = static_cast<int32_t>(offset);
+    }
+    carry += block;
+    __syncthreads();
+  }
+  if (rank == 0 && threadIdx.x == 0) a.offsets[G] = static_cast<int32_t>(carry);
+  // No CTA leaves, or writes over its totals, while others still read them.
+  cluster_barrier();
+
+  const uint32_t below = (1u << lane) - 1u;
+  for (int64_t i0 = begin; i0 < end; i0 += 32) {
+    const int64_t i = i0 + lane;
+    const uint32_t key = i < end ? static_cast<uint32_t>(a.keys[i]) : 0xffffffffu;
+    const bool valid = key < G;
+    uint32_t peers = __ballot_sync(kFull, valid);
+    for (int b = 0; b < a.bits; ++b) {
+      const bool bit = (key >> b) & 1u;
+      const uint32_t with = __ballot_sync(kFull, bit);
+      peers &= bit ? with : ~with;
+    }
+    uint32_t place = 0xffffffffu;
+    if (valid) place = mine[key] + __popc(peers & below);
+    __syncwarp();
+    if (valid && lane == 31 - __clz(peers)) mine[key] = place + 1;
+    __syncwarp();
+    if (i < end) a.position[i] = static_cast<int32_t>(place);
+    if (valid) a.order[place] = static_cast<int32_t>(i);
+  }
+  // Places behind the last group.
+  for (int64_t p = carry + static_cast<int64_t>(rank) * blockDim.x + threadIdx.x; p < a.n;
+       p += static_cast<int64_t>(P) * blockDim.x)
+    a.order[p] = -1;
+}
+
+constexpr int kGroupSmemLimit = 200 * 1024;
+
+}  // namespace
+
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
+  return dispatch_route(a, false, stream);
+}
+cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t stream) {
+  return dispatch_route(a, true, stream);
+}
+
+cudaError_t launch_group(const int32_t* keys, int64_t n, int num_groups, int32_t* offsets,
+                         int32_t* order, int32_t* position, cudaStream_t stream) {
+  GroupArgs a{keys, n, num_groups, 0, 0, 0, offsets, order, position};
+  while ((int64_t{1} << a.bits) < num_groups) ++a.bits;
+  // Warps: as many counter rows as shared memory holds beside the totals, but
+  // no more than the keys fill with 32 each.  CTAs: one cluster, doubled
+  // while every warp still has 128 keys or more.
+  // Where a row and the totals do not fit (25,585 groups or more), one warp
+  // in one CTA keeps both in one row.
+  const int64_t fit = (kGroupSmemLimit / 4 - 32) / num_groups - 1;
+  a.shared_totals = fit < 1;
+  int64_t warps = (n + 31) / 32;
+  if (warps > fit) warps = fit;
+  a.warps = static_cast<int>(warps < 1 ? 1 : (warps > 32 ? 32 : warps));
+  int P = 1;
+  while (P < 16 && !a.shared_totals && n >= int64_t{2} * P * a.warps * 128) P *= 2;
+  const size_t smem = (static_cast<size_t>(a.warps + !a.shared_totals) * num_groups + 32) * 4;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kGroupSmemLimit)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) !=
+          cudaSuccess)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(P);
+  cfg.blockDim = dim3(a.warps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = P;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, group_kernel, a);
+}
+
+}  // namespace dsmh

@@ -1,0 +1,96 @@
+// Internal interfaces between the expert-layer kernels and their host layer.
+// Not installed; the public C ABI is include/dsmem_experts.h.
+#pragma once
+
+#include <stdint.h>
+#include <cuda_runtime_api.h>
+
+#include "dsmem_experts.h"
+#include "internal.h"
+
+namespace dsmh {
+
+inline int dtype_size(int dtype) { return dtype == DSMEM_F32 ? 4 : 2; }
+
+// Status-word value of a launch of the product kernels whose wait gave up
+// (the ship kernel writes 1).
+constexpr uint32_t kStatusProduct = 2;
+
+// Host layer of api.cpp: reports an earlier launch's timeout on this stream
+// and hands out what a launch needs of the current device.
+struct CallContext {
+  uint32_t* status = nullptr;  // the stream's host-mapped status word
+  cudaMemPool_t pool = nullptr;
+  int sm_count = 0;
+};
+int begin_call(cudaStream_t stream, CallContext* out);
+// Scratch from the device's stream-ordered pool; given back on the same stream.
+int pool_alloc(const CallContext& ctx, void** out, size_t bytes, cudaStream_t stream);
+int pool_free(void* p, cudaStream_t stream);
+int fail_with(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int fail_with_cuda(cudaError_t e, const char* what);
+
+// Runs a C entry's body; a C++ exception becomes an error code.
+template <typename F>
+int guarded(F&& body) noexcept {
+  try {
+    return body();
+  } catch (...) {
+    return record_error(DSMEM_HIST_ENOMEM, "out of host memory");
+  }
+}
+
+struct RouteArgs {
+  const void* logits;
+  int64_t tokens, row_stride;
+  int experts, top_k, renormalize, dtype;
+  int32_t* ids;
+  float* weights;
+  const float* grad_weights;  // backward only
+  void* grad_logits;
+};
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
+cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t stream);
+
+cudaError_t launch_group(const int32_t* keys, int64_t n, int num_groups, int32_t* offsets,
+                         int32_t* order, int32_t* position, cudaStream_t stream);
+
+enum ProductKind { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
+struct ProductArgs {
+  int kind;
+  const void* x;       // rows' source: [x_rows, inner] (kInputGrad: [x_rows, outer])
+  int64_t x_rows, x_stride;
+  const void* w;       // [groups, outer, inner]; kWeightGrad: dy [n, outer]
+  int64_t w_stride, w_group_stride;
+  const int32_t* offsets;
+  const int32_t* order;  // may be null
+  int groups, fan;
+  int64_t n;
+  int outer, inner;
+  int dtype, out_dtype;
+  void* out;
+  uint32_t* status;
+  int sm_count;
+};
+cudaError_t launch_product(const ProductArgs& a, cudaStream_t stream);
+
+struct CombineArgs {
+  const void* z;
+  int64_t z_rows, z_stride;
+  const void* dy;
+  int64_t dy_stride;
+  const int32_t* position;
+  const int32_t* order;
+  const float* weights;  // may be null (forward)
+  int64_t tokens;
+  int top_k, width, dtype;
+  void* out;  // forward: [tokens, width]; backward: dz
+  float* dweights;
+};
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);
+cudaError_t launch_combine_backward(const CombineArgs& a, cudaStream_t stream);
+
+int run_grad_clip(const dsmem_grad_t* grads, int32_t num_grads, float max_norm, float* norm,
+                  const CallContext& ctx, cudaStream_t stream);
+
+}  // namespace dsmh
