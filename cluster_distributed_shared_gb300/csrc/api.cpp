@@ -1162,10 +1162,13 @@ void dsmem_hist_release(void) {
 
 int dsmem_hist_device_status(uint32_t* status) {
   uint32_t word = 0;
-  const cudaError_t e = read_and_clear_ship_status(&word);
+  uint32_t product = 0;
+  cudaError_t e = read_and_clear_ship_status(&word);
+  if (e == cudaSuccess) e = read_and_clear_product_status(&product);
+  word |= product;
   if (status) *status = word;
   if (e != cudaSuccess) return fail(DSMEM_HIST_ECUDA, "device_status: %s", cudaGetErrorString(e));
-  if (word) return fail(DSMEM_HIST_ETIMEOUT, "device_status: a bounded inbox wait gave up (word 0x%x)", word);
+  if (word) return fail(DSMEM_HIST_ETIMEOUT, "device_status: a bounded wait gave up (word 0x%x)", word);
   return DSMEM_HIST_OK;
 }
 

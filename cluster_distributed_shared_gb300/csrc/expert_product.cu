@@ -1,156 +1,636 @@
-// Products grouped by key: the simple form, one 64 x 64 tile per CTA with
-// 32-bit fused multiply-adds.
+// Products grouped by key on the tcgen05 tensor cores.
+//
+// All three products are D = A B with the weights' side as A, 128 channels
+// high, and the rows' side as B, kCols columns wide, so that the width of a
+// tile follows how many rows a group has while the weights keep full tiles:
+//   forward       D[outer, rows]  = W[g] x^T        depth inner; both operands K-major
+//   input grad    D[inner, rows]  = W[g]^T x^T      depth outer; A is MN-major
+//   weight grad   D[outer, inner] = dy^T x          depth: the group's rows; both MN-major
+// One persistent CTA per SM; warp 0 copies operand tiles of 64 depth
+// (128 bytes, swizzled) into a ring of stages by TMA, warp 1 issues the matrix
+// instructions into one of two accumulators in tensor memory, and warps 2..5
+// write the other one out.  Rows named by an order are fetched by gathering
+// copies, four rows each, so no reordered copy of x exists anywhere.
+//
+// The group sizes are on the device only: every CTA lays the groups' tiles
+// end to end from the offsets and takes every gridDim-th.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "dtypes.cuh"
 #include "experts.h"
+#include "ptx.cuh"
+#include "tcgen.cuh"
 
 namespace dsmh {
 namespace {
 
-constexpr int kTile = 64, kDepth = 16, kThreads = 256;
+using namespace ptx;
 
-__device__ __forceinline__ int64_t group_end(const ProductArgs& a, int g) {
-  const int64_t e = a.offsets[g + 1];
-  return e < 0 ? 0 : (e > a.n ? a.n : e);
-}
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kChannels = 128;              // height of a tile
+constexpr int kDepth = 64;                  // depth of a stage: 128 bytes of 16-bit elements
+constexpr int kThreads = 192;               // copies, matrix instructions, 4 warps of output
+constexpr int kABytes = kChannels * kDepth * 2;
 
-template <typename T>
-__device__ __forceinline__ float source(const ProductArgs& a, int64_t p, int c) {
-  int64_t row = p;
-  if (a.order) {
-    const int64_t o = a.order[p];
-    row = o < 0 ? -1 : o / a.fan;
+constexpr int kBarrierBytes = 256;
+
+// A ring of as many stages as fit beside the tables (227 KB in all).
+template <int kCols>
+struct Ring {
+  static constexpr int kStages = kCols == 256 ? 4 : (kCols == 128 ? 6 : (kCols == 64 ? 8 : 10));
+  static constexpr int kStage = kABytes + kCols * kDepth * 2;
+  static int smem_bytes(int groups) {
+    return 1024 + kStages * kStage + kBarrierBytes + 2 * 4 * (groups + 2);
   }
-  if (row < 0 || row >= a.x_rows) return 0.0f;
-  return to_float(static_cast<const T*>(a.x)[row * a.x_stride + c]);
-}
-
-// C[64 x 64] of A [64 x depth] times B [depth x 64], both staged in shared memory.
-struct Tile {
-  float a[kDepth][kTile + 1];
-  float b[kDepth][kTile + 1];
 };
-__device__ __forceinline__ void multiply(const Tile& s, float (&acc)[4][4]) {
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-#pragma unroll
-  for (int k = 0; k < kDepth; ++k) {
-    float x[4], y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = s.a[k][ty + 16 * i];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = s.b[k][tx + 16 * j];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
-  }
+
+struct Maps {
+  CUtensorMap a;         // weights (3-D), or dy
+  CUtensorMap a_gather;  // dy by single rows (weight gradient's ragged ends)
+  CUtensorMap b;         // x in boxes
+  CUtensorMap b_gather;  // x by single rows
+};
+struct TileArgs {
+  const int32_t* offsets;
+  const int32_t* order;
+  int64_t n;
+  int x_rows, groups, fan;
+  int channels;  // extent of the tiles' height: outer, inner, outer
+  int depth;     // extent of the contraction (forward and input gradient)
+  int width;     // weight gradient: extent of the tiles' width, inner
+  int dtype, out_dtype;
+  void* out;
+  uint32_t* status;
+  long long wait_cycles;
+};
+
+__device__ uint32_t g_product_status;  // kStatusProduct once a bounded wait gave up
+
+__device__ __forceinline__ uint32_t flag_set(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
 }
 
-template <typename T, typename O>
-__global__ void __launch_bounds__(kThreads) rows_kernel(ProductArgs a) {
-  __shared__ Tile s;
-  const int cols = a.kind == kForward ? a.outer : a.inner;
-  const int depth = a.kind == kForward ? a.inner : a.outer;
-  // Row tile blockIdx.y of the groups' tiles laid end to end; the rows behind
-  // the last group are one more group, of zeros.
-  int64_t tile = blockIdx.y, begin = 0, end = 0;
-  int g = 0;
-  for (; g <= a.groups; ++g) {
-    end = g < a.groups ? max(group_end(a, g), begin) : a.n;
-    const int64_t tiles = (end - begin + kTile - 1) / kTile;
-    if (tile < tiles) break;
-    tile -= tiles;
-    begin = end;
+// Waits for phase `parity` of an mbarrier, at most `limit` cycles or until
+// another wait of this CTA has given up.
+__device__ __noinline__ bool wait_slow(uint32_t mbar, uint32_t parity, uint32_t gave_up, long long limit,
+                                       uint32_t* status) {
+  const long long deadline = clock64() + limit;
+  do {
+    if (mbar_try_wait(mbar, parity)) return true;
+    if (flag_set(gave_up)) return false;
+  } while (clock64() < deadline);
+  asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(gave_up), "r"(1u) : "memory");
+  atomicOr(&g_product_status, kStatusProduct);
+  if (status) *reinterpret_cast<volatile uint32_t*>(status) = kStatusProduct;
+  return false;
+}
+__device__ __forceinline__ bool wait_for(uint32_t mbar, uint32_t parity, uint32_t gave_up,
+                                         long long limit, uint32_t* status) {
+  return mbar_try_wait(mbar, parity) || wait_slow(mbar, parity, gave_up, limit, status);
+}
+
+// Shared-memory matrix descriptors, 128-byte swizzle.  K-major: rows of 128
+// bytes, groups of 8 rows 1024 bytes apart.  MN-major: boxes of 64 elements by
+// 64 depth, 8192 bytes each, in them groups of 8 depth 1024 bytes apart.
+constexpr uint64_t kDescBase = (uint64_t{1} << 46) | (uint64_t{2} << 61) | (uint64_t{1024 >> 4} << 32);
+template <bool kMnMajor>
+__device__ __forceinline__ uint64_t descriptor(uint32_t addr) {
+  return kDescBase | (uint64_t{kMnMajor ? 8192 >> 4 : 1} << 16) | ((addr & 0x3ffffu) >> 4);
+}
+struct Tile {
+  int group;     // `groups`: the rows behind the last group
+  int begin, end;  // the group's rows
+  int col0;      // first row (weight gradient: first inner column) of the tile
+  int chan0;     // first channel
+  int blocks;    // stages of depth
+};
+
+template <int kKind, int kCols>
+struct Schedule {
+  const int32_t* begin;  // [groups + 2] first row of each group, in shared memory
+  const int32_t* first;  // [groups + 2] first tile of each group
+  int groups, chan_tiles, width_tiles, depth_blocks;
+  int group;
+
+  __device__ __forceinline__ Schedule(const int32_t* b, const int32_t* f, const TileArgs& a)
+      : begin(b), first(f), groups(a.groups), chan_tiles((a.channels + kChannels - 1) / kChannels),
+        width_tiles(kKind == kWeightGrad ? (a.width + kCols - 1) / kCols : 0),
+        depth_blocks((a.depth + kDepth - 1) / kDepth), group(0) {}
+  __device__ __forceinline__ int tiles_of(int rows) const {
+    return (kKind == kWeightGrad ? width_tiles : (rows + kCols - 1) / kCols) * chan_tiles;
   }
-  if (g > a.groups) return;
-  const int64_t p0 = begin + tile * kTile;
-  const int c0 = blockIdx.x * kTile;
-  float acc[4][4] = {};
-  if (g < a.groups) {
-    const T* w = static_cast<const T*>(a.w) + g * a.w_group_stride;
-    for (int k0 = 0; k0 < depth; k0 += kDepth) {
-      for (int i = threadIdx.x; i < kTile * kDepth; i += kThreads) {
-        const int r = i / kDepth, k = i % kDepth;
-        s.a[k][r] = p0 + r < end && k0 + k < depth ? source<T>(a, p0 + r, k0 + k) : 0.0f;
-        const int c = a.kind == kForward ? i / kDepth : i % kTile;
-        const int kw = a.kind == kForward ? i % kDepth : i / kTile;
-        const int64_t at = a.kind == kForward ? (c0 + c) * a.w_stride + k0 + kw
-                                              : (k0 + kw) * a.w_stride + c0 + c;
-        s.b[kw][c] = c0 + c < cols && k0 + kw < depth ? to_float(w[at]) : 0.0f;
+  // Groups that own tiles; the weight gradient has none for the rows behind.
+  __device__ __forceinline__ int owners() const { return kKind == kWeightGrad ? groups : groups + 1; }
+  __device__ __forceinline__ int total() const { return first[owners()]; }
+  // Tile t; t only grows from call to call.
+  __device__ __forceinline__ Tile at(int t) {
+    while (t >= first[group + 1]) ++group;
+    Tile r;
+    r.group = group;
+    r.begin = begin[group];
+    r.end = begin[group + 1];
+    const int i = t - first[group];
+    r.chan0 = i % chan_tiles * kChannels;
+    if (kKind == kWeightGrad) {
+      r.col0 = i / chan_tiles * kCols;
+      r.blocks = (r.end - r.begin + kDepth - 1) / kDepth;
+    } else {
+      r.col0 = r.begin + i / chan_tiles * kCols;
+      r.blocks = group < groups ? depth_blocks : 0;
+    }
+    return r;
+  }
+};
+
+template <typename O>
+__device__ __forceinline__ O* out_at(const TileArgs& a, int64_t i) {
+  return static_cast<O*>(a.out) + i;
+}
+
+// 16 or 32 accumulator columns of one lane (channel) to global memory.
+template <int kKind, int kN, typename O>
+__device__ __forceinline__ void store_columns(const TileArgs& a, const Tile& t, int col, int channel,
+                                              const uint32_t (&r)[kN]) {
+  if (channel >= a.channels) return;
+  if (kKind == kWeightGrad) {
+    // The lane's channel is a row of the output; its columns are contiguous.
+    O* out = out_at<O>(a, (static_cast<int64_t>(t.group) * a.channels + channel) * a.width + col);
+    constexpr int V = 16 / sizeof(O);
+    if (col + kN <= a.width && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
+#pragma unroll
+      for (int j = 0; j < kN; j += V) {
+        Pack<O, V> p;
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.v[v] = from_float<O>(__uint_as_float(r[j + v]));
+        *reinterpret_cast<Pack<O, V>*>(out + j) = p;
       }
-      __syncthreads();
-      multiply(s, acc);
-      __syncthreads();
+    } else {
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+        if (col + j < a.width) out[j] = from_float<O>(__uint_as_float(r[j]));
     }
-  }
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t p = p0 + ty + 16 * i;
-      const int c = c0 + tx + 16 * j;
-      if (p < end && c < cols) static_cast<O*>(a.out)[p * cols + c] = from_float<O>(acc[i][j]);
-    }
-}
-
-template <typename T, typename O>
-__global__ void __launch_bounds__(kThreads) weight_grad_kernel(ProductArgs a) {
-  __shared__ Tile s;
-  const int g = blockIdx.z;
-  int64_t begin = 0, end = 0;
-  for (int i = 0; i <= g; ++i) {
-    begin = end;
-    end = max(group_end(a, i), begin);
-  }
-  const int n0 = blockIdx.y * kTile, k0 = blockIdx.x * kTile;
-  float acc[4][4] = {};
-  for (int64_t p0 = begin; p0 < end; p0 += kDepth) {
-    for (int i = threadIdx.x; i < kTile * kDepth; i += kThreads) {
-      const int c = i % kTile;
-      const int64_t p = p0 + i / kTile;
-      s.a[i / kTile][c] = p < end && n0 + c < a.outer
-                              ? to_float(static_cast<const T*>(a.w)[p * a.w_stride + n0 + c]) : 0.0f;
-      s.b[i / kTile][c] = p < end && k0 + c < a.inner ? source<T>(a, p, k0 + c) : 0.0f;
-    }
-    __syncthreads();
-    multiply(s, acc);
-    __syncthreads();
-  }
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + ty + 16 * i, k = k0 + tx + 16 * j;
-      if (n < a.outer && k < a.inner)
-        static_cast<O*>(a.out)[(static_cast<int64_t>(g) * a.outer + n) * a.inner + k] =
-            from_float<O>(acc[i][j]);
-    }
-}
-
-template <typename T, typename O>
-cudaError_t launch(const ProductArgs& a, cudaStream_t stream) {
-  if (a.kind == kWeightGrad) {
-    const dim3 grid((a.inner + kTile - 1) / kTile, (a.outer + kTile - 1) / kTile, a.groups);
-    weight_grad_kernel<T, O><<<grid, kThreads, 0, stream>>>(a);
   } else {
-    const int cols = a.kind == kForward ? a.outer : a.inner;
-    const int64_t tiles = a.n / kTile + std::min<int64_t>(a.groups + 1, a.n);
-    rows_kernel<T, O><<<dim3((cols + kTile - 1) / kTile, static_cast<unsigned>(tiles)), kThreads, 0,
-                        stream>>>(a);
+    // Columns are output rows; the warp's 32 lanes write neighbouring channels.
+    O* out = out_at<O>(a, static_cast<int64_t>(col) * a.channels + channel);
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+      if (col + j < t.end) out[static_cast<int64_t>(j) * a.channels] = from_float<O>(__uint_as_float(r[j]));
   }
-  return cudaGetLastError();
+}
+template <int kKind, int kN>
+__device__ __forceinline__ void store_any(const TileArgs& a, const Tile& t, int col, int channel,
+                                          const uint32_t (&r)[kN]) {
+  if (a.out_dtype == DSMEM_F32) store_columns<kKind, kN, float>(a, t, col, channel, r);
+  else if (a.out_dtype == DSMEM_F16) store_columns<kKind, kN, __half>(a, t, col, channel, r);
+  else store_columns<kKind, kN, __nv_bfloat16>(a, t, col, channel, r);
+}
+
+template <int kKind, int kCols>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ TileArgs a) {
+  constexpr int kStages = Ring<kCols>::kStages, kStage = Ring<kCols>::kStage;
+  constexpr bool kAMn = kKind != kForward, kBMn = kKind == kWeightGrad;
+  constexpr uint32_t kTmemColumns = 2 * kCols < 32 ? 32 : 2 * kCols;
+  constexpr int kLoad = kCols < 32 ? 16 : 32;
+  // Descriptor steps of 16 depth, in 16-byte units.
+  constexpr uint64_t kAStep = (kAMn ? 2048 : 32) / 16, kBStep = (kBMn ? 2048 : 32) / 16;
+
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  uint8_t* base_ptr = raw + (base - smem_u32(raw));
+  const uint32_t bars = base + kStages * kStage;
+  const uint32_t full = bars, empty = bars + 8 * kStages;
+  const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
+  const uint32_t tmem_at = drained + 8, gave_up = tmem_at + 4;
+  static_assert(8 * (2 * kStages + 5) + 8 <= kBarrierBytes, "barriers");
+  int32_t* begin = reinterpret_cast<int32_t*>(base_ptr + kStages * kStage + kBarrierBytes);
+  int32_t* first = begin + a.groups + 2;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Schedule<kKind, kCols> schedule(begin, first, a);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + 8 * i, 1);
+      mbar_init(acc_empty + 8 * i, 4);
+    }
+    mbar_init(drained, 1);
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(gave_up), "r"(0u) : "memory");
+    fence_mbar_init();
+    prefetch_map(&maps.a);
+    prefetch_map(&maps.b);
+  }
+  // begin[g + 1] := the group's end, clamped into [0, n]; warp 2 then makes
+  // the ends monotone and lays the tiles end to end.
+  for (int g = threadIdx.x; g < a.groups; g += kThreads) {
+    const int64_t e = a.offsets[g + 1];
+    begin[g + 1] = static_cast<int32_t>(e < 0 ? 0 : (e > a.n ? a.n : e));
+  }
+  if (threadIdx.x == 0) {
+    begin[0] = first[0] = 0;
+    begin[a.groups + 1] = static_cast<int32_t>(a.n);
+  }
+  if (warp == 1) tmem_alloc(tmem_at, kTmemColumns);
+  __syncthreads();
+  if (warp == 2) {
+    int end_before = 0, tiles_before = 0;
+    for (int g0 = 0; g0 < schedule.owners(); g0 += 32) {
+      const int g = g0 + lane;
+      int end = g < schedule.owners() ? begin[g + 1] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(kFull, end, d);
+        if (lane >= d) end = max(end, up);
+      }
+      end = max(end, end_before);
+      int start = __shfl_up_sync(kFull, end, 1);
+      if (lane == 0) start = end_before;
+      int tiles = g < schedule.owners() ? schedule.tiles_of(end - start) : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(kFull, tiles, d);
+        if (lane >= d) tiles += up;
+      }
+      if (g < schedule.owners()) {
+        begin[g + 1] = end;
+        first[g + 1] = tiles_before + tiles;
+      }
+      end_before = __shfl_sync(kFull, end, 31);
+      tiles_before += __shfl_sync(kFull, tiles, 31);
+    }
+  }
+  tcgen_fence_before();
+  __syncthreads();
+  tcgen_fence_after();
+  uint32_t tmem;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_at));
+  const int total = schedule.total();
+
+  if (warp == 0) {
+    // Copies.
+    uint32_t stage = 0, phase = 0, issued = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+      const Tile t = schedule.at(i);
+      if (t.blocks == 0) continue;
+      // Forward and input gradient: the gathered rows are the same in every
+      // stage of the tile, four for each lane's copy.
+      constexpr int kQuads = kBMn ? 1 : (kCols + 127) / 128;
+      int rows[kQuads][4];
+      if (!kBMn && a.order) {
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int p = t.col0 + (q * 32 + lane) * 4 + v;
+            const int o = p < t.end ? a.order[p] : -1;
+            rows[q][v] = o < 0 ? -1 : o / a.fan;
+          }
+      }
+      for (int k = 0; k < t.blocks; ++k) {
+        // Weight gradient: this stage's 64 rows of the group, lane & 15 taking
+        // a quad of them; rows behind the group's end are read as zeros.
+        const int p0 = t.begin + k * kDepth;
+        const bool ragged = kBMn && p0 + kDepth > t.end;
+        if (kBMn && (a.order || ragged)) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int p = p0 + (lane & 15) * 4 + v;
+            int row = p < t.end ? p : -1;
+            if (a.order && row >= 0) {
+              const int o = a.order[p];
+              row = o < 0 ? -1 : o / a.fan;
+            }
+            rows[0][v] = row;
+          }
+        }
+        ok = wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
+        if (!__all_sync(kFull, ok)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = full + 8 * stage, sa = base + stage * kStage, sb = sa + kABytes;
+        if (lane == 0) mbar_expect_tx(bar, kStage);
+        __syncwarp();
+        if (kKind == kForward) {
+          if (lane == 0) tma_load_3d(sa, &maps.a, k * kDepth, t.chan0, t.group, bar);
+        } else if (kKind == kInputGrad) {
+          if (lane < 2) tma_load_3d(sa + lane * 8192, &maps.a, t.chan0 + lane * 64, k * kDepth, t.group, bar);
+        } else if (!ragged) {
+          if (lane < 2) tma_load_2d(sa + lane * 8192, &maps.a, t.chan0 + lane * 64, p0, bar);
+        } else {
+          const int p = p0 + (lane & 15) * 4, box = lane >> 4;
+          tma_gather4(sa + box * 8192 + (lane & 15) * 512, &maps.a_gather, t.chan0 + box * 64,
+                      p < t.end ? p : -1, p + 1 < t.end ? p + 1 : -1, p + 2 < t.end ? p + 2 : -1,
+                      p + 3 < t.end ? p + 3 : -1, bar);
+        }
+        if (kBMn) {
+          if (a.order || ragged) {
+#pragma unroll
+            for (int box = lane >> 4; box < kCols / 64; box += 2)
+              tma_gather4(sb + box * 8192 + (lane & 15) * 512, &maps.b_gather, t.col0 + box * 64,
+                          rows[0][0], rows[0][1], rows[0][2], rows[0][3], bar);
+          } else if (lane < kCols / 64) {
+            tma_load_2d(sb + lane * 8192, &maps.b, t.col0 + lane * 64, p0, bar);
+          }
+        } else if (a.order) {
+#pragma unroll
+          for (int q = 0; q < kQuads; ++q)
+            if ((q * 32 + lane) * 4 < kCols)
+              tma_gather4(sb + (q * 32 + lane) * 512, &maps.b_gather, k * kDepth, rows[q][0], rows[q][1],
+                          rows[q][2], rows[q][3], bar);
+        } else if (lane == 0) {
+          tma_load_2d(sb, &maps.b, k * kDepth, t.col0, bar);
+        }
+        ++issued;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    // After a wait that gave up: let this CTA's copies land before its shared
+    // memory goes.  Copy j (from 0) completes phase j / kStages of its stage.
+    if (flag_set(gave_up)) {
+      for (uint32_t j = issued > kStages ? issued - kStages : 0; j < issued; ++j) {
+        const long long deadline = clock64() + kDefaultWaitCycles;
+        while (!mbar_try_wait(full + 8 * (j % kStages), (j / kStages) & 1) && clock64() < deadline) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // Matrix instructions, by one thread.
+    if (lane == 0) {
+      const uint32_t idesc = (1u << 4) | (a.dtype == DSMEM_BF16 ? (1u << 7) | (1u << 10) : 0u) |
+                             (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u) |
+                             (uint32_t{kCols >> 3} << 17) | (uint32_t{kChannels >> 4} << 24);
+      uint32_t stage = 0, phase = 0, done = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+        const Tile t = schedule.at(i);
+        if (t.blocks == 0) continue;
+        const uint32_t buffer = done & 1, d = tmem + buffer * kCols;
+        ok = wait_for(acc_empty + 8 * buffer, ((done >> 1) & 1) ^ 1, gave_up, a.wait_cycles, a.status);
+        if (!ok) break;
+        tcgen_fence_after();
+        for (int k = 0; k < t.blocks; ++k) {
+          ok = wait_for(full + 8 * stage, phase, gave_up, a.wait_cycles, a.status);
+          if (!ok) break;
+          tcgen_fence_after();
+          const uint32_t sa = base + stage * kStage;
+          const uint64_t da = descriptor<kAMn>(sa), db = descriptor<kBMn>(sa + kABytes);
+#pragma unroll
+          for (int s = 0; s < kDepth / 16; ++s)
+            mma_f16(d, da + s * kAStep, db + s * kBStep, idesc, k > 0 || s > 0);
+          mma_commit(empty + 8 * stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit(acc_full + 8 * buffer);
+        ++done;
+      }
+      if (flag_set(gave_up)) {  // matrix instructions end before tensor memory is given back
+        mma_commit(drained);
+        const long long deadline = clock64() + kDefaultWaitCycles;
+        while (!mbar_try_wait(drained, 0) && clock64() < deadline) {
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // Output: warp w may read lanes 32 (w % 4) .. of tensor memory.
+    const int quadrant = warp & 3;
+    uint32_t done = 0;
+    for (int i = blockIdx.x; i < total; i += gridDim.x) {
+      const Tile t = schedule.at(i);
+      const int channel = t.chan0 + quadrant * 32 + lane;
+      const uint32_t buffer = done & 1;
+      if (t.blocks > 0) {
+        // A long contraction may take longer than one bounded wait of a copy.
+        const long long limit = a.wait_cycles + 4096ll * t.blocks;
+        const bool ok = wait_for(acc_full + 8 * buffer, (done >> 1) & 1, gave_up, limit, a.status);
+        if (!__all_sync(kFull, ok)) break;
+        tcgen_fence_after();
+      }
+      const uint32_t d = tmem + buffer * kCols + (static_cast<uint32_t>(quadrant * 32) << 16);
+      const int limit = kKind == kWeightGrad ? a.width : t.end;
+#pragma unroll 1
+      for (int c = 0; c < kCols; c += kLoad) {
+        if (t.col0 + c >= limit) break;
+        uint32_t r[kLoad];
+        if (t.blocks > 0) {
+          if constexpr (kLoad == 32) tmem_load32(d + c, r);
+          else tmem_load16(d + c, r);
+          tmem_wait_load();
+        } else {
+#pragma unroll
+          for (int j = 0; j < kLoad; ++j) r[j] = 0u;
+        }
+        store_any<kKind, kLoad>(a, t, t.col0 + c, channel, r);
+      }
+      if (t.blocks > 0) {
+        tcgen_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_local(acc_empty + 8 * buffer);
+        ++done;
+      }
+    }
+    __syncwarp();
+  }
+  tcgen_fence_before();
+  __syncthreads();
+  tcgen_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemColumns);
+}
+
+// Lays rows whose bases or strides TMA cannot take out with rows of a
+// multiple of 8 elements.  One thread per 8 elements of the result.
+__global__ void layout_kernel(const uint16_t* src, int64_t row_stride, int64_t group_stride, int rows,
+                              int cols, int64_t groups, uint16_t* dst, int dst_stride) {
+  const int chunks = dst_stride / 8;
+  const int64_t total = groups * rows * chunks;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t line = i / chunks;
+    const int c0 = static_cast<int>(i - line * chunks) * 8;
+    const uint16_t* s = src + line / rows * group_stride + line % rows * row_stride + c0;
+    Pack<uint16_t, 8> p;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) p.v[v] = c0 + v < cols ? s[v] : uint16_t{0};
+    *reinterpret_cast<Pack<uint16_t, 8>*>(dst + line * dst_stride + c0) = p;
+  }
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+  static EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess || found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// A 16-bit tensor [groups, rows, cols] in boxes of box_rows x 64.
+int make_map(CUtensorMap* map, int dtype, const void* data, int64_t cols, int64_t rows, int64_t groups,
+             int64_t row_stride, int64_t group_stride, int box_rows, bool three) {
+  const EncodeFn encode = encoder();
+  if (!encode) return fail_with(DSMEM_HIST_EUNSUPPORTED, "the driver has no tensor maps");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(groups)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_stride) * 2,
+                                 static_cast<cuuint64_t>(group_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, unit[3] = {1, 1, 1};
+  const CUresult r = encode(
+      map, dtype == DSMEM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+      three ? 3 : 2, const_cast<void*>(data), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail_with(DSMEM_HIST_ECUDA, "cuTensorMapEncodeTiled: error %d (%lld x %lld x %lld)",
+                     static_cast<int>(r), static_cast<long long>(cols), static_cast<long long>(rows),
+                     static_cast<long long>(groups));
+  return DSMEM_HIST_OK;
+}
+
+bool tma_ready(const void* p, int64_t row_stride, int64_t group_stride, int64_t groups) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row_stride % 8 == 0 &&
+         (groups == 1 || group_stride % 8 == 0);
+}
+
+// One source of a product, laid out again where TMA cannot read it in place.
+struct Source {
+  const void* data;
+  int64_t row_stride, group_stride;
+  void* scratch = nullptr;
+};
+int prepare(const CallContext& ctx, Source* s, int64_t rows, int64_t cols, int64_t groups,
+            cudaStream_t stream) {
+  if (tma_ready(s->data, s->row_stride, s->group_stride, groups)) {
+    if (groups == 1) s->group_stride = s->row_stride;  // unused, but checked
+    return DSMEM_HIST_OK;
+  }
+  const int64_t stride = (cols + 7) / 8 * 8;
+  int rc = pool_alloc(ctx, &s->scratch, static_cast<size_t>(groups * rows * stride * 2), stream);
+  if (rc) return rc;
+  const int64_t threads = groups * rows * (stride / 8);
+  const int grid = static_cast<int>(std::min<int64_t>((threads + 255) / 256, ctx.sm_count * 16));
+  layout_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(s->data), s->row_stride,
+                                          s->group_stride, static_cast<int>(rows), static_cast<int>(cols),
+                                          groups, static_cast<uint16_t*>(s->scratch),
+                                          static_cast<int>(stride));
+  s->data = s->scratch;
+  s->row_stride = stride;
+  s->group_stride = stride * rows;
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? DSMEM_HIST_OK : fail_with_cuda(e, "layout launch");
+}
+
+template <int kKind, int kCols>
+int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
+           cudaStream_t stream) {
+  TileArgs a{};
+  a.offsets = p.offsets, a.order = p.order, a.n = p.n;
+  a.x_rows = static_cast<int>(p.x_rows), a.groups = p.groups, a.fan = p.fan;
+  a.channels = kKind == kInputGrad ? p.inner : p.outer;
+  a.depth = kKind == kInputGrad ? p.outer : p.inner;
+  a.width = p.inner;
+  a.dtype = p.dtype, a.out_dtype = p.out_dtype, a.out = p.out;
+  a.status = ctx.status;
+  a.wait_cycles = kDefaultWaitCycles;
+
+  Maps m;
+  const int x_cols = kKind == kInputGrad ? p.outer : p.inner;
+  int rc;
+  if (kKind == kWeightGrad) {
+    if ((rc = make_map(&m.a, p.dtype, w.data, p.outer, p.n, 1, w.row_stride, 0, kDepth, false)) ||
+        (rc = make_map(&m.a_gather, p.dtype, w.data, p.outer, p.n, 1, w.row_stride, 0, 1, false)) ||
+        (rc = make_map(&m.b, p.dtype, x.data, x_cols, p.x_rows, 1, x.row_stride, 0, kDepth, false)))
+      return rc;
+  } else {
+    if ((rc = make_map(&m.a, p.dtype, w.data, p.inner, p.outer, p.groups, w.row_stride, w.group_stride,
+                       kKind == kForward ? kChannels : kDepth, true)) ||
+        (rc = make_map(&m.b, p.dtype, x.data, x_cols, p.x_rows, 1, x.row_stride, 0, kCols, false)))
+      return rc;
+    m.a_gather = m.a;
+  }
+  if ((rc = make_map(&m.b_gather, p.dtype, x.data, x_cols, p.x_rows, 1, x.row_stride, 0, 1, false)))
+    return rc;
+
+  const int64_t chan_tiles = (a.channels + kChannels - 1) / kChannels;
+  const int64_t tiles = kKind == kWeightGrad
+                            ? chan_tiles * ((p.inner + kCols - 1) / kCols) * p.groups
+                            : chan_tiles * (p.n / kCols + std::min<int64_t>(p.groups + 1, p.n));
+  if (tiles > INT32_MAX)
+    return fail_with(DSMEM_HIST_EINVAL, "grouped product: more than 2^31 output tiles");
+  const int smem = Ring<kCols>::smem_bytes(p.groups);
+  cudaError_t e = cudaFuncSetAttribute(product_kernel<kKind, kCols>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return fail_with_cuda(e, "cudaFuncSetAttribute");
+  const int grid = static_cast<int>(std::min<int64_t>(tiles, ctx.sm_count));
+  product_kernel<kKind, kCols><<<grid, kThreads, smem, stream>>>(m, a);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? DSMEM_HIST_OK : fail_with_cuda(e, "grouped product launch");
+}
+
+// Tiles as wide as the average group needs, so that few columns are padding.
+template <int kKind>
+int launch_rows(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
+                cudaStream_t stream) {
+  const int64_t average = p.n / p.groups;
+  if (average <= 12) return launch<kKind, 16>(p, ctx, x, w, stream);
+  if (average <= 64) return launch<kKind, 64>(p, ctx, x, w, stream);
+  if (average <= 256) return launch<kKind, 128>(p, ctx, x, w, stream);
+  return launch<kKind, 256>(p, ctx, x, w, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_product(const ProductArgs& a, cudaStream_t stream) {
-  if (a.dtype == DSMEM_F16)
-    return a.out_dtype == DSMEM_F32 ? launch<__half, float>(a, stream)
-                                    : launch<__half, __half>(a, stream);
-  return a.out_dtype == DSMEM_F32 ? launch<__nv_bfloat16, float>(a, stream)
-                                  : launch<__nv_bfloat16, __nv_bfloat16>(a, stream);
+int run_product(const ProductArgs& p, const CallContext& ctx, cudaStream_t stream) {
+  Source x{p.x, p.x_stride, 0}, w{p.w, p.w_stride, p.w_group_stride};
+  int rc = prepare(ctx, &x, p.x_rows, p.kind == kInputGrad ? p.outer : p.inner, 1, stream);
+  if (!rc) {
+    if (p.kind == kWeightGrad) rc = prepare(ctx, &w, p.n, p.outer, 1, stream);
+    else rc = prepare(ctx, &w, p.outer, p.inner, p.groups, stream);
+  }
+  if (!rc) {
+    if (p.kind == kForward) rc = launch_rows<kForward>(p, ctx, x, w, stream);
+    else if (p.kind == kInputGrad) rc = launch_rows<kInputGrad>(p, ctx, x, w, stream);
+    else if (p.inner <= 128) rc = launch<kWeightGrad, 128>(p, ctx, x, w, stream);
+    else rc = launch<kWeightGrad, 256>(p, ctx, x, w, stream);
+  }
+  for (Source* s : {&x, &w})
+    if (s->scratch) {
+      const int freed = pool_free(s->scratch, stream);
+      if (!rc) rc = freed;
+    }
+  return rc;
+}
+
+cudaError_t read_and_clear_product_status(uint32_t* out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_product_status, sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  const uint32_t zero = 0;
+  return *out ? cudaMemcpyToSymbol(g_product_status, &zero, sizeof(uint32_t)) : cudaSuccess;
 }
 
 }  // namespace dsmh

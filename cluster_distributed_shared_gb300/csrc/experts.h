@@ -69,10 +69,10 @@ struct ProductArgs {
   int outer, inner;
   int dtype, out_dtype;
   void* out;
-  uint32_t* status;
-  int sm_count;
 };
-cudaError_t launch_product(const ProductArgs& a, cudaStream_t stream);
+int run_product(const ProductArgs& a, const CallContext& ctx, cudaStream_t stream);
+// Reads (synchronously) and clears the product kernels' device status word.
+cudaError_t read_and_clear_product_status(uint32_t* out);
 
 struct CombineArgs {
   const void* z;

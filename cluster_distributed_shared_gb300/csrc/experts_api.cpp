@@ -114,19 +114,17 @@ int check_product(int64_t x_rows, int32_t groups, int32_t fan, int64_t n, int32_
                out_dtype);
   DSMH_REQUIRE(groups >= 1 && groups <= DSMEM_PRODUCT_MAX_GROUPS, "groups must be in [1, %d] (got %d)",
                DSMEM_PRODUCT_MAX_GROUPS, groups);
-  DSMH_REQUIRE(n >= 0 && n <= kMaxRows && x_rows >= 0 && x_rows <= kMaxRows,
-               "n and x_rows must be in [0, 2^31)");
+  DSMH_REQUIRE(n >= 0 && n <= kMaxRows - 512 && x_rows >= 0 && x_rows <= kMaxRows - 512,
+               "n and x_rows must be in [0, 2^31 - 512)");
   DSMH_REQUIRE(outer >= 1 && inner >= 1, "outer and inner must be >= 1 (got %d and %d)", outer, inner);
   DSMH_REQUIRE(fan >= 1, "fan must be >= 1 (got %d)", fan);
   return DSMEM_HIST_OK;
 }
 
-int run_product(ProductArgs& a, int64_t out_elements, cudaStream_t stream) {
+int multiply(const ProductArgs& a, int64_t out_elements, cudaStream_t stream) {
   CallContext ctx;
   int rc = begin_call(stream, &ctx);
   if (rc) return rc;
-  a.status = ctx.status;
-  a.sm_count = ctx.sm_count;
   // Without rows there is nothing to multiply: the gradient of the weights
   // is 0 and the other products are empty.
   if (a.n == 0 || a.x_rows == 0) {
@@ -134,7 +132,7 @@ int run_product(ProductArgs& a, int64_t out_elements, cudaStream_t stream) {
     return finish(cudaMemsetAsync(a.out, 0, static_cast<size_t>(out_elements) * dtype_size(a.out_dtype),
                                   stream), "cudaMemsetAsync");
   }
-  return finish(launch_product(a, stream), "grouped product launch");
+  return run_product(a, ctx, stream);
 }
 
 int run_grouped_matmul(const void* x, int64_t x_rows, int64_t x_stride, const void* weight,
@@ -160,7 +158,7 @@ int run_grouped_matmul(const void* x, int64_t x_rows, int64_t x_stride, const vo
   a.w = weight, a.w_stride = weight_row_stride, a.w_group_stride = weight_group_stride;
   a.offsets = offsets, a.order = order, a.groups = groups, a.fan = fan, a.n = n;
   a.outer = outer, a.inner = inner, a.dtype = dtype, a.out_dtype = out_dtype, a.out = out;
-  return run_product(a, n * cols, stream);
+  return multiply(a, n * cols, stream);
 }
 
 int run_wgrad(const void* dy, int64_t dy_stride, const void* x, int64_t x_rows, int64_t x_stride,
@@ -184,7 +182,7 @@ int run_wgrad(const void* dy, int64_t dy_stride, const void* x, int64_t x_rows, 
   a.w = dy, a.w_stride = dy_stride, a.w_group_stride = 0;
   a.offsets = offsets, a.order = order, a.groups = groups, a.fan = fan, a.n = n;
   a.outer = outer, a.inner = inner, a.dtype = dtype, a.out_dtype = out_dtype, a.out = out;
-  return run_product(a, static_cast<int64_t>(groups) * outer * inner, stream);
+  return multiply(a, static_cast<int64_t>(groups) * outer * inner, stream);
 }
 
 int check_combine(int64_t tokens, int32_t top_k, int32_t width, int32_t dtype) {
