@@ -9,8 +9,11 @@
 // One persistent CTA per SM; warp 0 copies operand tiles of 64 depth
 // (128 bytes, swizzled) into a ring of stages by TMA, warp 1 issues the matrix
 // instructions into one of two accumulators in tensor memory, and warps 2..5
-// write the other one out.  Rows named by an order are fetched by gathering
-// copies, four rows each, so no reordered copy of x exists anywhere.
+// write the other one out.  Rows named by an order are fetched by warps 6..9
+// with 16-byte asynchronous copies straight into the swizzled layout, so no
+// reordered copy of x exists anywhere.  (Four-row TMA gathers took about 70
+// cycles each, 4.5 times the time of the matrix instructions they feed.)
+// The same warps fill the ragged end of a group's contraction with zeros.
 //
 // The group sizes are on the device only: every CTA lays the groups' tiles
 // end to end from the offsets and takes every gridDim-th.
@@ -34,7 +37,9 @@ using namespace ptx;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kChannels = 128;              // height of a tile
 constexpr int kDepth = 64;                  // depth of a stage: 128 bytes of 16-bit elements
-constexpr int kThreads = 192;               // copies, matrix instructions, 4 warps of output
+constexpr int kThreads = 320;   // TMA, matrix instructions, 4 warps of output, 4 of gathered copies
+constexpr int kGatherThreads = 128;
+constexpr int kStageOut = 4096; // output staging of a warp: 32 x 32 values of up to 4 bytes
 constexpr int kABytes = kChannels * kDepth * 2;
 
 constexpr int kBarrierBytes = 256;
@@ -45,15 +50,13 @@ struct Ring {
   static constexpr int kStages = kCols == 256 ? 4 : (kCols == 128 ? 6 : (kCols == 64 ? 8 : 10));
   static constexpr int kStage = kABytes + kCols * kDepth * 2;
   static int smem_bytes(int groups) {
-    return 1024 + kStages * kStage + kBarrierBytes + 2 * 4 * (groups + 2);
+    return 1024 + kStages * kStage + 4 * kStageOut + kBarrierBytes + 2 * 4 * (groups + 2);
   }
 };
 
 struct Maps {
-  CUtensorMap a;         // weights (3-D), or dy
-  CUtensorMap a_gather;  // dy by single rows (weight gradient's ragged ends)
-  CUtensorMap b;         // x in boxes
-  CUtensorMap b_gather;  // x by single rows
+  CUtensorMap a;  // weights (3-D), or dy
+  CUtensorMap b;  // x
 };
 struct TileArgs {
   const int32_t* offsets;
@@ -64,7 +67,12 @@ struct TileArgs {
   int depth;     // extent of the contraction (forward and input gradient)
   int width;     // weight gradient: extent of the tiles' width, inner
   int dtype, out_dtype;
+  const uint16_t* x;   // for the gathered copies: rows 16-byte aligned
+  int64_t x_stride;
+  const uint16_t* dy;  // weight gradient
+  int64_t dy_stride;
   void* out;
+  int wide_out;        // rows of the output are 16-byte aligned
   uint32_t* status;
   long long wait_cycles;
 };
@@ -104,6 +112,30 @@ template <bool kMnMajor>
 __device__ __forceinline__ uint64_t descriptor(uint32_t addr) {
   return kDescBase | (uint64_t{kMnMajor ? 8192 >> 4 : 1} << 16) | ((addr & 0x3ffffu) >> 4);
 }
+__device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+template <typename P>
+__device__ __forceinline__ void st_shared_16(uint32_t addr, const P& p) {
+  static_assert(sizeof(P) == 16, "one vector");
+  const uint4 v = *reinterpret_cast<const uint4*>(&p);
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+template <typename O>
+__device__ __forceinline__ void st_shared_value(uint32_t addr, O v) {
+  if constexpr (sizeof(O) == 2) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(*reinterpret_cast<const uint16_t*>(&v)) : "memory");
+  } else {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(static_cast<float>(v)) : "memory");
+  }
+}
+
 struct Tile {
   int group;     // `groups`: the rows behind the last group
   int begin, end;  // the group's rows
@@ -149,47 +181,167 @@ struct Schedule {
   }
 };
 
-template <typename O>
-__device__ __forceinline__ O* out_at(const TileArgs& a, int64_t i) {
-  return static_cast<O*>(a.out) + i;
-}
-
-// 16 or 32 accumulator columns of one lane (channel) to global memory.
+// kN accumulator columns of a warp's 32 lanes (channels) to global memory.
+// Rows of the output are columns of the tile (forward, input gradient) or
+// channels (weight gradient); either way the warp's block becomes 16-byte
+// pieces of output rows through its staging memory.  Without 16-byte rows
+// each value goes by itself.
 template <int kKind, int kN, typename O>
-__device__ __forceinline__ void store_columns(const TileArgs& a, const Tile& t, int col, int channel,
-                                              const uint32_t (&r)[kN]) {
-  if (channel >= a.channels) return;
+__device__ __forceinline__ void store_block(const TileArgs& a, const Tile& t, int col, int channel0,
+                                            const uint32_t (&r)[kN], uint32_t staging) {
+  const int lane = threadIdx.x & 31;
+  constexpr int V = 16 / sizeof(O);
   if (kKind == kWeightGrad) {
-    // The lane's channel is a row of the output; its columns are contiguous.
-    O* out = out_at<O>(a, (static_cast<int64_t>(t.group) * a.channels + channel) * a.width + col);
-    constexpr int V = 16 / sizeof(O);
-    if (col + kN <= a.width && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
+    constexpr int kPieces = kN / V;  // 16-byte pieces of a staged row
+    const int channel = channel0 + lane;
+    O* out = static_cast<O*>(a.out) + static_cast<int64_t>(t.group) * a.channels * a.width;
+    if (a.wide_out) {
 #pragma unroll
-      for (int j = 0; j < kN; j += V) {
+      for (int q = 0; q < kPieces; ++q) {
         Pack<O, V> p;
 #pragma unroll
-        for (int v = 0; v < V; ++v) p.v[v] = from_float<O>(__uint_as_float(r[j + v]));
-        *reinterpret_cast<Pack<O, V>*>(out + j) = p;
+        for (int v = 0; v < V; ++v) p.v[v] = from_float<O>(__uint_as_float(r[q * V + v]));
+        st_shared_16(staging + lane * (kN * sizeof(O)) + ((q ^ (lane & (kPieces - 1))) << 4), p);
       }
-    } else {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int row = (i * 32 + lane) / kPieces, q = lane & (kPieces - 1);
+        const uint4 p = ld_shared_16(staging + row * (kN * sizeof(O)) + ((q ^ (row & (kPieces - 1))) << 4));
+        if (channel0 + row < a.channels && col + q * V < a.width)
+          *reinterpret_cast<uint4*>(out + static_cast<int64_t>(channel0 + row) * a.width + col + q * V) = p;
+      }
+      __syncwarp();
+    } else if (channel < a.channels) {
+      out += static_cast<int64_t>(channel) * a.width + col;
 #pragma unroll
       for (int j = 0; j < kN; ++j)
         if (col + j < a.width) out[j] = from_float<O>(__uint_as_float(r[j]));
     }
   } else {
-    // Columns are output rows; the warp's 32 lanes write neighbouring channels.
-    O* out = out_at<O>(a, static_cast<int64_t>(col) * a.channels + channel);
+    O* out = static_cast<O*>(a.out) + static_cast<int64_t>(col) * a.channels + channel0;
+    if (a.wide_out) {
+      constexpr int kPieces = 32 / V;  // of a staged row: 32 channels
 #pragma unroll
-    for (int j = 0; j < kN; ++j)
-      if (col + j < t.end) out[static_cast<int64_t>(j) * a.channels] = from_float<O>(__uint_as_float(r[j]));
+      for (int j = 0; j < kN; ++j)
+        st_shared_value(staging + (j * 32 + lane) * sizeof(O), from_float<O>(__uint_as_float(r[j])));
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kN * kPieces / 32; ++i) {
+        const int row = (i * 32 + lane) / kPieces, q = lane & (kPieces - 1);
+        const uint4 p = ld_shared_16(staging + (row * kPieces + q) * 16);
+        if (col + row < t.end && channel0 + q * V < a.channels)
+          *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row) * a.channels + q * V) = p;
+      }
+      __syncwarp();
+    } else if (channel0 + lane < a.channels) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+        if (col + j < t.end)
+          out[static_cast<int64_t>(j) * a.channels + lane] = from_float<O>(__uint_as_float(r[j]));
+    }
   }
 }
 template <int kKind, int kN>
-__device__ __forceinline__ void store_any(const TileArgs& a, const Tile& t, int col, int channel,
-                                          const uint32_t (&r)[kN]) {
-  if (a.out_dtype == DSMEM_F32) store_columns<kKind, kN, float>(a, t, col, channel, r);
-  else if (a.out_dtype == DSMEM_F16) store_columns<kKind, kN, __half>(a, t, col, channel, r);
-  else store_columns<kKind, kN, __nv_bfloat16>(a, t, col, channel, r);
+__device__ __forceinline__ void store_any(const TileArgs& a, const Tile& t, int col, int channel0,
+                                          const uint32_t (&r)[kN], uint32_t staging) {
+  if (a.out_dtype == DSMEM_F32) store_block<kKind, kN, float>(a, t, col, channel0, r, staging);
+  else if (a.out_dtype == DSMEM_F16) store_block<kKind, kN, __half>(a, t, col, channel0, r, staging);
+  else store_block<kKind, kN, __nv_bfloat16>(a, t, col, channel0, r, staging);
+}
+
+// The gathering warps: x's rows named by the order, and the rows of a ragged
+// stage of the weight gradient (dy's too), 16 bytes a copy.  Each thread's
+// arrival on the stage's barrier follows its copies by itself.
+template <int kKind, int kCols>
+__device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, kCols>& schedule, int total,
+                                            uint32_t base, uint32_t full, uint32_t empty,
+                                            uint32_t gave_up) {
+  constexpr int kStages = Ring<kCols>::kStages, kStage = Ring<kCols>::kStage;
+  constexpr bool kBMn = kKind == kWeightGrad;
+  const int tid = threadIdx.x - 6 * 32, lane = threadIdx.x & 31;
+  uint32_t stage = 0, phase = 0;
+  bool ok = true;
+
+  const auto source_row = [&](int p, int end) {
+    if (p >= end) return -1;
+    if (!a.order) return p < a.x_rows ? p : -1;
+    const int o = a.order[p];
+    const int row = o < 0 ? -1 : o / a.fan;
+    return row < a.x_rows ? row : -1;
+  };
+  for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+    const Tile t = schedule.at(i);
+    if (t.blocks == 0) continue;
+    // Forward and input gradient: 8 threads a row of 128 bytes; the rows are
+    // the same in every stage of the tile.
+    constexpr int kRows = kBMn ? 1 : kCols / (kGatherThreads / 8);
+    int row[kRows];
+    if (!kBMn) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) row[r] = source_row(t.col0 + r * (kGatherThreads / 8) + tid / 8, t.end);
+    }
+    // Weight gradient: kPieces threads a row of kCols elements.  A warp's 16
+    // rows of a stage are found by its lanes 0..15, one stage ahead.
+    constexpr int kPieces = kCols / 8, kAtOnce = kGatherThreads / kPieces, kPerWarp = 32 / kPieces;
+    const auto stage_row = [&](int k) {
+      const int l = lane & 15;
+      const int r = l / kPerWarp * kAtOnce + (tid >> 5) * kPerWarp + l % kPerWarp;
+      return source_row(t.begin + k * kDepth + r, t.end);
+    };
+    int ahead = kBMn ? stage_row(0) : 0;
+
+    for (int k = 0; k < t.blocks; ++k) {
+      const int here = ahead;
+      if (kBMn && k + 1 < t.blocks) ahead = stage_row(k + 1);
+      ok = __all_sync(kFull, wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status));
+      if (!ok) break;
+      const uint32_t sa = base + stage * kStage, sb = sa + kABytes;
+      if (!kBMn) {
+        const int c = tid & 7, col = k * kDepth + c * 8;
+        const int left = max(0, min(16, (a.depth - col) * 2));
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const int line = r * (kGatherThreads / 8) + tid / 8;
+          const bool read = row[r] >= 0 && left > 0;
+          copy16(sb + line * 128 + ((c ^ (line & 7)) << 4),
+                 a.x + (read ? row[r] * a.x_stride + col : 0), read ? left : 0);
+        }
+      } else {
+        const int p0 = t.begin + k * kDepth;
+        const bool ragged = p0 + kDepth > t.end;
+        if (a.order || ragged) {
+          const int c = tid % kPieces, col = t.col0 + c * 8;
+          const int left = max(0, min(16, (a.width - col) * 2));
+#pragma unroll
+          for (int r = 0; r < kDepth / kAtOnce; ++r) {
+            const int line = r * kAtOnce + tid / kPieces;
+            const int from = __shfl_sync(kFull, here, r * kPerWarp + lane / kPieces);
+            const bool read = from >= 0 && left > 0;
+            copy16(sb + (c >> 3) * 8192 + line * 128 + (((c & 7) ^ (line & 7)) << 4),
+                   a.x + (read ? from * a.x_stride + col : 0), read ? left : 0);
+          }
+        }
+        if (ragged) {
+          const int c = tid & 15, col = t.chan0 + c * 8;
+          const int left = max(0, min(16, (a.channels - col) * 2));
+#pragma unroll
+          for (int r = 0; r < kDepth / 8; ++r) {
+            const int line = r * 8 + tid / 16;
+            const bool read = p0 + line < t.end && left > 0;
+            copy16(sa + (c >> 3) * 8192 + line * 128 + (((c & 7) ^ (line & 7)) << 4),
+                   a.dy + (read ? (p0 + line) * a.dy_stride + col : 0), read ? left : 0);
+          }
+        }
+      }
+      copy_arrive(full + 8 * stage);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+  copy_wait_all();
 }
 
 template <int kKind, int kCols>
@@ -205,20 +357,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* base_ptr = raw + (base - smem_u32(raw));
-  const uint32_t bars = base + kStages * kStage;
+  const uint32_t out_staging = base + kStages * kStage;
+  const uint32_t bars = out_staging + 4 * kStageOut;
   const uint32_t full = bars, empty = bars + 8 * kStages;
   const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
   const uint32_t tmem_at = drained + 8, gave_up = tmem_at + 4;
   static_assert(8 * (2 * kStages + 5) + 8 <= kBarrierBytes, "barriers");
-  int32_t* begin = reinterpret_cast<int32_t*>(base_ptr + kStages * kStage + kBarrierBytes);
+  int32_t* begin = reinterpret_cast<int32_t*>(base_ptr + (bars - base) + kBarrierBytes);
   int32_t* first = begin + a.groups + 2;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Schedule<kKind, kCols> schedule(begin, first, a);
+  // The gathering warps take part in every stage where x is gathered, or
+  // where a contraction may end inside a stage.
+  const bool gathering = kBMn || a.order;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + 8 * s, 1);
+      mbar_init(full + 8 * s, gathering ? 1 + kGatherThreads : 1);
       mbar_init(empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -278,80 +434,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int total = schedule.total();
 
   if (warp == 0) {
-    // Copies.
+    // TMA copies, by one thread.
+    if (lane == 0) {
     uint32_t stage = 0, phase = 0, issued = 0;
     bool ok = true;
     for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
       const Tile t = schedule.at(i);
-      if (t.blocks == 0) continue;
-      // Forward and input gradient: the gathered rows are the same in every
-      // stage of the tile, four for each lane's copy.
-      constexpr int kQuads = kBMn ? 1 : (kCols + 127) / 128;
-      int rows[kQuads][4];
-      if (!kBMn && a.order) {
-#pragma unroll
-        for (int q = 0; q < kQuads; ++q)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int p = t.col0 + (q * 32 + lane) * 4 + v;
-            const int o = p < t.end ? a.order[p] : -1;
-            rows[q][v] = o < 0 ? -1 : o / a.fan;
-          }
-      }
       for (int k = 0; k < t.blocks; ++k) {
-        // Weight gradient: this stage's 64 rows of the group, lane & 15 taking
-        // a quad of them; rows behind the group's end are read as zeros.
-        const int p0 = t.begin + k * kDepth;
-        const bool ragged = kBMn && p0 + kDepth > t.end;
-        if (kBMn && (a.order || ragged)) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int p = p0 + (lane & 15) * 4 + v;
-            int row = p < t.end ? p : -1;
-            if (a.order && row >= 0) {
-              const int o = a.order[p];
-              row = o < 0 ? -1 : o / a.fan;
-            }
-            rows[0][v] = row;
-          }
-        }
         ok = wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
-        if (!__all_sync(kFull, ok)) {
-          ok = false;
-          break;
-        }
+        if (!ok) break;
         const uint32_t bar = full + 8 * stage, sa = base + stage * kStage, sb = sa + kABytes;
-        if (lane == 0) mbar_expect_tx(bar, kStage);
-        __syncwarp();
+        const int p0 = t.begin + k * kDepth;  // weight gradient: the stage's first row
+        const bool ragged = kBMn && p0 + kDepth > t.end;
+        mbar_expect_tx(bar, ragged ? 0 : (a.order ? kABytes : kStage));
         if (kKind == kForward) {
-          if (lane == 0) tma_load_3d(sa, &maps.a, k * kDepth, t.chan0, t.group, bar);
+          tma_load_3d(sa, &maps.a, k * kDepth, t.chan0, t.group, bar);
         } else if (kKind == kInputGrad) {
-          if (lane < 2) tma_load_3d(sa + lane * 8192, &maps.a, t.chan0 + lane * 64, k * kDepth, t.group, bar);
+          tma_load_3d(sa, &maps.a, t.chan0, k * kDepth, t.group, bar);
+          tma_load_3d(sa + 8192, &maps.a, t.chan0 + 64, k * kDepth, t.group, bar);
         } else if (!ragged) {
-          if (lane < 2) tma_load_2d(sa + lane * 8192, &maps.a, t.chan0 + lane * 64, p0, bar);
-        } else {
-          const int p = p0 + (lane & 15) * 4, box = lane >> 4;
-          tma_gather4(sa + box * 8192 + (lane & 15) * 512, &maps.a_gather, t.chan0 + box * 64,
-                      p < t.end ? p : -1, p + 1 < t.end ? p + 1 : -1, p + 2 < t.end ? p + 2 : -1,
-                      p + 3 < t.end ? p + 3 : -1, bar);
+          tma_load_2d(sa, &maps.a, t.chan0, p0, bar);
+          tma_load_2d(sa + 8192, &maps.a, t.chan0 + 64, p0, bar);
         }
-        if (kBMn) {
-          if (a.order || ragged) {
+        if (!a.order && !ragged) {
+          if (kBMn) {
 #pragma unroll
-            for (int box = lane >> 4; box < kCols / 64; box += 2)
-              tma_gather4(sb + box * 8192 + (lane & 15) * 512, &maps.b_gather, t.col0 + box * 64,
-                          rows[0][0], rows[0][1], rows[0][2], rows[0][3], bar);
-          } else if (lane < kCols / 64) {
-            tma_load_2d(sb + lane * 8192, &maps.b, t.col0 + lane * 64, p0, bar);
+            for (int box = 0; box < kCols / 64; ++box)
+              tma_load_2d(sb + box * 8192, &maps.b, t.col0 + box * 64, p0, bar);
+          } else {
+            tma_load_2d(sb, &maps.b, k * kDepth, t.col0, bar);
           }
-        } else if (a.order) {
-#pragma unroll
-          for (int q = 0; q < kQuads; ++q)
-            if ((q * 32 + lane) * 4 < kCols)
-              tma_gather4(sb + (q * 32 + lane) * 512, &maps.b_gather, k * kDepth, rows[q][0], rows[q][1],
-                          rows[q][2], rows[q][3], bar);
-        } else if (lane == 0) {
-          tma_load_2d(sb, &maps.b, k * kDepth, t.col0, bar);
         }
         ++issued;
         if (++stage == kStages) {
@@ -361,7 +473,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // After a wait that gave up: let this CTA's copies land before its shared
-    // memory goes.  Copy j (from 0) completes phase j / kStages of its stage.
+    // memory goes.  Copy j (from 0) completes phase j / kStages of its stage
+    // (where the gathering warps came along; else the wait runs out).
     if (flag_set(gave_up)) {
       for (uint32_t j = issued > kStages ? issued - kStages : 0; j < issued; ++j) {
         const long long deadline = clock64() + kDefaultWaitCycles;
@@ -369,7 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    }
     __syncwarp();
+  } else if (warp >= 6) {
+    if (gathering) gather_rows<kKind, kCols>(a, schedule, total, base, full, empty, gave_up);
   } else if (warp == 1) {
     // Matrix instructions, by one thread.
     if (lane == 0) {
@@ -388,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < t.blocks; ++k) {
           ok = wait_for(full + 8 * stage, phase, gave_up, a.wait_cycles, a.status);
           if (!ok) break;
+          if (gathering) fence_async_shared();
           tcgen_fence_after();
           const uint32_t sa = base + stage * kStage;
           const uint64_t da = descriptor<kAMn>(sa), db = descriptor<kBMn>(sa + kABytes);
@@ -418,7 +535,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t done = 0;
     for (int i = blockIdx.x; i < total; i += gridDim.x) {
       const Tile t = schedule.at(i);
-      const int channel = t.chan0 + quadrant * 32 + lane;
       const uint32_t buffer = done & 1;
       if (t.blocks > 0) {
         // A long contraction may take longer than one bounded wait of a copy.
@@ -441,7 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kLoad; ++j) r[j] = 0u;
         }
-        store_any<kKind, kLoad>(a, t, t.col0 + c, channel, r);
+        store_any<kKind, kLoad>(a, t, t.col0 + c, t.chan0 + quadrant * 32, r,
+                                out_staging + quadrant * kStageOut);
       }
       if (t.blocks > 0) {
         tcgen_fence_before();
@@ -555,6 +672,10 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
   a.depth = kKind == kInputGrad ? p.outer : p.inner;
   a.width = p.inner;
   a.dtype = p.dtype, a.out_dtype = p.out_dtype, a.out = p.out;
+  a.x = static_cast<const uint16_t*>(x.data), a.x_stride = x.row_stride;
+  a.dy = static_cast<const uint16_t*>(w.data), a.dy_stride = w.row_stride;
+  const int64_t out_cols = kKind == kWeightGrad ? a.width : a.channels;
+  a.wide_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && out_cols * dtype_size(p.out_dtype) % 16 == 0;
   a.status = ctx.status;
   a.wait_cycles = kDefaultWaitCycles;
 
@@ -563,7 +684,6 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
   int rc;
   if (kKind == kWeightGrad) {
     if ((rc = make_map(&m.a, p.dtype, w.data, p.outer, p.n, 1, w.row_stride, 0, kDepth, false)) ||
-        (rc = make_map(&m.a_gather, p.dtype, w.data, p.outer, p.n, 1, w.row_stride, 0, 1, false)) ||
         (rc = make_map(&m.b, p.dtype, x.data, x_cols, p.x_rows, 1, x.row_stride, 0, kDepth, false)))
       return rc;
   } else {
@@ -571,10 +691,7 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
                        kKind == kForward ? kChannels : kDepth, true)) ||
         (rc = make_map(&m.b, p.dtype, x.data, x_cols, p.x_rows, 1, x.row_stride, 0, kCols, false)))
       return rc;
-    m.a_gather = m.a;
   }
-  if ((rc = make_map(&m.b_gather, p.dtype, x.data, x_cols, p.x_rows, 1, x.row_stride, 0, 1, false)))
-    return rc;
 
   const int64_t chan_tiles = (a.channels + kChannels - 1) / kChannels;
   const int64_t tiles = kKind == kWeightGrad
