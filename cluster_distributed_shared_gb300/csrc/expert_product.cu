@@ -35,20 +35,25 @@ namespace {
 using namespace ptx;
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kChannels = 128;              // height of a tile
-constexpr int kDepth = 64;                  // depth of a stage: 128 bytes of 16-bit elements
-constexpr int kThreads = 320;   // TMA, matrix instructions, 4 warps of output, 4 of gathered copies
-constexpr int kGatherThreads = 128;
+constexpr int kChannels = 128;  // channels of a tile in one CTA
+constexpr int kDepth = 64;      // depth of a stage: 128 bytes of 16-bit elements
+constexpr int kGatherThreads = 256;
+constexpr int kThreads = 192 + kGatherThreads;  // TMA, matrix instructions, 4 warps of output, gathering
 constexpr int kStageOut = 4096; // output staging of a warp: 32 x 32 values of up to 4 bytes
 constexpr int kABytes = kChannels * kDepth * 2;
 
 constexpr int kBarrierBytes = 256;
 
-// A ring of as many stages as fit beside the tables (227 KB in all).
-template <int kCols>
+// Where two CTAs of a cluster pair up (kPair), a tile is 256 channels high:
+// each CTA holds 128 channels of A and half of the columns of B, and one
+// matrix instruction reads both.  That halves the bytes of B a CTA takes in.
+template <int kCols, bool kPair>
 struct Ring {
-  static constexpr int kStages = kCols == 256 ? 4 : (kCols == 128 ? 6 : (kCols == 64 ? 8 : 10));
-  static constexpr int kStage = kABytes + kCols * kDepth * 2;
+  static constexpr int kMine = kPair ? kCols / 2 : kCols;  // columns this CTA brings in
+  static constexpr int kStage = kABytes + kMine * kDepth * 2;
+  // As many stages as fit beside the tables (227 KB in all).
+  static constexpr int kStages = kMine == 256 ? 4 : (kMine == 128 ? 6 : (kMine == 64 ? 8 : 10));
+  static constexpr int kHeight = kPair ? 2 * kChannels : kChannels;  // channels of a tile
   static int smem_bytes(int groups) {
     return 1024 + kStages * kStage + 4 * kStageOut + kBarrierBytes + 2 * 4 * (groups + 2);
   }
@@ -58,11 +63,25 @@ struct Maps {
   CUtensorMap a;  // weights (3-D), or dy
   CUtensorMap b;  // x
 };
+// Division of 31-bit values by a fixed divisor: with l = ceil(log2 d) and
+// m = floor(2^32 (2^l - d) / d) + 1, the quotient is (mulhi(m, v) + v) >> l.
+struct Divisor {
+  uint32_t m, l;
+  Divisor(uint32_t d = 1) : m(0), l(0) {
+    while ((uint64_t{1} << l) < d) ++l;
+    m = static_cast<uint32_t>((uint64_t{1} << 32) * ((uint64_t{1} << l) - d) / d + 1);
+  }
+  __device__ __forceinline__ int quotient(int v) const {
+    return static_cast<int>((__umulhi(m, static_cast<uint32_t>(v)) + static_cast<uint32_t>(v)) >> l);
+  }
+};
+
 struct TileArgs {
   const int32_t* offsets;
   const int32_t* order;
   int64_t n;
-  int x_rows, groups, fan;
+  int x_rows, groups;
+  Divisor fan;
   int channels;  // extent of the tiles' height: outer, inner, outer
   int depth;     // extent of the contraction (forward and input gradient)
   int width;     // weight gradient: extent of the tiles' width, inner
@@ -144,15 +163,16 @@ struct Tile {
   int blocks;    // stages of depth
 };
 
-template <int kKind, int kCols>
+template <int kKind, int kCols, bool kPair>
 struct Schedule {
   const int32_t* begin;  // [groups + 2] first row of each group, in shared memory
   const int32_t* first;  // [groups + 2] first tile of each group
   int groups, chan_tiles, width_tiles, depth_blocks;
   int group;
+  static constexpr int kHeight = Ring<kCols, kPair>::kHeight;
 
   __device__ __forceinline__ Schedule(const int32_t* b, const int32_t* f, const TileArgs& a)
-      : begin(b), first(f), groups(a.groups), chan_tiles((a.channels + kChannels - 1) / kChannels),
+      : begin(b), first(f), groups(a.groups), chan_tiles((a.channels + kHeight - 1) / kHeight),
         width_tiles(kKind == kWeightGrad ? (a.width + kCols - 1) / kCols : 0),
         depth_blocks((a.depth + kDepth - 1) / kDepth), group(0) {}
   __device__ __forceinline__ int tiles_of(int rows) const {
@@ -169,7 +189,7 @@ struct Schedule {
     r.begin = begin[group];
     r.end = begin[group + 1];
     const int i = t - first[group];
-    r.chan0 = i % chan_tiles * kChannels;
+    r.chan0 = i % chan_tiles * kHeight;
     if (kKind == kWeightGrad) {
       r.col0 = i / chan_tiles * kCols;
       r.blocks = (r.end - r.begin + kDepth - 1) / kDepth;
@@ -251,50 +271,73 @@ __device__ __forceinline__ void store_any(const TileArgs& a, const Tile& t, int 
 }
 
 // The gathering warps: x's rows named by the order, and the rows of a ragged
-// stage of the weight gradient (dy's too), 16 bytes a copy.  Each thread's
-// arrival on the stage's barrier follows its copies by itself.
-template <int kKind, int kCols>
-__device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, kCols>& schedule, int total,
-                                            uint32_t base, uint32_t full, uint32_t empty,
-                                            uint32_t gave_up) {
-  constexpr int kStages = Ring<kCols>::kStages, kStage = Ring<kCols>::kStage;
+// stage of the weight gradient (dy's too), 16 bytes a copy.  A warp hands a
+// stage on, with one arrival on the leader's barrier, when its copies have
+// landed, kLag stages after it issued them.  (Arrivals by each thread's copies
+// themselves, 128 a stage on one barrier, held a stage up for 1000 cycles.)
+template <int kKind, int kCols, bool kPair>
+__device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, kCols, kPair>& schedule,
+                                            int unit, int units, uint32_t rank, int total, uint32_t base,
+                                            uint32_t full, uint32_t empty, uint32_t gave_up) {
+  using R = Ring<kCols, kPair>;
+  constexpr int kStages = R::kStages, kStage = R::kStage, kMine = R::kMine;
   constexpr bool kBMn = kKind == kWeightGrad;
+  constexpr int kLag = 2;
   const int tid = threadIdx.x - 6 * 32, lane = threadIdx.x & 31;
-  uint32_t stage = 0, phase = 0;
+  uint32_t stage = 0, phase = 0, pending = 0, oldest = 0;
   bool ok = true;
 
-  const auto source_row = [&](int p, int end) {
-    if (p >= end) return -1;
-    if (!a.order) return p < a.x_rows ? p : -1;
-    const int o = a.order[p];
-    const int row = o < 0 ? -1 : o / a.fan;
+  // The order's entry for place p and the row of x it names.  Apart, so that
+  // the load's latency is not waited for where it is issued.
+  const auto place = [&](int p, int end) { return p < end ? (a.order ? a.order[p] : p) : -1; };
+  const auto named_row = [&](int o) {
+    const int row = o < 0 ? -1 : (a.order ? a.fan.quotient(o) : o);
     return row < a.x_rows ? row : -1;
   };
-  for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+  const auto hand_on = [&] {
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (kPair) mbar_arrive_pair(map_rank(full + 8 * oldest, 0));
+      else mbar_arrive_local(full + 8 * oldest);
+    }
+    if (++oldest == kStages) oldest = 0;
+    --pending;
+  };
+
+  for (int i = unit; i < total && ok; i += units) {
     const Tile t = schedule.at(i);
     if (t.blocks == 0) continue;
+    const int col0 = t.col0 + rank * kMine, chan0 = t.chan0 + rank * kChannels;
     // Forward and input gradient: 8 threads a row of 128 bytes; the rows are
     // the same in every stage of the tile.
-    constexpr int kRows = kBMn ? 1 : kCols / (kGatherThreads / 8);
+    constexpr int kLines = kGatherThreads / 8, kRows = kBMn ? 1 : (kMine + kLines - 1) / kLines;
     int row[kRows];
     if (!kBMn) {
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) row[r] = source_row(t.col0 + r * (kGatherThreads / 8) + tid / 8, t.end);
+      for (int r = 0; r < kRows; ++r) row[r] = place(col0 + r * kLines + tid / 8, t.end);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) row[r] = named_row(row[r]);
     }
-    // Weight gradient: kPieces threads a row of kCols elements.  A warp's 16
-    // rows of a stage are found by its lanes 0..15, one stage ahead.
-    constexpr int kPieces = kCols / 8, kAtOnce = kGatherThreads / kPieces, kPerWarp = 32 / kPieces;
-    const auto stage_row = [&](int k) {
-      const int l = lane & 15;
+    // Weight gradient: kPieces threads a row of kMine elements.  A warp needs
+    // kFound rows of a stage; its lanes look up those of kBatch stages at once,
+    // a batch ahead, as the order's entries take longer to arrive than a stage.
+    constexpr int kPieces = kMine / 8, kAtOnce = kGatherThreads / kPieces, kPerWarp = 32 / kPieces;
+    constexpr int kFound = kDepth / (kGatherThreads / 32), kBatch = 32 / kFound;
+    const auto batch_place = [&](int k) {
+      const int l = lane % kFound;
       const int r = l / kPerWarp * kAtOnce + (tid >> 5) * kPerWarp + l % kPerWarp;
-      return source_row(t.begin + k * kDepth + r, t.end);
+      return place(t.begin + (k + lane / kFound) * kDepth + r, t.end);
     };
-    int ahead = kBMn ? stage_row(0) : 0;
+    int ahead = kBMn ? batch_place(0) : 0, here = 0;
 
     for (int k = 0; k < t.blocks; ++k) {
-      const int here = ahead;
-      if (kBMn && k + 1 < t.blocks) ahead = stage_row(k + 1);
-      ok = __all_sync(kFull, wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status));
+      if (kBMn && k % kBatch == 0) {
+        here = named_row(ahead);
+        ahead = batch_place(k + kBatch);
+      }
+      if (lane == 0) ok = wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
+      ok = __shfl_sync(kFull, ok, 0);
       if (!ok) break;
       const uint32_t sa = base + stage * kStage, sb = sa + kABytes;
       if (!kBMn) {
@@ -302,52 +345,59 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
         const int left = max(0, min(16, (a.depth - col) * 2));
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-          const int line = r * (kGatherThreads / 8) + tid / 8;
+          const int line = r * kLines + tid / 8;
           const bool read = row[r] >= 0 && left > 0;
-          copy16(sb + line * 128 + ((c ^ (line & 7)) << 4),
+          if (kMine % kLines == 0 || line < kMine)
+            copy16(sb + line * 128 + ((c ^ (line & 7)) << 4),
                  a.x + (read ? row[r] * a.x_stride + col : 0), read ? left : 0);
         }
       } else {
         const int p0 = t.begin + k * kDepth;
         const bool ragged = p0 + kDepth > t.end;
         if (a.order || ragged) {
-          const int c = tid % kPieces, col = t.col0 + c * 8;
+          const int c = tid % kPieces, col = col0 + c * 8;
           const int left = max(0, min(16, (a.width - col) * 2));
 #pragma unroll
           for (int r = 0; r < kDepth / kAtOnce; ++r) {
             const int line = r * kAtOnce + tid / kPieces;
-            const int from = __shfl_sync(kFull, here, r * kPerWarp + lane / kPieces);
+            const int from = __shfl_sync(kFull, here, k % kBatch * kFound + r * kPerWarp + lane / kPieces);
             const bool read = from >= 0 && left > 0;
             copy16(sb + (c >> 3) * 8192 + line * 128 + (((c & 7) ^ (line & 7)) << 4),
                    a.x + (read ? from * a.x_stride + col : 0), read ? left : 0);
           }
         }
         if (ragged) {
-          const int c = tid & 15, col = t.chan0 + c * 8;
+          const int c = tid & 15, col = chan0 + c * 8;
           const int left = max(0, min(16, (a.channels - col) * 2));
 #pragma unroll
-          for (int r = 0; r < kDepth / 8; ++r) {
-            const int line = r * 8 + tid / 16;
+          for (int r = 0; r < kDepth * 16 / kGatherThreads; ++r) {
+            const int line = r * (kGatherThreads / 16) + tid / 16;
             const bool read = p0 + line < t.end && left > 0;
             copy16(sa + (c >> 3) * 8192 + line * 128 + (((c & 7) ^ (line & 7)) << 4),
                    a.dy + (read ? (p0 + line) * a.dy_stride + col : 0), read ? left : 0);
           }
         }
       }
-      copy_arrive(full + 8 * stage);
+      copy_commit();
+      if (++pending > kLag) {
+        copy_wait<kLag>();
+        hand_on();
+      }
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1;
       }
     }
   }
-  copy_wait_all();
+  copy_wait<0>();
+  while (pending > 0) hand_on();
 }
 
-template <int kKind, int kCols>
+template <int kKind, int kCols, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ TileArgs a) {
-  constexpr int kStages = Ring<kCols>::kStages, kStage = Ring<kCols>::kStage;
+  using R = Ring<kCols, kPair>;
+  constexpr int kStages = R::kStages, kStage = R::kStage, kMine = R::kMine;
   constexpr bool kAMn = kKind != kForward, kBMn = kKind == kWeightGrad;
   constexpr uint32_t kTmemColumns = 2 * kCols < 32 ? 32 : 2 * kCols;
   constexpr int kLoad = kCols < 32 ? 16 : 32;
@@ -367,19 +417,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t* first = begin + a.groups + 2;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Schedule<kKind, kCols> schedule(begin, first, a);
+  Schedule<kKind, kCols, kPair> schedule(begin, first, a);
+  // A unit works on a tile: a CTA, or a pair whose first CTA leads.
+  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+  const int unit = kPair ? blockIdx.x / 2 : blockIdx.x, units = kPair ? gridDim.x / 2 : gridDim.x;
   // The gathering warps take part in every stage where x is gathered, or
   // where a contraction may end inside a stage.
   const bool gathering = kBMn || a.order;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + 8 * s, gathering ? 1 + kGatherThreads : 1);
+      // Of a pair, the leader's barriers count both CTAs' arrivals.
+      mbar_init(full + 8 * s, 1 + (gathering ? kGatherThreads / 32 * (kPair ? 2 : 1) : 0));
       mbar_init(empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + 8 * i, 1);
-      mbar_init(acc_empty + 8 * i, 4);
+      mbar_init(acc_empty + 8 * i, kPair ? 8 : 4);
     }
     mbar_init(drained, 1);
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(gave_up), "r"(0u) : "memory");
@@ -397,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     begin[0] = first[0] = 0;
     begin[a.groups + 1] = static_cast<int32_t>(a.n);
   }
-  if (warp == 1) tmem_alloc(tmem_at, kTmemColumns);
+  if (warp == 1) tmem_alloc<kPair>(tmem_at, kTmemColumns);
   __syncthreads();
   if (warp == 2) {
     int end_before = 0, tiles_before = 0;
@@ -427,7 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   tcgen_fence_before();
-  __syncthreads();
+  if (kPair) cluster_barrier();
+  else __syncthreads();
   tcgen_fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_at));
@@ -438,31 +493,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
     uint32_t stage = 0, phase = 0, issued = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+    for (int i = unit; i < total && ok; i += units) {
       const Tile t = schedule.at(i);
       for (int k = 0; k < t.blocks; ++k) {
         ok = wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
         if (!ok) break;
-        const uint32_t bar = full + 8 * stage, sa = base + stage * kStage, sb = sa + kABytes;
+        const uint32_t sa = base + stage * kStage, sb = sa + kABytes;
+        const uint32_t bar = kPair ? map_rank(full + 8 * stage, 0) : full + 8 * stage;
         const int p0 = t.begin + k * kDepth;  // weight gradient: the stage's first row
+        const int chan0 = t.chan0 + rank * kChannels, col0 = t.col0 + rank * kMine;
         const bool ragged = kBMn && p0 + kDepth > t.end;
-        mbar_expect_tx(bar, ragged ? 0 : (a.order ? kABytes : kStage));
+        if (rank == 0) mbar_expect_tx(full + 8 * stage, (ragged ? 0 : (a.order ? kABytes : kStage)) * (kPair ? 2 : 1));
         if (kKind == kForward) {
-          tma_load_3d(sa, &maps.a, k * kDepth, t.chan0, t.group, bar);
+          tma_load_3d<kPair>(sa, &maps.a, k * kDepth, chan0, t.group, bar);
         } else if (kKind == kInputGrad) {
-          tma_load_3d(sa, &maps.a, t.chan0, k * kDepth, t.group, bar);
-          tma_load_3d(sa + 8192, &maps.a, t.chan0 + 64, k * kDepth, t.group, bar);
+          tma_load_3d<kPair>(sa, &maps.a, chan0, k * kDepth, t.group, bar);
+          tma_load_3d<kPair>(sa + 8192, &maps.a, chan0 + 64, k * kDepth, t.group, bar);
         } else if (!ragged) {
-          tma_load_2d(sa, &maps.a, t.chan0, p0, bar);
-          tma_load_2d(sa + 8192, &maps.a, t.chan0 + 64, p0, bar);
+          tma_load_2d<kPair>(sa, &maps.a, chan0, p0, bar);
+          tma_load_2d<kPair>(sa + 8192, &maps.a, chan0 + 64, p0, bar);
         }
         if (!a.order && !ragged) {
           if (kBMn) {
 #pragma unroll
-            for (int box = 0; box < kCols / 64; ++box)
-              tma_load_2d(sb + box * 8192, &maps.b, t.col0 + box * 64, p0, bar);
+            for (int box = 0; box < kMine / 64; ++box)
+              tma_load_2d<kPair>(sb + box * 8192, &maps.b, col0 + box * 64, p0, bar);
           } else {
-            tma_load_2d(sb, &maps.b, k * kDepth, t.col0, bar);
+            tma_load_2d<kPair>(sb, &maps.b, k * kDepth, col0, bar);
           }
         }
         ++issued;
@@ -474,8 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // After a wait that gave up: let this CTA's copies land before its shared
     // memory goes.  Copy j (from 0) completes phase j / kStages of its stage
-    // (where the gathering warps came along; else the wait runs out).
-    if (flag_set(gave_up)) {
+    // (where the gathering warps came along; else the wait runs out).  The
+    // leader's barriers count the pair's copies, and the other CTA stays until
+    // the leader is done.
+    if (rank == 0 && flag_set(gave_up)) {
       for (uint32_t j = issued > kStages ? issued - kStages : 0; j < issued; ++j) {
         const long long deadline = clock64() + kDefaultWaitCycles;
         while (!mbar_try_wait(full + 8 * (j % kStages), (j / kStages) & 1) && clock64() < deadline) {
@@ -485,16 +544,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp >= 6) {
-    if (gathering) gather_rows<kKind, kCols>(a, schedule, total, base, full, empty, gave_up);
+    if (gathering)
+      gather_rows<kKind, kCols, kPair>(a, schedule, unit, units, rank, total, base, full, empty, gave_up);
   } else if (warp == 1) {
-    // Matrix instructions, by one thread.
-    if (lane == 0) {
+    // Matrix instructions, by one thread of the leader.
+    if (rank == 0 && lane == 0) {
       const uint32_t idesc = (1u << 4) | (a.dtype == DSMEM_BF16 ? (1u << 7) | (1u << 10) : 0u) |
                              (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u) |
-                             (uint32_t{kCols >> 3} << 17) | (uint32_t{kChannels >> 4} << 24);
+                             (uint32_t{kCols >> 3} << 17) | (uint32_t{R::kHeight >> 4} << 24);
       uint32_t stage = 0, phase = 0, done = 0;
       bool ok = true;
-      for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+      for (int i = unit; i < total && ok; i += units) {
         const Tile t = schedule.at(i);
         if (t.blocks == 0) continue;
         const uint32_t buffer = done & 1, d = tmem + buffer * kCols;
@@ -504,25 +564,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < t.blocks; ++k) {
           ok = wait_for(full + 8 * stage, phase, gave_up, a.wait_cycles, a.status);
           if (!ok) break;
-          if (gathering) fence_async_shared();
           tcgen_fence_after();
           const uint32_t sa = base + stage * kStage;
           const uint64_t da = descriptor<kAMn>(sa), db = descriptor<kBMn>(sa + kABytes);
 #pragma unroll
           for (int s = 0; s < kDepth / 16; ++s)
-            mma_f16(d, da + s * kAStep, db + s * kBStep, idesc, k > 0 || s > 0);
-          mma_commit(empty + 8 * stage);
+            mma_f16<kPair>(d, da + s * kAStep, db + s * kBStep, idesc, k > 0 || s > 0);
+          mma_commit<kPair>(empty + 8 * stage);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        mma_commit(acc_full + 8 * buffer);
+        mma_commit<kPair>(acc_full + 8 * buffer);
         ++done;
       }
       if (flag_set(gave_up)) {  // matrix instructions end before tensor memory is given back
-        mma_commit(drained);
+        mma_commit<kPair>(drained);
         const long long deadline = clock64() + kDefaultWaitCycles;
         while (!mbar_try_wait(drained, 0) && clock64() < deadline) {
         }
@@ -533,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Output: warp w may read lanes 32 (w % 4) .. of tensor memory.
     const int quadrant = warp & 3;
     uint32_t done = 0;
-    for (int i = blockIdx.x; i < total; i += gridDim.x) {
+    for (int i = unit; i < total; i += units) {
       const Tile t = schedule.at(i);
       const uint32_t buffer = done & 1;
       if (t.blocks > 0) {
@@ -557,22 +616,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kLoad; ++j) r[j] = 0u;
         }
-        store_any<kKind, kLoad>(a, t, t.col0 + c, t.chan0 + quadrant * 32, r,
+        store_any<kKind, kLoad>(a, t, t.col0 + c, t.chan0 + rank * kChannels + quadrant * 32, r,
                                 out_staging + quadrant * kStageOut);
       }
       if (t.blocks > 0) {
         tcgen_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_local(acc_empty + 8 * buffer);
+        if (lane == 0) {
+          if (kPair) mbar_arrive_pair(map_rank(acc_empty + 8 * buffer, 0));
+          else mbar_arrive_local(acc_empty + 8 * buffer);
+        }
         ++done;
       }
     }
     __syncwarp();
   }
+  // Nothing of a pair leaves while the other may read its memory or arrive on
+  // its barriers.
   tcgen_fence_before();
-  __syncthreads();
+  if (kPair) cluster_barrier();
+  else __syncthreads();
   tcgen_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kTmemColumns);
+  if (warp == 1) tmem_dealloc<kPair>(tmem, kTmemColumns);
 }
 
 // Lays rows whose bases or strides TMA cannot take out with rows of a
@@ -662,12 +727,13 @@ int prepare(const CallContext& ctx, Source* s, int64_t rows, int64_t cols, int64
   return e == cudaSuccess ? DSMEM_HIST_OK : fail_with_cuda(e, "layout launch");
 }
 
-template <int kKind, int kCols>
+template <int kKind, int kCols, bool kPair>
 int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
            cudaStream_t stream) {
+  using R = Ring<kCols, kPair>;
   TileArgs a{};
   a.offsets = p.offsets, a.order = p.order, a.n = p.n;
-  a.x_rows = static_cast<int>(p.x_rows), a.groups = p.groups, a.fan = p.fan;
+  a.x_rows = static_cast<int>(p.x_rows), a.groups = p.groups, a.fan = Divisor(static_cast<uint32_t>(p.fan));
   a.channels = kKind == kInputGrad ? p.inner : p.outer;
   a.depth = kKind == kInputGrad ? p.outer : p.inner;
   a.width = p.inner;
@@ -689,23 +755,33 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
   } else {
     if ((rc = make_map(&m.a, p.dtype, w.data, p.inner, p.outer, p.groups, w.row_stride, w.group_stride,
                        kKind == kForward ? kChannels : kDepth, true)) ||
-        (rc = make_map(&m.b, p.dtype, x.data, x_cols, p.x_rows, 1, x.row_stride, 0, kCols, false)))
+        (rc = make_map(&m.b, p.dtype, x.data, x_cols, p.x_rows, 1, x.row_stride, 0, R::kMine, false)))
       return rc;
   }
 
-  const int64_t chan_tiles = (a.channels + kChannels - 1) / kChannels;
+  const int64_t chan_tiles = (a.channels + R::kHeight - 1) / R::kHeight;
   const int64_t tiles = kKind == kWeightGrad
                             ? chan_tiles * ((p.inner + kCols - 1) / kCols) * p.groups
                             : chan_tiles * (p.n / kCols + std::min<int64_t>(p.groups + 1, p.n));
   if (tiles > INT32_MAX)
     return fail_with(DSMEM_HIST_EINVAL, "grouped product: more than 2^31 output tiles");
-  const int smem = Ring<kCols>::smem_bytes(p.groups);
-  cudaError_t e = cudaFuncSetAttribute(product_kernel<kKind, kCols>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = R::smem_bytes(p.groups);
+  const auto kernel = product_kernel<kKind, kCols, kPair>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return fail_with_cuda(e, "cudaFuncSetAttribute");
-  const int grid = static_cast<int>(std::min<int64_t>(tiles, ctx.sm_count));
-  product_kernel<kKind, kCols><<<grid, kThreads, smem, stream>>>(m, a);
-  e = cudaGetLastError();
+  const int per_unit = kPair ? 2 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, ctx.sm_count / per_unit)) * per_unit);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = per_unit;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, m, a);
   return e == cudaSuccess ? DSMEM_HIST_OK : fail_with_cuda(e, "grouped product launch");
 }
 
@@ -714,10 +790,11 @@ template <int kKind>
 int launch_rows(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
                 cudaStream_t stream) {
   const int64_t average = p.n / p.groups;
-  if (average <= 12) return launch<kKind, 16>(p, ctx, x, w, stream);
-  if (average <= 64) return launch<kKind, 64>(p, ctx, x, w, stream);
-  if (average <= 256) return launch<kKind, 128>(p, ctx, x, w, stream);
-  return launch<kKind, 256>(p, ctx, x, w, stream);
+  const int channels = kKind == kInputGrad ? p.inner : p.outer;
+  if (average <= 12) return launch<kKind, 16, false>(p, ctx, x, w, stream);
+  if (average <= 64) return launch<kKind, 64, false>(p, ctx, x, w, stream);
+  if (average <= 128 || channels <= kChannels) return launch<kKind, 128, false>(p, ctx, x, w, stream);
+  return launch<kKind, 256, true>(p, ctx, x, w, stream);
 }
 
 }  // namespace
@@ -732,8 +809,8 @@ int run_product(const ProductArgs& p, const CallContext& ctx, cudaStream_t strea
   if (!rc) {
     if (p.kind == kForward) rc = launch_rows<kForward>(p, ctx, x, w, stream);
     else if (p.kind == kInputGrad) rc = launch_rows<kInputGrad>(p, ctx, x, w, stream);
-    else if (p.inner <= 128) rc = launch<kWeightGrad, 128>(p, ctx, x, w, stream);
-    else rc = launch<kWeightGrad, 256>(p, ctx, x, w, stream);
+    else if (p.inner <= 128 || p.outer <= 128) rc = launch<kWeightGrad, 128, false>(p, ctx, x, w, stream);
+    else rc = launch<kWeightGrad, 256, true>(p, ctx, x, w, stream);
   }
   for (Source* s : {&x, &w})
     if (s->scratch) {
