@@ -883,6 +883,9 @@ int begin_call(cudaStream_t stream, CallContext* out) {
   if ((rc = stream_slot(st, stream, true, &sr))) return rc;
   if ((rc = take_pending_timeout(sr.h_status))) return rc;
   if ((rc = ensure_pool(st))) return rc;
+  cudaGetDevice(&out->device);
+  if (out->device >= kMaxDevices)
+    return fail(DSMEM_HIST_EUNSUPPORTED, "device ordinal beyond %d", kMaxDevices - 1);
   out->status = sr.d_status;
   out->pool = st->pool;
   out->sm_count = st->dev.sm_count;

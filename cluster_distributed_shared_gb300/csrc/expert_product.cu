@@ -767,7 +767,8 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
     return fail_with(DSMEM_HIST_EINVAL, "grouped product: more than 2^31 output tiles");
   const int smem = R::smem_bytes(p.groups);
   const auto kernel = product_kernel<kKind, kCols, kPair>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit;
+  cudaError_t e = limit.need(reinterpret_cast<const void*>(kernel), ctx.device, smem);
   if (e != cudaSuccess) return fail_with_cuda(e, "cudaFuncSetAttribute");
   const int per_unit = kPair ? 2 : 1;
   cudaLaunchConfig_t cfg = {};

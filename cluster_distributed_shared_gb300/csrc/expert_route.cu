@@ -321,7 +321,8 @@ cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_group(const int32_t* keys, int64_t n, int num_groups, int32_t* offsets,
-                         int32_t* order, int32_t* position, cudaStream_t stream) {
+                         int32_t* order, int32_t* position, const CallContext& ctx,
+                         cudaStream_t stream) {
   GroupArgs a{keys, n, num_groups, 0, 0, 0, offsets, order, position};
   while ((int64_t{1} << a.bits) < num_groups) ++a.bits;
   // Warps: as many counter rows as shared memory holds beside the totals, but
@@ -337,12 +338,10 @@ cudaError_t launch_group(const int32_t* keys, int64_t n, int num_groups, int32_t
   int P = 1;
   while (P < 16 && !a.shared_totals && n >= int64_t{2} * P * a.warps * 128) P *= 2;
   const size_t smem = (static_cast<size_t>(a.warps + !a.shared_totals) * num_groups + 32) * 4;
-  cudaError_t e;
-  if ((e = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kGroupSmemLimit)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) !=
-          cudaSuccess)
-    return e;
+  static SmemLimit limit;
+  const cudaError_t e = limit.need(reinterpret_cast<const void*>(group_kernel), ctx.device,
+                                   kGroupSmemLimit, true);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(P);
   cfg.blockDim = dim3(a.warps * 32);

@@ -3,6 +3,9 @@
 #pragma once
 
 #include <stdint.h>
+
+#include <atomic>
+
 #include <cuda_runtime_api.h>
 
 #include "dsmem_experts.h"
@@ -18,7 +21,9 @@ constexpr uint32_t kStatusProduct = 2;
 
 // Host layer of api.cpp: reports an earlier launch's timeout on this stream
 // and hands out what a launch needs of the current device.
+constexpr int kMaxDevices = 64;
 struct CallContext {
+  int device = 0;
   uint32_t* status = nullptr;  // the stream's host-mapped status word
   cudaMemPool_t pool = nullptr;
   int sm_count = 0;
@@ -40,6 +45,25 @@ int guarded(F&& body) noexcept {
   }
 }
 
+// A kernel's largest dynamic shared memory so far on each device.  need()
+// raises the kernel's limit where a launch wants more (and, once, allows
+// clusters of 16).
+class SmemLimit {
+ public:
+  cudaError_t need(const void* kernel, int device, int bytes, bool wide_clusters = false) {
+    std::atomic<int>& set = set_[device];
+    if (set.load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && wide_clusters)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) set.store(bytes, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<int> set_[kMaxDevices] = {};
+};
+
 struct RouteArgs {
   const void* logits;
   int64_t tokens, row_stride;
@@ -53,7 +77,8 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
 cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t stream);
 
 cudaError_t launch_group(const int32_t* keys, int64_t n, int num_groups, int32_t* offsets,
-                         int32_t* order, int32_t* position, cudaStream_t stream);
+                         int32_t* order, int32_t* position, const CallContext& ctx,
+                         cudaStream_t stream);
 
 enum ProductKind { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 struct ProductArgs {

@@ -103,7 +103,7 @@ int run_group(const int32_t* keys, int64_t n, int32_t num_groups, int32_t* offse
   CallContext ctx;
   int rc = begin_call(stream, &ctx);
   if (rc) return rc;
-  return finish(launch_group(keys, n, num_groups, offsets, order, position, stream), "group launch");
+  return finish(launch_group(keys, n, num_groups, offsets, order, position, ctx, stream), "group launch");
 }
 
 int check_product(int64_t x_rows, int32_t groups, int32_t fan, int64_t n, int32_t outer, int32_t inner,

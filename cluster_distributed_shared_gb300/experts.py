@@ -15,23 +15,9 @@ the inputs on other streams is the caller's to order.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 F32, F16, BF16 = 0, 1, 2
-
-_EXPORTS = {}
-
-
-class Grad(ctypes.Structure):
-    _fields_ = [
-        ("grad", ctypes.c_void_p),
-        ("out", ctypes.c_void_p),
-        ("count", ctypes.c_int64),
-        ("dtype", ctypes.c_int32),
-        ("reserved", ctypes.c_int32),
-    ]
-
 
 _p, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 SIGNATURES = {
@@ -48,37 +34,44 @@ SIGNATURES = {
 }
 
 
-def _call(name, *args):
-    fn = _EXPORTS.get(name)
-    if fn is None:
+class _Library:
+    """The library's entry points and torch, looked up once."""
+
+    def __getattr__(self, name):
+        import torch
         from . import lib
-        fn = getattr(lib(), name)
-        fn.argtypes = SIGNATURES[name]
-        fn.restype = ctypes.c_int
-        _EXPORTS[name] = fn
-    rc = fn(*args)
+        loaded = lib()
+        for fn, args in SIGNATURES.items():
+            entry = getattr(loaded, fn)
+            entry.argtypes = args
+            entry.restype = ctypes.c_int
+            self.__dict__[fn] = entry
+        self.torch = torch
+        self.codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+        return self.__dict__[name]
+
+
+_lib = _Library()
+
+
+def _check(rc):
     if rc:
-        from . import _check
-        _check(rc)
-
-
-def _dtype_code(dtype):
-    import torch
-    return {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}.get(dtype)
+        from . import _check as check
+        check(rc)
 
 
 def _float_tensor(name, t, dims, dtype=None):
-    """A CUDA float tensor of `dims` dimensions whose rows are contiguous."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or _dtype_code(t.dtype) is None:
+    """The type code of a CUDA float tensor of `dims` dimensions whose rows
+    are contiguous."""
+    if not isinstance(t, _lib.torch.Tensor) or not t.is_cuda or t.dtype not in _lib.codes:
         raise TypeError(f"{name} must be a CUDA float32, float16 or bfloat16 tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions (got {t.dim()})")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    return t
+    return _lib.codes[t.dtype]
 
 
 def _row_stride(t):
@@ -87,8 +80,7 @@ def _row_stride(t):
 
 
 def _int_tensor(name, t, count, device):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda:
+    if not isinstance(t, _lib.torch.Tensor) or t.dtype != _lib.torch.int32 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA torch.int32 tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -96,7 +88,6 @@ def _int_tensor(name, t, count, device):
         raise ValueError(f"{name} must have {count} elements (got {t.numel()})")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    return t
 
 
 def _same_device(device, **tensors):
@@ -105,19 +96,20 @@ def _same_device(device, **tensors):
             raise ValueError(f"{name} must be on {device}")
 
 
-@contextlib.contextmanager
-def _on(device, stream, inputs):
-    """The stream handle, with `device` (and a given `stream`) made current."""
-    import torch
-    if stream is None:
-        with torch.cuda.device(device):
-            yield torch.cuda.current_stream().cuda_stream
-        return
-    with torch.cuda.stream(stream):
-        yield stream.cuda_stream
-    for t in inputs:
-        if t is not None:
-            t.record_stream(stream)
+def _on(device, stream, inputs, run):
+    """run(stream handle) with `device`, and a given `stream`, made current."""
+    torch = _lib.torch
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            result = run(stream.cuda_stream)
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+        return result
+    if device.index == torch.cuda.current_device():
+        return run(torch._C._cuda_getCurrentRawStream(device.index))
+    with torch.cuda.device(device):
+        return run(torch.cuda.current_stream().cuda_stream)
 
 
 def dsmem_route(logits, top_k: int, renormalize: bool = True, stream=None):
@@ -127,39 +119,44 @@ def dsmem_route(logits, top_k: int, renormalize: bool = True, stream=None):
     largest logits, equal ones by lowest index, with their share of the
     softmax over the chosen (`renormalize`) or over all experts.  Logits of
     -inf and NaN are never chosen; missing choices are id -1 with weight 0."""
-    import torch
-    _float_tensor("logits", logits, 2)
+    dtype = _float_tensor("logits", logits, 2)
     tokens, experts = logits.shape
-    with _on(logits.device, stream, (logits,)) as s:
-        ids = torch.empty((tokens, top_k), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((tokens, top_k), dtype=torch.float32, device=logits.device)
-        _call("dsmem_route", logits.data_ptr(), _dtype_code(logits.dtype), tokens, experts,
-              _row_stride(logits), int(top_k), int(renormalize), ids.data_ptr(), weights.data_ptr(),
-              s)
-    return ids, weights
+
+    def run(s):
+        ids = _lib.torch.empty((tokens, top_k), dtype=_lib.torch.int32, device=logits.device)
+        weights = _lib.torch.empty((tokens, top_k), dtype=_lib.torch.float32, device=logits.device)
+        _check(_lib.dsmem_route(
+            logits.data_ptr(), dtype, tokens, experts, _row_stride(logits), int(top_k),
+            int(renormalize), ids.data_ptr(), weights.data_ptr(), s))
+        return ids, weights
+
+    return _on(logits.device, stream, (logits,), run)
 
 
 def dsmem_route_backward(logits, ids, weights, grad_weights, renormalize: bool = True, stream=None):
     """Gradient of dsmem_route's weights with respect to `logits` (of its
     type); `ids` and `weights` are the forward call's."""
-    import torch
-    _float_tensor("logits", logits, 2)
+    dtype = _float_tensor("logits", logits, 2)
     tokens, experts = logits.shape
     if ids.dim() != 2 or ids.shape[0] != tokens:
         raise ValueError("ids must be [tokens, top_k]")
     top_k = ids.shape[1]
     _int_tensor("ids", ids, None, logits.device)
     for name, t in (("weights", weights), ("grad_weights", grad_weights)):
-        _float_tensor(name, t, 2, torch.float32)
+        _float_tensor(name, t, 2, _lib.torch.float32)
         if t.shape != ids.shape or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous and of the shape of ids")
     _same_device(logits.device, weights=weights, grad_weights=grad_weights)
-    with _on(logits.device, stream, (logits, ids, weights, grad_weights)) as s:
-        out = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
-        _call("dsmem_route_backward", logits.data_ptr(), _dtype_code(logits.dtype), tokens, experts,
-              _row_stride(logits), top_k, int(renormalize), ids.data_ptr(), weights.data_ptr(),
-              grad_weights.data_ptr(), out.data_ptr(), s)
-    return out
+
+    def run(s):
+        out = _lib.torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+        _check(_lib.dsmem_route_backward(
+            logits.data_ptr(), dtype, tokens, experts, _row_stride(logits), top_k,
+            int(renormalize), ids.data_ptr(), weights.data_ptr(), grad_weights.data_ptr(),
+            out.data_ptr(), s))
+        return out
+
+    return _on(logits.device, stream, (logits, ids, weights, grad_weights), run)
 
 
 def dsmem_group(keys, num_groups: int, stream=None):
@@ -167,27 +164,31 @@ def dsmem_group(keys, num_groups: int, stream=None):
     1], order [n], position [n]), int32: group g has the places offsets[g] ..
     offsets[g + 1]; order[p] is the key at place p (-1 behind the last group),
     position[i] the place of key i (-1 for keys outside [0, num_groups))."""
-    import torch
     _int_tensor("keys", keys, None, None)
     n = keys.numel()
-    with _on(keys.device, stream, (keys,)) as s:
-        offsets = torch.empty(max(int(num_groups), 0) + 1, dtype=torch.int32, device=keys.device)
-        order = torch.empty(n, dtype=torch.int32, device=keys.device)
-        position = torch.empty(n, dtype=torch.int32, device=keys.device)
-        _call("dsmem_group", keys.data_ptr(), n, int(num_groups), offsets.data_ptr(),
-              order.data_ptr(), position.data_ptr(), s)
-    return offsets, order, position
+
+    def run(s):
+        torch = _lib.torch
+        like = dict(dtype=torch.int32, device=keys.device)
+        offsets = torch.empty(max(int(num_groups), 0) + 1, **like)
+        order, position = torch.empty(n, **like), torch.empty(n, **like)
+        _check(_lib.dsmem_group(
+            keys.data_ptr(), n, int(num_groups), offsets.data_ptr(), order.data_ptr(),
+            position.data_ptr(), s))
+        return offsets, order, position
+
+    return _on(keys.device, stream, (keys,), run)
 
 
-def _product_dtypes(x, out_dtype):
-    import torch
-    if x.dtype == torch.float32:
+def _product_types(code, dtype, out_dtype):
+    """The output's type and its code, for inputs of the type `dtype`."""
+    if code == F32:
         raise TypeError("grouped products take float16 or bfloat16")
-    out_dtype = x.dtype if out_dtype is None else out_dtype
-    code = _dtype_code(out_dtype)
-    if code is None or (out_dtype != x.dtype and code != F32):
+    if out_dtype is None or out_dtype == dtype:
+        return dtype, code
+    if out_dtype != _lib.torch.float32:
         raise TypeError("out_dtype must be the inputs' type or torch.float32")
-    return _dtype_code(x.dtype), out_dtype, code
+    return out_dtype, F32
 
 
 def dsmem_grouped_matmul(x, weight, offsets, order=None, fan: int = 1, transpose: bool = False,
@@ -196,37 +197,39 @@ def dsmem_grouped_matmul(x, weight, offsets, order=None, fan: int = 1, transpose
     x[row(p)] @ weight[g]) for the group g that holds place p, where row(p) is
     order[p] // fan, or p without `order`.  weight is [groups, outer, inner];
     places of no group give zeros."""
-    import torch
-    _float_tensor("x", x, 2)
+    dtype = _float_tensor("x", x, 2)
     _float_tensor("weight", weight, 3, x.dtype)
     groups, outer, inner = weight.shape
     depth, cols = (outer, inner) if transpose else (inner, outer)
     if x.shape[1] != depth:
         raise ValueError(f"x must have {depth} columns (got {x.shape[1]})")
-    dtype, out_dtype, out_code = _product_dtypes(x, out_dtype)
+    out_dtype, out_code = _product_types(dtype, x.dtype, out_dtype)
     _int_tensor("offsets", offsets, groups + 1, x.device)
     if order is not None:
         _int_tensor("order", order, None, x.device)
     _same_device(x.device, weight=weight)
     n = x.shape[0] if order is None else order.numel()
-    with _on(x.device, stream, (x, weight, offsets, order)) as s:
-        out = torch.empty((n, cols), dtype=out_dtype, device=x.device)
-        _call("dsmem_grouped_matmul", x.data_ptr(), x.shape[0], _row_stride(x), weight.data_ptr(),
-              weight.stride(1) if outer > 1 else inner,
-              weight.stride(0) if groups > 1 else outer * inner, offsets.data_ptr(), groups,
-              None if order is None else order.data_ptr(), int(fan), n, outer, inner,
-              int(transpose), dtype, out.data_ptr(), out_code, s)
-    return out
+
+    def run(s):
+        out = _lib.torch.empty((n, cols), dtype=out_dtype, device=x.device)
+        _check(_lib.dsmem_grouped_matmul(
+            x.data_ptr(), x.shape[0], _row_stride(x), weight.data_ptr(), weight.stride(1) if outer
+            > 1 else inner, weight.stride(0) if groups > 1 else outer * inner, offsets.data_ptr(),
+            groups, None if order is None else order.data_ptr(), int(fan), n, outer, inner,
+            int(transpose), dtype, out.data_ptr(), out_code, s))
+        return out
+
+    return _on(x.device, stream, (x, weight, offsets, order), run)
 
 
-def dsmem_grouped_matmul_wgrad(dy, x, offsets, order=None, fan: int = 1, out_dtype=None, stream=None):
+def dsmem_grouped_matmul_wgrad(dy, x, offsets, order=None, fan: int = 1, out_dtype=None,
+                               stream=None):
     """Gradient of dsmem_grouped_matmul(x, weight, ...) with respect to its
     weight [groups, outer, inner]: out[g] = sum over the places p of group g of
     dy[p]^T x[row(p)]."""
-    import torch
-    _float_tensor("dy", dy, 2)
+    dtype = _float_tensor("dy", dy, 2)
     _float_tensor("x", x, 2, dy.dtype)
-    dtype, out_dtype, out_code = _product_dtypes(dy, out_dtype)
+    out_dtype, out_code = _product_types(dtype, dy.dtype, out_dtype)
     _int_tensor("offsets", offsets, None, dy.device)
     n, outer, inner, groups = dy.shape[0], dy.shape[1], x.shape[1], offsets.numel() - 1
     if order is not None:
@@ -234,22 +237,24 @@ def dsmem_grouped_matmul_wgrad(dy, x, offsets, order=None, fan: int = 1, out_dty
     elif x.shape[0] != n:
         raise ValueError(f"x must have {n} rows (got {x.shape[0]})")
     _same_device(dy.device, x=x)
-    with _on(dy.device, stream, (dy, x, offsets, order)) as s:
-        out = torch.empty((groups, outer, inner), dtype=out_dtype, device=dy.device)
-        _call("dsmem_grouped_matmul_wgrad", dy.data_ptr(), _row_stride(dy), x.data_ptr(), x.shape[0],
-              _row_stride(x), offsets.data_ptr(), groups,
-              None if order is None else order.data_ptr(), int(fan), n, outer, inner, dtype,
-              out.data_ptr(), out_code, s)
-    return out
+
+    def run(s):
+        out = _lib.torch.empty((groups, outer, inner), dtype=out_dtype, device=dy.device)
+        _check(_lib.dsmem_grouped_matmul_wgrad(
+            dy.data_ptr(), _row_stride(dy), x.data_ptr(), x.shape[0], _row_stride(x),
+            offsets.data_ptr(), groups, None if order is None else order.data_ptr(), int(fan), n,
+            outer, inner, dtype, out.data_ptr(), out_code, s))
+        return out
+
+    return _on(dy.device, stream, (dy, x, offsets, order), run)
 
 
 def _positions(position, weights):
-    import torch
     _int_tensor("position", position, None, None)
     if position.dim() != 2:
         raise ValueError("position must be [tokens, top_k]")
     if weights is not None:
-        _float_tensor("weights", weights, 2, torch.float32)
+        _float_tensor("weights", weights, 2, _lib.torch.float32)
         if weights.shape != position.shape or not weights.is_contiguous():
             raise ValueError("weights must be contiguous and of the shape of position")
 
@@ -257,25 +262,26 @@ def _positions(position, weights):
 def dsmem_combine(z, position, weights=None, stream=None):
     """out[t] = sum over j of weights[t, j] * z[position[t, j]] (weights of 1
     when None); positions outside z are dropped."""
-    import torch
-    _float_tensor("z", z, 2)
+    dtype = _float_tensor("z", z, 2)
     _positions(position, weights)
     _same_device(z.device, position=position, weights=weights)
     (tokens, top_k), width = position.shape, z.shape[1]
-    with _on(z.device, stream, (z, position, weights)) as s:
-        out = torch.empty((tokens, width), dtype=z.dtype, device=z.device)
-        _call("dsmem_combine", z.data_ptr(), z.shape[0], _row_stride(z), position.data_ptr(),
-              None if weights is None else weights.data_ptr(), tokens, top_k, width,
-              _dtype_code(z.dtype), out.data_ptr(), s)
-    return out
+
+    def run(s):
+        out = _lib.torch.empty((tokens, width), dtype=z.dtype, device=z.device)
+        _check(_lib.dsmem_combine(
+            z.data_ptr(), z.shape[0], _row_stride(z), position.data_ptr(), None if weights is None
+            else weights.data_ptr(), tokens, top_k, width, dtype, out.data_ptr(), s))
+        return out
+
+    return _on(z.device, stream, (z, position, weights), run)
 
 
 def dsmem_combine_backward(dy, z, position, order, weights, stream=None):
     """Gradients (dz, dweights) of dsmem_combine; `position` and `order` are
     one dsmem_group call's."""
-    import torch
     _float_tensor("dy", dy, 2)
-    _float_tensor("z", z, 2, dy.dtype)
+    dtype = _float_tensor("z", z, 2, dy.dtype)
     _positions(position, weights)
     if weights is None:
         raise TypeError("weights must be a CUDA float32 tensor")
@@ -286,39 +292,50 @@ def dsmem_combine_backward(dy, z, position, order, weights, stream=None):
         raise ValueError(f"z must have {tokens * top_k} rows (got {z.shape[0]})")
     _int_tensor("order", order, tokens * top_k, dy.device)
     _same_device(dy.device, z=z, position=position, weights=weights)
-    with _on(dy.device, stream, (dy, z, position, order, weights)) as s:
-        dz = torch.empty((tokens * top_k, width), dtype=z.dtype, device=z.device)
-        dweights = torch.empty((tokens, top_k), dtype=torch.float32, device=z.device)
-        _call("dsmem_combine_backward", dy.data_ptr(), _row_stride(dy), z.data_ptr(), _row_stride(z),
-              position.data_ptr(), order.data_ptr(), weights.data_ptr(), tokens, top_k, width,
-              _dtype_code(z.dtype), dz.data_ptr(), dweights.data_ptr(), s)
-    return dz, dweights
+
+    def run(s):
+        dz = _lib.torch.empty((tokens * top_k, width), dtype=z.dtype, device=z.device)
+        dweights = _lib.torch.empty((tokens, top_k), dtype=_lib.torch.float32, device=z.device)
+        _check(_lib.dsmem_combine_backward(
+            dy.data_ptr(), _row_stride(dy), z.data_ptr(), _row_stride(z), position.data_ptr(),
+            order.data_ptr(), weights.data_ptr(), tokens, top_k, width, dtype, dz.data_ptr(),
+            dweights.data_ptr(), s))
+        return dz, dweights
+
+    return _on(dy.device, stream, (dy, z, position, order, weights), run)
 
 
 def dsmem_grad_clip(grads, max_norm: float, out=None, stream=None):
     """Global norm of `grads` (a list of contiguous CUDA tensors), returned as
     a float32 tensor without dimensions; the gradients times min(1, max_norm /
     (norm + 1e-6)) go to `out`, a list of tensors like them, or in place."""
-    import torch
     grads = list(grads)
     out = grads if out is None else list(out)
     if len(out) != len(grads):
         raise ValueError("out must have one tensor for each gradient")
+    torch, codes = _lib.torch, _lib.codes
     device = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
-    table = (Grad * max(len(grads), 1))()
-    codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
-    for entry, g, o in zip(table, grads, out):
+    index = device.index if device.type == "cuda" else -1
+    words = []                     # dsmem_grad_t: two addresses, count, type and 32 zero bits
+    for g, o in zip(grads, out):
         code = codes.get(g.dtype)
         if code is None or not g.is_cuda:
             raise TypeError("grads must be CUDA float32, float16 or bfloat16 tensors")
-        if not g.is_contiguous() or g.device != device:
+        if g.get_device() != index or not g.is_contiguous():
             raise ValueError("grads must be contiguous and on one device")
-        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or not o.is_contiguous()
-                           or o.device != device):
+        at = g.data_ptr()
+        if o is g:
+            words += (at, at, g.numel(), code)
+            continue
+        if o.dtype != g.dtype or o.shape != g.shape or o.get_device() != index \
+                or not o.is_contiguous():
             raise ValueError("out must match grads in type, shape and device and be contiguous")
-        entry.grad, entry.out, entry.count, entry.dtype = g.data_ptr(), o.data_ptr(), g.numel(), code
-    with _on(device, stream, (*grads, *out)) as s:
+        words += (at, o.data_ptr(), g.numel(), code)
+    table = (ctypes.c_uint64 * max(len(words), 4))(*words)
+
+    def run(s):
         norm = torch.empty((), dtype=torch.float32, device=device)
-        _call("dsmem_grad_clip", ctypes.addressof(table), len(grads), float(max_norm),
-              norm.data_ptr(), s)
-    return norm
+        _check(_lib.dsmem_grad_clip(table, len(grads), float(max_norm), norm.data_ptr(), s))
+        return norm
+
+    return _on(device, stream, (*grads, *out), run)
