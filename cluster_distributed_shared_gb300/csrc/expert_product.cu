@@ -44,18 +44,29 @@ constexpr int kABytes = kChannels * kDepth * 2;
 
 constexpr int kBarrierBytes = 256;
 
-// Where two CTAs of a cluster pair up (kPair), a tile is 256 channels high:
-// each CTA holds 128 channels of A and half of the columns of B, and one
-// matrix instruction reads both.  That halves the bytes of B a CTA takes in.
-template <int kCols, bool kPair>
+// How CTAs work on a tile.
+//   kSolo   each on its own.
+//   kPair   two of a cluster on one 256 channels high: each holds 128 channels
+//           of A and half of the columns of B, and one matrix instruction
+//           reads both.  That halves the bytes of B a CTA takes in.
+//   kSplit  a cluster of up to kMaxSplit on one tile, each on a part of its
+//           depth; the first CTA adds the others' sums, which they write into
+//           its shared memory, in the order of their ranks.
+enum Team { kSolo, kPair, kSplit };
+
+template <int kCols, int kTeam>
 struct Ring {
-  static constexpr int kMine = kPair ? kCols / 2 : kCols;  // columns this CTA brings in
+  static constexpr int kMine = kTeam == kPair ? kCols / 2 : kCols;  // columns this CTA brings in
   static constexpr int kStage = kABytes + kMine * kDepth * 2;
-  // As many stages as fit beside the tables (227 KB in all).
-  static constexpr int kStages = kMine == 256 ? 4 : (kMine == 128 ? 6 : (kMine == 64 ? 8 : 10));
-  static constexpr int kHeight = kPair ? 2 * kChannels : kChannels;  // channels of a tile
+  static constexpr int kHeight = kTeam == kPair ? 2 * kChannels : kChannels;  // channels of a tile
+  static constexpr int kMaxSplit = kTeam != kSplit ? 1 : (kCols == 16 ? 8 : 4);
+  static constexpr int kJoin = kChannels * kCols * 4;  // one CTA's sums
+  // As many stages as fit beside the sums and the tables (227 KB in all).
+  static constexpr int kStages = kTeam == kSplit ? (kCols == 16 ? 6 : 4)
+                                                 : (kMine == 128 ? 6 : (kMine == 64 ? 8 : 10));
   static int smem_bytes(int groups) {
-    return 1024 + kStages * kStage + 4 * kStageOut + kBarrierBytes + 2 * 4 * (groups + 2);
+    return 1024 + kStages * kStage + (kMaxSplit - 1) * kJoin + 4 * kStageOut + kBarrierBytes +
+           2 * 4 * (groups + 2);
   }
 };
 
@@ -155,26 +166,44 @@ __device__ __forceinline__ void st_shared_value(uint32_t addr, O v) {
   }
 }
 
+template <typename O>
+__device__ __forceinline__ O ld_shared_value(uint32_t addr) {
+  O v;
+  if constexpr (sizeof(O) == 2) {
+    uint16_t bits;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(bits) : "r"(addr) : "memory");
+    *reinterpret_cast<uint16_t*>(&v) = bits;
+  } else {
+    float bits;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(bits) : "r"(addr) : "memory");
+    v = static_cast<O>(bits);
+  }
+  return v;
+}
+
 struct Tile {
   int group;     // `groups`: the rows behind the last group
   int begin, end;  // the group's rows
   int col0;      // first row (weight gradient: first inner column) of the tile
   int chan0;     // first channel
-  int blocks;    // stages of depth
+  int block0;    // this CTA's first stage of depth
+  int blocks;    // and how many it has
 };
 
-template <int kKind, int kCols, bool kPair>
+template <int kKind, int kCols, int kTeam>
 struct Schedule {
   const int32_t* begin;  // [groups + 2] first row of each group, in shared memory
   const int32_t* first;  // [groups + 2] first tile of each group
   int groups, chan_tiles, width_tiles, depth_blocks;
   int group;
-  static constexpr int kHeight = Ring<kCols, kPair>::kHeight;
+  uint32_t rank, split;
+  static constexpr int kHeight = Ring<kCols, kTeam>::kHeight;
 
-  __device__ __forceinline__ Schedule(const int32_t* b, const int32_t* f, const TileArgs& a)
+  __device__ __forceinline__ Schedule(const int32_t* b, const int32_t* f, const TileArgs& a, uint32_t rank,
+                                      uint32_t split)
       : begin(b), first(f), groups(a.groups), chan_tiles((a.channels + kHeight - 1) / kHeight),
         width_tiles(kKind == kWeightGrad ? (a.width + kCols - 1) / kCols : 0),
-        depth_blocks((a.depth + kDepth - 1) / kDepth), group(0) {}
+        depth_blocks((a.depth + kDepth - 1) / kDepth), group(0), rank(rank), split(split) {}
   __device__ __forceinline__ int tiles_of(int rows) const {
     return (kKind == kWeightGrad ? width_tiles : (rows + kCols - 1) / kCols) * chan_tiles;
   }
@@ -197,7 +226,18 @@ struct Schedule {
       r.col0 = r.begin + i / chan_tiles * kCols;
       r.blocks = group < groups ? depth_blocks : 0;
     }
+    r.block0 = 0;
+    if (kTeam == kSplit) {
+      const int all = r.blocks;
+      r.block0 = part(all, rank);
+      r.blocks = part(all, rank + 1) - r.block0;
+    }
     return r;
+  }
+  // First stage of a rank's part of `blocks`; the first rank's part is empty
+  // only if all are.
+  __device__ __forceinline__ int part(int blocks, uint32_t of) const {
+    return static_cast<int>((static_cast<int64_t>(blocks) * of + split - 1) / split);
   }
 };
 
@@ -205,7 +245,7 @@ struct Schedule {
 // Rows of the output are columns of the tile (forward, input gradient) or
 // channels (weight gradient); either way the warp's block becomes 16-byte
 // pieces of output rows through its staging memory.  Without 16-byte rows
-// each value goes by itself.
+// values go one by one, neighbouring lanes to neighbouring places.
 template <int kKind, int kN, typename O>
 __device__ __forceinline__ void store_block(const TileArgs& a, const Tile& t, int col, int channel0,
                                             const uint32_t (&r)[kN], uint32_t staging) {
@@ -213,17 +253,16 @@ __device__ __forceinline__ void store_block(const TileArgs& a, const Tile& t, in
   constexpr int V = 16 / sizeof(O);
   if (kKind == kWeightGrad) {
     constexpr int kPieces = kN / V;  // 16-byte pieces of a staged row
-    const int channel = channel0 + lane;
     O* out = static_cast<O*>(a.out) + static_cast<int64_t>(t.group) * a.channels * a.width;
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+      Pack<O, V> p;
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.v[v] = from_float<O>(__uint_as_float(r[q * V + v]));
+      st_shared_16(staging + lane * (kN * sizeof(O)) + ((q ^ (lane & (kPieces - 1))) << 4), p);
+    }
+    __syncwarp();
     if (a.wide_out) {
-#pragma unroll
-      for (int q = 0; q < kPieces; ++q) {
-        Pack<O, V> p;
-#pragma unroll
-        for (int v = 0; v < V; ++v) p.v[v] = from_float<O>(__uint_as_float(r[q * V + v]));
-        st_shared_16(staging + lane * (kN * sizeof(O)) + ((q ^ (lane & (kPieces - 1))) << 4), p);
-      }
-      __syncwarp();
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int row = (i * 32 + lane) / kPieces, q = lane & (kPieces - 1);
@@ -231,13 +270,14 @@ __device__ __forceinline__ void store_block(const TileArgs& a, const Tile& t, in
         if (channel0 + row < a.channels && col + q * V < a.width)
           *reinterpret_cast<uint4*>(out + static_cast<int64_t>(channel0 + row) * a.width + col + q * V) = p;
       }
-      __syncwarp();
-    } else if (channel < a.channels) {
-      out += static_cast<int64_t>(channel) * a.width + col;
-#pragma unroll
-      for (int j = 0; j < kN; ++j)
-        if (col + j < a.width) out[j] = from_float<O>(__uint_as_float(r[j]));
+    } else if (lane < kN && col + lane < a.width) {
+      out += static_cast<int64_t>(channel0) * a.width + col + lane;
+      const int rows = min(32, a.channels - channel0);
+      for (int row = 0; row < rows; ++row, out += a.width)
+        *out = ld_shared_value<O>(staging + row * (kN * sizeof(O)) +
+                                  (((lane / V) ^ (row & (kPieces - 1))) << 4) + lane % V * sizeof(O));
     }
+    __syncwarp();
   } else {
     O* out = static_cast<O*>(a.out) + static_cast<int64_t>(col) * a.channels + channel0;
     if (a.wide_out) {
@@ -275,11 +315,11 @@ __device__ __forceinline__ void store_any(const TileArgs& a, const Tile& t, int 
 // stage on, with one arrival on the leader's barrier, when its copies have
 // landed, kLag stages after it issued them.  (Arrivals by each thread's copies
 // themselves, 128 a stage on one barrier, held a stage up for 1000 cycles.)
-template <int kKind, int kCols, bool kPair>
-__device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, kCols, kPair>& schedule,
-                                            int unit, int units, uint32_t rank, int total, uint32_t base,
+template <int kKind, int kCols, int kTeam>
+__device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, kCols, kTeam>& schedule,
+                                            int unit, int units, uint32_t half, int total, uint32_t base,
                                             uint32_t full, uint32_t empty, uint32_t gave_up) {
-  using R = Ring<kCols, kPair>;
+  using R = Ring<kCols, kTeam>;
   constexpr int kStages = R::kStages, kStage = R::kStage, kMine = R::kMine;
   constexpr bool kBMn = kKind == kWeightGrad;
   constexpr int kLag = 2;
@@ -298,7 +338,7 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
     fence_async_shared();
     __syncwarp();
     if (lane == 0) {
-      if (kPair) mbar_arrive_pair(map_rank(full + 8 * oldest, 0));
+      if (kTeam == kPair) mbar_arrive_pair(map_rank(full + 8 * oldest, 0));
       else mbar_arrive_local(full + 8 * oldest);
     }
     if (++oldest == kStages) oldest = 0;
@@ -308,7 +348,7 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
   for (int i = unit; i < total && ok; i += units) {
     const Tile t = schedule.at(i);
     if (t.blocks == 0) continue;
-    const int col0 = t.col0 + rank * kMine, chan0 = t.chan0 + rank * kChannels;
+    const int col0 = t.col0 + half * kMine, chan0 = t.chan0 + half * kChannels;
     // Forward and input gradient: 8 threads a row of 128 bytes; the rows are
     // the same in every stage of the tile.
     constexpr int kLines = kGatherThreads / 8, kRows = kBMn ? 1 : (kMine + kLines - 1) / kLines;
@@ -327,7 +367,7 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
     const auto batch_place = [&](int k) {
       const int l = lane % kFound;
       const int r = l / kPerWarp * kAtOnce + (tid >> 5) * kPerWarp + l % kPerWarp;
-      return place(t.begin + (k + lane / kFound) * kDepth + r, t.end);
+      return place(t.begin + (t.block0 + k + lane / kFound) * kDepth + r, t.end);
     };
     int ahead = kBMn ? batch_place(0) : 0, here = 0;
 
@@ -341,7 +381,7 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
       if (!ok) break;
       const uint32_t sa = base + stage * kStage, sb = sa + kABytes;
       if (!kBMn) {
-        const int c = tid & 7, col = k * kDepth + c * 8;
+        const int c = tid & 7, col = (t.block0 + k) * kDepth + c * 8;
         const int left = max(0, min(16, (a.depth - col) * 2));
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
@@ -352,7 +392,7 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
                  a.x + (read ? row[r] * a.x_stride + col : 0), read ? left : 0);
         }
       } else {
-        const int p0 = t.begin + k * kDepth;
+        const int p0 = t.begin + (t.block0 + k) * kDepth;
         const bool ragged = p0 + kDepth > t.end;
         if (a.order || ragged) {
           const int c = tid % kPieces, col = col0 + c * 8;
@@ -393,10 +433,11 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
   while (pending > 0) hand_on();
 }
 
-template <int kKind, int kCols, bool kPair>
+template <int kKind, int kCols, int kTeam>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ TileArgs a) {
-  using R = Ring<kCols, kPair>;
+  using R = Ring<kCols, kTeam>;
+  constexpr bool kTwo = kTeam == kPair;
   constexpr int kStages = R::kStages, kStage = R::kStage, kMine = R::kMine;
   constexpr bool kAMn = kKind != kForward, kBMn = kKind == kWeightGrad;
   constexpr uint32_t kTmemColumns = 2 * kCols < 32 ? 32 : 2 * kCols;
@@ -407,7 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* base_ptr = raw + (base - smem_u32(raw));
-  const uint32_t out_staging = base + kStages * kStage;
+  const uint32_t join = base + kStages * kStage;
+  const uint32_t out_staging = join + (R::kMaxSplit - 1) * R::kJoin;
   const uint32_t bars = out_staging + 4 * kStageOut;
   const uint32_t full = bars, empty = bars + 8 * kStages;
   const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
@@ -417,10 +459,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t* first = begin + a.groups + 2;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Schedule<kKind, kCols, kPair> schedule(begin, first, a);
-  // A unit works on a tile: a CTA, or a pair whose first CTA leads.
-  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
-  const int unit = kPair ? blockIdx.x / 2 : blockIdx.x, units = kPair ? gridDim.x / 2 : gridDim.x;
+  // A unit works on a tile: a CTA, or a cluster whose first CTA leads.
+  const uint32_t rank = kTeam != kSolo ? cluster_ctarank() : 0u;
+  const uint32_t members = kTeam == kSplit ? cluster_nctarank() : (kTwo ? 2u : 1u);
+  const uint32_t half = kTwo ? rank : 0u;
+  const int unit = blockIdx.x / members, units = gridDim.x / members;
+  Schedule<kKind, kCols, kTeam> schedule(begin, first, a, rank, members);
   // The gathering warps take part in every stage where x is gathered, or
   // where a contraction may end inside a stage.
   const bool gathering = kBMn || a.order;
@@ -428,12 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       // Of a pair, the leader's barriers count both CTAs' arrivals.
-      mbar_init(full + 8 * s, 1 + (gathering ? kGatherThreads / 32 * (kPair ? 2 : 1) : 0));
+      mbar_init(full + 8 * s, 1 + (gathering ? kGatherThreads / 32 * (kTwo ? 2 : 1) : 0));
       mbar_init(empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + 8 * i, 1);
-      mbar_init(acc_empty + 8 * i, kPair ? 8 : 4);
+      mbar_init(acc_empty + 8 * i, kTwo ? 8 : 4);
     }
     mbar_init(drained, 1);
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(gave_up), "r"(0u) : "memory");
@@ -451,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     begin[0] = first[0] = 0;
     begin[a.groups + 1] = static_cast<int32_t>(a.n);
   }
-  if (warp == 1) tmem_alloc<kPair>(tmem_at, kTmemColumns);
+  if (warp == 1) tmem_alloc<kTwo>(tmem_at, kTmemColumns);
   __syncthreads();
   if (warp == 2) {
     int end_before = 0, tiles_before = 0;
@@ -481,12 +525,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   tcgen_fence_before();
-  if (kPair) cluster_barrier();
+  if (kTeam != kSolo) cluster_barrier();
   else __syncthreads();
   tcgen_fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_at));
   const int total = schedule.total();
+
+  // Output: warp w may read lanes 32 (w % 4) .. of tensor memory.
+  const int quadrant = warp & 3;
 
   if (warp == 0) {
     // TMA copies, by one thread.
@@ -499,27 +546,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
         if (!ok) break;
         const uint32_t sa = base + stage * kStage, sb = sa + kABytes;
-        const uint32_t bar = kPair ? map_rank(full + 8 * stage, 0) : full + 8 * stage;
-        const int p0 = t.begin + k * kDepth;  // weight gradient: the stage's first row
-        const int chan0 = t.chan0 + rank * kChannels, col0 = t.col0 + rank * kMine;
+        const uint32_t bar = kTwo ? map_rank(full + 8 * stage, 0) : full + 8 * stage;
+        const int k0 = (t.block0 + k) * kDepth;
+        const int p0 = t.begin + k0;  // weight gradient: the stage's first row
+        const int chan0 = t.chan0 + half * kChannels, col0 = t.col0 + half * kMine;
         const bool ragged = kBMn && p0 + kDepth > t.end;
-        if (rank == 0) mbar_expect_tx(full + 8 * stage, (ragged ? 0 : (a.order ? kABytes : kStage)) * (kPair ? 2 : 1));
+        if (half == 0)
+          mbar_expect_tx(full + 8 * stage, (ragged ? 0 : (a.order ? kABytes : kStage)) * (kTwo ? 2 : 1));
         if (kKind == kForward) {
-          tma_load_3d<kPair>(sa, &maps.a, k * kDepth, chan0, t.group, bar);
+          tma_load_3d<kTwo>(sa, &maps.a, k0, chan0, t.group, bar);
         } else if (kKind == kInputGrad) {
-          tma_load_3d<kPair>(sa, &maps.a, chan0, k * kDepth, t.group, bar);
-          tma_load_3d<kPair>(sa + 8192, &maps.a, chan0 + 64, k * kDepth, t.group, bar);
+          tma_load_3d<kTwo>(sa, &maps.a, chan0, k0, t.group, bar);
+          tma_load_3d<kTwo>(sa + 8192, &maps.a, chan0 + 64, k0, t.group, bar);
         } else if (!ragged) {
-          tma_load_2d<kPair>(sa, &maps.a, chan0, p0, bar);
-          tma_load_2d<kPair>(sa + 8192, &maps.a, chan0 + 64, p0, bar);
+          tma_load_2d<kTwo>(sa, &maps.a, chan0, p0, bar);
+          tma_load_2d<kTwo>(sa + 8192, &maps.a, chan0 + 64, p0, bar);
         }
         if (!a.order && !ragged) {
           if (kBMn) {
 #pragma unroll
             for (int box = 0; box < kMine / 64; ++box)
-              tma_load_2d<kPair>(sb + box * 8192, &maps.b, col0 + box * 64, p0, bar);
+              tma_load_2d<kTwo>(sb + box * 8192, &maps.b, col0 + box * 64, p0, bar);
           } else {
-            tma_load_2d<kPair>(sb, &maps.b, k * kDepth, col0, bar);
+            tma_load_2d<kTwo>(sb, &maps.b, k0, col0, bar);
           }
         }
         ++issued;
@@ -534,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (where the gathering warps came along; else the wait runs out).  The
     // leader's barriers count the pair's copies, and the other CTA stays until
     // the leader is done.
-    if (rank == 0 && flag_set(gave_up)) {
+    if (half == 0 && flag_set(gave_up)) {
       for (uint32_t j = issued > kStages ? issued - kStages : 0; j < issued; ++j) {
         const long long deadline = clock64() + kDefaultWaitCycles;
         while (!mbar_try_wait(full + 8 * (j % kStages), (j / kStages) & 1) && clock64() < deadline) {
@@ -545,10 +594,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= 6) {
     if (gathering)
-      gather_rows<kKind, kCols, kPair>(a, schedule, unit, units, rank, total, base, full, empty, gave_up);
+      gather_rows<kKind, kCols, kTeam>(a, schedule, unit, units, half, total, base, full, empty, gave_up);
   } else if (warp == 1) {
-    // Matrix instructions, by one thread of the leader.
-    if (rank == 0 && lane == 0) {
+    // Matrix instructions, by one thread; a pair's by its leader's.
+    if (half == 0 && lane == 0) {
       const uint32_t idesc = (1u << 4) | (a.dtype == DSMEM_BF16 ? (1u << 7) | (1u << 10) : 0u) |
                              (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u) |
                              (uint32_t{kCols >> 3} << 17) | (uint32_t{R::kHeight >> 4} << 24);
@@ -569,28 +618,49 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t da = descriptor<kAMn>(sa), db = descriptor<kBMn>(sa + kABytes);
 #pragma unroll
           for (int s = 0; s < kDepth / 16; ++s)
-            mma_f16<kPair>(d, da + s * kAStep, db + s * kBStep, idesc, k > 0 || s > 0);
-          mma_commit<kPair>(empty + 8 * stage);
+            mma_f16<kTwo>(d, da + s * kAStep, db + s * kBStep, idesc, k > 0 || s > 0);
+          mma_commit<kTwo>(empty + 8 * stage);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        mma_commit<kPair>(acc_full + 8 * buffer);
+        mma_commit<kTwo>(acc_full + 8 * buffer);
         ++done;
       }
       if (flag_set(gave_up)) {  // matrix instructions end before tensor memory is given back
-        mma_commit<kPair>(drained);
+        mma_commit<kTwo>(drained);
         const long long deadline = clock64() + kDefaultWaitCycles;
         while (!mbar_try_wait(drained, 0) && clock64() < deadline) {
         }
       }
     }
     __syncwarp();
+  } else if (kTeam == kSplit) {
+    // A unit has one tile at most.  All but the leader hand it their sums.
+    if (unit < total) {
+      const Tile t = schedule.at(unit);
+      if (t.blocks > 0) {
+        const bool ok = wait_for(acc_full, 0, gave_up, a.wait_cycles + 4096ll * t.blocks, a.status);
+        if (__all_sync(kFull, ok) && rank != 0) {
+          tcgen_fence_after();
+          const uint32_t d = tmem + (static_cast<uint32_t>(quadrant * 32) << 16);
+          const uint32_t to = map_rank(join + (rank - 1) * R::kJoin + (quadrant * 32 + lane) * 16, 0);
+#pragma unroll 1
+          for (int c = 0; c < kCols; c += 16) {
+            uint32_t r[16];
+            tmem_load16(d + c, r);
+            tmem_wait_load();
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+              st_cluster_16(to + (c + j) / 4 * (kChannels * 16), r[j], r[j + 1], r[j + 2], r[j + 3]);
+          }
+        }
+      }
+    }
+    __syncwarp();
   } else {
-    // Output: warp w may read lanes 32 (w % 4) .. of tensor memory.
-    const int quadrant = warp & 3;
     uint32_t done = 0;
     for (int i = unit; i < total; i += units) {
       const Tile t = schedule.at(i);
@@ -616,14 +686,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kLoad; ++j) r[j] = 0u;
         }
-        store_any<kKind, kLoad>(a, t, t.col0 + c, t.chan0 + rank * kChannels + quadrant * 32, r,
+        store_any<kKind, kLoad>(a, t, t.col0 + c, t.chan0 + half * kChannels + quadrant * 32, r,
                                 out_staging + quadrant * kStageOut);
       }
       if (t.blocks > 0) {
         tcgen_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (kPair) mbar_arrive_pair(map_rank(acc_empty + 8 * buffer, 0));
+          if (kTwo) mbar_arrive_pair(map_rank(acc_empty + 8 * buffer, 0));
           else mbar_arrive_local(acc_empty + 8 * buffer);
         }
         ++done;
@@ -631,30 +701,80 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   }
-  // Nothing of a pair leaves while the other may read its memory or arrive on
-  // its barriers.
+  // Nothing of a cluster leaves while another CTA may read or write its memory
+  // or arrive on its barriers.
   tcgen_fence_before();
-  if (kPair) cluster_barrier();
+  if (kTeam != kSolo) cluster_barrier();
   else __syncthreads();
   tcgen_fence_after();
-  if (warp == 1) tmem_dealloc<kPair>(tmem, kTmemColumns);
+  if (kTeam == kSplit && rank == 0 && warp >= 2 && warp < 6 && unit < total) {
+    // The leader's sums, then the other ranks', in their order.
+    const Tile t = schedule.at(unit);
+    const int all = t.group < a.groups ? (kKind == kWeightGrad ? (t.end - t.begin + kDepth - 1) / kDepth
+                                                               : schedule.depth_blocks) : 0;
+    const uint32_t d = tmem + (static_cast<uint32_t>(quadrant * 32) << 16);
+    const uint32_t from = join + (quadrant * 32 + lane) * 16;
+    const int limit = kKind == kWeightGrad ? a.width : t.end;
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 16) {
+      if (t.col0 + c >= limit) break;
+      uint32_t r[16];
+      if (all > 0) {
+        tmem_load16(d + c, r);
+        tmem_wait_load();
+        for (uint32_t o = 1; o < members; ++o) {
+          if (schedule.part(all, o) == schedule.part(all, o + 1)) continue;
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const uint4 v = ld_shared_16(from + (o - 1) * R::kJoin + (c + j) / 4 * (kChannels * 16));
+            r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(v.x));
+            r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) + __uint_as_float(v.y));
+            r[j + 2] = __float_as_uint(__uint_as_float(r[j + 2]) + __uint_as_float(v.z));
+            r[j + 3] = __float_as_uint(__uint_as_float(r[j + 3]) + __uint_as_float(v.w));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) r[j] = 0u;
+      }
+      store_any<kKind, 16>(a, t, t.col0 + c, t.chan0 + quadrant * 32, r, out_staging + quadrant * kStageOut);
+    }
+  }
+  if (kTeam == kSplit) {
+    tcgen_fence_before();
+    __syncthreads();
+    tcgen_fence_after();
+  }
+  if (warp == 1) tmem_dealloc<kTwo>(tmem, kTmemColumns);
 }
 
 // Lays rows whose bases or strides TMA cannot take out with rows of a
-// multiple of 8 elements.  One thread per 8 elements of the result.
-__global__ void layout_kernel(const uint16_t* src, int64_t row_stride, int64_t group_stride, int rows,
-                              int cols, int64_t groups, uint16_t* dst, int dst_stride) {
-  const int chunks = dst_stride / 8;
-  const int64_t total = groups * rows * chunks;
+// multiple of 8 elements; both sources of a product in one launch.  One
+// thread per 8 elements of the result.
+struct Layout {
+  const uint16_t* src;
+  int64_t row_stride, group_stride, chunks;  // chunks: 8-element pieces in all
+  uint16_t* dst;
+  int rows, cols, dst_stride;
+};
+struct Layouts {
+  Layout of[2];
+};
+__global__ void layout_kernel(const __grid_constant__ Layouts layouts) {
+  const int64_t total = layouts.of[0].chunks + layouts.of[1].chunks;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t line = i / chunks;
-    const int c0 = static_cast<int>(i - line * chunks) * 8;
-    const uint16_t* s = src + line / rows * group_stride + line % rows * row_stride + c0;
+    const bool second = i >= layouts.of[0].chunks;
+    const Layout& l = layouts.of[second];
+    const int64_t j = second ? i - layouts.of[0].chunks : i;
+    const int per_row = l.dst_stride / 8;
+    const int64_t line = j / per_row;
+    const int c0 = static_cast<int>(j - line * per_row) * 8;
+    const uint16_t* s = l.src + line / l.rows * l.group_stride + line % l.rows * l.row_stride + c0;
     Pack<uint16_t, 8> p;
 #pragma unroll
-    for (int v = 0; v < 8; ++v) p.v[v] = c0 + v < cols ? s[v] : uint16_t{0};
-    *reinterpret_cast<Pack<uint16_t, 8>*>(dst + line * dst_stride + c0) = p;
+    for (int v = 0; v < 8; ++v) p.v[v] = c0 + v < l.cols ? s[v] : uint16_t{0};
+    *reinterpret_cast<Pack<uint16_t, 8>*>(l.dst + line * l.dst_stride + c0) = p;
   }
 }
 
@@ -699,38 +819,63 @@ bool tma_ready(const void* p, int64_t row_stride, int64_t group_stride, int64_t 
          (groups == 1 || group_stride % 8 == 0);
 }
 
-// One source of a product, laid out again where TMA cannot read it in place.
+// One source of a product, [groups, rows, cols] of 16-bit elements.
 struct Source {
   const void* data;
-  int64_t row_stride, group_stride;
-  void* scratch = nullptr;
+  int64_t row_stride, group_stride, rows, cols, groups;
 };
-int prepare(const CallContext& ctx, Source* s, int64_t rows, int64_t cols, int64_t groups,
-            cudaStream_t stream) {
-  if (tma_ready(s->data, s->row_stride, s->group_stride, groups)) {
-    if (groups == 1) s->group_stride = s->row_stride;  // unused, but checked
-    return DSMEM_HIST_OK;
+
+// Lays the sources TMA cannot read in place out in scratch, which the caller
+// gives back.
+int lay_out(const CallContext& ctx, Source* sources[2], void** scratch, cudaStream_t stream) {
+  Layouts layouts = {};
+  int64_t bytes = 0, chunks = 0;
+  for (int i = 0; i < 2; ++i) {
+    Source& s = *sources[i];
+    if (tma_ready(s.data, s.row_stride, s.group_stride, s.groups)) {
+      if (s.groups == 1) s.group_stride = s.row_stride;  // unused, but checked
+      continue;
+    }
+    Layout& l = layouts.of[i];
+    l.src = static_cast<const uint16_t*>(s.data);
+    l.row_stride = s.row_stride, l.group_stride = s.group_stride;
+    l.rows = static_cast<int>(s.rows), l.cols = static_cast<int>(s.cols);
+    l.dst_stride = static_cast<int>((s.cols + 7) / 8 * 8);
+    l.chunks = s.groups * s.rows * (l.dst_stride / 8);
+    chunks += l.chunks;
+    bytes += l.chunks * 16;
   }
-  const int64_t stride = (cols + 7) / 8 * 8;
-  int rc = pool_alloc(ctx, &s->scratch, static_cast<size_t>(groups * rows * stride * 2), stream);
+  if (chunks == 0) return DSMEM_HIST_OK;
+  int rc = pool_alloc(ctx, scratch, static_cast<size_t>(bytes), stream);
   if (rc) return rc;
-  const int64_t threads = groups * rows * (stride / 8);
-  const int grid = static_cast<int>(std::min<int64_t>((threads + 255) / 256, ctx.sm_count * 16));
-  layout_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(s->data), s->row_stride,
-                                          s->group_stride, static_cast<int>(rows), static_cast<int>(cols),
-                                          groups, static_cast<uint16_t*>(s->scratch),
-                                          static_cast<int>(stride));
-  s->data = s->scratch;
-  s->row_stride = stride;
-  s->group_stride = stride * rows;
+  uint16_t* at = static_cast<uint16_t*>(*scratch);
+  for (int i = 0; i < 2; ++i) {
+    Layout& l = layouts.of[i];
+    if (l.chunks == 0) continue;
+    l.dst = at;
+    at += l.chunks * 8;
+    sources[i]->data = l.dst;
+    sources[i]->row_stride = l.dst_stride;
+    sources[i]->group_stride = static_cast<int64_t>(l.dst_stride) * l.rows;
+  }
+  const int grid = static_cast<int>(std::min<int64_t>((chunks + 255) / 256, ctx.sm_count * 16));
+  layout_kernel<<<grid, 256, 0, stream>>>(layouts);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? DSMEM_HIST_OK : fail_with_cuda(e, "layout launch");
 }
 
-template <int kKind, int kCols, bool kPair>
-int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
+// Upper bound of a product's tiles: the group sizes are not known here.
+int64_t tile_bound(const ProductArgs& p, int cols, int height) {
+  const int64_t channels = p.kind == kInputGrad ? p.inner : p.outer;
+  const int64_t across = p.kind == kWeightGrad ? static_cast<int64_t>(p.groups) * ((p.inner + cols - 1) / cols)
+                                               : p.n / cols + std::min<int64_t>(p.groups + 1, p.n);
+  return across * ((channels + height - 1) / height);
+}
+
+template <int kKind, int kCols, int kTeam>
+int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w, int split,
            cudaStream_t stream) {
-  using R = Ring<kCols, kPair>;
+  using R = Ring<kCols, kTeam>;
   TileArgs a{};
   a.offsets = p.offsets, a.order = p.order, a.n = p.n;
   a.x_rows = static_cast<int>(p.x_rows), a.groups = p.groups, a.fan = Divisor(static_cast<uint32_t>(p.fan));
@@ -759,18 +904,15 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
       return rc;
   }
 
-  const int64_t chan_tiles = (a.channels + R::kHeight - 1) / R::kHeight;
-  const int64_t tiles = kKind == kWeightGrad
-                            ? chan_tiles * ((p.inner + kCols - 1) / kCols) * p.groups
-                            : chan_tiles * (p.n / kCols + std::min<int64_t>(p.groups + 1, p.n));
+  const int64_t tiles = tile_bound(p, kCols, R::kHeight);
   if (tiles > INT32_MAX)
     return fail_with(DSMEM_HIST_EINVAL, "grouped product: more than 2^31 output tiles");
   const int smem = R::smem_bytes(p.groups);
-  const auto kernel = product_kernel<kKind, kCols, kPair>;
+  const auto kernel = product_kernel<kKind, kCols, kTeam>;
   static SmemLimit limit;
   cudaError_t e = limit.need(reinterpret_cast<const void*>(kernel), ctx.device, smem);
   if (e != cudaSuccess) return fail_with_cuda(e, "cudaFuncSetAttribute");
-  const int per_unit = kPair ? 2 : 1;
+  const int per_unit = kTeam == kSplit ? split : (kTeam == kPair ? 2 : 1);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, ctx.sm_count / per_unit)) * per_unit);
   cfg.blockDim = dim3(kThreads);
@@ -786,38 +928,70 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
   return e == cudaSuccess ? DSMEM_HIST_OK : fail_with_cuda(e, "grouped product launch");
 }
 
-// Tiles as wide as the average group needs, so that few columns are padding.
+// CTAs to split a tile's depth over, where whole tiles leave SMs idle.
+int split_for(int64_t tiles, int64_t depth_blocks, int most, int sm_count) {
+  int split = 1;
+  while (split < most && tiles * split * 2 <= sm_count && depth_blocks >= split * 4) split *= 2;
+  return split;
+}
+
+template <int kKind, int kCols>
+int launch_narrow(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
+                  cudaStream_t stream) {
+  const int64_t depth = kKind == kForward ? p.inner : (kKind == kInputGrad ? p.outer : p.n / p.groups);
+  const int split = split_for(tile_bound(p, kCols, kChannels), depth / kDepth, Ring<kCols, kSplit>::kMaxSplit,
+                              ctx.sm_count);
+  if (split > 1) return launch<kKind, kCols, kSplit>(p, ctx, x, w, split, stream);
+  return launch<kKind, kCols, kSolo>(p, ctx, x, w, 1, stream);
+}
+template <int kKind, int kCols>
+int launch_wide(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
+                cudaStream_t stream) {
+  return launch<kKind, kCols, kPair>(p, ctx, x, w, 1, stream);
+}
+
+// Tiles as wide as the average group needs, so that few columns are padding;
+// 256 channels high where that still gives every pair of SMs a tile.
 template <int kKind>
 int launch_rows(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
                 cudaStream_t stream) {
-  const int64_t average = p.n / p.groups;
+  const int64_t average = p.n / p.groups, pairs = ctx.sm_count / 2;
   const int channels = kKind == kInputGrad ? p.inner : p.outer;
-  if (average <= 12) return launch<kKind, 16, false>(p, ctx, x, w, stream);
-  if (average <= 64) return launch<kKind, 64, false>(p, ctx, x, w, stream);
-  if (average <= 128 || channels <= kChannels) return launch<kKind, 128, false>(p, ctx, x, w, stream);
-  return launch<kKind, 256, true>(p, ctx, x, w, stream);
+  if (average <= 12) return launch_narrow<kKind, 16>(p, ctx, x, w, stream);
+  if (average <= 64 || tile_bound(p, 128, 128) < pairs) return launch_narrow<kKind, 64>(p, ctx, x, w, stream);
+  if (channels > kChannels && average > 128 && tile_bound(p, 256, 256) >= pairs)
+    return launch_wide<kKind, 256>(p, ctx, x, w, stream);
+  if (channels > kChannels && tile_bound(p, 128, 256) >= pairs)
+    return launch_wide<kKind, 128>(p, ctx, x, w, stream);
+  return launch<kKind, 128, kSolo>(p, ctx, x, w, 1, stream);
+}
+int launch_weight_grad(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
+                       cudaStream_t stream) {
+  const int64_t pairs = ctx.sm_count / 2;
+  if (p.outer > kChannels && tile_bound(p, 256, 256) >= pairs)
+    return launch_wide<kWeightGrad, 256>(p, ctx, x, w, stream);
+  if (tile_bound(p, 128, 128) >= pairs) return launch<kWeightGrad, 128, kSolo>(p, ctx, x, w, 1, stream);
+  return launch_narrow<kWeightGrad, 64>(p, ctx, x, w, stream);
 }
 
 }  // namespace
 
 int run_product(const ProductArgs& p, const CallContext& ctx, cudaStream_t stream) {
-  Source x{p.x, p.x_stride, 0}, w{p.w, p.w_stride, p.w_group_stride};
-  int rc = prepare(ctx, &x, p.x_rows, p.kind == kInputGrad ? p.outer : p.inner, 1, stream);
-  if (!rc) {
-    if (p.kind == kWeightGrad) rc = prepare(ctx, &w, p.n, p.outer, 1, stream);
-    else rc = prepare(ctx, &w, p.outer, p.inner, p.groups, stream);
-  }
+  Source x{p.x, p.x_stride, 0, p.x_rows, p.kind == kInputGrad ? p.outer : p.inner, 1};
+  Source w{p.w, p.w_stride, p.w_group_stride, p.outer, p.inner, p.groups};
+  if (p.kind == kWeightGrad) w = Source{p.w, p.w_stride, 0, p.n, p.outer, 1};
+  Source* sources[2] = {&x, &w};
+  void* scratch = nullptr;
+  int rc = lay_out(ctx, sources, &scratch, stream);
   if (!rc) {
     if (p.kind == kForward) rc = launch_rows<kForward>(p, ctx, x, w, stream);
     else if (p.kind == kInputGrad) rc = launch_rows<kInputGrad>(p, ctx, x, w, stream);
-    else if (p.inner <= 128 || p.outer <= 128) rc = launch<kWeightGrad, 128, false>(p, ctx, x, w, stream);
-    else rc = launch<kWeightGrad, 256, true>(p, ctx, x, w, stream);
+    else rc = launch_weight_grad(p, ctx, x, w, stream);
   }
-  for (Source* s : {&x, &w})
-    if (s->scratch) {
-      const int freed = pool_free(s->scratch, stream);
-      if (!rc) rc = freed;
-    }
+  if (scratch) {
+    const int freed = pool_free(scratch, stream);
+    if (!rc) rc = freed;
+  }
   return rc;
 }
 

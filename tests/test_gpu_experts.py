@@ -190,6 +190,17 @@ PRODUCTS = [
     (515, 3, 2, 328, 256, 0.0),
     (1100, 4, 2, 136, 392, 0.5),
     (2, 300, 2, 136, 64, 0.0),
+    # one group, few rows or few channels: the depth is split over a cluster
+    (1, 1, 1, 4096, 256, 0.0),
+    (3, 2, 2, 1032, 1032, 0.0),
+    (40, 1, 1, 1024, 136, 0.0),
+    (60, 2, 1, 264, 2048, 0.0),
+    (2100, 1, 1, 64, 128, 0.0),
+    # enough tiles for pairs of CTAs, 128 and 256 rows wide
+    (1300, 16, 1, 520, 800, 0.5),
+    (3000, 4, 1, 776, 1304, 0.5),
+    (2500, 5, 2, 1100, 1001, 1.0),
+    (700, 30, 1, 520, 264, 0.0),
 ]
 
 
