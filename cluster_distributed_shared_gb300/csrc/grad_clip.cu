@@ -1,9 +1,11 @@
 // The global norm of many gradients, and clipping by it.
 //
 // Two passes over the gradients: squares, then scaling.  Tensors are cut into
-// chunks of kChunk elements; CTA b of a launch takes chunks b, b + grid, ..
-// The table of tensors travels as a kernel parameter, so nothing is copied to
-// the device first and nothing is kept between calls.
+// chunks of 16 KB laid end to end, and every CTA takes an equal run of them in
+// each pass.  The second pass goes through its run backwards, so that it
+// begins with what the first left in L2, and stores past the cache.  The table
+// of tensors travels as a kernel parameter: nothing is copied to the device
+// first and nothing is kept between calls.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -17,9 +19,9 @@ namespace dsmh {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPerThread = 32;                    // elements of one thread in a chunk
-constexpr int kChunk = kThreads * kPerThread;     // 8192
-constexpr int kMaxTensors = 960;                  // per launch; the table stays under 32,764 bytes
+constexpr int kCtasPerSm = 4;
+constexpr int kVectors = 4;                              // 16-byte vectors of one thread in a chunk
+constexpr int kChunkBytes = kThreads * kVectors * 16;    // 16 KB
 
 struct Tensor {
   const void* grad;
@@ -27,15 +29,20 @@ struct Tensor {
   int64_t count : 60;
   int64_t dtype : 4;
 };
+// kTensors: 128 for short lists, else as many as 32,764 bytes of parameters hold.
+constexpr int kFewTensors = 128, kMostTensors = 1100;
+template <int kTensors>
 struct Table {
-  Tensor t[kMaxTensors];
-  uint32_t first_chunk[kMaxTensors + 1];
+  Tensor t[kTensors];
+  uint32_t first_chunk[kTensors + 1];
   int32_t tensors;
   uint32_t chunks;
 };
-static_assert(sizeof(Table) + 64 <= 32764, "kernel parameters");
+static_assert(sizeof(Table<kMostTensors>) + 64 <= 32764, "kernel parameters");
 
-__device__ __forceinline__ int find_tensor(const Table& tab, uint32_t chunk) {
+// The tensor of a chunk, from the chunks before or behind it.
+template <typename Tab>
+__device__ __forceinline__ int find_tensor(const Tab& tab, uint32_t chunk) {
   int lo = 0, hi = tab.tensors - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -44,170 +51,293 @@ __device__ __forceinline__ int find_tensor(const Table& tab, uint32_t chunk) {
   return lo;
 }
 
-// One thread's elements of a chunk: vectors of V, interleaved over the CTA.
-template <typename T, int V>
+// One thread's elements of a chunk: 16-byte vectors, or (kWide false, where
+// the addresses allow none) single elements, interleaved over the CTA.
+template <typename T, bool kWide>
 struct Slice {
-  Pack<T, V> p[kPerThread / V];
-  int64_t base;
-  __device__ __forceinline__ static int64_t at(int64_t base, int k) {
-    return base + (static_cast<int64_t>(k) * kThreads + threadIdx.x) * V;
+  static constexpr int kEach = kWide ? 16 / static_cast<int>(sizeof(T)) : 2;  // elements of a piece
+  static constexpr int kPieces = kVectors * 16 / static_cast<int>(sizeof(T)) / kEach;
+  static constexpr int kPairs = kEach / 2;
+  Vector16<T> p[kWide ? kPieces : 1];
+  T single[kWide ? 1 : kPieces][2];
+
+  // The i-th element of piece k is element first(k) + i * step() of the tensor.
+  __device__ __forceinline__ static int64_t first(int64_t base, int k) {
+    return kWide ? base + (k * kThreads + static_cast<int>(threadIdx.x)) * kEach
+                 : base + k * 2 * kThreads + static_cast<int>(threadIdx.x);
   }
-  __device__ __forceinline__ void load(const T* x, int64_t b, int64_t count) {
-    base = b;
+  static constexpr int kStep = kWide ? 1 : kThreads;
+
+  __device__ __forceinline__ float2 get(int k, int pair) const {
+    if constexpr (kWide) return p[k].get(pair);
+    else return make_float2(to_float(single[k][0]), to_float(single[k][1]));
+  }
+  template <bool kLast>
+  __device__ __forceinline__ void load(const T* x, int64_t base, int64_t count) {
 #pragma unroll
-    for (int k = 0; k < kPerThread / V; ++k) {
-      const int64_t i = at(base, k);
-      if (i + V <= count) {
-        p[k] = *reinterpret_cast<const Pack<T, V>*>(x + i);
+    for (int k = 0; k < kPieces; ++k) {
+      const int64_t i = first(base, k);
+      if constexpr (kWide) {
+        if (i + kEach <= count) {
+          const uint4* q = reinterpret_cast<const uint4*>(x + i);
+          p[k].words(kLast ? __ldcs(q) : __ldg(q));
+        } else {
+          alignas(16) T part[kEach];
+#pragma unroll
+          for (int v = 0; v < kEach; ++v) part[v] = i + v < count ? x[i + v] : from_float<T>(0.0f);
+          p[k].words(*reinterpret_cast<const uint4*>(part));
+        }
       } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) p[k].v[v] = i + v < count ? x[i + v] : from_float<T>(0.0f);
+        for (int v = 0; v < 2; ++v)
+          single[k][v] = i + v * kStep < count ? x[i + v * kStep] : from_float<T>(0.0f);
+      }
+    }
+  }
+  // Stores every element times `scale`.
+  __device__ __forceinline__ void store_scaled(T* out, int64_t base, int64_t count, float scale) {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int64_t i = first(base, k);
+      if constexpr (kWide) {
+#pragma unroll
+        for (int q = 0; q < kPairs; ++q) p[k].set(q, mul2(p[k].get(q), make_float2(scale, scale)));
+        if (i + kEach <= count) {
+          __stcs(reinterpret_cast<uint4*>(out + i), p[k].words());
+        } else {
+          alignas(16) T part[kEach];
+          *reinterpret_cast<uint4*>(part) = p[k].words();
+#pragma unroll
+          for (int v = 0; v < kEach; ++v)
+            if (i + v < count) out[i + v] = part[v];
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+          if (i + v * kStep < count) out[i + v * kStep] = from_float<T>(to_float(single[k][v]) * scale);
       }
     }
   }
 };
 
-// Sum of squares of a slice.  32 squares are summed in 32 bits; where that
-// left their range (a sum that overflowed, or so small that squares may have
-// been lost) they are summed again in 64.
-template <typename T, int V>
-__device__ __forceinline__ double squares(const Slice<T, V>& s) {
-  float sum = 0.0f, top = 0.0f;
+// A sum held as two floats, hi + lo, with lo the rounding errors of hi
+// (Knuth's two-sum), about 48 bits.  Doubles would do, but their adder takes
+// 16 clocks for a warp here: sums in doubles cost a sixth of the norm pass.
+struct Sum {
+  float hi = 0.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float x) {
+    const float s = hi + x, b = s - hi;
+    lo += (hi - (s - b)) + (x - b);
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const Sum& o) {
+    add(o.hi);
+    lo += o.lo;
+  }
+};
+// What one thread, or one CTA, has seen: ordinary squares in `sum`, those
+// outside its range in `rest`.
+struct Squares {
+  Sum sum;
+  double rest = 0.0;
+};
+
+// Adds the squares of a slice.  Up to 32 squares are summed in 32 bits; where
+// that leaves the range in which nothing overflows or is lost, they are summed
+// again in 64.
+template <typename S>
+__device__ __forceinline__ void add_squares(const S& s, Squares* to) {
+  float2 pair = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int k = 0; k < kPerThread / V; ++k)
+  for (int k = 0; k < S::kPieces; ++k)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float x = to_float(s.p[k].v[v]);
-      sum = fmaf(x, x, sum);
-      top = fmaxf(top, fabsf(x));
+    for (int q = 0; q < S::kPairs; ++q) {
+      const float2 x = s.get(k, q);
+      pair = fma2(x, x, pair);
     }
-  if ((sum > 1e-30f && sum < 1e37f) || (sum == 0.0f && top == 0.0f)) return sum;
+  const float sum = pair.x + pair.y;
+  if (sum > 1e-30f && sum < 1e30f) {
+    to->sum.add(sum);
+    return;
+  }
+  float top = 0.0f;
+#pragma unroll
+  for (int k = 0; k < S::kPieces; ++k)
+#pragma unroll
+    for (int q = 0; q < S::kPairs; ++q) {
+      const float2 x = s.get(k, q);
+      top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+    }
+  if (sum == 0.0f && top == 0.0f) return;
   double exact = 0.0;
 #pragma unroll
-  for (int k = 0; k < kPerThread / V; ++k)
+  for (int k = 0; k < S::kPieces; ++k)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const double x = to_float(s.p[k].v[v]);
-      exact = fma(x, x, exact);
+    for (int q = 0; q < S::kPairs; ++q) {
+      const float2 x = s.get(k, q);
+      exact = fma(static_cast<double>(x.x), static_cast<double>(x.x), exact);
+      exact = fma(static_cast<double>(x.y), static_cast<double>(x.y), exact);
     }
-  return exact;
+  to->rest += exact;
 }
 
-template <typename T>
 __device__ __forceinline__ bool wide(const Tensor& t) {
   return ((reinterpret_cast<uintptr_t>(t.grad) | reinterpret_cast<uintptr_t>(t.out)) & 15u) == 0;
 }
 
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const Tensor& t, int64_t base) {
+__device__ __forceinline__ void chunk_squares(const Tensor& t, int64_t chunk, Squares* to) {
+  const int64_t base = chunk * (kChunkBytes / static_cast<int>(sizeof(T)));
   const T* x = static_cast<const T*>(t.grad);
-  if (wide<T>(t)) {
-    Slice<T, 16 / sizeof(T)> s;
-    s.load(x, base, t.count);
-    return squares(s);
+  if (wide(t)) {
+    Slice<T, true> s;
+    s.template load<false>(x, base, t.count);
+    add_squares(s, to);
+  } else {
+    Slice<T, false> s;
+    s.template load<false>(x, base, t.count);
+    add_squares(s, to);
   }
-  Slice<T, 1> s;
-  s.load(x, base, t.count);
-  return squares(s);
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void scale_slice(const Tensor& t, int64_t base, float scale) {
-  Slice<T, V> s;
-  s.load(static_cast<const T*>(t.grad), base, t.count);
-  T* out = static_cast<T*>(t.out);
-#pragma unroll
-  for (int k = 0; k < kPerThread / V; ++k) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) s.p[k].v[v] = from_float<T>(to_float(s.p[k].v[v]) * scale);
-    const int64_t i = Slice<T, V>::at(base, k);
-    if (i + V <= t.count) {
-      *reinterpret_cast<Pack<T, V>*>(out + i) = s.p[k];
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (i + v < t.count) out[i + v] = s.p[k].v[v];
-    }
-  }
-}
 template <typename T>
-__device__ __forceinline__ void chunk_scale(const Tensor& t, int64_t base, float scale) {
-  if (wide<T>(t)) scale_slice<T, 16 / sizeof(T)>(t, base, scale);
-  else scale_slice<T, 1>(t, base, scale);
+__device__ __forceinline__ void chunk_scale(const Tensor& t, int64_t chunk, float scale) {
+  const int64_t base = chunk * (kChunkBytes / static_cast<int>(sizeof(T)));
+  const T* x = static_cast<const T*>(t.grad);
+  if (wide(t)) {
+    Slice<T, true> s;
+    s.template load<true>(x, base, t.count);
+    s.store_scaled(static_cast<T*>(t.out), base, t.count, scale);
+  } else {
+    Slice<T, false> s;
+    s.template load<true>(x, base, t.count);
+    s.store_scaled(static_cast<T*>(t.out), base, t.count, scale);
+  }
 }
 
-// Sum over the CTA in a fixed order (valid in every thread).
-__device__ __forceinline__ double cta_sum(double v) {
+// Sum over the CTA in a fixed order, valid in thread 0.
+__device__ __forceinline__ double cta_sum(Squares v) {
   __shared__ double part[kThreads / 32];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  for (int d = 16; d > 0; d >>= 1) {
+    Sum o;
+    o.hi = __shfl_xor_sync(0xffffffffu, v.sum.hi, d);
+    o.lo = __shfl_xor_sync(0xffffffffu, v.sum.lo, d);
+    v.sum.add(o);
+  }
+  if (__any_sync(0xffffffffu, !(v.rest == 0.0)))
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v.rest += __shfl_xor_sync(0xffffffffu, v.rest, d);
+  if ((threadIdx.x & 31) == 0)
+    part[threadIdx.x >> 5] = static_cast<double>(v.sum.hi) + v.sum.lo + v.rest;
   __syncthreads();
   double sum = 0.0;
-#pragma unroll
-  for (int k = 0; k < kThreads / 32; ++k) sum += part[k];
+  if (threadIdx.x == 0)
+    for (int k = 0; k < kThreads / 32; ++k) sum += part[k];
   return sum;
 }
 
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table tab,
-                                                        double* partial) {
-  double sum = 0.0;
-  for (uint32_t c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
-    const int i = find_tensor(tab, c);
-    const Tensor& t = tab.t[i];
-    const int64_t base = static_cast<int64_t>(c - tab.first_chunk[i]) * kChunk;
-    if (t.dtype == DSMEM_F32) sum += chunk_squares<float>(t, base);
-    else if (t.dtype == DSMEM_F16) sum += chunk_squares<__half>(t, base);
-    else sum += chunk_squares<__nv_bfloat16>(t, base);
-  }
-  sum = cta_sum(sum);
-  if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+// A CTA's squares; `hi` and `lo` hold them too where they are in a float's
+// ordinary range, else `hi` is NaN.
+struct alignas(16) Partial {
+  double exact;
+  Sum sum;
+};
+
+// This CTA's run of a table's chunks.
+__device__ __forceinline__ void my_chunks(uint32_t chunks, uint32_t* begin, uint32_t* end) {
+  *begin = static_cast<uint32_t>(static_cast<uint64_t>(chunks) * blockIdx.x / gridDim.x);
+  *end = static_cast<uint32_t>(static_cast<uint64_t>(chunks) * (blockIdx.x + 1) / gridDim.x);
 }
 
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table tab,
-                                                         const double* partial, int partials,
-                                                         float max_norm, float* norm) {
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < partials; i += kThreads) sum += partial[i];
-  const double total = sqrt(cta_sum(sum));
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(total);
-  const double ratio = max_norm / (total + 1e-6);
-  const float scale = ratio > 1.0 ? 1.0f : static_cast<float>(ratio);  // NaN stays NaN
-  for (uint32_t c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
-    const int i = find_tensor(tab, c);
+template <int kTensors>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    norm_kernel(const __grid_constant__ Table<kTensors> tab, Partial* partial) {
+  uint32_t c, end;
+  my_chunks(tab.chunks, &c, &end);
+  Squares mine;
+  int i = c < end ? find_tensor(tab, c) : 0;
+  for (; c < end; ++c) {
+    while (c >= tab.first_chunk[i + 1]) ++i;
     const Tensor& t = tab.t[i];
-    const int64_t base = static_cast<int64_t>(c - tab.first_chunk[i]) * kChunk;
-    if (t.dtype == DSMEM_F32) chunk_scale<float>(t, base, scale);
-    else if (t.dtype == DSMEM_F16) chunk_scale<__half>(t, base, scale);
-    else chunk_scale<__nv_bfloat16>(t, base, scale);
+    const int64_t k = c - tab.first_chunk[i];
+    if (t.dtype == DSMEM_F32) chunk_squares<float>(t, k, &mine);
+    else if (t.dtype == DSMEM_F16) chunk_squares<__half>(t, k, &mine);
+    else chunk_squares<__nv_bfloat16>(t, k, &mine);
+  }
+  const double sum = cta_sum(mine);
+  if (threadIdx.x == 0) {
+    Partial p;
+    p.exact = sum;
+    const bool ordinary = sum == 0.0 || (sum > 1e-25 && sum < 1e33);
+    p.sum.hi = ordinary ? static_cast<float>(sum) : NAN;
+    p.sum.lo = ordinary ? static_cast<float>(sum - p.sum.hi) : 0.0f;
+    partial[blockIdx.x] = p;
   }
 }
 
-// Fills a launch's table from grads[first..]; returns the next index.  A
-// tensor too long for the chunk counter continues in the next launch.
+template <int kTensors>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    scale_kernel(const __grid_constant__ Table<kTensors> tab, const Partial* partial, int partials,
+                 float max_norm, float* norm) {
+  // Every CTA adds the partial sums, thread 0 turns them into the factor.
+  __shared__ float factor;
+  Squares mine;
+  for (int i = threadIdx.x; i < partials; i += kThreads) {
+    const Partial p = partial[i];
+    if (p.sum.hi == p.sum.hi) mine.sum.add(p.sum);
+    else mine.rest += p.exact;
+  }
+  const double squares = cta_sum(mine);
+  if (threadIdx.x == 0) {
+    const double total = sqrt(squares);
+    if (norm && blockIdx.x == 0) *norm = static_cast<float>(total);
+    const double ratio = max_norm / (total + 1e-6);
+    factor = ratio > 1.0 ? 1.0f : static_cast<float>(ratio);  // NaN stays NaN
+  }
+  __syncthreads();
+  const float scale = factor;
+  uint32_t begin, c;
+  my_chunks(tab.chunks, &begin, &c);
+  int i = begin < c ? find_tensor(tab, c - 1) : 0;
+  while (c-- > begin) {
+    while (c < tab.first_chunk[i]) --i;
+    const Tensor& t = tab.t[i];
+    const int64_t k = c - tab.first_chunk[i];
+    if (t.dtype == DSMEM_F32) chunk_scale<float>(t, k, scale);
+    else if (t.dtype == DSMEM_F16) chunk_scale<__half>(t, k, scale);
+    else chunk_scale<__nv_bfloat16>(t, k, scale);
+  }
+}
+
+// Fills a launch's table from the cursor on.  A tensor whose two addresses
+// share a misalignment becomes its head up to the next 16 bytes and the rest;
+// one too long for the chunk counter goes on in the next launch.
 struct Cursor {
   int tensor = 0;
   int64_t done = 0;  // elements of that tensor already taken
 };
-void fill(Table* tab, const dsmem_grad_t* grads, int num, Cursor* at) {
-  tab->tensors = 0;
+template <int kTensors>
+void fill(Table<kTensors>* tab, const dsmem_grad_t* grads, int num, Cursor* at) {
+  int n = 0;
   uint32_t chunks = 0;
   constexpr uint32_t kMaxChunks = 1u << 30;
-  while (at->tensor < num && tab->tensors < kMaxTensors && chunks < kMaxChunks) {
+  while (at->tensor < num && n < kTensors && chunks < kMaxChunks) {
     const dsmem_grad_t& g = grads[at->tensor];
-    const int64_t left = g.count - at->done;
+    const int size = dtype_size(g.dtype);
+    const int64_t left = g.count - at->done, per_chunk = kChunkBytes / size;
     if (left > 0) {
-      const int64_t room = static_cast<int64_t>(kMaxChunks - chunks) * kChunk;
-      const int64_t take = std::min(left, room);
-      Tensor& t = tab->t[tab->tensors];
-      const int64_t skip = at->done * dtype_size(g.dtype);
-      t.grad = static_cast<const char*>(g.grad) + skip;
-      t.out = static_cast<char*>(g.out) + skip;
+      Tensor& t = tab->t[n];
+      t.grad = static_cast<const char*>(g.grad) + at->done * size;
+      t.out = static_cast<char*>(g.out) + at->done * size;
+      const uintptr_t off = reinterpret_cast<uintptr_t>(t.grad) & 15u;
+      int64_t take = std::min(left, static_cast<int64_t>(kMaxChunks - chunks) * per_chunk);
+      if (off != 0 && off == (reinterpret_cast<uintptr_t>(t.out) & 15u))
+        take = std::min<int64_t>(take, (16 - off) / size);
       t.count = take;
       t.dtype = g.dtype;
-      tab->first_chunk[tab->tensors++] = chunks;
-      chunks += static_cast<uint32_t>((take + kChunk - 1) / kChunk);
+      tab->first_chunk[n++] = chunks;
+      chunks += static_cast<uint32_t>((take + per_chunk - 1) / per_chunk);
       at->done += take;
     }
     if (at->done == g.count) {
@@ -215,43 +345,53 @@ void fill(Table* tab, const dsmem_grad_t* grads, int num, Cursor* at) {
       at->done = 0;
     }
   }
-  tab->first_chunk[tab->tensors] = chunks;
+  tab->first_chunk[n] = chunks;
+  tab->tensors = n;
   tab->chunks = chunks;
+}
+
+template <int kTensors>
+int run(const dsmem_grad_t* grads, int32_t num, float max_norm, float* norm, const CallContext& ctx,
+        cudaStream_t stream) {
+  const uint32_t most = static_cast<uint32_t>(ctx.sm_count * kCtasPerSm);
+  Table<kTensors> tab;
+  // One launch of each kernel for every table the list takes.
+  int launches = 0;
+  for (Cursor at; at.tensor < num || launches == 0; ++launches) fill(&tab, grads, num, &at);
+  Partial* partial = nullptr;
+  int rc = pool_alloc(ctx, reinterpret_cast<void**>(&partial),
+                      sizeof(Partial) * static_cast<size_t>(most) * launches, stream);
+  if (rc) return rc;
+  cudaError_t e = cudaSuccess;
+  int partials = 0;
+  Cursor at;
+  for (int l = 0; l < launches && e == cudaSuccess; ++l) {
+    if (launches > 1) fill(&tab, grads, num, &at);
+    const uint32_t grid = std::min(std::max(tab.chunks, 1u), most);
+    norm_kernel<kTensors><<<grid, kThreads, 0, stream>>>(tab, partial + partials);
+    partials += static_cast<int>(grid);
+    e = cudaGetLastError();
+  }
+  at = Cursor();
+  for (int l = 0; l < launches && e == cudaSuccess; ++l) {
+    if (launches > 1) fill(&tab, grads, num, &at);
+    const uint32_t grid = std::min(std::max(tab.chunks, 1u), most);
+    scale_kernel<kTensors><<<grid, kThreads, 0, stream>>>(tab, partial, partials, max_norm,
+                                                          l == 0 ? norm : nullptr);
+    e = cudaGetLastError();
+  }
+  rc = pool_free(partial, stream);
+  if (e != cudaSuccess) return fail_with_cuda(e, "gradient clipping launch");
+  return rc;
 }
 
 }  // namespace
 
 int run_grad_clip(const dsmem_grad_t* grads, int32_t num, float max_norm, float* norm,
                   const CallContext& ctx, cudaStream_t stream) {
-  const int grid_max = ctx.sm_count * 8;
-  int launches = 0;
-  Table tab;
-  for (Cursor at; at.tensor < num || launches == 0; ++launches) fill(&tab, grads, num, &at);
-  double* partial = nullptr;
-  int rc = pool_alloc(ctx, reinterpret_cast<void**>(&partial),
-                      sizeof(double) * static_cast<size_t>(grid_max) * launches, stream);
-  if (rc) return rc;
-  cudaError_t e = cudaSuccess;
-  int partials = 0;
-  Cursor at;
-  for (int l = 0; l < launches && e == cudaSuccess; ++l) {
-    fill(&tab, grads, num, &at);
-    const int grid = static_cast<int>(std::min<uint32_t>(std::max(tab.chunks, 1u), grid_max));
-    norm_kernel<<<grid, kThreads, 0, stream>>>(tab, partial + partials);
-    partials += grid;
-    e = cudaGetLastError();
-  }
-  at = Cursor();
-  for (int l = 0; l < launches && e == cudaSuccess; ++l) {
-    if (launches > 1) fill(&tab, grads, num, &at);
-    const int grid = static_cast<int>(std::min<uint32_t>(std::max(tab.chunks, 1u), grid_max));
-    scale_kernel<<<grid, kThreads, 0, stream>>>(tab, partial, partials, max_norm,
-                                                l == 0 ? norm : nullptr);
-    e = cudaGetLastError();
-  }
-  rc = pool_free(partial, stream);
-  if (e != cudaSuccess) return fail_with_cuda(e, "gradient clipping launch");
-  return rc;
+  // Each tensor may take two entries (a misaligned head and the rest).
+  if (2 * num <= kFewTensors) return run<kFewTensors>(grads, num, max_norm, norm, ctx, stream);
+  return run<kMostTensors>(grads, num, max_norm, norm, ctx, stream);
 }
 
 }  // namespace dsmh

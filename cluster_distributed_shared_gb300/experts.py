@@ -15,9 +15,12 @@ the inputs on other streams is the caller's to order.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 
 F32, F16, BF16 = 0, 1, 2
+_DTYPE, _IS_CUDA = operator.attrgetter("dtype"), operator.attrgetter("is_cuda")
 
 _p, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 SIGNATURES = {
@@ -308,34 +311,37 @@ def dsmem_combine_backward(dy, z, position, order, weights, stream=None):
 def dsmem_grad_clip(grads, max_norm: float, out=None, stream=None):
     """Global norm of `grads` (a list of contiguous CUDA tensors), returned as
     a float32 tensor without dimensions; the gradients times min(1, max_norm /
-    (norm + 1e-6)) go to `out`, a list of tensors like them, or in place."""
+    (norm + 1e-6)) go to `out`, a list of tensors of their types and sizes, or
+    in place."""
     grads = list(grads)
     out = grads if out is None else list(out)
     if len(out) != len(grads):
         raise ValueError("out must have one tensor for each gradient")
-    torch, codes = _lib.torch, _lib.codes
+    torch, tensor = _lib.torch, _lib.torch.Tensor
     device = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
-    index = device.index if device.type == "cuda" else -1
-    words = []                     # dsmem_grad_t: two addresses, count, type and 32 zero bits
-    for g, o in zip(grads, out):
-        code = codes.get(g.dtype)
-        if code is None or not g.is_cuda:
-            raise TypeError("grads must be CUDA float32, float16 or bfloat16 tensors")
-        if g.get_device() != index or not g.is_contiguous():
-            raise ValueError("grads must be contiguous and on one device")
-        at = g.data_ptr()
-        if o is g:
-            words += (at, at, g.numel(), code)
-            continue
-        if o.dtype != g.dtype or o.shape != g.shape or o.get_device() != index \
-                or not o.is_contiguous():
-            raise ValueError("out must match grads in type, shape and device and be contiguous")
-        words += (at, o.data_ptr(), g.numel(), code)
-    table = (ctypes.c_uint64 * max(len(words), 4))(*words)
+    types = list(map(_DTYPE, grads))
+    codes = list(map(_lib.codes.get, types))
+    counts = list(map(tensor.numel, grads))
+    if None in codes or not all(map(_IS_CUDA, grads)):
+        raise TypeError("grads must be CUDA float32, float16 or bfloat16 tensors")
+    if set(map(tensor.get_device, grads)) - {device.index} or \
+            not all(map(tensor.is_contiguous, grads)):
+        raise ValueError("grads must be contiguous and on one device")
+    if out is not grads and (
+            list(map(_DTYPE, out)) != types or list(map(tensor.numel, out)) != counts
+            or set(map(tensor.get_device, out)) - {device.index}
+            or not all(map(tensor.is_contiguous, out))):
+        raise ValueError("out must match grads in type, size and device and be contiguous")
+    table = array.array("Q", bytes(32 * max(len(grads), 1)))   # entries of dsmem_grad_t
+    table[0:4 * len(grads):4] = array.array("Q", map(tensor.data_ptr, grads))
+    table[1:4 * len(grads):4] = array.array("Q", map(tensor.data_ptr, out))
+    table[2:4 * len(grads):4] = array.array("Q", counts)
+    table[3:4 * len(grads):4] = array.array("Q", codes)
 
     def run(s):
         norm = torch.empty((), dtype=torch.float32, device=device)
-        _check(_lib.dsmem_grad_clip(table, len(grads), float(max_norm), norm.data_ptr(), s))
+        _check(_lib.dsmem_grad_clip(
+            table.buffer_info()[0], len(grads), float(max_norm), norm.data_ptr(), s))
         return norm
 
     return _on(device, stream, (*grads, *out), run)
