@@ -10,109 +10,191 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// One CTA per token and kThreads * V columns: out = sum_j w_j z[p_j], summed in
-// 32 bits in the order of j.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a) {
+// What one thread handles of a row at a time: 16 bytes, or (kWide false, where
+// addresses allow none) two elements kThreads apart.  Rows of z, the outputs
+// and dz go by once and pass the caches.
+template <typename T, bool kWide>
+struct Piece {
+  static constexpr int kPairs = kWide ? Vector16<T>::kPairs : 1;
+  static constexpr int kEach = 2 * kPairs;
+  Vector16<T> wide;
+  T single[kWide ? 1 : 2];
+
+  // First column of a thread's piece, of those beginning at column `base`.
+  __device__ __forceinline__ static int column(int base) {
+    return base + static_cast<int>(threadIdx.x) * (kWide ? kEach : 1);
+  }
+  template <bool kOnce>
+  __device__ __forceinline__ void load(const T* p, int left) {
+    if constexpr (kWide) {
+      const uint4* q = reinterpret_cast<const uint4*>(p);
+      wide.words(kOnce ? __ldcs(q) : *q);
+    } else {
+      single[0] = p[0];
+      single[1] = kThreads < left ? p[kThreads] : from_float<T>(0.0f);
+    }
+  }
+  __device__ __forceinline__ float2 get(int i) const {
+    if constexpr (kWide) return wide.get(i);
+    else return make_float2(to_float(single[0]), to_float(single[1]));
+  }
+  __device__ __forceinline__ void set(int i, float2 v) {
+    if constexpr (kWide) {
+      wide.set(i, v);
+    } else {
+      single[0] = from_float<T>(v.x);
+      single[1] = from_float<T>(v.y);
+    }
+  }
+  __device__ __forceinline__ void store(T* p, int left) const {
+    if constexpr (kWide) {
+      __stcs(reinterpret_cast<uint4*>(p), wide.words());
+    } else {
+      p[0] = single[0];
+      if (kThreads < left) p[kThreads] = single[1];
+    }
+  }
+};
+
+// The rows of a token are taken kAtOnce at a time: their positions first, then
+// a piece of each in flight together.
+constexpr int kAtOnce = 4;
+constexpr int kCtas = 5;
+
+// One CTA per token and kThreads pieces: out = sum_j w_j z[p_j], summed in 32
+// bits in the order of j.  Bound by reading z.
+template <typename T, bool kWide>
+__global__ void __launch_bounds__(kThreads, kCtas) combine_kernel(CombineArgs a) {
+  using P = Piece<T, kWide>;
   const int64_t token = blockIdx.x;
-  const int col = (blockIdx.y * kThreads + threadIdx.x) * V;
-  if (col >= a.width) return;
-  using P = Pack<T, V>;
+  const int col = P::column(blockIdx.y * kThreads * P::kEach), left = a.width - col;
+  if (left <= 0) return;
   const T* z = static_cast<const T*>(a.z) + col;
-  float acc[V];
+  float2 acc[P::kPairs];
 #pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-  for (int j = 0; j < a.top_k; ++j) {
-    const int64_t i = token * a.top_k + j;
-    const int64_t p = a.position[i];
-    if (p < 0 || p >= a.z_rows) continue;
-    const float w = a.weights ? a.weights[i] : 1.0f;
-    const P x = *reinterpret_cast<const P*>(z + p * a.z_stride);
+  for (int q = 0; q < P::kPairs; ++q) acc[q] = make_float2(0.0f, 0.0f);
+  for (int j0 = 0; j0 < a.top_k; j0 += kAtOnce) {
+    int p[kAtOnce];
+    float w[kAtOnce];
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] += w * to_float(x.v[v]);
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int64_t i = token * a.top_k + j0 + j;
+      p[j] = j0 + j < a.top_k ? a.position[i] : -1;
+      if (p[j] >= a.z_rows) p[j] = -1;
+      w[j] = a.weights && j0 + j < a.top_k ? a.weights[i] : 1.0f;
+    }
+    P x[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+      if (p[j] >= 0) x[j].template load<true>(z + p[j] * a.z_stride, left);
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+      if (p[j] >= 0) {
+#pragma unroll
+        for (int q = 0; q < P::kPairs; ++q) acc[q] = fma2(make_float2(w[j], w[j]), x[j].get(q), acc[q]);
+      }
   }
   P y;
 #pragma unroll
-  for (int v = 0; v < V; ++v) y.v[v] = from_float<T>(acc[v]);
-  *reinterpret_cast<P*>(static_cast<T*>(a.out) + token * a.width + col) = y;
+  for (int q = 0; q < P::kPairs; ++q) y.set(q, acc[q]);
+  y.store(static_cast<T*>(a.out) + token * a.width + col, left);
 }
 
 // One CTA per token: its dy row against each of its z rows.  dz is written on
 // the way; the dot products are summed in 32 bits by thread, warp and CTA.
 // The CTA also clears those of the rows [token * top_k, (token + 1) * top_k)
-// that lie behind the last group.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) combine_backward_kernel(CombineArgs a) {
-  __shared__ float part[kThreads / 32];
+// that lie behind the last group.  Bound by reading z and writing dz.
+template <typename T, bool kWide>
+__global__ void __launch_bounds__(kThreads, kCtas) combine_backward_kernel(CombineArgs a) {
+  using P = Piece<T, kWide>;
+  __shared__ float part[kThreads / 32][kAtOnce];
   const int64_t token = blockIdx.x;
-  using P = Pack<T, V>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const T* dy = static_cast<const T*>(a.dy) + token * a.dy_stride;
-  for (int j = 0; j < a.top_k; ++j) {
-    const int64_t i = token * a.top_k + j;
-    const int64_t p = a.position[i];
-    const bool found = p >= 0 && p < a.z_rows;
-    float dot = 0.0f;
-    if (found) {
-      const float w = a.weights[i];
-      const T* z = static_cast<const T*>(a.z) + p * a.z_stride;
-      T* dz = static_cast<T*>(a.out) + p * a.width;
-      for (int col = threadIdx.x * V; col < a.width; col += kThreads * V) {
-        const P g = *reinterpret_cast<const P*>(dy + col);
-        const P x = *reinterpret_cast<const P*>(z + col);
-        P d;
+  T* dz = static_cast<T*>(a.out);
+  for (int j0 = 0; j0 < a.top_k; j0 += kAtOnce) {
+    int p[kAtOnce];
+    uint32_t behind = 0;
+    float w[kAtOnce];
+    float2 dot[kAtOnce];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float gv = to_float(g.v[v]);
-          dot += gv * to_float(x.v[v]);
-          d.v[v] = from_float<T>(w * gv);
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int64_t i = token * a.top_k + j0 + j;
+      const bool in = j0 + j < a.top_k;
+      p[j] = in ? a.position[i] : -1;
+      if (p[j] >= a.z_rows) p[j] = -1;
+      w[j] = in ? a.weights[i] : 0.0f;
+      if (in && a.order[i] < 0) behind |= 1u << j;
+      dot[j] = make_float2(0.0f, 0.0f);
+    }
+    for (int base = 0; base < a.width; base += kThreads * P::kEach) {
+      const int col = P::column(base), left = a.width - col;
+      if (left <= 0) break;
+      P g;
+      g.template load<false>(dy + col, left);
+      P x[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (p[j] >= 0) x[j].template load<true>(static_cast<const T*>(a.z) + p[j] * a.z_stride + col, left);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (p[j] >= 0) {
+#pragma unroll
+          for (int q = 0; q < P::kPairs; ++q) {
+            const float2 v = g.get(q);
+            dot[j] = fma2(v, x[j].get(q), dot[j]);
+            x[j].set(q, mul2(make_float2(w[j], w[j]), v));
+          }
+          x[j].store(dz + static_cast<int64_t>(p[j]) * a.width + col, left);
         }
-        *reinterpret_cast<P*>(dz + col) = d;
+      if (behind) {
+#pragma unroll
+        for (int q = 0; q < P::kPairs; ++q) g.set(q, make_float2(0.0f, 0.0f));
+        for (int j = 0; j < kAtOnce; ++j)
+          if (behind >> j & 1u) g.store(dz + (token * a.top_k + j0 + j) * a.width + col, left);
       }
     }
+    float sum[kAtOnce];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      float sum = 0.0f;
-      for (int k = 0; k < kThreads / 32; ++k) sum += part[k];
-      a.dweights[i] = found ? sum : 0.0f;
+    for (int j = 0; j < kAtOnce; ++j) {
+      sum[j] = dot[j].x + dot[j].y;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+      if (lane == j) part[warp][j] = sum[j];
     }
     __syncthreads();
-    if (a.order[i] < 0) {
-      P zero;
+    if (threadIdx.x < kAtOnce && j0 + static_cast<int>(threadIdx.x) < a.top_k) {
+      float all = 0.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) zero.v[v] = from_float<T>(0.0f);
-      T* dz = static_cast<T*>(a.out) + i * a.width;
-      for (int col = threadIdx.x * V; col < a.width; col += kThreads * V)
-        *reinterpret_cast<P*>(dz + col) = zero;
+      for (int k = 0; k < kThreads / 32; ++k) all += part[k][threadIdx.x];
+      a.dweights[token * a.top_k + j0 + threadIdx.x] = all;
     }
+    __syncthreads();
   }
 }
 
-// Elements per access: 16 bytes where every base and row allows it, else one.
 bool wide(const void* p, int64_t stride, int size) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * size % 16 == 0;
 }
 
-template <typename T, int V>
+template <typename T, bool kWide>
 cudaError_t launch(const CombineArgs& a, bool backward, cudaStream_t stream) {
-  if (backward) {
-    combine_backward_kernel<T, V><<<dim3(static_cast<unsigned>(a.tokens)), kThreads, 0, stream>>>(a);
-  } else {
-    const dim3 grid(static_cast<unsigned>(a.tokens), (a.width + kThreads * V - 1) / (kThreads * V));
-    combine_kernel<T, V><<<grid, kThreads, 0, stream>>>(a);
-  }
+  const unsigned tokens = static_cast<unsigned>(a.tokens);
+  const int columns = kThreads * Piece<T, kWide>::kEach;
+  if (backward)
+    combine_backward_kernel<T, kWide><<<tokens, kThreads, 0, stream>>>(a);
+  else
+    combine_kernel<T, kWide><<<dim3(tokens, (a.width + columns - 1) / columns), kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
+// 16 bytes at a time where every base and row allows it.
 template <typename T>
 cudaError_t dispatch(const CombineArgs& a, bool backward, cudaStream_t stream) {
-  constexpr int kWide = 16 / sizeof(T);
   const int s = sizeof(T);
   const bool ok = wide(a.z, a.z_stride, s) && wide(a.out, a.width, s) &&
-                  (!backward || wide(a.dy, a.dy_stride, s)) && a.width % kWide == 0;
-  return ok ? launch<T, kWide>(a, backward, stream) : launch<T, 1>(a, backward, stream);
+                  (!backward || wide(a.dy, a.dy_stride, s));
+  return ok ? launch<T, true>(a, backward, stream) : launch<T, false>(a, backward, stream);
 }
 
 cudaError_t dispatch_type(const CombineArgs& a, bool backward, cudaStream_t stream) {

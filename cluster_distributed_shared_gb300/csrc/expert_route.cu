@@ -38,25 +38,52 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// One warp per token, the row in registers: lane l holds logits l, l + 32, ..
-// Each of the top_k picks is a warp maximum over rank keys, then a warp
-// minimum over the indexes that hold it, so equal logits go to the lowest
-// index.  Softmax statistics are 32-bit.
-template <typename T, int R>
+// R logits of a row, contiguous ones, in lane l those from l * R on.  kVector:
+// rows are 16-byte aligned and their length is a multiple of R.
+template <typename T, int R, bool kVector>
+__device__ __forceinline__ void load_row(const T* row, int experts, float (&v)[R]) {
+  const int first = (threadIdx.x & 31) * R;
+  constexpr int kEach = 16 / static_cast<int>(sizeof(T));
+  if constexpr (kVector && R % kEach == 0) {
+#pragma unroll
+    for (int r = 0; r < R; r += kEach) {
+      Vector16<T> p;
+      p.words(first < experts ? *reinterpret_cast<const uint4*>(row + first + r) : make_uint4(0, 0, 0, 0));
+#pragma unroll
+      for (int q = 0; q < kEach / 2; ++q) {
+        const float2 x = p.get(q);
+        v[r + 2 * q] = first < experts ? x.x : -INFINITY;
+        v[r + 2 * q + 1] = first < experts ? x.y : -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = first + r < experts ? to_float(row[first + r]) : -INFINITY;
+  }
+}
+
+// One warp per token, the row in registers.  Each lane keeps the largest of
+// its rank keys and where it is; a pick is a warp maximum, the lowest lane
+// that holds it, and a new maximum in that lane.  Lanes hold contiguous runs,
+// so the lowest lane and the first place in it are the lowest index.  Softmax
+// statistics are 32-bit.
+template <typename T, int R, bool kVector>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
   const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   if (token >= a.tokens) return;
   const int lane = threadIdx.x & 31;
-  const T* row = static_cast<const T*>(a.logits) + token * a.row_stride;
   uint32_t key[R];
+  {
+    float v[R];
+    load_row<T, R, kVector>(static_cast<const T*>(a.logits) + token * a.row_stride, a.experts, v);
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int e = r * 32 + lane;
-    key[r] = e < a.experts ? rank_key(to_float(row[e])) : 0u;
+    for (int r = 0; r < R; ++r) key[r] = rank_key(v[r]);
   }
   uint32_t best = 0;
+  int at = 0;
 #pragma unroll
-  for (int r = 0; r < R; ++r) best = max(best, key[r]);
+  for (int r = 0; r < R; ++r)
+    if (key[r] > best) best = key[r], at = r;
   const uint32_t top_key = __reduce_max_sync(kFull, best);
   const float top = rank_value(top_key);
   float all = 0.0f;
@@ -67,26 +94,25 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
     all = warp_sum(all);
   }
   int my_id = -1;
-  float mine = 0.0f;
+  uint32_t my_key = 0;
   for (int j = 0; j < a.top_k; ++j) {
-    best = 0;
-#pragma unroll
-    for (int r = 0; r < R; ++r) best = max(best, key[r]);
     const uint32_t m = __reduce_max_sync(kFull, best);
     if (m == 0u) break;
-    uint32_t first = 0xffffffffu;
+    const int holder = __ffs(__ballot_sync(kFull, best == m)) - 1;
+    const int id = __shfl_sync(kFull, lane * R + at, holder);
+    if (lane == j) my_id = id, my_key = m;
+    if (lane == holder) {
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r)
-      if (key[r] == m) first = r * 32 + lane;
-    const uint32_t id = __reduce_min_sync(kFull, first);
+      for (int r = 0; r < R; ++r)
+        if (r == at) key[r] = 0u;
+      best = 0u;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (static_cast<uint32_t>(r * 32 + lane) == id) key[r] = 0u;
-    if (lane == j) {
-      my_id = static_cast<int>(id);
-      mine = raised(rank_value(m), top);
+      for (int r = 0; r < R; ++r)
+        if (key[r] > best) best = key[r], at = r;
     }
+    __syncwarp();
   }
+  const float mine = my_id >= 0 ? raised(rank_value(my_key), top) : 0.0f;
   if (a.renormalize) all = warp_sum(mine);
   if (lane < a.top_k) {
     a.ids[token * a.top_k + lane] = my_id;
@@ -98,7 +124,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
 // s = sum_j w_j g_j:  renormalised, d logit[ids_j] = w_j (g_j - s) and 0
 // elsewhere; else d logit[e] = [e = ids_j] w_j g_j - p_e s with the softmax p
 // taken again from the row.
-template <typename T, int R>
+template <typename T, int R, bool kVector>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteArgs a) {
   const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   if (token >= a.tokens) return;
@@ -118,15 +144,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
 #pragma unroll
   for (int r = 0; r < R; ++r) grad[r] = 0.0f;
   if (!a.renormalize) {
-    const T* row = static_cast<const T*>(a.logits) + token * a.row_stride;
     float v[R];
     float top = -INFINITY, all = 0.0f;
+    load_row<T, R, kVector>(static_cast<const T*>(a.logits) + token * a.row_stride, a.experts, v);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int e = r * 32 + lane;
-      v[r] = e < a.experts ? to_float(row[e]) : -INFINITY;
+    for (int r = 0; r < R; ++r)
       if (v[r] > top) top = v[r];
-    }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
 #pragma unroll
@@ -139,32 +162,54 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
 #pragma unroll
     for (int r = 0; r < R; ++r) grad[r] *= scale;
   }
+  const int first = lane * R;
   for (int j = 0; j < a.top_k; ++j) {
     const int id = __shfl_sync(kFull, my_id, j);
     const float g = __shfl_sync(kFull, mine, j);
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (r * 32 + lane == id) grad[r] += g;
+      if (first + r == id) grad[r] += g;
   }
-  T* out = static_cast<T*>(a.grad_logits) + token * a.experts;
+  T* out = static_cast<T*>(a.grad_logits) + token * a.experts + first;
+  constexpr int kEach = 16 / static_cast<int>(sizeof(T));
+  if constexpr (kVector && R % kEach == 0) {
+    if (first < a.experts) {
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (r * 32 + lane < a.experts) out[r * 32 + lane] = from_float<T>(grad[r]);
+      for (int r = 0; r < R; r += kEach) {
+        Vector16<T> p;
+#pragma unroll
+        for (int q = 0; q < kEach / 2; ++q) p.set(q, make_float2(grad[r + 2 * q], grad[r + 2 * q + 1]));
+        *reinterpret_cast<uint4*>(out + r) = p.words();
+      }
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (first + r < a.experts) out[r] = from_float<T>(grad[r]);
+  }
 }
 
 template <typename T>
 cudaError_t launch_route_t(const RouteArgs& a, bool backward, cudaStream_t stream) {
   const int64_t blocks = (a.tokens + kRouteWarps - 1) / kRouteWarps;
   const dim3 grid(static_cast<unsigned>(blocks)), block(kRouteWarps * 32);
-#define DSMH_ROUTE(R)                                                  \
-  if (a.experts <= 32 * R) {                                           \
-    if (backward)                                                      \
-      route_backward_kernel<T, R><<<grid, block, 0, stream>>>(a);      \
-    else                                                               \
-      route_kernel<T, R><<<grid, block, 0, stream>>>(a);               \
-    return cudaGetLastError();                                         \
+  const auto aligned = [&](const void* p, int64_t stride) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * static_cast<int64_t>(sizeof(T)) % 16 == 0;
+  };
+  const bool vector = aligned(a.logits, a.row_stride) && (!backward || aligned(a.grad_logits, a.experts));
+#define DSMH_ROUTE(R)                                                                 \
+  if (a.experts <= 32 * R) {                                                          \
+    if (vector && a.experts % R == 0) {                                               \
+      if (backward) route_backward_kernel<T, R, true><<<grid, block, 0, stream>>>(a); \
+      else route_kernel<T, R, true><<<grid, block, 0, stream>>>(a);                   \
+    } else {                                                                          \
+      if (backward) route_backward_kernel<T, R, false><<<grid, block, 0, stream>>>(a);\
+      else route_kernel<T, R, false><<<grid, block, 0, stream>>>(a);                  \
+    }                                                                                 \
+    return cudaGetLastError();                                                        \
   }
   DSMH_ROUTE(2)
+  DSMH_ROUTE(4)
   DSMH_ROUTE(8)
   DSMH_ROUTE(32)
 #undef DSMH_ROUTE
