@@ -230,7 +230,7 @@ cudaError_t dispatch_route(const RouteArgs& a, bool backward, cudaStream_t strea
 //      and the CTA's total; the totals of the cluster's CTAs are read through
 //      distributed shared memory, so every CTA knows what precedes it in the
 //      group and how large the group is; a scan over the groups gives the
-//      offsets.  Each row then holds where its warp's next key of a group goes.
+//      offsets.  Row and base then say where a warp's next key of a group goes.
 //   3. Each warp goes over its keys again, 32 at a time: lanes with equal
 //      keys are found by one ballot per key bit, take consecutive places in
 //      lane order and move the counter on.
@@ -252,51 +252,82 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
   return v;
 }
 
+constexpr int kGroupBatch = 8;  // keys of a lane that are loaded together
+
+// The batch of a warp's run that begins at `i0`; ~0 behind the run's end.
+__device__ __forceinline__ void load_keys(const GroupArgs& a, int64_t i0, int64_t end,
+                                          uint32_t (&key)[kGroupBatch]) {
+#pragma unroll
+  for (int u = 0; u < kGroupBatch; ++u) {
+    const int64_t i = i0 + u * 32 + (threadIdx.x & 31);
+    key[u] = i < end ? static_cast<uint32_t>(a.keys[i]) : 0xffffffffu;
+  }
+}
+
 __global__ void __launch_bounds__(1024) group_kernel(GroupArgs a) {
-  extern __shared__ uint32_t smem[];  // rows [warps][groups], totals [groups], scan [32]
+  extern __shared__ uint32_t smem[];  // rows [warps][groups], totals and bases [groups], scan [32]
   const uint32_t rank = cluster_ctarank(), P = cluster_nctarank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t G = static_cast<uint32_t>(a.groups);
   uint32_t* total = smem + (a.shared_totals ? 0 : static_cast<size_t>(a.warps) * G);
-  uint32_t* scan = total + G;
+  uint32_t* base = total + (a.shared_totals ? 0 : G);
+  uint32_t* scan = base + G;
   uint32_t* mine = smem + static_cast<size_t>(warp) * G;
-  for (uint32_t i = threadIdx.x; i < a.warps * G; i += blockDim.x) smem[i] = 0;
-  __syncthreads();
 
-  // Each warp's run of keys, a multiple of 32 long.
+  // Each warp's run of keys, a multiple of 32 long; its first batch stays in
+  // registers for both passes.
   const int64_t parts = static_cast<int64_t>(P) * a.warps;
   const int64_t run = ((a.n + parts - 1) / parts + 31) / 32 * 32;
   int64_t begin = (static_cast<int64_t>(rank) * a.warps + warp) * run;
   int64_t end = begin + run;
   if (begin > a.n) begin = a.n;
   if (end > a.n) end = a.n;
+  uint32_t key[kGroupBatch];
+  load_keys(a, begin, end, key);
 
-  for (int64_t i = begin + lane; i < end; i += 32) {
-    const uint32_t key = static_cast<uint32_t>(a.keys[i]);
-    if (key < G) atomicAdd(mine + key, 1u);
+  for (uint32_t i = threadIdx.x; i < a.warps * G; i += blockDim.x) smem[i] = 0;
+  __syncthreads();
+  for (int64_t i0 = begin; i0 < end; i0 += 32 * kGroupBatch) {
+    if (i0 != begin) load_keys(a, i0, end, key);
+#pragma unroll
+    for (int u = 0; u < kGroupBatch; ++u)
+      if (key[u] < G) atomicAdd(mine + key[u], 1u);
   }
   __syncthreads();
   for (uint32_t g = threadIdx.x; g < G && !a.shared_totals; g += blockDim.x) {
     uint32_t sum = 0;
-    for (int w = 0; w < a.warps; ++w) {
-      const uint32_t c = smem[static_cast<size_t>(w) * G + g];
-      smem[static_cast<size_t>(w) * G + g] = sum;
-      sum += c;
+    for (int w0 = 0; w0 < a.warps; w0 += 8) {
+      uint32_t c[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) c[w] = w0 + w < a.warps ? smem[static_cast<size_t>(w0 + w) * G + g] : 0u;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        if (w0 + w < a.warps) smem[static_cast<size_t>(w0 + w) * G + g] = sum;
+        sum += c[w];
+      }
     }
     total[g] = sum;
   }
-  cluster_barrier();
+  if (P > 1) cluster_barrier();
+  else __syncthreads();
   // Scan over the groups, blockDim.x at a time, carrying the sum so far.
   uint32_t carry = 0;
   for (uint32_t g0 = 0; g0 < G; g0 += blockDim.x) {
     const uint32_t g = g0 + threadIdx.x;
     uint32_t before = 0, size = 0;
     if (g < G) {
-      const uint32_t addr = smem_u32(total + g);
-      for (uint32_t r = 0; r < P; ++r) {
-        const uint32_t c = ld_cluster_u32(map_rank(addr, r));
-        if (r < rank) before += c;
-        size += c;
+      if (P > 1) {
+        const uint32_t addr = smem_u32(total + g);
+        uint32_t c[16];
+#pragma unroll
+        for (uint32_t r = 0; r < 16; ++r) c[r] = r < P ? ld_cluster_u32(map_rank(addr, r)) : 0u;
+#pragma unroll
+        for (uint32_t r = 0; r < 16; ++r) {
+          if (r < rank) before += c[r];
+          size += c[r];
+        }
+      } else {
+        size = total[g];
       }
     }
     uint32_t incl = size;
@@ -307,51 +338,54 @@ __global__ void __launch_bounds__(1024) group_kernel(GroupArgs a) {
     }
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    uint32_t ahead = carry, block = 0;
-    for (int w = 0; w < a.warps; ++w) {
-      const uint32_t c = scan[w];
-      if (w < warp) ahead += c;
-      block += c;
-    }
-    const uint32_t offset = ahead + incl - size;
+    uint32_t ahead = lane < a.warps ? scan[lane] : 0u;
+    const uint32_t block = __reduce_add_sync(kFull, ahead);
+    ahead = __reduce_add_sync(kFull, lane < warp ? ahead : 0u);
+    const uint32_t offset = carry + ahead + incl - size;
     if (g < G) {
-      if (a.shared_totals) {
-        smem[g] = offset;
-      } else {
-        for (int w = 0; w < a.warps; ++w) smem[static_cast<size_t>(w) * G + g] += offset + before;
-      }
+      base[g] = offset + before;
       if (rank == 0) a.offsets[g] = static_cast<int32_t>(offset);
     }
     carry += block;
     __syncthreads();
   }
   if (rank == 0 && threadIdx.x == 0) a.offsets[G] = static_cast<int32_t>(carry);
-  // No CTA leaves, or writes over its totals, while others still read them.
-  cluster_barrier();
+  // No CTA leaves while others still read its totals: the arrival here, the
+  // wait at the end.
+  if (P > 1) cluster_arrive_relaxed();
 
   const uint32_t below = (1u << lane) - 1u;
-  for (int64_t i0 = begin; i0 < end; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const uint32_t key = i < end ? static_cast<uint32_t>(a.keys[i]) : 0xffffffffu;
-    const bool valid = key < G;
-    uint32_t peers = __ballot_sync(kFull, valid);
-    for (int b = 0; b < a.bits; ++b) {
-      const bool bit = (key >> b) & 1u;
-      const uint32_t with = __ballot_sync(kFull, bit);
-      peers &= bit ? with : ~with;
+  for (int64_t i0 = begin; i0 < end; i0 += 32 * kGroupBatch) {
+    if (run > 32 * kGroupBatch) load_keys(a, i0, end, key);
+#pragma unroll
+    for (int u = 0; u < kGroupBatch; ++u) {
+      const int64_t i = i0 + u * 32 + lane;
+      if (i0 + u * 32 >= end) break;
+      const bool valid = key[u] < G;
+      uint32_t peers = __ballot_sync(kFull, valid);
+      for (int b = 0; b < a.bits; ++b) {
+        const bool bit = (key[u] >> b) & 1u;
+        const uint32_t with = __ballot_sync(kFull, bit);
+        peers &= bit ? with : ~with;
+      }
+      uint32_t place = 0xffffffffu;
+      if (valid) {
+        // With shared totals the row holds the places themselves.
+        place = mine[key[u]] + __popc(peers & below);
+        if (!a.shared_totals) place += base[key[u]];
+      }
+      __syncwarp();
+      if (valid && lane == 31 - __clz(peers)) mine[key[u]] += __popc(peers);
+      __syncwarp();
+      if (i < end) a.position[i] = static_cast<int32_t>(place);
+      if (valid) a.order[place] = static_cast<int32_t>(i);
     }
-    uint32_t place = 0xffffffffu;
-    if (valid) place = mine[key] + __popc(peers & below);
-    __syncwarp();
-    if (valid && lane == 31 - __clz(peers)) mine[key] = place + 1;
-    __syncwarp();
-    if (i < end) a.position[i] = static_cast<int32_t>(place);
-    if (valid) a.order[place] = static_cast<int32_t>(i);
   }
   // Places behind the last group.
   for (int64_t p = carry + static_cast<int64_t>(rank) * blockDim.x + threadIdx.x; p < a.n;
        p += static_cast<int64_t>(P) * blockDim.x)
     a.order[p] = -1;
+  if (P > 1) cluster_wait();
 }
 
 constexpr int kGroupSmemLimit = 200 * 1024;
@@ -373,16 +407,16 @@ cudaError_t launch_group(const int32_t* keys, int64_t n, int num_groups, int32_t
   // Warps: as many counter rows as shared memory holds beside the totals, but
   // no more than the keys fill with 32 each.  CTAs: one cluster, doubled
   // while every warp still has 128 keys or more.
-  // Where a row and the totals do not fit (25,585 groups or more), one warp
-  // in one CTA keeps both in one row.
-  const int64_t fit = (kGroupSmemLimit / 4 - 32) / num_groups - 1;
+  // Where a row, the totals and the bases do not fit (17,057 groups or more),
+  // one warp in one CTA keeps all in one row.
+  const int64_t fit = (kGroupSmemLimit / 4 - 32) / num_groups - 2;
   a.shared_totals = fit < 1;
   int64_t warps = (n + 31) / 32;
   if (warps > fit) warps = fit;
   a.warps = static_cast<int>(warps < 1 ? 1 : (warps > 32 ? 32 : warps));
   int P = 1;
   while (P < 16 && !a.shared_totals && n >= int64_t{2} * P * a.warps * 128) P *= 2;
-  const size_t smem = (static_cast<size_t>(a.warps + !a.shared_totals) * num_groups + 32) * 4;
+  const size_t smem = (static_cast<size_t>(a.warps + (a.shared_totals ? 0 : 2)) * num_groups + 32) * 4;
   static SmemLimit limit;
   const cudaError_t e = limit.need(reinterpret_cast<const void*>(group_kernel), ctx.device,
                                    kGroupSmemLimit, true);
