@@ -38,11 +38,13 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kChannels = 128;  // channels of a tile in one CTA
 constexpr int kDepth = 64;      // depth of a stage: 128 bytes of 16-bit elements
 constexpr int kGatherThreads = 256;
-constexpr int kThreads = 192 + kGatherThreads;  // TMA, matrix instructions, 4 warps of output, gathering
+constexpr int kRelayWarp = 6 + kGatherThreads / 32;
+// TMA, matrix instructions, 4 warps of output, gathering, relay.
+constexpr int kThreads = (kRelayWarp + 1) * 32;
 constexpr int kStageOut = 4096; // output staging of a warp: 32 x 32 values of up to 4 bytes
 constexpr int kABytes = kChannels * kDepth * 2;
 
-constexpr int kBarrierBytes = 256;
+constexpr int kBarrierBytes = 320;
 
 // How CTAs work on a tile.
 //   kSolo   each on its own.
@@ -311,20 +313,20 @@ __device__ __forceinline__ void store_any(const TileArgs& a, const Tile& t, int 
 }
 
 // The gathering warps: x's rows named by the order, and the rows of a ragged
-// stage of the weight gradient (dy's too), 16 bytes a copy.  A warp hands a
-// stage on, with one arrival on the leader's barrier, when its copies have
-// landed, kLag stages after it issued them.  (Arrivals by each thread's copies
-// themselves, 128 a stage on one barrier, held a stage up for 1000 cycles.)
+// stage of the weight gradient (dy's too), 16 bytes a copy.  Each thread's
+// copies of a stage arrive on `landed` by themselves, so that the warps go on
+// to the next stage at once; the relay warp passes a landed stage on.  (Warps
+// that waited for their own copies had three stages in flight at most, and
+// the forward product took 370 instead of 360 us.)
 template <int kKind, int kCols, int kTeam>
 __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, kCols, kTeam>& schedule,
                                             int unit, int units, uint32_t half, int total, uint32_t base,
-                                            uint32_t full, uint32_t empty, uint32_t gave_up) {
+                                            uint32_t landed, uint32_t empty, uint32_t gave_up) {
   using R = Ring<kCols, kTeam>;
   constexpr int kStages = R::kStages, kStage = R::kStage, kMine = R::kMine;
   constexpr bool kBMn = kKind == kWeightGrad;
-  constexpr int kLag = 2;
   const int tid = threadIdx.x - 6 * 32, lane = threadIdx.x & 31;
-  uint32_t stage = 0, phase = 0, pending = 0, oldest = 0;
+  uint32_t stage = 0, phase = 0;
   bool ok = true;
 
   // The order's entry for place p and the row of x it names.  Apart, so that
@@ -334,17 +336,6 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
     const int row = o < 0 ? -1 : (a.order ? a.fan.quotient(o) : o);
     return row < a.x_rows ? row : -1;
   };
-  const auto hand_on = [&] {
-    fence_async_shared();
-    __syncwarp();
-    if (lane == 0) {
-      if (kTeam == kPair) mbar_arrive_pair(map_rank(full + 8 * oldest, 0));
-      else mbar_arrive_local(full + 8 * oldest);
-    }
-    if (++oldest == kStages) oldest = 0;
-    --pending;
-  };
-
   for (int i = unit; i < total && ok; i += units) {
     const Tile t = schedule.at(i);
     if (t.blocks == 0) continue;
@@ -418,19 +409,14 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
           }
         }
       }
-      copy_commit();
-      if (++pending > kLag) {
-        copy_wait<kLag>();
-        hand_on();
-      }
+      copy_arrive(landed + 8 * stage);
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1;
       }
     }
   }
-  copy_wait<0>();
-  while (pending > 0) hand_on();
+  copy_wait_all();
 }
 
 template <int kKind, int kCols, int kTeam>
@@ -452,9 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t out_staging = join + (R::kMaxSplit - 1) * R::kJoin;
   const uint32_t bars = out_staging + 4 * kStageOut;
   const uint32_t full = bars, empty = bars + 8 * kStages;
-  const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
+  const uint32_t landed = empty + 8 * kStages;
+  const uint32_t acc_full = landed + 8 * kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
   const uint32_t tmem_at = drained + 8, gave_up = tmem_at + 4;
-  static_assert(8 * (2 * kStages + 5) + 8 <= kBarrierBytes, "barriers");
+  static_assert(8 * (3 * kStages + 5) + 8 <= kBarrierBytes, "barriers");
   int32_t* begin = reinterpret_cast<int32_t*>(base_ptr + (bars - base) + kBarrierBytes);
   int32_t* first = begin + a.groups + 2;
 
@@ -471,8 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      // Of a pair, the leader's barriers count both CTAs' arrivals.
-      mbar_init(full + 8 * s, 1 + (gathering ? kGatherThreads / 32 * (kTwo ? 2 : 1) : 0));
+      // The TMA thread and the relays; of a pair, the leader's barriers count
+      // both CTAs.
+      mbar_init(full + 8 * s, 1 + (gathering ? (kTwo ? 2 : 1) : 0));
+      mbar_init(landed + 8 * s, kGatherThreads);
       mbar_init(empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -592,9 +581,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     }
     __syncwarp();
+  } else if (warp == kRelayWarp) {
+    // Gathered stages, once landed, on to the matrix instructions.
+    if (gathering && lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (int i = unit; i < total && ok; i += units) {
+        const Tile t = schedule.at(i);
+        for (int k = 0; k < t.blocks; ++k) {
+          ok = wait_for(landed + 8 * stage, phase, gave_up, a.wait_cycles, a.status);
+          if (!ok) break;
+          fence_async_shared();
+          if (kTwo) mbar_arrive_pair(map_rank(full + 8 * stage, 0));
+          else mbar_arrive_local(full + 8 * stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    }
+    __syncwarp();
   } else if (warp >= 6) {
     if (gathering)
-      gather_rows<kKind, kCols, kTeam>(a, schedule, unit, units, half, total, base, full, empty, gave_up);
+      gather_rows<kKind, kCols, kTeam>(a, schedule, unit, units, half, total, base, landed, empty, gave_up);
   } else if (warp == 1) {
     // Matrix instructions, by one thread; a pair's by its leader's.
     if (half == 0 && lane == 0) {

@@ -158,13 +158,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but this thread's latest kPending groups of copies have landed.
-template <int kPending>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+// Arrives on an mbarrier of this CTA once this thread's copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint32_t mbar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(mbar) : "memory");
 }
-// Makes this thread's shared-memory writes visible to the matrix
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Makes shared-memory writes this thread has seen visible to the matrix
 // instructions, which read through the asynchronous proxy.  (The form for
 // this CTA's shared memory alone cost nothing measurable; the one for all
 // memory added 300 us to a 640 us launch.)
