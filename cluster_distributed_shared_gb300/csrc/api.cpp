@@ -889,6 +889,8 @@ int begin_call(cudaStream_t stream, CallContext* out) {
   out->status = sr.d_status;
   out->pool = st->pool;
   out->sm_count = st->dev.sm_count;
+  out->wait_cycles = wait_cycles_setting();
+  out->withhold = env_flag("DSMEM_HIST_TEST_WITHHOLD_LAST_ROUND");
   return DSMEM_HIST_OK;
 }
 

@@ -107,6 +107,7 @@ struct TileArgs {
   int wide_out;        // rows of the output are 16-byte aligned
   uint32_t* status;
   long long wait_cycles;
+  int withhold;        // test hook: each unit's last stage is not copied
 };
 
 __device__ uint32_t g_product_status;  // kStatusProduct once a bounded wait gave up
@@ -255,20 +256,24 @@ __device__ __forceinline__ void store_block(const TileArgs& a, const Tile& t, in
   constexpr int V = 16 / sizeof(O);
   if (kKind == kWeightGrad) {
     constexpr int kPieces = kN / V;  // 16-byte pieces of a staged row
+    // Exchanged within a row so that rows 128 bytes on meet other banks.
+    const auto piece_at = [&](int row, int q) {
+      return staging + row * (kN * sizeof(O)) + ((q ^ (row * kPieces / 8 & (kPieces - 1))) << 4);
+    };
     O* out = static_cast<O*>(a.out) + static_cast<int64_t>(t.group) * a.channels * a.width;
 #pragma unroll
     for (int q = 0; q < kPieces; ++q) {
       Pack<O, V> p;
 #pragma unroll
       for (int v = 0; v < V; ++v) p.v[v] = from_float<O>(__uint_as_float(r[q * V + v]));
-      st_shared_16(staging + lane * (kN * sizeof(O)) + ((q ^ (lane & (kPieces - 1))) << 4), p);
+      st_shared_16(piece_at(lane, q), p);
     }
     __syncwarp();
     if (a.wide_out) {
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int row = (i * 32 + lane) / kPieces, q = lane & (kPieces - 1);
-        const uint4 p = ld_shared_16(staging + row * (kN * sizeof(O)) + ((q ^ (row & (kPieces - 1))) << 4));
+        const uint4 p = ld_shared_16(piece_at(row, q));
         if (channel0 + row < a.channels && col + q * V < a.width)
           *reinterpret_cast<uint4*>(out + static_cast<int64_t>(channel0 + row) * a.width + col + q * V) = p;
       }
@@ -276,8 +281,7 @@ __device__ __forceinline__ void store_block(const TileArgs& a, const Tile& t, in
       out += static_cast<int64_t>(channel0) * a.width + col + lane;
       const int rows = min(32, a.channels - channel0);
       for (int row = 0; row < rows; ++row, out += a.width)
-        *out = ld_shared_value<O>(staging + row * (kN * sizeof(O)) +
-                                  (((lane / V) ^ (row & (kPieces - 1))) << 4) + lane % V * sizeof(O));
+        *out = ld_shared_value<O>(piece_at(row, lane / V) + lane % V * sizeof(O));
     }
     __syncwarp();
   } else {
@@ -367,8 +371,8 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
         here = named_row(ahead);
         ahead = batch_place(k + kBatch);
       }
-      if (lane == 0) ok = wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
-      ok = __shfl_sync(kFull, ok, 0);
+      ok = wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
+      ok = __all_sync(kFull, ok);
       if (!ok) break;
       const uint32_t sa = base + stage * kStage, sb = sa + kABytes;
       if (!kBMn) {
@@ -533,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile t = schedule.at(i);
       for (int k = 0; k < t.blocks; ++k) {
         ok = wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
-        if (!ok) break;
+        if (!ok || (a.withhold && i + units >= total && k + 1 == t.blocks)) break;
         const uint32_t sa = base + stage * kStage, sb = sa + kABytes;
         const uint32_t bar = kTwo ? map_rank(full + 8 * stage, 0) : full + 8 * stage;
         const int k0 = (t.block0 + k) * kDepth;
@@ -898,7 +902,8 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
   const int64_t out_cols = kKind == kWeightGrad ? a.width : a.channels;
   a.wide_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && out_cols * dtype_size(p.out_dtype) % 16 == 0;
   a.status = ctx.status;
-  a.wait_cycles = kDefaultWaitCycles;
+  a.wait_cycles = ctx.wait_cycles;
+  a.withhold = ctx.withhold;
 
   Maps m;
   const int x_cols = kKind == kInputGrad ? p.outer : p.inner;

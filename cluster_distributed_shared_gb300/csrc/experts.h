@@ -27,6 +27,8 @@ struct CallContext {
   uint32_t* status = nullptr;  // the stream's host-mapped status word
   cudaMemPool_t pool = nullptr;
   int sm_count = 0;
+  long long wait_cycles = 0;  // bound of one wait
+  bool withhold = false;      // test hook: the last stage's copies are not issued
 };
 int begin_call(cudaStream_t stream, CallContext* out);
 // Scratch from the device's stream-ordered pool; given back on the same stream.

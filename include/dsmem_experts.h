@@ -19,14 +19,18 @@
  * orders and positions that are out of range read and write nothing outside
  * the stated buffers.
  *
- * Results do not depend on the launch: sums are taken in a fixed order, in
- * 32 bits or more, and rounded once to the output's type.
+ * The same call gives the same bits: sums are taken in an order that sizes
+ * alone decide, in 32 bits or more, and rounded once to the output's type.
  *
  * The product kernels wait for their own copies and matrix instructions with
  * bounded waits (about 50 ms each).  A wait that gives up makes the launch's
  * output wrong and is reported as in dsmem_hist.h: the next call on the same
  * stream returns DSMEM_HIST_ETIMEOUT and enqueues nothing, and
- * dsmem_hist_device_status() shows bit 1.
+ * dsmem_hist_device_status() shows bit 1.  The test hooks of dsmem_hist.h hold
+ * here too: DSMEM_HIST_TEST_WAIT_CYCLES bounds these waits,
+ * DSMEM_HIST_TEST_WITHHOLD_LAST_ROUND leaves out the copies of the last stage of
+ * depth, so that the wait for them runs out with none of them in flight, and
+ * DSMEM_HIST_TEST_FAIL_ALLOC fails the calls that take scratch.
  */
 #ifndef DSMEM_EXPERTS_H
 #define DSMEM_EXPERTS_H

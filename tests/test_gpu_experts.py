@@ -482,3 +482,24 @@ def test_a_failed_scratch_allocation_is_reported(monkeypatch):
     assert e.value.code == dh.DSMEM_HIST_ENOMEM
     monkeypatch.delenv("DSMEM_HIST_TEST_FAIL_ALLOC")
     assert float(dh.dsmem_grad_clip(f, 1e9)) == pytest.approx(math.sqrt(8), rel=1e-6)
+
+
+@pytest.mark.parametrize("case", [PRODUCTS[0], PRODUCTS[11], PRODUCTS[16], PRODUCTS[17]])
+def test_a_wait_that_gives_up_is_reported_by_the_next_call(case, monkeypatch):
+    """The copies of the last stage are withheld, so the wait for them runs
+    out with nothing of it in flight (a solo, a split and two paired shapes)."""
+    x, w, dy, offsets, source, rows_of = product_inputs(case, torch.bfloat16, True)
+    args = (x.cuda(), w.cuda(), offsets.cuda())
+    want = dh.dsmem_grouped_matmul(*args, **rows_of)
+    torch.cuda.synchronize()
+    monkeypatch.setenv("DSMEM_HIST_TEST_WAIT_CYCLES", "200000")
+    monkeypatch.setenv("DSMEM_HIST_TEST_WITHHOLD_LAST_ROUND", "1")
+    dh.dsmem_grouped_matmul(*args, **rows_of)
+    torch.cuda.synchronize()
+    monkeypatch.delenv("DSMEM_HIST_TEST_WAIT_CYCLES")
+    monkeypatch.delenv("DSMEM_HIST_TEST_WITHHOLD_LAST_ROUND")
+    with pytest.raises(dh.DsmemHistError) as e:
+        dh.dsmem_grouped_matmul(*args, **rows_of)
+    assert e.value.code == dh.DSMEM_HIST_ETIMEOUT and "grouped product" in str(e.value)
+    assert dh.dsmem_hist_device_status() == 2 and dh.dsmem_hist_device_status() == 0
+    assert torch.equal(dh.dsmem_grouped_matmul(*args, **rows_of), want)
