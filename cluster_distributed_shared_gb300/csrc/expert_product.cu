@@ -920,7 +920,7 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
   }
 
   const int64_t tiles = tile_bound(p, kCols, R::kHeight);
-  if (tiles > INT32_MAX)
+  if (tiles > INT32_MAX - 1024)  // tile counters step past the last tile
     return fail_with(DSMEM_HIST_EINVAL, "grouped product: more than 2^31 output tiles");
   const int smem = R::smem_bytes(p.groups);
   const auto kernel = product_kernel<kKind, kCols, kTeam>;

@@ -20,7 +20,7 @@ import ctypes
 import operator
 
 F32, F16, BF16 = 0, 1, 2
-_DTYPE, _IS_CUDA = operator.attrgetter("dtype"), operator.attrgetter("is_cuda")
+_DTYPE = operator.attrgetter("dtype")
 
 _p, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 SIGNATURES = {
@@ -322,14 +322,14 @@ def dsmem_grad_clip(grads, max_norm: float, out=None, stream=None):
     types = list(map(_DTYPE, grads))
     codes = list(map(_lib.codes.get, types))
     counts = list(map(tensor.numel, grads))
-    if None in codes or not all(map(_IS_CUDA, grads)):
+    devices = set(map(tensor.get_device, grads))
+    if None in codes or -1 in devices:
         raise TypeError("grads must be CUDA float32, float16 or bfloat16 tensors")
-    if set(map(tensor.get_device, grads)) - {device.index} or \
-            not all(map(tensor.is_contiguous, grads)):
+    if len(devices) > 1 or not all(map(tensor.is_contiguous, grads)):
         raise ValueError("grads must be contiguous and on one device")
     if out is not grads and (
             list(map(_DTYPE, out)) != types or list(map(tensor.numel, out)) != counts
-            or set(map(tensor.get_device, out)) - {device.index}
+            or set(map(tensor.get_device, out)) != devices
             or not all(map(tensor.is_contiguous, out))):
         raise ValueError("out must match grads in type, size and device and be contiguous")
     table = array.array("Q", bytes(32 * max(len(grads), 1)))   # entries of dsmem_grad_t
