@@ -763,32 +763,49 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Lays rows whose bases or strides TMA cannot take out with rows of a
-// multiple of 8 elements; both sources of a product in one launch.  One
-// thread per 8 elements of the result.
+// multiple of 8 elements; both sources of a product in one launch.  One warp
+// per 256 elements of a row, 8 elements a lane: 32-bit words, joined where the
+// row begins between two of them, and single elements at a row's ends.
 struct Layout {
   const uint16_t* src;
-  int64_t row_stride, group_stride, chunks;  // chunks: 8-element pieces in all
+  int64_t row_stride, group_stride, pieces;  // pieces: of all rows
   uint16_t* dst;
-  int rows, cols, dst_stride;
+  int rows, cols, dst_stride, pieces_of_row;
 };
 struct Layouts {
   Layout of[2];
 };
-__global__ void layout_kernel(const __grid_constant__ Layouts layouts) {
-  const int64_t total = layouts.of[0].chunks + layouts.of[1].chunks;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const bool second = i >= layouts.of[0].chunks;
+__device__ __forceinline__ int64_t quotient(int64_t v, int d) {
+  return v <= INT32_MAX ? static_cast<int>(v) / d : v / d;
+}
+__global__ void __launch_bounds__(256) layout_kernel(const __grid_constant__ Layouts layouts) {
+  const int64_t total = layouts.of[0].pieces + layouts.of[1].pieces;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < total;
+       i += static_cast<int64_t>(gridDim.x) * 8) {
+    const bool second = i >= layouts.of[0].pieces;
     const Layout& l = layouts.of[second];
-    const int64_t j = second ? i - layouts.of[0].chunks : i;
-    const int per_row = l.dst_stride / 8;
-    const int64_t line = j / per_row;
-    const int c0 = static_cast<int>(j - line * per_row) * 8;
-    const uint16_t* s = l.src + line / l.rows * l.group_stride + line % l.rows * l.row_stride + c0;
-    Pack<uint16_t, 8> p;
+    const int64_t piece = second ? i - layouts.of[0].pieces : i;
+    const int64_t line = quotient(piece, l.pieces_of_row), group = quotient(line, l.rows);
+    const int c = static_cast<int>(piece - line * l.pieces_of_row) * 256 + (threadIdx.x & 31) * 8;
+    if (c >= l.dst_stride) continue;
+    const uint16_t* row = l.src + group * l.group_stride + (line - group * l.rows) * l.row_stride;
+    const bool between = (reinterpret_cast<uintptr_t>(row) & 2u) != 0;
+    uint4 v;
+    if (!between && c + 8 <= l.cols) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(row + c);
+      v = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if (between && c > 0 && c + 8 < l.cols) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(row + c - 1);
+      const uint32_t w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3], w4 = w[4];
+      v = make_uint4(__funnelshift_r(w0, w1, 16), __funnelshift_r(w1, w2, 16),
+                     __funnelshift_r(w2, w3, 16), __funnelshift_r(w3, w4, 16));
+    } else {
+      uint32_t e[8];
 #pragma unroll
-    for (int v = 0; v < 8; ++v) p.v[v] = c0 + v < l.cols ? s[v] : uint16_t{0};
-    *reinterpret_cast<Pack<uint16_t, 8>*>(l.dst + line * l.dst_stride + c0) = p;
+      for (int k = 0; k < 8; ++k) e[k] = c + k < l.cols ? row[c + k] : 0u;
+      v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+    }
+    *reinterpret_cast<uint4*>(l.dst + line * l.dst_stride + c) = v;
   }
 }
 
@@ -843,7 +860,7 @@ struct Source {
 // gives back.
 int lay_out(const CallContext& ctx, Source* sources[2], void** scratch, cudaStream_t stream) {
   Layouts layouts = {};
-  int64_t bytes = 0, chunks = 0;
+  int64_t bytes = 0, pieces = 0;
   for (int i = 0; i < 2; ++i) {
     Source& s = *sources[i];
     if (tma_ready(s.data, s.row_stride, s.group_stride, s.groups)) {
@@ -855,24 +872,25 @@ int lay_out(const CallContext& ctx, Source* sources[2], void** scratch, cudaStre
     l.row_stride = s.row_stride, l.group_stride = s.group_stride;
     l.rows = static_cast<int>(s.rows), l.cols = static_cast<int>(s.cols);
     l.dst_stride = static_cast<int>((s.cols + 7) / 8 * 8);
-    l.chunks = s.groups * s.rows * (l.dst_stride / 8);
-    chunks += l.chunks;
-    bytes += l.chunks * 16;
+    l.pieces_of_row = (l.dst_stride + 255) / 256;
+    l.pieces = s.groups * s.rows * l.pieces_of_row;
+    pieces += l.pieces;
+    bytes += s.groups * s.rows * l.dst_stride * 2;
   }
-  if (chunks == 0) return DSMEM_HIST_OK;
+  if (pieces == 0) return DSMEM_HIST_OK;
   int rc = pool_alloc(ctx, scratch, static_cast<size_t>(bytes), stream);
   if (rc) return rc;
   uint16_t* at = static_cast<uint16_t*>(*scratch);
   for (int i = 0; i < 2; ++i) {
     Layout& l = layouts.of[i];
-    if (l.chunks == 0) continue;
+    if (l.pieces == 0) continue;
     l.dst = at;
-    at += l.chunks * 8;
+    at += sources[i]->groups * sources[i]->rows * l.dst_stride;
     sources[i]->data = l.dst;
     sources[i]->row_stride = l.dst_stride;
     sources[i]->group_stride = static_cast<int64_t>(l.dst_stride) * l.rows;
   }
-  const int grid = static_cast<int>(std::min<int64_t>((chunks + 255) / 256, ctx.sm_count * 16));
+  const int grid = static_cast<int>(std::min<int64_t>((pieces + 7) / 8, ctx.sm_count * 32));
   layout_kernel<<<grid, 256, 0, stream>>>(layouts);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? DSMEM_HIST_OK : fail_with_cuda(e, "layout launch");
