@@ -38,6 +38,8 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kChannels = 128;  // channels of a tile in one CTA
 constexpr int kDepth = 64;      // depth of a stage: 128 bytes of 16-bit elements
 constexpr int kGatherThreads = 256;
+constexpr int kShifts = 2;                        // groups of gathering warps that take stages in turn
+constexpr int kShift = kGatherThreads / kShifts;  // threads of one
 constexpr int kRelayWarp = 6 + kGatherThreads / 32;
 // TMA, matrix instructions, 4 warps of output, gathering, relay.
 constexpr int kThreads = (kRelayWarp + 1) * 32;
@@ -329,8 +331,9 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
   using R = Ring<kCols, kTeam>;
   constexpr int kStages = R::kStages, kStage = R::kStage, kMine = R::kMine;
   constexpr bool kBMn = kKind == kWeightGrad;
-  const int tid = threadIdx.x - 6 * 32, lane = threadIdx.x & 31;
-  uint32_t stage = 0, phase = 0;
+  const int shift = (threadIdx.x - 6 * 32) / kShift, tid = (threadIdx.x - 6 * 32) % kShift;
+  const int lane = threadIdx.x & 31;
+  uint32_t before = 0;  // stages of earlier tiles
   bool ok = true;
 
   // The order's entry for place p and the row of x it names.  Apart, so that
@@ -346,7 +349,7 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
     const int col0 = t.col0 + half * kMine, chan0 = t.chan0 + half * kChannels;
     // Forward and input gradient: 8 threads a row of 128 bytes; the rows are
     // the same in every stage of the tile.
-    constexpr int kLines = kGatherThreads / 8, kRows = kBMn ? 1 : (kMine + kLines - 1) / kLines;
+    constexpr int kLines = kShift / 8, kRows = kBMn ? 1 : (kMine + kLines - 1) / kLines;
     int row[kRows];
     if (!kBMn) {
 #pragma unroll
@@ -357,20 +360,24 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
     // Weight gradient: kPieces threads a row of kMine elements.  A warp needs
     // kFound rows of a stage; its lanes look up those of kBatch stages at once,
     // a batch ahead, as the order's entries take longer to arrive than a stage.
-    constexpr int kPieces = kMine / 8, kAtOnce = kGatherThreads / kPieces, kPerWarp = 32 / kPieces;
-    constexpr int kFound = kDepth / (kGatherThreads / 32), kBatch = 32 / kFound;
-    const auto batch_place = [&](int k) {
+    constexpr int kPieces = kMine / 8, kAtOnce = kShift / kPieces, kPerWarp = 32 / kPieces;
+    constexpr int kFound = kDepth / (kShift / 32), kBatch = 32 / kFound;
+    // This shift's stages of the tile: mine_at(0), mine_at(1), ..
+    const int first_k = (shift - before % kShifts + kShifts) % kShifts;
+    const auto mine_at = [&](int m) { return first_k + m * kShifts; };
+    const auto batch_place = [&](int m) {
       const int l = lane % kFound;
       const int r = l / kPerWarp * kAtOnce + (tid >> 5) * kPerWarp + l % kPerWarp;
-      return place(t.begin + (t.block0 + k + lane / kFound) * kDepth + r, t.end);
+      return place(t.begin + (t.block0 + mine_at(m + lane / kFound)) * kDepth + r, t.end);
     };
     int ahead = kBMn ? batch_place(0) : 0, here = 0;
 
-    for (int k = 0; k < t.blocks; ++k) {
-      if (kBMn && k % kBatch == 0) {
+    for (int m = 0, k = first_k; k < t.blocks; ++m, k = mine_at(m)) {
+      if (kBMn && m % kBatch == 0) {
         here = named_row(ahead);
-        ahead = batch_place(k + kBatch);
+        ahead = batch_place(m + kBatch);
       }
+      const uint32_t stage = (before + k) % kStages, phase = (before + k) / kStages & 1;
       ok = wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
       ok = __all_sync(kFull, ok);
       if (!ok) break;
@@ -395,7 +402,7 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
 #pragma unroll
           for (int r = 0; r < kDepth / kAtOnce; ++r) {
             const int line = r * kAtOnce + tid / kPieces;
-            const int from = __shfl_sync(kFull, here, k % kBatch * kFound + r * kPerWarp + lane / kPieces);
+            const int from = __shfl_sync(kFull, here, m % kBatch * kFound + r * kPerWarp + lane / kPieces);
             const bool read = from >= 0 && left > 0;
             copy16(sb + (c >> 3) * 8192 + line * 128 + (((c & 7) ^ (line & 7)) << 4),
                    a.x + (read ? from * a.x_stride + col : 0), read ? left : 0);
@@ -405,8 +412,8 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
           const int c = tid & 15, col = chan0 + c * 8;
           const int left = max(0, min(16, (a.channels - col) * 2));
 #pragma unroll
-          for (int r = 0; r < kDepth * 16 / kGatherThreads; ++r) {
-            const int line = r * (kGatherThreads / 16) + tid / 16;
+          for (int r = 0; r < kDepth * 16 / kShift; ++r) {
+            const int line = r * (kShift / 16) + tid / 16;
             const bool read = p0 + line < t.end && left > 0;
             copy16(sa + (c >> 3) * 8192 + line * 128 + (((c & 7) ^ (line & 7)) << 4),
                    a.dy + (read ? (p0 + line) * a.dy_stride + col : 0), read ? left : 0);
@@ -414,11 +421,8 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
         }
       }
       copy_arrive(landed + 8 * stage);
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
     }
+    before += t.blocks;
   }
   copy_wait_all();
 }
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The TMA thread and the relays; of a pair, the leader's barriers count
       // both CTAs.
       mbar_init(full + 8 * s, 1 + (gathering ? (kTwo ? 2 : 1) : 0));
-      mbar_init(landed + 8 * s, kGatherThreads);
+      mbar_init(landed + 8 * s, kShift);
       mbar_init(empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
