@@ -37,7 +37,7 @@ using namespace ptx;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kChannels = 128;  // channels of a tile in one CTA
 constexpr int kDepth = 64;      // depth of a stage: 128 bytes of 16-bit elements
-constexpr int kGatherThreads = 256;
+constexpr int kGatherThreads = 128;
 constexpr int kShifts = 2;                        // groups of gathering warps that take stages in turn
 constexpr int kShift = kGatherThreads / kShifts;  // threads of one
 constexpr int kRelayWarp = 6 + kGatherThreads / 32;
@@ -47,6 +47,7 @@ constexpr int kStageOut = 4096; // output staging of a warp: 32 x 32 values of u
 constexpr int kABytes = kChannels * kDepth * 2;
 
 constexpr int kBarrierBytes = 320;
+constexpr int kMostSorted = 512;  // groups
 
 // How CTAs work on a tile.
 //   kSolo   each on its own.
@@ -198,7 +199,8 @@ struct Tile {
 template <int kKind, int kCols, int kTeam>
 struct Schedule {
   const int32_t* begin;  // [groups + 2] first row of each group, in shared memory
-  const int32_t* first;  // [groups + 2] first tile of each group
+  const int32_t* first;  // [groups + 2] first tile of each group; weight gradient: the groups
+                         // by falling size
   int groups, chan_tiles, width_tiles, depth_blocks;
   int group;
   uint32_t rank, split;
@@ -214,15 +216,30 @@ struct Schedule {
   }
   // Groups that own tiles; the weight gradient has none for the rows behind.
   __device__ __forceinline__ int owners() const { return kKind == kWeightGrad ? groups : groups + 1; }
-  __device__ __forceinline__ int total() const { return first[owners()]; }
+  __device__ __forceinline__ int total() const {
+    return kKind == kWeightGrad ? groups * tiles_of(0) : first[owners()];
+  }
+  // The j-th tile of a unit.  Tiles of the weight gradient differ in depth:
+  // with the deepest first, and every other round the other way, units differ
+  // by a fraction of a tile.
+  __device__ __forceinline__ static int turn(int j, int unit, int units) {
+    return j * units + (kKind == kWeightGrad && (j & 1) ? units - 1 - unit : unit);
+  }
   // Tile t; t only grows from call to call.
   __device__ __forceinline__ Tile at(int t) {
-    while (t >= first[group + 1]) ++group;
+    int i;
+    if (kKind == kWeightGrad) {
+      const int each = tiles_of(0), place = t / each;
+      group = first[place];
+      i = t - place * each;
+    } else {
+      while (t >= first[group + 1]) ++group;
+      i = t - first[group];
+    }
     Tile r;
     r.group = group;
     r.begin = begin[group];
     r.end = begin[group + 1];
-    const int i = t - first[group];
     r.chan0 = i % chan_tiles * kHeight;
     if (kKind == kWeightGrad) {
       r.col0 = i / chan_tiles * kCols;
@@ -343,7 +360,7 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
     const int row = o < 0 ? -1 : (a.order ? a.fan.quotient(o) : o);
     return row < a.x_rows ? row : -1;
   };
-  for (int i = unit; i < total && ok; i += units) {
+  for (int j = 0, i = unit; i < total && ok; i = schedule.turn(++j, unit, units)) {
     const Tile t = schedule.at(i);
     if (t.blocks == 0) continue;
     const int col0 = t.col0 + half * kMine, chan0 = t.chan0 + half * kChannels;
@@ -489,7 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     begin[g + 1] = static_cast<int32_t>(e < 0 ? 0 : (e > a.n ? a.n : e));
   }
   if (threadIdx.x == 0) {
-    begin[0] = first[0] = 0;
+    begin[0] = 0;
+    if (kKind != kWeightGrad) first[0] = 0;
     begin[a.groups + 1] = static_cast<int32_t>(a.n);
   }
   if (warp == 1) tmem_alloc<kTwo>(tmem_at, kTmemColumns);
@@ -515,10 +533,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (g < schedule.owners()) {
         begin[g + 1] = end;
-        first[g + 1] = tiles_before + tiles;
+        if (kKind != kWeightGrad) first[g + 1] = tiles_before + tiles;
       }
       end_before = __shfl_sync(kFull, end, 31);
       tiles_before += __shfl_sync(kFull, tiles, 31);
+    }
+  }
+  if (kKind == kWeightGrad) {
+    // The groups by falling size (by number alone where counting the larger
+    // ones of each would take longer than it saves).
+    __syncthreads();
+    for (int g = threadIdx.x; g < a.groups; g += kThreads) {
+      int place = g;
+      if (a.groups <= kMostSorted) {
+        const int size = begin[g + 1] - begin[g];
+        place = 0;
+        for (int h = 0; h < a.groups; ++h) {
+          const int other = begin[h + 1] - begin[h];
+          place += other > size || (other == size && h < g);
+        }
+      }
+      first[place] = g;
     }
   }
   tcgen_fence_before();
@@ -537,11 +572,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
     uint32_t stage = 0, phase = 0, issued = 0;
     bool ok = true;
-    for (int i = unit; i < total && ok; i += units) {
+    for (int j = 0, i = unit; i < total && ok; i = schedule.turn(++j, unit, units)) {
       const Tile t = schedule.at(i);
       for (int k = 0; k < t.blocks; ++k) {
         ok = wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
-        if (!ok || (a.withhold && i + units >= total && k + 1 == t.blocks)) break;
+        if (!ok || (a.withhold && schedule.turn(j + 1, unit, units) >= total && k + 1 == t.blocks)) break;
         const uint32_t sa = base + stage * kStage, sb = sa + kABytes;
         const uint32_t bar = kTwo ? map_rank(full + 8 * stage, 0) : full + 8 * stage;
         const int k0 = (t.block0 + k) * kDepth;
@@ -594,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (gathering && lane == 0) {
       uint32_t stage = 0, phase = 0;
       bool ok = true;
-      for (int i = unit; i < total && ok; i += units) {
+      for (int j = 0, i = unit; i < total && ok; i = schedule.turn(++j, unit, units)) {
         const Tile t = schedule.at(i);
         for (int k = 0; k < t.blocks; ++k) {
           ok = wait_for(landed + 8 * stage, phase, gave_up, a.wait_cycles, a.status);
@@ -621,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              (uint32_t{kCols >> 3} << 17) | (uint32_t{R::kHeight >> 4} << 24);
       uint32_t stage = 0, phase = 0, done = 0;
       bool ok = true;
-      for (int i = unit; i < total && ok; i += units) {
+      for (int j = 0, i = unit; i < total && ok; i = schedule.turn(++j, unit, units)) {
         const Tile t = schedule.at(i);
         if (t.blocks == 0) continue;
         const uint32_t buffer = done & 1, d = tmem + buffer * kCols;
@@ -680,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     uint32_t done = 0;
-    for (int i = unit; i < total; i += units) {
+    for (int j = 0, i = unit; i < total; i = schedule.turn(++j, unit, units)) {
       const Tile t = schedule.at(i);
       const uint32_t buffer = done & 1;
       if (t.blocks > 0) {
