@@ -44,6 +44,7 @@ int fail_cuda(cudaError_t e, const char* what) {
 
 struct DeviceState {
   bool ready = false;
+  int ordinal = 0;
   dsmem_hist_device_t dev = {};
   cudaMemPool_t pool = nullptr;
   cudaStream_t copy_stream = nullptr;
@@ -147,6 +148,7 @@ int device_state(DeviceState** out) {
   if (e != cudaSuccess) return fail_cuda(e, "cudaGetDevice");
   DeviceState*& st = g_devices[dev];
   if (!st) st = new DeviceState();
+  st->ordinal = dev;
   if (!st->ready) {
     cudaDeviceProp p;
     if ((e = cudaGetDeviceProperties(&p, dev)) != cudaSuccess)
@@ -883,16 +885,16 @@ int begin_call(cudaStream_t stream, CallContext* out) {
   if ((rc = stream_slot(st, stream, true, &sr))) return rc;
   if ((rc = take_pending_timeout(sr.h_status))) return rc;
   if ((rc = ensure_pool(st))) return rc;
-  cudaGetDevice(&out->device);
+  out->device = st->ordinal;
   if (out->device >= kMaxDevices)
     return fail(DSMEM_HIST_EUNSUPPORTED, "device ordinal beyond %d", kMaxDevices - 1);
   out->status = sr.d_status;
   out->pool = st->pool;
   out->sm_count = st->dev.sm_count;
-  out->wait_cycles = wait_cycles_setting();
-  out->withhold = env_flag("DSMEM_HIST_TEST_WITHHOLD_LAST_ROUND");
   return DSMEM_HIST_OK;
 }
+long long call_wait_cycles() { return wait_cycles_setting(); }
+bool call_withholds() { return env_flag("DSMEM_HIST_TEST_WITHHOLD_LAST_ROUND"); }
 
 int pool_alloc(const CallContext& ctx, void** out, size_t bytes, cudaStream_t stream) {
   if (injected_alloc_failure())

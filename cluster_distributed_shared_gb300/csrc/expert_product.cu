@@ -959,8 +959,8 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
   const int64_t out_cols = kKind == kWeightGrad ? a.width : a.channels;
   a.wide_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && out_cols * dtype_size(p.out_dtype) % 16 == 0;
   a.status = ctx.status;
-  a.wait_cycles = ctx.wait_cycles;
-  a.withhold = ctx.withhold;
+  a.wait_cycles = call_wait_cycles();
+  a.withhold = call_withholds();
 
   Maps m;
   const int x_cols = kKind == kInputGrad ? p.outer : p.inner;

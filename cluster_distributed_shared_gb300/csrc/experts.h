@@ -27,10 +27,12 @@ struct CallContext {
   uint32_t* status = nullptr;  // the stream's host-mapped status word
   cudaMemPool_t pool = nullptr;
   int sm_count = 0;
-  long long wait_cycles = 0;  // bound of one wait
-  bool withhold = false;      // test hook: the last stage's copies are not issued
 };
 int begin_call(cudaStream_t stream, CallContext* out);
+// The bound of one device-side wait, and the test hook that leaves out the
+// copies of a last stage (both from the environment, read at every call).
+long long call_wait_cycles();
+bool call_withholds();
 // Scratch from the device's stream-ordered pool; given back on the same stream.
 int pool_alloc(const CallContext& ctx, void** out, size_t bytes, cudaStream_t stream);
 int pool_free(void* p, cudaStream_t stream);

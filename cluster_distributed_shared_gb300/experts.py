@@ -50,6 +50,8 @@ class _Library:
             entry.restype = ctypes.c_int
             self.__dict__[fn] = entry
         self.torch = torch
+        self.device = torch._C._cuda_getDevice
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
         self.codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
         return self.__dict__[name]
 
@@ -99,20 +101,29 @@ def _same_device(device, **tensors):
             raise ValueError(f"{name} must be on {device}")
 
 
-def _on(device, stream, inputs, run):
-    """run(stream handle) with `device`, and a given `stream`, made current."""
+def _elsewhere(call, device, stream, *args, **options):
+    """call(*args, **options) with `device`, and a given `stream`, made current."""
     torch = _lib.torch
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            result = run(stream.cuda_stream)
-        for t in inputs:
-            if t is not None:
-                t.record_stream(stream)
-        return result
-    if device.index == torch.cuda.current_device():
-        return run(torch._C._cuda_getCurrentRawStream(device.index))
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream must be on {device}")
     with torch.cuda.device(device):
-        return run(torch.cuda.current_stream().cuda_stream)
+        if stream is None:
+            return call(*args, **options)
+        with torch.cuda.stream(stream):
+            result = call(*args, **options)
+    for t in (*args, *options.values()):
+        for each in t if isinstance(t, list) else (t,):
+            if isinstance(each, torch.Tensor):
+                each.record_stream(stream)
+    return result
+
+
+def _current(device):
+    """The current stream's handle, or None when `device` is not the current one."""
+    index = device.index
+    if index != _lib.device():
+        return None
+    return _lib.raw_stream(index)
 
 
 def dsmem_route(logits, top_k: int, renormalize: bool = True, stream=None):
@@ -124,16 +135,15 @@ def dsmem_route(logits, top_k: int, renormalize: bool = True, stream=None):
     -inf and NaN are never chosen; missing choices are id -1 with weight 0."""
     dtype = _float_tensor("logits", logits, 2)
     tokens, experts = logits.shape
-
-    def run(s):
-        ids = _lib.torch.empty((tokens, top_k), dtype=_lib.torch.int32, device=logits.device)
-        weights = _lib.torch.empty((tokens, top_k), dtype=_lib.torch.float32, device=logits.device)
-        _check(_lib.dsmem_route(
-            logits.data_ptr(), dtype, tokens, experts, _row_stride(logits), int(top_k),
-            int(renormalize), ids.data_ptr(), weights.data_ptr(), s))
-        return ids, weights
-
-    return _on(logits.device, stream, (logits,), run)
+    s = None if stream is not None else _current(logits.device)
+    if s is None:
+        return _elsewhere(dsmem_route, logits.device, stream, logits, top_k, renormalize)
+    ids = _lib.torch.empty((tokens, top_k), dtype=_lib.torch.int32, device=logits.device)
+    weights = _lib.torch.empty((tokens, top_k), dtype=_lib.torch.float32, device=logits.device)
+    _check(_lib.dsmem_route(
+        logits.data_ptr(), dtype, tokens, experts, _row_stride(logits), int(top_k),
+        int(renormalize), ids.data_ptr(), weights.data_ptr(), s))
+    return ids, weights
 
 
 def dsmem_route_backward(logits, ids, weights, grad_weights, renormalize: bool = True, stream=None):
@@ -150,16 +160,16 @@ def dsmem_route_backward(logits, ids, weights, grad_weights, renormalize: bool =
         if t.shape != ids.shape or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous and of the shape of ids")
     _same_device(logits.device, weights=weights, grad_weights=grad_weights)
-
-    def run(s):
-        out = _lib.torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
-        _check(_lib.dsmem_route_backward(
-            logits.data_ptr(), dtype, tokens, experts, _row_stride(logits), top_k,
-            int(renormalize), ids.data_ptr(), weights.data_ptr(), grad_weights.data_ptr(),
-            out.data_ptr(), s))
-        return out
-
-    return _on(logits.device, stream, (logits, ids, weights, grad_weights), run)
+    s = None if stream is not None else _current(logits.device)
+    if s is None:
+        return _elsewhere(dsmem_route_backward, logits.device, stream, logits, ids, weights,
+                          grad_weights, renormalize)
+    out = _lib.torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+    _check(_lib.dsmem_route_backward(
+        logits.data_ptr(), dtype, tokens, experts, _row_stride(logits), top_k,
+        int(renormalize), ids.data_ptr(), weights.data_ptr(), grad_weights.data_ptr(),
+        out.data_ptr(), s))
+    return out
 
 
 def dsmem_group(keys, num_groups: int, stream=None):
@@ -169,18 +179,17 @@ def dsmem_group(keys, num_groups: int, stream=None):
     position[i] the place of key i (-1 for keys outside [0, num_groups))."""
     _int_tensor("keys", keys, None, None)
     n = keys.numel()
-
-    def run(s):
-        torch = _lib.torch
-        like = dict(dtype=torch.int32, device=keys.device)
-        offsets = torch.empty(max(int(num_groups), 0) + 1, **like)
-        order, position = torch.empty(n, **like), torch.empty(n, **like)
-        _check(_lib.dsmem_group(
-            keys.data_ptr(), n, int(num_groups), offsets.data_ptr(), order.data_ptr(),
-            position.data_ptr(), s))
-        return offsets, order, position
-
-    return _on(keys.device, stream, (keys,), run)
+    s = None if stream is not None else _current(keys.device)
+    if s is None:
+        return _elsewhere(dsmem_group, keys.device, stream, keys, num_groups)
+    torch = _lib.torch
+    like = dict(dtype=torch.int32, device=keys.device)
+    offsets = torch.empty(max(int(num_groups), 0) + 1, **like)
+    order, position = torch.empty(n, **like), torch.empty(n, **like)
+    _check(_lib.dsmem_group(
+        keys.data_ptr(), n, int(num_groups), offsets.data_ptr(), order.data_ptr(),
+        position.data_ptr(), s))
+    return offsets, order, position
 
 
 def _product_types(code, dtype, out_dtype):
@@ -212,17 +221,17 @@ def dsmem_grouped_matmul(x, weight, offsets, order=None, fan: int = 1, transpose
         _int_tensor("order", order, None, x.device)
     _same_device(x.device, weight=weight)
     n = x.shape[0] if order is None else order.numel()
-
-    def run(s):
-        out = _lib.torch.empty((n, cols), dtype=out_dtype, device=x.device)
-        _check(_lib.dsmem_grouped_matmul(
-            x.data_ptr(), x.shape[0], _row_stride(x), weight.data_ptr(), weight.stride(1) if outer
-            > 1 else inner, weight.stride(0) if groups > 1 else outer * inner, offsets.data_ptr(),
-            groups, None if order is None else order.data_ptr(), int(fan), n, outer, inner,
-            int(transpose), dtype, out.data_ptr(), out_code, s))
-        return out
-
-    return _on(x.device, stream, (x, weight, offsets, order), run)
+    s = None if stream is not None else _current(x.device)
+    if s is None:
+        return _elsewhere(dsmem_grouped_matmul, x.device, stream, x, weight, offsets, order, fan,
+                          transpose, out_dtype)
+    out = _lib.torch.empty((n, cols), dtype=out_dtype, device=x.device)
+    _check(_lib.dsmem_grouped_matmul(
+        x.data_ptr(), x.shape[0], _row_stride(x), weight.data_ptr(), weight.stride(1) if outer
+        > 1 else inner, weight.stride(0) if groups > 1 else outer * inner, offsets.data_ptr(),
+        groups, None if order is None else order.data_ptr(), int(fan), n, outer, inner,
+        int(transpose), dtype, out.data_ptr(), out_code, s))
+    return out
 
 
 def dsmem_grouped_matmul_wgrad(dy, x, offsets, order=None, fan: int = 1, out_dtype=None,
@@ -240,16 +249,16 @@ def dsmem_grouped_matmul_wgrad(dy, x, offsets, order=None, fan: int = 1, out_dty
     elif x.shape[0] != n:
         raise ValueError(f"x must have {n} rows (got {x.shape[0]})")
     _same_device(dy.device, x=x)
-
-    def run(s):
-        out = _lib.torch.empty((groups, outer, inner), dtype=out_dtype, device=dy.device)
-        _check(_lib.dsmem_grouped_matmul_wgrad(
-            dy.data_ptr(), _row_stride(dy), x.data_ptr(), x.shape[0], _row_stride(x),
-            offsets.data_ptr(), groups, None if order is None else order.data_ptr(), int(fan), n,
-            outer, inner, dtype, out.data_ptr(), out_code, s))
-        return out
-
-    return _on(dy.device, stream, (dy, x, offsets, order), run)
+    s = None if stream is not None else _current(dy.device)
+    if s is None:
+        return _elsewhere(dsmem_grouped_matmul_wgrad, dy.device, stream, dy, x, offsets, order,
+                          fan, out_dtype)
+    out = _lib.torch.empty((groups, outer, inner), dtype=out_dtype, device=dy.device)
+    _check(_lib.dsmem_grouped_matmul_wgrad(
+        dy.data_ptr(), _row_stride(dy), x.data_ptr(), x.shape[0], _row_stride(x),
+        offsets.data_ptr(), groups, None if order is None else order.data_ptr(), int(fan), n,
+        outer, inner, dtype, out.data_ptr(), out_code, s))
+    return out
 
 
 def _positions(position, weights):
@@ -269,15 +278,14 @@ def dsmem_combine(z, position, weights=None, stream=None):
     _positions(position, weights)
     _same_device(z.device, position=position, weights=weights)
     (tokens, top_k), width = position.shape, z.shape[1]
-
-    def run(s):
-        out = _lib.torch.empty((tokens, width), dtype=z.dtype, device=z.device)
-        _check(_lib.dsmem_combine(
-            z.data_ptr(), z.shape[0], _row_stride(z), position.data_ptr(), None if weights is None
-            else weights.data_ptr(), tokens, top_k, width, dtype, out.data_ptr(), s))
-        return out
-
-    return _on(z.device, stream, (z, position, weights), run)
+    s = None if stream is not None else _current(z.device)
+    if s is None:
+        return _elsewhere(dsmem_combine, z.device, stream, z, position, weights)
+    out = _lib.torch.empty((tokens, width), dtype=z.dtype, device=z.device)
+    _check(_lib.dsmem_combine(
+        z.data_ptr(), z.shape[0], _row_stride(z), position.data_ptr(), None if weights is None
+        else weights.data_ptr(), tokens, top_k, width, dtype, out.data_ptr(), s))
+    return out
 
 
 def dsmem_combine_backward(dy, z, position, order, weights, stream=None):
@@ -295,17 +303,17 @@ def dsmem_combine_backward(dy, z, position, order, weights, stream=None):
         raise ValueError(f"z must have {tokens * top_k} rows (got {z.shape[0]})")
     _int_tensor("order", order, tokens * top_k, dy.device)
     _same_device(dy.device, z=z, position=position, weights=weights)
-
-    def run(s):
-        dz = _lib.torch.empty((tokens * top_k, width), dtype=z.dtype, device=z.device)
-        dweights = _lib.torch.empty((tokens, top_k), dtype=_lib.torch.float32, device=z.device)
-        _check(_lib.dsmem_combine_backward(
-            dy.data_ptr(), _row_stride(dy), z.data_ptr(), _row_stride(z), position.data_ptr(),
-            order.data_ptr(), weights.data_ptr(), tokens, top_k, width, dtype, dz.data_ptr(),
-            dweights.data_ptr(), s))
-        return dz, dweights
-
-    return _on(dy.device, stream, (dy, z, position, order, weights), run)
+    s = None if stream is not None else _current(dy.device)
+    if s is None:
+        return _elsewhere(dsmem_combine_backward, dy.device, stream, dy, z, position, order,
+                          weights)
+    dz = _lib.torch.empty((tokens * top_k, width), dtype=z.dtype, device=z.device)
+    dweights = _lib.torch.empty((tokens, top_k), dtype=_lib.torch.float32, device=z.device)
+    _check(_lib.dsmem_combine_backward(
+        dy.data_ptr(), _row_stride(dy), z.data_ptr(), _row_stride(z), position.data_ptr(),
+        order.data_ptr(), weights.data_ptr(), tokens, top_k, width, dtype, dz.data_ptr(),
+        dweights.data_ptr(), s))
+    return dz, dweights
 
 
 def dsmem_grad_clip(grads, max_norm: float, out=None, stream=None):
@@ -337,11 +345,10 @@ def dsmem_grad_clip(grads, max_norm: float, out=None, stream=None):
     table[1:4 * len(grads):4] = array.array("Q", map(tensor.data_ptr, out))
     table[2:4 * len(grads):4] = array.array("Q", counts)
     table[3:4 * len(grads):4] = array.array("Q", codes)
-
-    def run(s):
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        _check(_lib.dsmem_grad_clip(
-            table.buffer_info()[0], len(grads), float(max_norm), norm.data_ptr(), s))
-        return norm
-
-    return _on(device, stream, (*grads, *out), run)
+    s = None if stream is not None else _current(device)
+    if s is None:
+        return _elsewhere(dsmem_grad_clip, device, stream, grads, max_norm, out)
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    _check(_lib.dsmem_grad_clip(
+        table.buffer_info()[0], len(grads), float(max_norm), norm.data_ptr(), s))
+    return norm

@@ -474,6 +474,35 @@ def test_refusals():
             call()
 
 
+def test_every_operator_on_a_given_stream():
+    """With `stream`, outputs belong to it and equal the current stream's."""
+    g = generator(11)
+    logits = torch.randn(300, 24, generator=g).cuda()
+    x = torch.randn(300, 64, generator=g).to(torch.bfloat16).cuda()
+    up = torch.randn(24, 128, 64, generator=g).to(torch.bfloat16).cuda()
+
+    def layer(**on):
+        ids, w = dh.dsmem_route(logits, 3, **on)
+        off, order, pos = dh.dsmem_group(ids, 24, **on)
+        pos = pos.view(300, 3)
+        h = dh.dsmem_grouped_matmul(x, up, off, order=order, fan=3, **on)
+        y = dh.dsmem_combine(h, pos, w, **on)
+        dz, dw = dh.dsmem_combine_backward(y, h, pos, order, w, **on)
+        dx = dh.dsmem_grouped_matmul(dz, up, off, transpose=True, **on)
+        dup = dh.dsmem_grouped_matmul_wgrad(dz, x, off, order=order, fan=3, **on)
+        dl = dh.dsmem_route_backward(logits, ids, w, dw, **on)
+        norm = dh.dsmem_grad_clip([dup, dl], 1.0, **on)
+        return [ids, w, off, order, pos, h, y, dz, dw, dx, dup, dl, norm]
+
+    want = layer()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = layer(stream=side)
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_a_failed_scratch_allocation_is_reported(monkeypatch):
     f = [torch.ones(8, device="cuda")]
     monkeypatch.setenv("DSMEM_HIST_TEST_FAIL_ALLOC", "1")
