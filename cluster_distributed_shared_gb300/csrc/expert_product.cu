@@ -296,11 +296,13 @@ __device__ __forceinline__ void store_block(const TileArgs& a, const Tile& t, in
         if (channel0 + row < a.channels && col + q * V < a.width)
           *reinterpret_cast<uint4*>(out + static_cast<int64_t>(channel0 + row) * a.width + col + q * V) = p;
       }
-    } else if (lane < kN && col + lane < a.width) {
-      out += static_cast<int64_t>(channel0) * a.width + col + lane;
+    } else {
+      out += static_cast<int64_t>(channel0) * a.width + col;
       const int rows = min(32, a.channels - channel0);
       for (int row = 0; row < rows; ++row, out += a.width)
-        *out = ld_shared_value<O>(piece_at(row, lane / V) + lane % V * sizeof(O));
+#pragma unroll
+        for (int j = lane; j < kN; j += 32)
+          if (col + j < a.width) out[j] = ld_shared_value<O>(piece_at(row, j / V) + j % V * sizeof(O));
     }
     __syncwarp();
   } else {
@@ -327,10 +329,38 @@ __device__ __forceinline__ void store_block(const TileArgs& a, const Tile& t, in
     }
   }
 }
+// Zeros in a warp's 32 channels of a tile without any depth: the rows behind
+// the last group, the matrices of empty groups.
+template <int kKind, int kCols>
+__device__ __forceinline__ void store_zeros(const TileArgs& a, const Tile& t, int channel0) {
+  // In bytes: `lines` lines of `length`, `pitch` apart.
+  const int size = a.out_dtype == DSMEM_F32 ? 4 : 2, lane = threadIdx.x & 31;
+  const int channels = min(32, a.channels - channel0);
+  if (channels <= 0) return;
+  const int cols = min(kCols, (kKind == kWeightGrad ? a.width : t.end) - t.col0);
+  const int lines = kKind == kWeightGrad ? channels : cols;
+  const int length = (kKind == kWeightGrad ? cols : channels) * size;
+  const int64_t pitch = static_cast<int64_t>(kKind == kWeightGrad ? a.width : a.channels) * size;
+  const int64_t first = kKind == kWeightGrad
+                            ? (static_cast<int64_t>(t.group) * a.channels + channel0) * a.width + t.col0
+                            : static_cast<int64_t>(t.col0) * a.channels + channel0;
+  uint8_t* out = static_cast<uint8_t*>(a.out) + first * size;
+  const int step = a.wide_out ? 16 : size, per_line = length / step;
+  int shift = 0;  // 1 << shift lanes a line
+  while (shift < 5 && (1 << shift) < per_line) ++shift;
+  for (int line = lane >> shift; line < lines; line += 32 >> shift)
+    for (int i = lane & ((1 << shift) - 1); i < per_line; i += 1 << shift) {
+      uint8_t* p = out + line * pitch + i * step;
+      if (step == 16) *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
+      else if (step == 4) *reinterpret_cast<uint32_t*>(p) = 0u;
+      else *reinterpret_cast<uint16_t*>(p) = 0;
+    }
+}
+
 template <int kKind, int kN>
 __device__ __forceinline__ void store_any(const TileArgs& a, const Tile& t, int col, int channel0,
                                           const uint32_t (&r)[kN], uint32_t staging) {
-  if (a.out_dtype == DSMEM_F32) store_block<kKind, kN, float>(a, t, col, channel0, r, staging);
+  if (kN <= 32 && a.out_dtype == DSMEM_F32) store_block<kKind, kN, float>(a, t, col, channel0, r, staging);
   else if (a.out_dtype == DSMEM_F16) store_block<kKind, kN, __half>(a, t, col, channel0, r, staging);
   else store_block<kKind, kN, __nv_bfloat16>(a, t, col, channel0, r, staging);
 }
@@ -726,31 +756,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         tcgen_fence_after();
       }
       const uint32_t d = tmem + buffer * kCols + (static_cast<uint32_t>(quadrant * 32) << 16);
+      const uint32_t staging = out_staging + quadrant * kStageOut;
       const int limit = kKind == kWeightGrad ? a.width : t.end;
+      const int channel0 = t.chan0 + half * kChannels + quadrant * 32;
+      if (t.blocks == 0) {
+        store_zeros<kKind, kCols>(a, t, channel0);
+        continue;
+      }
+      if (kKind == kWeightGrad && kCols >= 64 && a.out_dtype != DSMEM_F32) {
+        // 128 bytes of an output row at a time.
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += kLoad) {
-        if (t.col0 + c >= limit) break;
-        uint32_t r[kLoad];
-        if (t.blocks > 0) {
+        for (int c = 0; c < kCols && t.col0 + c < limit; c += 64) {
+          uint32_t r[64];
+          tmem_load32(d + c, reinterpret_cast<uint32_t(&)[32]>(r[0]));
+          tmem_load32(d + c + 32, reinterpret_cast<uint32_t(&)[32]>(r[32]));
+          tmem_wait_load();
+          store_any<kKind, 64>(a, t, t.col0 + c, channel0, r, staging);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < kCols && t.col0 + c < limit; c += kLoad) {
+          uint32_t r[kLoad];
           if constexpr (kLoad == 32) tmem_load32(d + c, r);
           else tmem_load16(d + c, r);
           tmem_wait_load();
-        } else {
-#pragma unroll
-          for (int j = 0; j < kLoad; ++j) r[j] = 0u;
+          store_any<kKind, kLoad>(a, t, t.col0 + c, channel0, r, staging);
         }
-        store_any<kKind, kLoad>(a, t, t.col0 + c, t.chan0 + half * kChannels + quadrant * 32, r,
-                                out_staging + quadrant * kStageOut);
       }
-      if (t.blocks > 0) {
-        tcgen_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (kTwo) mbar_arrive_pair(map_rank(acc_empty + 8 * buffer, 0));
-          else mbar_arrive_local(acc_empty + 8 * buffer);
-        }
-        ++done;
+      tcgen_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (kTwo) mbar_arrive_pair(map_rank(acc_empty + 8 * buffer, 0));
+        else mbar_arrive_local(acc_empty + 8 * buffer);
       }
+      ++done;
     }
     __syncwarp();
   }
