@@ -67,10 +67,10 @@ struct Ring {
   static constexpr int kMaxSplit = kTeam != kSplit ? 1 : (kCols == 16 ? 8 : 4);
   static constexpr int kJoin = kChannels * kCols * 4;  // one CTA's sums
   // As many stages as fit beside the sums and the tables (227 KB in all).
-  static constexpr int kStages = kTeam == kSplit ? (kCols == 16 ? 6 : 4)
+  static constexpr int kStages = kTeam == kSplit ? (kCols == 16 ? 8 : 4)
                                                  : (kMine == 128 ? 6 : (kMine == 64 ? 8 : 10));
-  static int smem_bytes(int groups) {
-    return 1024 + kStages * kStage + (kMaxSplit - 1) * kJoin + 4 * kStageOut + kBarrierBytes +
+  static int smem_bytes(int groups, int split) {
+    return 1024 + kStages * kStage + (split - 1) * kJoin + 4 * kStageOut + kBarrierBytes +
            2 * 4 * (groups + 2);
   }
 };
@@ -233,7 +233,17 @@ struct Schedule {
       group = first[place];
       i = t - place * each;
     } else {
-      while (t >= first[group + 1]) ++group;
+      // The next group with tiles is often one of the next, but many may be empty.
+      for (int near = 0; near < 3 && t >= first[group + 1]; ++near) ++group;
+      if (t >= first[group + 1]) {
+        int low = group + 1, high = owners() - 1;
+        while (low < high) {
+          const int mid = (low + high) >> 1;
+          if (t >= first[mid + 1]) low = mid + 1;
+          else high = mid;
+        }
+        group = low;
+      }
       i = t - first[group];
     }
     Tile r;
@@ -255,6 +265,13 @@ struct Schedule {
       r.blocks = part(all, rank + 1) - r.block0;
     }
     return r;
+  }
+  // Stages of tile t, all that the matrix instructions and the relay need to
+  // know: a tile's whole description would hold them up between two tiles.
+  __device__ __forceinline__ int blocks_at(int t, int of_groups) {
+    if (kKind == kWeightGrad) return at(t).blocks;
+    const int all = t < of_groups ? depth_blocks : 0;
+    return kTeam == kSplit ? part(all, rank + 1) - part(all, rank) : all;
   }
   // First stage of a rank's part of `blocks`; the first rank's part is empty
   // only if all are.
@@ -322,10 +339,11 @@ __device__ __forceinline__ void store_block(const TileArgs& a, const Tile& t, in
       }
       __syncwarp();
     } else if (channel0 + lane < a.channels) {
+      out += lane;
+      const int rows = t.end - col;
 #pragma unroll
-      for (int j = 0; j < kN; ++j)
-        if (col + j < t.end)
-          out[static_cast<int64_t>(j) * a.channels + lane] = from_float<O>(__uint_as_float(r[j]));
+      for (int j = 0; j < kN; ++j, out += a.channels)
+        if (j < rows) *out = from_float<O>(__uint_as_float(r[j]));
     }
   }
 }
@@ -345,16 +363,20 @@ __device__ __forceinline__ void store_zeros(const TileArgs& a, const Tile& t, in
                             ? (static_cast<int64_t>(t.group) * a.channels + channel0) * a.width + t.col0
                             : static_cast<int64_t>(t.col0) * a.channels + channel0;
   uint8_t* out = static_cast<uint8_t*>(a.out) + first * size;
-  const int step = a.wide_out ? 16 : size, per_line = length / step;
-  int shift = 0;  // 1 << shift lanes a line
-  while (shift < 5 && (1 << shift) < per_line) ++shift;
-  for (int line = lane >> shift; line < lines; line += 32 >> shift)
+  const auto clear = [&](auto zero) {
+    const int per_line = length / static_cast<int>(sizeof(zero));
+    int shift = 0;  // 1 << shift lanes a line
+    while (shift < 5 && (1 << shift) < per_line) ++shift;
     for (int i = lane & ((1 << shift) - 1); i < per_line; i += 1 << shift) {
-      uint8_t* p = out + line * pitch + i * step;
-      if (step == 16) *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
-      else if (step == 4) *reinterpret_cast<uint32_t*>(p) = 0u;
-      else *reinterpret_cast<uint16_t*>(p) = 0;
+      uint8_t* p = out + (lane >> shift) * pitch + i * static_cast<int>(sizeof(zero));
+#pragma unroll 8
+      for (int line = lane >> shift; line < lines; line += 32 >> shift, p += (32 >> shift) * pitch)
+        *reinterpret_cast<decltype(zero)*>(p) = zero;
     }
+  };
+  if (a.wide_out) clear(make_uint4(0, 0, 0, 0));
+  else if (size == 4) clear(uint32_t{0});
+  else clear(uint16_t{0});
 }
 
 template <int kKind, int kN>
@@ -370,7 +392,7 @@ __device__ __forceinline__ void store_any(const TileArgs& a, const Tile& t, int 
 // copies of a stage arrive on `landed` by themselves, so that the warps go on
 // to the next stage at once; the relay warp passes a landed stage on.  (Warps
 // that waited for their own copies had three stages in flight at most, and
-// the forward product took 370 instead of 360 us.)
+// the forward product took 370 instead of 360 us at that step.)
 template <int kKind, int kCols, int kTeam>
 __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, kCols, kTeam>& schedule,
                                             int unit, int units, uint32_t half, int total, uint32_t base,
@@ -390,39 +412,56 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
     const int row = o < 0 ? -1 : (a.order ? a.fan.quotient(o) : o);
     return row < a.x_rows ? row : -1;
   };
-  for (int j = 0, i = unit; i < total && ok; i = schedule.turn(++j, unit, units)) {
-    const Tile t = schedule.at(i);
-    if (t.blocks == 0) continue;
+  // Forward and input gradient: 8 threads a row of 128 bytes; the rows are the
+  // same in every stage of a tile.
+  constexpr int kLines = kShift / 8, kRows = kBMn ? 1 : (kMine + kLines - 1) / kLines;
+  // Weight gradient: kPieces threads a row of kMine elements.  A warp needs
+  // kFound rows of a stage; its lanes look up those of kBatch stages at once,
+  // a batch ahead.
+  constexpr int kPieces = kMine / 8, kAtOnce = kShift / kPieces, kPerWarp = 32 / kPieces;
+  constexpr int kFound = kDepth / (kShift / 32), kBatch = 32 / kFound;
+  // This shift's stages of a tile are first_of(before), and every kShifts-th.
+  const auto first_of = [&](uint32_t stages) { return static_cast<int>((shift - stages % kShifts + kShifts) % kShifts); };
+  const auto batch_place = [&](const Tile& t, int first_k, int m) {
+    const int l = lane % kFound;
+    const int r = l / kPerWarp * kAtOnce + (tid >> 5) * kPerWarp + l % kPerWarp;
+    return place(t.begin + (t.block0 + first_k + (m + lane / kFound) * kShifts) * kDepth + r, t.end);
+  };
+  // A tile's entries of the order are asked for while the tile before is
+  // copied: they take longer to arrive than a stage.
+  int ahead[kRows];
+  const auto ask = [&](const Tile& t, uint32_t stages) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      ahead[r] = kBMn ? batch_place(t, first_of(stages), 0)
+                      : place(t.col0 + static_cast<int>(half) * kMine + r * kLines + tid / 8, t.end);
+  };
+
+  Tile next;
+  if (unit < total) {
+    next = schedule.at(unit);
+    ask(next, 0);
+  }
+  for (int j = 0, i = unit; i < total && ok;) {
+    const Tile t = next;
     const int col0 = t.col0 + half * kMine, chan0 = t.chan0 + half * kChannels;
-    // Forward and input gradient: 8 threads a row of 128 bytes; the rows are
-    // the same in every stage of the tile.
-    constexpr int kLines = kShift / 8, kRows = kBMn ? 1 : (kMine + kLines - 1) / kLines;
+    const int first_k = first_of(before);
     int row[kRows];
+    int here = 0, later = kBMn ? ahead[0] : 0;
     if (!kBMn) {
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) row[r] = place(col0 + r * kLines + tid / 8, t.end);
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) row[r] = named_row(row[r]);
+      for (int r = 0; r < kRows; ++r) row[r] = named_row(ahead[r]);
     }
-    // Weight gradient: kPieces threads a row of kMine elements.  A warp needs
-    // kFound rows of a stage; its lanes look up those of kBatch stages at once,
-    // a batch ahead, as the order's entries take longer to arrive than a stage.
-    constexpr int kPieces = kMine / 8, kAtOnce = kShift / kPieces, kPerWarp = 32 / kPieces;
-    constexpr int kFound = kDepth / (kShift / 32), kBatch = 32 / kFound;
-    // This shift's stages of the tile: mine_at(0), mine_at(1), ..
-    const int first_k = (shift - before % kShifts + kShifts) % kShifts;
-    const auto mine_at = [&](int m) { return first_k + m * kShifts; };
-    const auto batch_place = [&](int m) {
-      const int l = lane % kFound;
-      const int r = l / kPerWarp * kAtOnce + (tid >> 5) * kPerWarp + l % kPerWarp;
-      return place(t.begin + (t.block0 + mine_at(m + lane / kFound)) * kDepth + r, t.end);
-    };
-    int ahead = kBMn ? batch_place(0) : 0, here = 0;
+    i = schedule.turn(++j, unit, units);
+    if (i < total) {
+      next = schedule.at(i);
+      ask(next, before + t.blocks);
+    }
 
-    for (int m = 0, k = first_k; k < t.blocks; ++m, k = mine_at(m)) {
+    for (int m = 0, k = first_k; k < t.blocks; ++m, k += kShifts) {
       if (kBMn && m % kBatch == 0) {
-        here = named_row(ahead);
-        ahead = batch_place(m + kBatch);
+        here = named_row(later);
+        later = batch_place(t, first_k, m + kBatch);
       }
       const uint32_t stage = (before + k) % kStages, phase = (before + k) / kStages & 1;
       ok = wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
@@ -490,7 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* base_ptr = raw + (base - smem_u32(raw));
   const uint32_t join = base + kStages * kStage;
-  const uint32_t out_staging = join + (R::kMaxSplit - 1) * R::kJoin;
+  const uint32_t members = kTeam == kSplit ? cluster_nctarank() : (kTwo ? 2u : 1u);
+  const uint32_t out_staging = join + (kTeam == kSplit ? members - 1 : 0) * R::kJoin;
   const uint32_t bars = out_staging + 4 * kStageOut;
   const uint32_t full = bars, empty = bars + 8 * kStages;
   const uint32_t landed = empty + 8 * kStages;
@@ -503,7 +543,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // A unit works on a tile: a CTA, or a cluster whose first CTA leads.
   const uint32_t rank = kTeam != kSolo ? cluster_ctarank() : 0u;
-  const uint32_t members = kTeam == kSplit ? cluster_nctarank() : (kTwo ? 2u : 1u);
   const uint32_t half = kTwo ? rank : 0u;
   const int unit = blockIdx.x / members, units = gridDim.x / members;
   Schedule<kKind, kCols, kTeam> schedule(begin, first, a, rank, members);
@@ -529,8 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_map(&maps.a);
     prefetch_map(&maps.b);
   }
-  // begin[g + 1] := the group's end, clamped into [0, n]; warp 2 then makes
-  // the ends monotone and lays the tiles end to end.
+  // begin[g + 1] := the group's end, clamped into [0, n]; then the ends are made
+  // monotone and the tiles laid end to end.
   for (int g = threadIdx.x; g < a.groups; g += kThreads) {
     const int64_t e = a.offsets[g + 1];
     begin[g + 1] = static_cast<int32_t>(e < 0 ? 0 : (e > a.n ? a.n : e));
@@ -542,31 +581,43 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tmem_alloc<kTwo>(tmem_at, kTmemColumns);
   __syncthreads();
-  if (warp == 2) {
-    int end_before = 0, tiles_before = 0;
-    for (int g0 = 0; g0 < schedule.owners(); g0 += 32) {
-      const int g = g0 + lane;
-      int end = g < schedule.owners() ? begin[g + 1] : 0;
+  // Each warp takes 32 groups of a round of kWarps * 32: the running maximum
+  // of their ends, then the running sum of their tiles.
+  constexpr int kWarps = kThreads / 32;
+  __shared__ int of_warp[2][32];
+  int end_before = 0, tiles_before = 0;
+  for (int g0 = 0; g0 < schedule.owners(); g0 += kWarps * 32) {
+    const int g = g0 + warp * 32 + lane;
+    const bool owner = g < schedule.owners();
+    int end = owner ? begin[g + 1] : 0;
+    const int most = __reduce_max_sync(kFull, end);
+    if (lane == 0) of_warp[0][warp] = most;
+    __syncthreads();
+    const int other = lane < kWarps ? of_warp[0][lane] : 0;
+    const int earlier = max(end_before, __reduce_max_sync(kFull, lane < warp ? other : 0));
+    end_before = max(end_before, __reduce_max_sync(kFull, other));
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int up = __shfl_up_sync(kFull, end, d);
-        if (lane >= d) end = max(end, up);
-      }
-      end = max(end, end_before);
-      int start = __shfl_up_sync(kFull, end, 1);
-      if (lane == 0) start = end_before;
-      int tiles = g < schedule.owners() ? schedule.tiles_of(end - start) : 0;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(kFull, end, d);
+      if (lane >= d) end = max(end, up);
+    }
+    end = max(end, earlier);
+    int start = __shfl_up_sync(kFull, end, 1);
+    if (lane == 0) start = earlier;
+    int tiles = owner ? schedule.tiles_of(end - start) : 0;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int up = __shfl_up_sync(kFull, tiles, d);
-        if (lane >= d) tiles += up;
-      }
-      if (g < schedule.owners()) {
-        begin[g + 1] = end;
-        if (kKind != kWeightGrad) first[g + 1] = tiles_before + tiles;
-      }
-      end_before = __shfl_sync(kFull, end, 31);
-      tiles_before += __shfl_sync(kFull, tiles, 31);
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(kFull, tiles, d);
+      if (lane >= d) tiles += up;
+    }
+    if (lane == 31) of_warp[1][warp] = tiles;
+    __syncthreads();
+    const int sum = lane < kWarps ? of_warp[1][lane] : 0;
+    tiles += tiles_before + __reduce_add_sync(kFull, lane < warp ? sum : 0);
+    tiles_before += __reduce_add_sync(kFull, sum);
+    if (owner) {
+      begin[g + 1] = end;
+      if (kKind != kWeightGrad) first[g + 1] = tiles;
     }
   }
   if (kKind == kWeightGrad) {
@@ -593,6 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_at));
   const int total = schedule.total();
+  const int of_groups = kKind == kWeightGrad ? total : first[a.groups];  // tiles of real groups
 
   // Output: warp w may read lanes 32 (w % 4) .. of tensor memory.
   const int quadrant = warp & 3;
@@ -660,8 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       for (int j = 0, i = unit; i < total && ok; i = schedule.turn(++j, unit, units)) {
-        const Tile t = schedule.at(i);
-        for (int k = 0; k < t.blocks; ++k) {
+        const int blocks = schedule.blocks_at(i, of_groups);
+        for (int k = 0; k < blocks; ++k) {
           ok = wait_for(landed + 8 * stage, phase, gave_up, a.wait_cycles, a.status);
           if (!ok) break;
           fence_async_shared();
@@ -687,13 +739,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t stage = 0, phase = 0, done = 0;
       bool ok = true;
       for (int j = 0, i = unit; i < total && ok; i = schedule.turn(++j, unit, units)) {
-        const Tile t = schedule.at(i);
-        if (t.blocks == 0) continue;
+        const int blocks = schedule.blocks_at(i, of_groups);
+        if (blocks == 0) continue;
         const uint32_t buffer = done & 1, d = tmem + buffer * kCols;
         ok = wait_for(acc_empty + 8 * buffer, ((done >> 1) & 1) ^ 1, gave_up, a.wait_cycles, a.status);
         if (!ok) break;
         tcgen_fence_after();
-        for (int k = 0; k < t.blocks; ++k) {
+        for (int k = 0; k < blocks; ++k) {
           ok = wait_for(full + 8 * stage, phase, gave_up, a.wait_cycles, a.status);
           if (!ok) break;
           tcgen_fence_after();
@@ -1018,7 +1070,7 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
   const int64_t tiles = tile_bound(p, kCols, R::kHeight);
   if (tiles > INT32_MAX - 1024)  // tile counters step past the last tile
     return fail_with(DSMEM_HIST_EINVAL, "grouped product: more than 2^31 output tiles");
-  const int smem = R::smem_bytes(p.groups);
+  const int smem = R::smem_bytes(p.groups, kTeam == kSplit ? split : 1);
   const auto kernel = product_kernel<kKind, kCols, kTeam>;
   static SmemLimit limit;
   cudaError_t e = limit.need(reinterpret_cast<const void*>(kernel), ctx.device, smem);
@@ -1050,8 +1102,9 @@ template <int kKind, int kCols>
 int launch_narrow(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
                   cudaStream_t stream) {
   const int64_t depth = kKind == kForward ? p.inner : (kKind == kInputGrad ? p.outer : p.n / p.groups);
-  const int split = split_for(tile_bound(p, kCols, kChannels), depth / kDepth, Ring<kCols, kSplit>::kMaxSplit,
-                              ctx.sm_count);
+  // The sums of 8 CTAs fit beside tables of up to 1024 groups.
+  const int most = std::min(Ring<kCols, kSplit>::kMaxSplit, p.groups > 1024 ? 4 : 8);
+  const int split = split_for(tile_bound(p, kCols, kChannels), depth / kDepth, most, ctx.sm_count);
   if (split > 1) return launch<kKind, kCols, kSplit>(p, ctx, x, w, split, stream);
   return launch<kKind, kCols, kSolo>(p, ctx, x, w, 1, stream);
 }
