@@ -276,7 +276,7 @@ struct Schedule {
   // First stage of a rank's part of `blocks`; the first rank's part is empty
   // only if all are.
   __device__ __forceinline__ int part(int blocks, uint32_t of) const {
-    return static_cast<int>((static_cast<int64_t>(blocks) * of + split - 1) / split);
+    return static_cast<int>((blocks * of + split - 1) >> (31 - __clz(split)));  // split: a power of 2
   }
 };
 
