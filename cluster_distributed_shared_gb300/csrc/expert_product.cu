@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t* begin = reinterpret_cast<int32_t*>(base_ptr + (bars - base) + kBarrierBytes);
   int32_t* first = begin + a.groups + 2;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // A unit works on a tile: a CTA, or a cluster whose first CTA leads.
   const uint32_t rank = kTeam != kSolo ? cluster_ctarank() : 0u;
   const uint32_t half = kTwo ? rank : 0u;
@@ -650,14 +650,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int quadrant = warp & 3;
 
   if (warp == 0) {
-    // TMA copies, by one thread.
-    if (lane == 0) {
+    // TMA copies.
     uint32_t stage = 0, phase = 0, issued = 0;
     bool ok = true;
     for (int j = 0, i = unit; i < total && ok; i = schedule.turn(++j, unit, units)) {
       const Tile t = schedule.at(i);
       for (int k = 0; k < t.blocks; ++k) {
-        ok = wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
+        ok = __all_sync(kFull, wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status));
         if (!ok || (a.withhold && schedule.turn(j + 1, unit, units) >= total && k + 1 == t.blocks)) break;
         const uint32_t sa = base + stage * kStage, sb = sa + kABytes;
         const uint32_t bar = kTwo ? map_rank(full + 8 * stage, 0) : full + 8 * stage;
@@ -665,26 +664,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int p0 = t.begin + k0;  // weight gradient: the stage's first row
         const int chan0 = t.chan0 + half * kChannels, col0 = t.col0 + half * kMine;
         const bool ragged = kBMn && p0 + kDepth > t.end;
-        if (half == 0)
-          mbar_expect_tx(full + 8 * stage, (ragged ? 0 : (a.order ? kABytes : kStage)) * (kTwo ? 2 : 1));
-        if (kKind == kForward) {
-          tma_load_3d<kTwo>(sa, &maps.a, k0, chan0, t.group, bar);
-        } else if (kKind == kInputGrad) {
-          tma_load_3d<kTwo>(sa, &maps.a, chan0, k0, t.group, bar);
-          tma_load_3d<kTwo>(sa + 8192, &maps.a, chan0 + 64, k0, t.group, bar);
-        } else if (!ragged) {
-          tma_load_2d<kTwo>(sa, &maps.a, chan0, p0, bar);
-          tma_load_2d<kTwo>(sa + 8192, &maps.a, chan0 + 64, p0, bar);
-        }
-        if (!a.order && !ragged) {
-          if (kBMn) {
+        if (elect_one()) {
+          if (half == 0)
+            mbar_expect_tx(full + 8 * stage, (ragged ? 0 : (a.order ? kABytes : kStage)) * (kTwo ? 2 : 1));
+          if (kKind == kForward) {
+            tma_load_3d<kTwo>(sa, &maps.a, k0, chan0, t.group, bar);
+          } else if (kKind == kInputGrad) {
+            tma_load_3d<kTwo>(sa, &maps.a, chan0, k0, t.group, bar);
+            tma_load_3d<kTwo>(sa + 8192, &maps.a, chan0 + 64, k0, t.group, bar);
+          } else if (!ragged) {
+            tma_load_2d<kTwo>(sa, &maps.a, chan0, p0, bar);
+            tma_load_2d<kTwo>(sa + 8192, &maps.a, chan0 + 64, p0, bar);
+          }
+          if (!a.order && !ragged) {
+            if (kBMn) {
 #pragma unroll
-            for (int box = 0; box < kMine / 64; ++box)
-              tma_load_2d<kTwo>(sb + box * 8192, &maps.b, col0 + box * 64, p0, bar);
-          } else {
-            tma_load_2d<kTwo>(sb, &maps.b, k0, col0, bar);
+              for (int box = 0; box < kMine / 64; ++box)
+                tma_load_2d<kTwo>(sb + box * 8192, &maps.b, col0 + box * 64, p0, bar);
+            } else {
+              tma_load_2d<kTwo>(sb, &maps.b, k0, col0, bar);
+            }
           }
         }
+        __syncwarp();
         ++issued;
         if (++stage == kStages) {
           stage = 0;
@@ -703,7 +705,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (!mbar_try_wait(full + 8 * (j % kStages), (j / kStages) & 1) && clock64() < deadline) {
         }
       }
-    }
     }
     __syncwarp();
   } else if (warp == kRelayWarp) {
@@ -731,8 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (gathering)
       gather_rows<kKind, kCols, kTeam>(a, schedule, unit, units, half, total, base, landed, empty, gave_up);
   } else if (warp == 1) {
-    // Matrix instructions, by one thread; a pair's by its leader's.
-    if (half == 0 && lane == 0) {
+    // Matrix instructions; a pair's by its leader.
+    if (half == 0) {
       const uint32_t idesc = (1u << 4) | (a.dtype == DSMEM_BF16 ? (1u << 7) | (1u << 10) : 0u) |
                              (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u) |
                              (uint32_t{kCols >> 3} << 17) | (uint32_t{R::kHeight >> 4} << 24);
@@ -742,30 +743,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int blocks = schedule.blocks_at(i, of_groups);
         if (blocks == 0) continue;
         const uint32_t buffer = done & 1, d = tmem + buffer * kCols;
-        ok = wait_for(acc_empty + 8 * buffer, ((done >> 1) & 1) ^ 1, gave_up, a.wait_cycles, a.status);
+        ok = __all_sync(kFull, wait_for(acc_empty + 8 * buffer, ((done >> 1) & 1) ^ 1, gave_up, a.wait_cycles,
+                                        a.status));
         if (!ok) break;
         tcgen_fence_after();
         for (int k = 0; k < blocks; ++k) {
-          ok = wait_for(full + 8 * stage, phase, gave_up, a.wait_cycles, a.status);
+          ok = __all_sync(kFull, wait_for(full + 8 * stage, phase, gave_up, a.wait_cycles, a.status));
           if (!ok) break;
           tcgen_fence_after();
           const uint32_t sa = base + stage * kStage;
           const uint64_t da = descriptor<kAMn>(sa), db = descriptor<kBMn>(sa + kABytes);
+          if (elect_one()) {
 #pragma unroll
-          for (int s = 0; s < kDepth / 16; ++s)
-            mma_f16<kTwo>(d, da + s * kAStep, db + s * kBStep, idesc, k > 0 || s > 0);
-          mma_commit<kTwo>(empty + 8 * stage);
+            for (int s = 0; s < kDepth / 16; ++s)
+              mma_f16<kTwo>(d, da + s * kAStep, db + s * kBStep, idesc, k > 0 || s > 0);
+            mma_commit<kTwo>(empty + 8 * stage);
+            if (k + 1 == blocks) mma_commit<kTwo>(acc_full + 8 * buffer);
+          }
+          __syncwarp();
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
-        if (!ok) break;
-        mma_commit<kTwo>(acc_full + 8 * buffer);
         ++done;
       }
       if (flag_set(gave_up)) {  // matrix instructions end before tensor memory is given back
-        mma_commit<kTwo>(drained);
+        if (elect_one()) mma_commit<kTwo>(drained);
+        __syncwarp();
         const long long deadline = clock64() + kDefaultWaitCycles;
         while (!mbar_try_wait(drained, 0) && clock64() < deadline) {
         }

@@ -8,6 +8,15 @@
 namespace dsmh {
 namespace ptx {
 
+// True in one lane of a converged warp, always the same one.  Loops that the
+// whole warp runs, with only the issue inside, keep the operands of copies and
+// matrix instructions in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // kPair: the instruction works for both CTAs of a pair (cta_group::2).
 
 // Tensor memory (one warp, all lanes; of a pair, one warp of either CTA).
