@@ -37,7 +37,7 @@ using namespace ptx;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kChannels = 128;  // channels of a tile in one CTA
 constexpr int kDepth = 64;      // depth of a stage: 128 bytes of 16-bit elements
-constexpr int kGatherThreads = 128;
+constexpr int kGatherThreads = 256;
 constexpr int kShifts = 2;                        // groups of gathering warps that take stages in turn
 constexpr int kShift = kGatherThreads / kShifts;  // threads of one
 constexpr int kRelayWarp = 6 + kGatherThreads / 32;
@@ -420,6 +420,7 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
   // a batch ahead.
   constexpr int kPieces = kMine / 8, kAtOnce = kShift / kPieces, kPerWarp = 32 / kPieces;
   constexpr int kFound = kDepth / (kShift / 32), kBatch = 32 / kFound;
+  static_assert(kFound <= 32 && kPerWarp >= 1 && kAtOnce >= 1, "a warp looks up a stage's rows at once");
   // This shift's stages of a tile are first_of(before), and every kShifts-th.
   const auto first_of = [&](uint32_t stages) { return static_cast<int>((shift - stages % kShifts + kShifts) % kShifts); };
   const auto batch_place = [&](const Tile& t, int first_k, int m) {
