@@ -62,7 +62,8 @@ constexpr int kAtOnce = 4;
 constexpr int kCtas = 5;
 
 // One CTA per token and kThreads pieces: out = sum_j w_j z[p_j], summed in 32
-// bits in the order of j.  Bound by reading z.
+// bits in the order of j.  Bound by reading z: 16384 tokens x 8 rows of 2048
+// bf16 in 90 us, 6.7 TB/s (eight rows in flight: 93; one: 102).
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads, kCtas) combine_kernel(CombineArgs a) {
   using P = Piece<T, kWide>;
@@ -103,7 +104,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) combine_kernel(CombineArgs a)
 // One CTA per token: its dy row against each of its z rows.  dz is written on
 // the way; the dot products are summed in 32 bits by thread, warp and CTA.
 // The CTA also clears those of the rows [token * top_k, (token + 1) * top_k)
-// that lie behind the last group.  Bound by reading z and writing dz.
+// that lie behind the last group.  Bound by reading z and writing dz: 174 us at
+// that size, 6.6 TB/s.
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads, kCtas) combine_backward_kernel(CombineArgs a) {
   using P = Piece<T, kWide>;

@@ -9,11 +9,19 @@
 // One persistent CTA per SM; warp 0 copies operand tiles of 64 depth
 // (128 bytes, swizzled) into a ring of stages by TMA, warp 1 issues the matrix
 // instructions into one of two accumulators in tensor memory, and warps 2..5
-// write the other one out.  Rows named by an order are fetched by warps 6..9
-// with 16-byte asynchronous copies straight into the swizzled layout, so no
-// reordered copy of x exists anywhere.  (Four-row TMA gathers took about 70
-// cycles each, 4.5 times the time of the matrix instructions they feed.)
-// The same warps fill the ragged end of a group's contraction with zeros.
+// write the other one out.  Rows named by an order are fetched by the warps
+// behind them with 16-byte asynchronous copies straight into the swizzled
+// layout, so no reordered copy of x exists anywhere.  (Four-row TMA gathers
+// took about 70 cycles each, 4.5 times the time of the matrix instructions
+// they feed.)  The same warps fill the ragged end of a group's contraction
+// with zeros.
+//
+// Large products are bound by the tensor cores, and over long runs by the
+// card's power: 131072 rows in 64 equal groups, 2048 x 1024, bf16, take 318 us
+// (forward, gathered rows), 309 (input gradient) and 329 (weight gradient,
+// gathered rows) or 1.67 to 1.78 PFLOP/s, where one library product of that
+// size takes 288.  Few rows are bound by reading the weights: 32 tokens over
+// 128 experts (469 MB) 73 us, 95% of the copy rate.
 //
 // The group sizes are on the device only: every CTA lays the groups' tiles
 // end to end from the offsets and takes every gridDim-th.
@@ -1097,7 +1105,11 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
   return e == cudaSuccess ? DSMEM_HIST_OK : fail_with_cuda(e, "grouped product launch");
 }
 
-// CTAs to split a tile's depth over, where whole tiles leave SMs idle.
+// CTAs to split a tile's depth over, where whole tiles leave SMs idle; each
+// keeps two stages or more.  Split / whole, us: one row of 4096 by 1024
+// channels 7.7 / 15.3, 64 rows 11.2 / 17.1, 16384 rows' weight gradient of
+// 512 x 512 22 / 57; no difference where little is idle (64 rows of 1024 by
+// 4096 channels 7.9 / 7.8).
 int split_for(int64_t tiles, int64_t depth_blocks, int most, int sm_count) {
   int split = 1;
   while (split < most && tiles * split * 2 <= sm_count && depth_blocks >= split * 4) split *= 2;
@@ -1114,32 +1126,41 @@ int launch_narrow(const ProductArgs& p, const CallContext& ctx, const Source& x,
   if (split > 1) return launch<kKind, kCols, kSplit>(p, ctx, x, w, split, stream);
   return launch<kKind, kCols, kSolo>(p, ctx, x, w, 1, stream);
 }
-template <int kKind, int kCols>
-int launch_wide(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
-                cudaStream_t stream) {
-  return launch<kKind, kCols, kPair>(p, ctx, x, w, 1, stream);
-}
 
-// Tiles as wide as the average group needs, so that few columns are padding;
-// 256 channels high where that still gives every pair of SMs a tile.
+// Tiles about as wide as the average group, so that few columns are padding,
+// and narrower where wide ones would not give every SM (pair of SMs) one.
+// Forward, 64 groups of 2048 x 1024, us at this many rows a group:
+//   16 / 64 wide    12: 47.3 / 47.7    24: 49.9 / 48.4
+//   64 / 128 (pair) 64: 51.2 / 51.1    80: 57.2 / 52.3
+//   128 / 256       128: 55.4 / 60.4   160: 69.9 / 62.4
+//   4 groups of 512 rows by 1024 x 1024 (52 tiles 256 wide): 8.7 / 11.8;
+//   by 2048 x 2048 (104): 18.4 / 17.6
+//   4 groups of 512 rows by 1024 x 512 (42 pairs' tiles 128 wide), 64 / 128: 8.1 / 8.5,
+//   by 1024 x 1024: 11.6 / 8.7
+// 128 wide, pairs against single CTAs: 8.7 / 9.1 to 18.4 / 20.7; single ones
+// are left for up to 128 channels.
 template <int kKind>
 int launch_rows(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
                 cudaStream_t stream) {
   const int64_t average = p.n / p.groups, pairs = ctx.sm_count / 2;
   const int channels = kKind == kInputGrad ? p.inner : p.outer;
-  if (average <= 12) return launch_narrow<kKind, 16>(p, ctx, x, w, stream);
+  if (average <= 16) return launch_narrow<kKind, 16>(p, ctx, x, w, stream);
   if (average <= 64 || tile_bound(p, 128, 128) < pairs) return launch_narrow<kKind, 64>(p, ctx, x, w, stream);
-  if (channels > kChannels && average > 128 && tile_bound(p, 256, 256) >= pairs)
-    return launch_wide<kKind, 256>(p, ctx, x, w, stream);
-  if (channels > kChannels && tile_bound(p, 128, 256) >= pairs)
-    return launch_wide<kKind, 128>(p, ctx, x, w, stream);
-  return launch<kKind, 128, kSolo>(p, ctx, x, w, 1, stream);
+  if (channels <= kChannels) return launch<kKind, 128, kSolo>(p, ctx, x, w, 1, stream);
+  if (average > 128 && tile_bound(p, 256, 256) >= pairs) return launch<kKind, 256, kPair>(p, ctx, x, w, 1, stream);
+  return launch<kKind, 128, kPair>(p, ctx, x, w, 1, stream);
 }
+
+// 256 x 256 tiles of pairs while there are half as many as pairs, 128 x 128
+// ones while there are as many, else 128 x 64 with their depth split.  us,
+// 256 / 128 / 64: 4 groups of 1024 rows, 1024 x 1024 (64 tiles of 256)
+// 12.2 / 15.3 / 20.2; 7 of 333, 512 x 1024 (56) 8.7 / 9.7 / 10.8; 2 of 2048,
+// 512 x 1024 (16; 64 tiles of 128) 15.3 / 13.8 / 11.8.
 int launch_weight_grad(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
                        cudaStream_t stream) {
   const int64_t pairs = ctx.sm_count / 2;
-  if (p.outer > kChannels && tile_bound(p, 256, 256) >= pairs)
-    return launch_wide<kWeightGrad, 256>(p, ctx, x, w, stream);
+  if (p.outer > kChannels && 2 * tile_bound(p, 256, 256) >= pairs)
+    return launch<kWeightGrad, 256, kPair>(p, ctx, x, w, 1, stream);
   if (tile_bound(p, 128, 128) >= pairs) return launch<kWeightGrad, 128, kSolo>(p, ctx, x, w, 1, stream);
   return launch_narrow<kWeightGrad, 64>(p, ctx, x, w, stream);
 }

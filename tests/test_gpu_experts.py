@@ -201,6 +201,8 @@ PRODUCTS = [
     (3000, 4, 1, 776, 1304, 0.5),
     (2500, 5, 2, 1100, 1001, 1.0),
     (700, 30, 1, 520, 264, 0.0),
+    # many rows of few channels
+    (9900, 3, 1, 72, 104, 0.5),
 ]
 
 
