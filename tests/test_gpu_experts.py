@@ -476,6 +476,41 @@ def test_refusals():
             call()
 
 
+def test_offsets_past_32_bits():
+    """Outputs and inputs of more than 2^31 elements, looked at near their ends."""
+    g = generator(8)
+    n, inner, outer = 70001, 16, 32768
+    x = torch.randn(n, inner, generator=g).to(torch.bfloat16)
+    w = torch.randn(2, outer, inner, generator=g).to(torch.bfloat16)
+    off = torch.tensor([0, 30000, n], dtype=torch.int32, device="cuda")
+    y = dh.dsmem_grouped_matmul(x.cuda(), w.cuda(), off)
+    xd, wd = x[-3:].double(), w[1].double()
+    close(y[-3:], xd @ wd.T, xd.abs() @ wd.abs().T, inner)
+    position = torch.tensor([[n - 1, n - 2], [n - 3, -1]], dtype=torch.int32, device="cuda")
+    z = dh.dsmem_combine(y, position).cpu().double()
+    last = y[-3:].cpu().double()
+    want = torch.stack([last[2] + last[1], last[0]])
+    assert ((z - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -22 * last.abs().sum(0)).all()
+    # the same rows as a source
+    dx = dh.dsmem_grouped_matmul(y, w.cuda(), off, transpose=True)[-3:]
+    close(dx, last @ wd, last.abs() @ wd.abs(), outer)
+    del y
+    groups, inner, outer = 70, 4096, 8192
+    x, dy = (torch.randn(groups, c, generator=g).to(torch.bfloat16) for c in (inner, outer))
+    off = torch.arange(groups + 1, dtype=torch.int32, device="cuda")
+    dw = dh.dsmem_grouped_matmul_wgrad(dy.cuda(), x.cuda(), off)
+    want = dy[-1].double()[:, None] * x[-1].double()[None]
+    close(dw[-1], want, want.abs(), 1)
+    del dw
+    count = 2 ** 31 + 5
+    grad = torch.full((count,), 2.0 ** -10, dtype=torch.bfloat16, device="cuda")
+    norm = dh.dsmem_grad_clip([grad], 1.0)
+    want = 2.0 ** -10 * math.sqrt(count)
+    assert abs(float(norm) - want) <= 1e-6 * want
+    ends = torch.stack([grad[0], grad[2 ** 31 - 1], grad[-1]]).double().cpu()
+    assert ((ends - 2.0 ** -10 / want).abs() <= 2.0 ** -8 * 2.0 ** -10 / want).all()
+
+
 def test_every_operator_on_a_given_stream():
     """With `stream`, outputs belong to it and equal the current stream's."""
     g = generator(11)
