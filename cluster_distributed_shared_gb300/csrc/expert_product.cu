@@ -30,7 +30,6 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "dtypes.cuh"
 #include "experts.h"
@@ -51,7 +50,7 @@ constexpr int kShift = kGatherThreads / kShifts;  // threads of one
 constexpr int kRelayWarp = 6 + kGatherThreads / 32;
 // TMA, matrix instructions, 4 warps of output, gathering, relay.
 constexpr int kThreads = (kRelayWarp + 1) * 32;
-constexpr int kStageOut = 4096; // output staging of a warp: 32 x 32 values of up to 4 bytes
+constexpr int kStageOut = 4096;  // output staging of a warp: 32 x 32 values of 4 bytes, or 32 x 64 of 2
 constexpr int kABytes = kChannels * kDepth * 2;
 
 constexpr int kBarrierBytes = 320;
@@ -87,6 +86,7 @@ struct Maps {
   CUtensorMap a;  // weights (3-D), or dy
   CUtensorMap b;  // x
 };
+
 // Division of 31-bit values by a fixed divisor: with l = ceil(log2 d) and
 // m = floor(2^32 (2^l - d) / d) + 1, the quotient is (mulhi(m, v) + v) >> l.
 struct Divisor {
@@ -156,6 +156,7 @@ template <bool kMnMajor>
 __device__ __forceinline__ uint64_t descriptor(uint32_t addr) {
   return kDescBase | (uint64_t{kMnMajor ? 8192 >> 4 : 1} << 16) | ((addr & 0x3ffffu) >> 4);
 }
+
 __device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -196,12 +197,12 @@ __device__ __forceinline__ O ld_shared_value(uint32_t addr) {
 }
 
 struct Tile {
-  int group;     // `groups`: the rows behind the last group
+  int group;       // `groups`: the rows behind the last group
   int begin, end;  // the group's rows
-  int col0;      // first row (weight gradient: first inner column) of the tile
-  int chan0;     // first channel
-  int block0;    // this CTA's first stage of depth
-  int blocks;    // and how many it has
+  int col0;        // first row (weight gradient: first inner column) of the tile
+  int chan0;       // first channel
+  int block0;      // this CTA's first stage of depth
+  int blocks;      // and how many it has
 };
 
 template <int kKind, int kCols, int kTeam>
@@ -355,6 +356,7 @@ __device__ __forceinline__ void store_block(const TileArgs& a, const Tile& t, in
     }
   }
 }
+
 // Zeros in a warp's 32 channels of a tile without any depth: the rows behind
 // the last group, the matrices of empty groups.
 template <int kKind, int kCols>
@@ -430,7 +432,9 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
   constexpr int kFound = kDepth / (kShift / 32), kBatch = 32 / kFound;
   static_assert(kFound <= 32 && kPerWarp >= 1 && kAtOnce >= 1, "a warp looks up a stage's rows at once");
   // This shift's stages of a tile are first_of(before), and every kShifts-th.
-  const auto first_of = [&](uint32_t stages) { return static_cast<int>((shift - stages % kShifts + kShifts) % kShifts); };
+  const auto first_of = [&](uint32_t stages) {
+    return static_cast<int>((shift - stages % kShifts + kShifts) % kShifts);
+  };
   const auto batch_place = [&](const Tile& t, int first_k, int m) {
     const int l = lane % kFound;
     const int r = l / kPerWarp * kAtOnce + (tid >> 5) * kPerWarp + l % kPerWarp;
