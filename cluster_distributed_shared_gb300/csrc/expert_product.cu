@@ -229,7 +229,7 @@ struct Schedule {
     return kKind == kWeightGrad ? groups * tiles_of(0) : first[owners()];
   }
   // The j-th tile of a unit.  Tiles of the weight gradient differ in depth:
-  // with the deepest first, and every other round the other way, units differ
+  // with the deepest first, and every other turn the other way, units differ
   // by a fraction of a tile.
   __device__ __forceinline__ static int turn(int j, int unit, int units) {
     return j * units + (kKind == kWeightGrad && (j & 1) ? units - 1 - unit : unit);
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tmem_alloc<kTwo>(tmem_at, kTmemColumns);
   __syncthreads();
-  // Each warp takes 32 groups of a round of kWarps * 32: the running maximum
+  // Each warp takes 32 groups of every kWarps * 32: the running maximum
   // of their ends, then the running sum of their tiles.
   constexpr int kWarps = kThreads / 32;
   __shared__ int of_warp[2][32];

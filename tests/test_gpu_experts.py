@@ -101,6 +101,22 @@ def test_route_and_gradient(tokens, experts, k, dtype, renormalize):
     assert ((got.cpu().double() - full).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_route_with_masks_of_the_lowest_value(dtype):
+    """The type's lowest value is a number: chosen after all others, with no
+    weight beside them, and an even share where it is all there is."""
+    low = torch.finfo(dtype).min
+    logits = torch.full((3, 40), low, dtype=dtype)
+    logits[0, 7], logits[0, 31] = 1.0, 2.0
+    logits[2, :38] = -math.inf
+    ids, w = dh.dsmem_route(logits.cuda(), 3)
+    assert ids.tolist() == [[31, 7, 0], [0, 1, 2], [38, 39, -1]]
+    want = torch.tensor([[1 / (1 + math.exp(-1)), 1 / (1 + math.exp(1)), 0], [1 / 3] * 3, [0.5, 0.5, 0]])
+    assert (w.cpu() - want).abs().max() <= 2.0 ** -22
+    grad = dh.dsmem_route_backward(logits.cuda(), ids, w, torch.ones(3, 3).cuda())
+    assert torch.isfinite(grad).all() and grad.abs().max() <= 2.0 ** -20   # equal gradients cancel
+
+
 @pytest.mark.parametrize("renormalize", [True, False])
 def test_route_gradient_against_differences(renormalize):
     g = generator(3)
