@@ -258,6 +258,11 @@ cudaError_t dispatch_route(const RouteArgs& a, bool backward, cudaStream_t strea
 // needs no atomics whose order could matter (the counts of step 1 commute).
 // Bound by the latency of its steps: 4 keys 2.4 us, 131072 keys into 256
 // groups 10.4 us (16 CTAs).
+// More keys than a cluster's 16 SMs are good for (kClusterKeys) take three
+// launches over all SMs: every CTA's counts, their prefixes over the CTAs, and
+// the same kernel with these in place of the cluster's totals.  256 groups, one
+// cluster / all SMs, us: 2^18 keys 17.1 / 17.7, 2^20 55 / 23, 2^24 770 / 175,
+// 2^26 7009 / 1349 (bound by scattered 4-byte writes of the order).
 struct GroupArgs {
   const int32_t* keys;
   int64_t n;
@@ -266,6 +271,10 @@ struct GroupArgs {
   int32_t* offsets;
   int32_t* order;
   int32_t* position;
+  // Many keys: the CTAs are no cluster, and an earlier launch has left each
+  // group's size and, for each CTA, what precedes it in the group.
+  const uint32_t* sizes;   // [groups], or null
+  const uint32_t* before;  // [CTAs][groups]
 };
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
@@ -288,7 +297,7 @@ __device__ __forceinline__ void load_keys(const GroupArgs& a, int64_t i0, int64_
 
 __global__ void __launch_bounds__(1024) group_kernel(GroupArgs a) {
   extern __shared__ uint32_t smem[];  // rows [warps][groups], totals and bases [groups], scan [32]
-  const uint32_t rank = cluster_ctarank(), P = cluster_nctarank();
+  const uint32_t rank = blockIdx.x, ctas = gridDim.x, P = cluster_nctarank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t G = static_cast<uint32_t>(a.groups);
   uint32_t* total = smem + (a.shared_totals ? 0 : static_cast<size_t>(a.warps) * G);
@@ -298,7 +307,7 @@ __global__ void __launch_bounds__(1024) group_kernel(GroupArgs a) {
 
   // Each warp's run of keys, a multiple of 32 long; its first batch stays in
   // registers for both passes.
-  const int64_t parts = static_cast<int64_t>(P) * a.warps;
+  const int64_t parts = static_cast<int64_t>(ctas) * a.warps;
   const int64_t run = ((a.n + parts - 1) / parts + 31) / 32 * 32;
   int64_t begin = (static_cast<int64_t>(rank) * a.warps + warp) * run;
   int64_t end = begin + run;
@@ -338,7 +347,10 @@ __global__ void __launch_bounds__(1024) group_kernel(GroupArgs a) {
     const uint32_t g = g0 + threadIdx.x;
     uint32_t before = 0, size = 0;
     if (g < G) {
-      if (P > 1) {
+      if (a.sizes) {
+        size = a.sizes[g];
+        before = a.before[static_cast<size_t>(rank) * G + g];
+      } else if (P > 1) {
         const uint32_t addr = smem_u32(total + g);
         uint32_t c[16];
 #pragma unroll
@@ -405,12 +417,64 @@ __global__ void __launch_bounds__(1024) group_kernel(GroupArgs a) {
   }
   // Places behind the last group.
   for (int64_t p = carry + static_cast<int64_t>(rank) * blockDim.x + threadIdx.x; p < a.n;
-       p += static_cast<int64_t>(P) * blockDim.x)
+       p += static_cast<int64_t>(ctas) * blockDim.x)
     a.order[p] = -1;
   if (P > 1) cluster_wait();
 }
 
 constexpr int kGroupSmemLimit = 200 * 1024;
+constexpr int64_t kClusterKeys = int64_t{1} << 18;
+
+// The CTAs' counts of their keys, [CTAs][groups]; CTAs and their keys are
+// those of group_kernel.
+__global__ void __launch_bounds__(1024) group_count_kernel(const int32_t* keys, int64_t n, int groups,
+                                                           int64_t run, uint32_t* counts) {
+  extern __shared__ uint32_t smem[];
+  const uint32_t G = static_cast<uint32_t>(groups);
+  for (uint32_t g = threadIdx.x; g < G; g += blockDim.x) smem[g] = 0;
+  __syncthreads();
+  const int64_t begin = static_cast<int64_t>(blockIdx.x) * run;
+  const int64_t end = begin + run < n ? begin + run : n;
+  for (int64_t i0 = begin + threadIdx.x; i0 < end; i0 += 4 * blockDim.x) {
+    uint32_t key[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t i = i0 + static_cast<int64_t>(u) * blockDim.x;
+      key[u] = i < end ? static_cast<uint32_t>(keys[i]) : 0xffffffffu;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (key[u] < G) atomicAdd(smem + key[u], 1u);
+  }
+  __syncthreads();
+  for (uint32_t g = threadIdx.x; g < G; g += blockDim.x)
+    counts[static_cast<size_t>(blockIdx.x) * G + g] = smem[g];
+}
+
+// counts[c][g] -> the sum of counts[c'][g] over c' < c, and the groups' sizes.
+// A CTA has 32 groups, each of its 8 warps a run of the CTAs' rows.
+__global__ void __launch_bounds__(256) group_prefix_kernel(uint32_t* counts, int ctas, int groups,
+                                                           uint32_t* sizes) {
+  __shared__ uint32_t part[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.x * 32 + lane;
+  const int begin = ctas * warp / 8, end = ctas * (warp + 1) / 8;
+  uint32_t sum = 0;
+  if (g < groups)
+#pragma unroll 8
+    for (int c = begin; c < end; ++c) sum += counts[static_cast<size_t>(c) * groups + g];
+  part[warp][lane] = sum;
+  __syncthreads();
+  if (g >= groups) return;
+  uint32_t before = 0;
+  for (int w = 0; w < warp; ++w) before += part[w][lane];
+#pragma unroll 8
+  for (int c = begin; c < end; ++c) {
+    const uint32_t count = counts[static_cast<size_t>(c) * groups + g];
+    counts[static_cast<size_t>(c) * groups + g] = before;
+    before += count;
+  }
+  if (warp == 7) sizes[g] = before;
+}
 
 }  // namespace
 
@@ -421,14 +485,14 @@ cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t stream) {
   return dispatch_route(a, true, stream);
 }
 
-cudaError_t launch_group(const int32_t* keys, int64_t n, int num_groups, int32_t* offsets,
-                         int32_t* order, int32_t* position, const CallContext& ctx,
-                         cudaStream_t stream) {
-  GroupArgs a{keys, n, num_groups, 0, 0, 0, offsets, order, position};
+int run_group(const int32_t* keys, int64_t n, int num_groups, int32_t* offsets, int32_t* order,
+              int32_t* position, const CallContext& ctx, cudaStream_t stream) {
+  GroupArgs a{};
+  a.keys = keys, a.n = n, a.groups = num_groups;
+  a.offsets = offsets, a.order = order, a.position = position;
   while ((int64_t{1} << a.bits) < num_groups) ++a.bits;
   // Warps: as many counter rows as shared memory holds beside the totals, but
-  // no more than the keys fill with 32 each.  CTAs: one cluster, doubled
-  // while every warp still has 128 keys or more.
+  // no more than the keys fill with 32 each.
   // Where a row, the totals and the bases do not fit (17,057 groups or more),
   // one warp in one CTA keeps all in one row.
   const int64_t fit = (kGroupSmemLimit / 4 - 32) / num_groups - 2;
@@ -436,25 +500,51 @@ cudaError_t launch_group(const int32_t* keys, int64_t n, int num_groups, int32_t
   int64_t warps = (n + 31) / 32;
   if (warps > fit) warps = fit;
   a.warps = static_cast<int>(warps < 1 ? 1 : (warps > 32 ? 32 : warps));
-  int P = 1;
-  while (P < 16 && !a.shared_totals && n >= int64_t{2} * P * a.warps * 128) P *= 2;
   const size_t smem = (static_cast<size_t>(a.warps + (a.shared_totals ? 0 : 2)) * num_groups + 32) * 4;
-  static SmemLimit limit;
-  const cudaError_t e = limit.need(reinterpret_cast<const void*>(group_kernel), ctx.device,
-                                   kGroupSmemLimit, true);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(P);
-  cfg.blockDim = dim3(a.warps * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = P;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, group_kernel, a);
+
+  static SmemLimit limit, count_limit;
+  cudaError_t e = limit.need(reinterpret_cast<const void*>(group_kernel), ctx.device, kGroupSmemLimit, true);
+  if (e != cudaSuccess) return fail_with_cuda(e, "cudaFuncSetAttribute");
+  // CTAs: one cluster, doubled while every warp still has 128 keys or more,
+  // or two an SM (one where the rows take its shared memory).
+  int P = 1, ctas = 1;
+  uint32_t* scratch = nullptr;
+  if (n <= kClusterKeys || a.shared_totals) {
+    while (P < 16 && !a.shared_totals && n >= int64_t{2} * P * a.warps * 128) P *= 2;
+    ctas = P;
+  } else {
+    ctas = ctx.sm_count * (smem <= 100 * 1024 ? 2 : 1);
+    const size_t counts = static_cast<size_t>(ctas) * num_groups;
+    int rc = pool_alloc(ctx, reinterpret_cast<void**>(&scratch), (counts + num_groups) * 4, stream);
+    if (rc) return rc;
+    uint32_t* sizes = scratch + counts;
+    a.sizes = sizes, a.before = scratch;
+    // The keys of a CTA as group_kernel gives them to its warps.
+    const int64_t parts = static_cast<int64_t>(ctas) * a.warps;
+    const int64_t run = ((n + parts - 1) / parts + 31) / 32 * 32 * a.warps;
+    e = count_limit.need(reinterpret_cast<const void*>(group_count_kernel), ctx.device, num_groups * 4);
+    if (e == cudaSuccess) {
+      group_count_kernel<<<ctas, 1024, num_groups * 4, stream>>>(keys, n, num_groups, run, scratch);
+      group_prefix_kernel<<<(num_groups + 31) / 32, 256, 0, stream>>>(scratch, ctas, num_groups, sizes);
+      e = cudaGetLastError();
+    }
+  }
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(a.warps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = P;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, group_kernel, a);
+  }
+  const int rc = scratch ? pool_free(scratch, stream) : DSMEM_HIST_OK;
+  return e == cudaSuccess ? rc : fail_with_cuda(e, "group launch");
 }
 
 }  // namespace dsmh

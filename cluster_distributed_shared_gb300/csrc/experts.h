@@ -80,9 +80,8 @@ struct RouteArgs {
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
 cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t stream);
 
-cudaError_t launch_group(const int32_t* keys, int64_t n, int num_groups, int32_t* offsets,
-                         int32_t* order, int32_t* position, const CallContext& ctx,
-                         cudaStream_t stream);
+int run_group(const int32_t* keys, int64_t n, int num_groups, int32_t* offsets, int32_t* order,
+              int32_t* position, const CallContext& ctx, cudaStream_t stream);
 
 enum ProductKind { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 struct ProductArgs {

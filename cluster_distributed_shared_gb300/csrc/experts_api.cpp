@@ -89,8 +89,8 @@ int run_route_backward(const void* logits, int32_t dtype, int64_t tokens, int32_
   return finish(launch_route_backward(a, stream), "route_backward launch");
 }
 
-int run_group(const int32_t* keys, int64_t n, int32_t num_groups, int32_t* offsets, int32_t* order,
-              int32_t* position, cudaStream_t stream) {
+int group(const int32_t* keys, int64_t n, int32_t num_groups, int32_t* offsets, int32_t* order,
+          int32_t* position, cudaStream_t stream) {
   DSMH_REQUIRE(n >= 0 && n <= kMaxRows, "n must be in [0, 2^31) (got %lld)", static_cast<long long>(n));
   DSMH_REQUIRE(num_groups >= 1 && num_groups <= DSMEM_GROUP_MAX_GROUPS,
                "num_groups must be in [1, %d] (got %d)", DSMEM_GROUP_MAX_GROUPS, num_groups);
@@ -103,7 +103,7 @@ int run_group(const int32_t* keys, int64_t n, int32_t num_groups, int32_t* offse
   CallContext ctx;
   int rc = begin_call(stream, &ctx);
   if (rc) return rc;
-  return finish(launch_group(keys, n, num_groups, offsets, order, position, ctx, stream), "group launch");
+  return run_group(keys, n, num_groups, offsets, order, position, ctx, stream);
 }
 
 int check_product(int64_t x_rows, int32_t groups, int32_t fan, int64_t n, int32_t outer, int32_t inner,
@@ -286,7 +286,7 @@ int dsmem_route_backward(const void* logits, int32_t dtype, int64_t tokens, int3
 int dsmem_group(const int32_t* keys, int64_t n, int32_t num_groups, int32_t* offsets, int32_t* order,
                 int32_t* position, cudaStream_t stream) {
   return dsmh::guarded([&] {
-    return dsmh::run_group(keys, n, num_groups, offsets, order, position, stream);
+    return dsmh::group(keys, n, num_groups, offsets, order, position, stream);
   });
 }
 

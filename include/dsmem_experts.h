@@ -82,7 +82,8 @@ DSMEM_HIST_API int dsmem_route_backward(const void* logits, int32_t dtype, int64
  *   position[i]  = offsets[keys[i]] + number of i' < i with the same key; -1 if dropped
  *   order[p]     = the i with position[i] == p;   -1 for p >= offsets[num_groups]
  *   num_groups  1 .. 32768
- *   offsets int32 [num_groups + 1], order and position int32 [n] */
+ *   offsets int32 [num_groups + 1], order and position int32 [n]
+ * Takes scratch from the pool for more than 2^18 keys. */
 DSMEM_HIST_API int dsmem_group(const int32_t* keys, int64_t n, int32_t num_groups, int32_t* offsets,
                                int32_t* order, int32_t* position, cudaStream_t stream);
 

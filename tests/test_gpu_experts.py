@@ -159,7 +159,8 @@ def group_exact(keys, groups):
 
 @pytest.mark.parametrize("n,groups", [(0, 5), (1, 1), (1, 7), (31, 3), (32, 32), (33, 64), (1000, 257),
                                       (4097, 8), (70001, 60), (131072, 256), (300000, 1024),
-                                      (50000, 5000), (40000, 32768)])
+                                      (50000, 5000), (40000, 32768), (262145, 77), (1000003, 256),
+                                      (700000, 5000), (300001, 20000)])
 @pytest.mark.parametrize("kind", ["uniform", "skewed", "one", "dropped"])
 def test_group(n, groups, kind):
     g = generator(n + groups)
