@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <mutex>
 
 #include <cuda_runtime_api.h>
 
@@ -57,6 +58,8 @@ class SmemLimit {
   cudaError_t need(const void* kernel, int device, int bytes, bool wide_clusters = false) {
     std::atomic<int>& set = set_[device];
     if (set.load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+    std::lock_guard<std::mutex> guard(mutex_);  // never lowers another thread's limit
+    if (set.load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && wide_clusters)
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -66,6 +69,7 @@ class SmemLimit {
 
  private:
   std::atomic<int> set_[kMaxDevices] = {};
+  std::mutex mutex_;
 };
 
 struct RouteArgs {

@@ -24,8 +24,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kCtasPerSm = 4;
-constexpr int kVectors = 4;                              // 16-byte vectors of one thread in a chunk
-constexpr int kChunkBytes = kThreads * kVectors * 16;    // 16 KB
+constexpr int kVectors = 4;                            // 16-byte vectors of one thread in a chunk
+constexpr int kChunkBytes = kThreads * kVectors * 16;  // 16 KB
 
 struct Tensor {
   const void* grad;
@@ -65,7 +65,7 @@ struct Slice {
   Vector16<T> p[kWide ? kPieces : 1];
   T single[kWide ? 1 : kPieces][2];
 
-  // The i-th element of piece k is element first(k) + i * step() of the tensor.
+  // The i-th element of piece k is element first(base, k) + i * kStep of the tensor.
   __device__ __forceinline__ static int64_t first(int64_t base, int k) {
     return kWide ? base + (k * kThreads + static_cast<int>(threadIdx.x)) * kEach
                  : base + k * 2 * kThreads + static_cast<int>(threadIdx.x);
