@@ -2,14 +2,17 @@
 //
 // Two passes over the gradients: squares, then scaling.  Tensors are cut into
 // chunks of 16 KB laid end to end, and every CTA takes an equal run of them in
-// each pass.  The second pass goes through its run backwards, so that it
-// begins with what the first left in L2, and stores past the cache.  The table
-// of tensors travels as a kernel parameter: nothing is copied to the device
-// first and nothing is kept between calls.
+// the first pass, so that the order of the sums depends on the sizes alone.
+// The second pass goes through the runs backwards, so that it begins with what
+// the first left in L2, and stores past the cache; a CTA scales the end of its
+// own run and then pieces of any, as SMs differ in how fast they reach memory.
+// The table of tensors travels as a kernel parameter: nothing is copied to the
+// device first and nothing is kept between calls.
 //
-// Bound by memory: 1 GiB of bf16 takes 511 us, 6.3 TB/s over its two reads and
-// one write (four CTAs an SM with four 16-byte vectors a thread; six CTAs: 541,
-// eight vectors: 533).
+// Bound by memory: 1 GiB of bf16 takes 488 us, 6.6 TB/s over its two reads and
+// one write (four CTAs an SM with four 16-byte vectors a thread; before the
+// second pass shared its pieces 511, and with that six CTAs 541, eight vectors
+// 533).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -248,17 +251,17 @@ struct alignas(16) Partial {
   Sum sum;
 };
 
-// This CTA's run of a table's chunks.
-__device__ __forceinline__ void my_chunks(uint32_t chunks, uint32_t* begin, uint32_t* end) {
-  *begin = static_cast<uint32_t>(static_cast<uint64_t>(chunks) * blockIdx.x / gridDim.x);
-  *end = static_cast<uint32_t>(static_cast<uint64_t>(chunks) * (blockIdx.x + 1) / gridDim.x);
+// The run of a table's chunks that belongs to a CTA.
+__device__ __forceinline__ void run_of(uint32_t cta, uint32_t chunks, uint32_t* begin, uint32_t* end) {
+  *begin = static_cast<uint32_t>(static_cast<uint64_t>(chunks) * cta / gridDim.x);
+  *end = static_cast<uint32_t>(static_cast<uint64_t>(chunks) * (cta + 1) / gridDim.x);
 }
 
 template <int kTensors>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
-    norm_kernel(const __grid_constant__ Table<kTensors> tab, Partial* partial) {
+    norm_kernel(const __grid_constant__ Table<kTensors> tab, Partial* partial, uint32_t* taken) {
   uint32_t c, end;
-  my_chunks(tab.chunks, &c, &end);
+  run_of(blockIdx.x, tab.chunks, &c, &end);
   Squares mine;
   int i = c < end ? find_tensor(tab, c) : 0;
   for (; c < end; ++c) {
@@ -277,13 +280,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     p.sum.hi = ordinary ? static_cast<float>(sum) : NAN;
     p.sum.lo = ordinary ? static_cast<float>(sum - p.sum.hi) : 0.0f;
     partial[blockIdx.x] = p;
+    if (blockIdx.x == 0) *taken = 0;  // for the scaling
   }
 }
 
 template <int kTensors>
+__device__ __forceinline__ void scale_chunks(const Table<kTensors>& tab, uint32_t begin, uint32_t c,
+                                             float scale) {
+  int i = begin < c ? find_tensor(tab, c - 1) : 0;
+  while (c-- > begin) {
+    while (c < tab.first_chunk[i]) --i;
+    const Tensor& t = tab.t[i];
+    const int64_t k = c - tab.first_chunk[i];
+    if (t.dtype == DSMEM_F32) chunk_scale<float>(t, k, scale);
+    else if (t.dtype == DSMEM_F16) chunk_scale<__half>(t, k, scale);
+    else chunk_scale<__nv_bfloat16>(t, k, scale);
+  }
+}
+
+// Of runs of kShared chunks and more a CTA scales the last quarter of its own,
+// and pieces of kPiece chunks as `taken` hands them out: the first of every
+// run, the second of every run and so on, from the end.  1 GiB of bf16, us: own
+// quarter 488, half 490, none 490 (pieces of 8 chunks: 490, 492, 490), without
+// pieces 505.  Shorter runs are mostly in L2 and gain nothing; without pieces /
+// with: 128 MiB (13 chunks) 69.7 / 74.4, 256 MiB (26) 134.1 / 135.7, 384 MiB
+// (40) 202.2 / 200.4, 512 MiB (53) 262.6 / 256.3.
+constexpr uint32_t kShared = 32, kPiece = 4;
+
+template <int kTensors>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     scale_kernel(const __grid_constant__ Table<kTensors> tab, const Partial* partial, int partials,
-                 float max_norm, float* norm) {
+                 uint32_t* taken, float max_norm, float* norm) {
   // Every CTA adds the partial sums, thread 0 turns them into the factor.
   __shared__ float factor;
   Squares mine;
@@ -301,16 +328,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
   __syncthreads();
   const float scale = factor;
-  uint32_t begin, c;
-  my_chunks(tab.chunks, &begin, &c);
-  int i = begin < c ? find_tensor(tab, c - 1) : 0;
-  while (c-- > begin) {
-    while (c < tab.first_chunk[i]) --i;
-    const Tensor& t = tab.t[i];
-    const int64_t k = c - tab.first_chunk[i];
-    if (t.dtype == DSMEM_F32) chunk_scale<float>(t, k, scale);
-    else if (t.dtype == DSMEM_F16) chunk_scale<__half>(t, k, scale);
-    else chunk_scale<__nv_bfloat16>(t, k, scale);
+  uint32_t begin, end;
+  run_of(blockIdx.x, tab.chunks, &begin, &end);
+  const uint32_t shortest = tab.chunks / gridDim.x;  // the others have one more
+  if (shortest < kShared) {
+    scale_chunks(tab, begin, end, scale);
+    return;
+  }
+  const uint32_t own = shortest / 4, pieces = (shortest + 1 - own + kPiece - 1) / kPiece;
+  scale_chunks(tab, end - own, end, scale);
+  __shared__ uint32_t next;
+  for (;;) {
+    __syncthreads();
+    if (threadIdx.x == 0) next = atomicAdd(taken, 1u);
+    __syncthreads();
+    const uint32_t piece = next / gridDim.x;
+    if (piece >= pieces) return;
+    run_of(next - piece * gridDim.x, tab.chunks, &begin, &end);
+    const uint32_t length = end - begin, from = own + piece * kPiece;
+    if (from < length) scale_chunks(tab, end - min(from + kPiece, length), end - from, scale);
   }
 }
 
@@ -364,15 +400,16 @@ int run(const dsmem_grad_t* grads, int32_t num, float max_norm, float* norm, con
   for (Cursor at; at.tensor < num || launches == 0; ++launches) fill(&tab, grads, num, &at);
   Partial* partial = nullptr;
   int rc = pool_alloc(ctx, reinterpret_cast<void**>(&partial),
-                      sizeof(Partial) * static_cast<size_t>(most) * launches, stream);
+                      (sizeof(Partial) * most + sizeof(uint32_t)) * launches, stream);
   if (rc) return rc;
+  uint32_t* const taken = reinterpret_cast<uint32_t*>(partial + static_cast<size_t>(most) * launches);
   cudaError_t e = cudaSuccess;
   int partials = 0;
   Cursor at;
   for (int l = 0; l < launches && e == cudaSuccess; ++l) {
     if (launches > 1) fill(&tab, grads, num, &at);
     const uint32_t grid = std::min(std::max(tab.chunks, 1u), most);
-    norm_kernel<kTensors><<<grid, kThreads, 0, stream>>>(tab, partial + partials);
+    norm_kernel<kTensors><<<grid, kThreads, 0, stream>>>(tab, partial + partials, taken + l);
     partials += static_cast<int>(grid);
     e = cudaGetLastError();
   }
@@ -380,7 +417,7 @@ int run(const dsmem_grad_t* grads, int32_t num, float max_norm, float* norm, con
   for (int l = 0; l < launches && e == cudaSuccess; ++l) {
     if (launches > 1) fill(&tab, grads, num, &at);
     const uint32_t grid = std::min(std::max(tab.chunks, 1u), most);
-    scale_kernel<kTensors><<<grid, kThreads, 0, stream>>>(tab, partial, partials, max_norm,
+    scale_kernel<kTensors><<<grid, kThreads, 0, stream>>>(tab, partial, partials, taken + l, max_norm,
                                                           l == 0 ? norm : nullptr);
     e = cudaGetLastError();
   }

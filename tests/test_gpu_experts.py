@@ -454,6 +454,31 @@ def test_clip_of_views_and_extremes():
     assert float(dh.dsmem_grad_clip([], 1.0)) == 0.0
 
 
+# Runs long enough that CTAs share their pieces, in lists of one table and of
+# two (the second with short runs), beside sizes that end inside a chunk.
+@pytest.mark.parametrize("count,size", [(3, 83_000_011), (1300, 300_007)])
+def test_clip_of_long_runs(count, size):
+    g = torch.Generator(device="cuda").manual_seed(count)
+    flat = torch.randn(count * (size + 5), generator=g, device="cuda", dtype=torch.bfloat16)
+    grads = [flat[i * (size + 5):i * (size + 5) + size] for i in range(count)]
+    kept = flat.clone()
+    out = torch.full_like(flat, math.nan)
+    clipped = [out[i * (size + 5):i * (size + 5) + size] for i in range(count)]
+    total = math.sqrt(math.fsum(float((t.double() ** 2).sum()) for t in grads))
+    norm = dh.dsmem_grad_clip(grads, 2.0, out=clipped)
+    assert abs(float(norm) - total) <= 35 * 2.0 ** -24 * total
+    assert torch.equal(flat, kept)
+    assert torch.equal(dh.dsmem_grad_clip(grads, 2.0), norm)          # in place
+    for i in range(count):
+        want = kept[i * (size + 5):i * (size + 5) + size].double() * (2.0 / (total + 1e-6))
+        # the factor: 35 steps of 2^-24 of the norm and one of its own; one of the product, and bf16
+        assert ((clipped[i].double() - want).abs() <= want.abs() * (2.0 ** -8 + 37 * 2.0 ** -24)).all()
+        assert torch.equal(clipped[i], grads[i])
+    gaps = out.view(count, size + 5)[:, size:]
+    assert gaps.isnan().all() and torch.equal(flat.view(count, size + 5)[:, size:],
+                                              kept.view(count, size + 5)[:, size:])
+
+
 # ---------------------------------------------------------------- refusals
 
 def test_refusals():
