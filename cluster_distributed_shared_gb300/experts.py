@@ -20,6 +20,7 @@ import ctypes
 import operator
 
 F32, F16, BF16 = 0, 1, 2
+_MOST = 2 ** 31 - 1   # of the C entries' 32-bit arguments; ctypes would wrap what lies beyond
 _DTYPE = operator.attrgetter("dtype")
 
 _p, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
@@ -90,6 +91,12 @@ def _like(name, t, dims, code, index):
         raise ValueError(f"{name} must be on device {index}")
 
 
+def _out_of_range(**sizes):
+    """The error for sizes of which one does not fit a 32-bit argument."""
+    name, value = next((n, v) for n, v in sizes.items() if not 0 <= v <= _MOST)
+    return ValueError(f"{name} must be in [0, 2^31) (got {value})")
+
+
 def _row_stride(t, columns):
     """Elements between rows; rows of a single one have no stride of their own."""
     return columns if t.is_contiguous() or t.shape[0] <= 1 else t.stride(0)
@@ -150,6 +157,8 @@ def dsmem_route(logits, top_k: int, renormalize: bool = True, stream=None):
     if s is None:
         return _elsewhere(dsmem_route, logits.device, stream, logits, top_k, renormalize)
     tokens, experts = logits.shape
+    if experts > _MOST or not 0 <= top_k <= _MOST:
+        raise _out_of_range(experts=experts, top_k=top_k)
     shape, device = (tokens, top_k), logits.device
     ids = _lib.empty(shape, dtype=_lib.int32, device=device)
     weights = _lib.empty(shape, dtype=_lib.float32, device=device)
@@ -170,6 +179,8 @@ def dsmem_route_backward(logits, ids, weights, grad_weights, renormalize: bool =
     top_k = ids.shape[1]
     _weights("weights", weights, ids.shape, index)
     _weights("grad_weights", grad_weights, ids.shape, index)
+    if experts > _MOST or top_k > _MOST:
+        raise _out_of_range(experts=experts, top_k=top_k)
     s = _current(index, stream)
     if s is None:
         return _elsewhere(dsmem_route_backward, logits.device, stream, logits, ids, weights,
@@ -190,6 +201,8 @@ def dsmem_group(keys, num_groups: int, stream=None):
     s = _current(_int_tensor("keys", keys), stream)
     if s is None:
         return _elsewhere(dsmem_group, keys.device, stream, keys, num_groups)
+    if not -_MOST <= num_groups <= _MOST:
+        raise _out_of_range(num_groups=num_groups)
     n, empty, int32, device = keys.numel(), _lib.empty, _lib.int32, keys.device
     offsets = empty(max(int(num_groups), 0) + 1, dtype=int32, device=device)
     order, position = empty(n, dtype=int32, device=device), empty(n, dtype=int32, device=device)
@@ -220,6 +233,8 @@ def dsmem_grouped_matmul(x, weight, offsets, order=None, fan: int = 1, transpose
     _like("weight", weight, 3, code, index)
     groups, outer, inner = weight.shape
     rows, columns = x.shape
+    if max(groups, outer, inner) > _MOST or not -_MOST <= fan <= _MOST:
+        raise _out_of_range(groups=groups, outer=outer, inner=inner, fan=fan)
     depth, cols = (outer, inner) if transpose else (inner, outer)
     if columns != depth:
         raise ValueError(f"x must have {depth} columns (got {columns})")
@@ -255,6 +270,8 @@ def dsmem_grouped_matmul_wgrad(dy, x, offsets, order=None, fan: int = 1, out_dty
     dtype, out_code = _out_type(code, dy.dtype, out_dtype)
     _int_tensor("offsets", offsets, None, index)
     (n, outer), (rows, inner), groups = dy.shape, x.shape, offsets.numel() - 1
+    if max(groups, outer, inner) > _MOST or not -_MOST <= fan <= _MOST:
+        raise _out_of_range(groups=groups, outer=outer, inner=inner, fan=fan)
     if order is not None:
         _int_tensor("order", order, n, index)
     elif rows != n:
@@ -284,6 +301,8 @@ def dsmem_combine(z, position, weights=None, stream=None):
     if s is None:
         return _elsewhere(dsmem_combine, z.device, stream, z, position, weights)
     (tokens, top_k), (rows, width) = position.shape, z.shape
+    if max(top_k, width) > _MOST:
+        raise _out_of_range(top_k=top_k, width=width)
     out = _lib.empty((tokens, width), dtype=z.dtype, device=z.device)
     _check(_lib.dsmem_combine(
         z.data_ptr(), rows, _row_stride(z, width), position.data_ptr(),
@@ -302,6 +321,8 @@ def dsmem_combine_backward(dy, z, position, order, weights, stream=None):
         raise ValueError("position must be [tokens, top_k]")
     _weights("weights", weights, position.shape, index)
     (tokens, top_k), (rows, width) = position.shape, z.shape
+    if max(top_k, width) > _MOST:
+        raise _out_of_range(top_k=top_k, width=width)
     if dy.shape != (tokens, width):
         raise ValueError(f"dy must be [{tokens}, {width}]")
     if rows != tokens * top_k:

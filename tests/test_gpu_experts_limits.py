@@ -1,0 +1,56 @@
+"""The expert-layer operators at the ends of their ranges: sizes that the C
+entries' 32-bit arguments cannot hold, and the widest rows they can."""
+from __future__ import annotations
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import cluster_distributed_shared_gb300 as dh  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda_ready():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
+def test_sizes_past_32_bits_are_refused():
+    """None of them is taken modulo 2^32."""
+    past = 2 ** 32
+    i = torch.zeros(4, dtype=torch.int32, device="cuda")
+    f = torch.zeros(1, 8, device="cuda")
+    h = torch.zeros(4, 16, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(2, 8, 16, dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+
+    def wide(dtype=torch.bfloat16):               # no rows, so no memory
+        return torch.empty(0, past + 16, dtype=dtype, device="cuda")
+
+    no = torch.empty(0, 2, dtype=torch.int32, device="cuda")
+    real = torch.empty(0, 2, device="cuda")
+    for call in [
+        lambda: dh.dsmem_route(f, past + 2),
+        lambda: dh.dsmem_route(f, 2 - past),
+        lambda: dh.dsmem_route(f, -1),
+        lambda: dh.dsmem_route(wide(torch.float32), 2),
+        lambda: dh.dsmem_route_backward(wide(torch.float32), no, real, real),
+        lambda: dh.dsmem_group(i, past + 4),
+        lambda: dh.dsmem_group(i, 4 - past),
+        lambda: dh.dsmem_grouped_matmul(h, w, off, order=i, fan=past + 1),
+        lambda: dh.dsmem_grouped_matmul(h, w, off, order=i, fan=1 - past),
+        lambda: dh.dsmem_grouped_matmul_wgrad(h, h, off, order=i, fan=past + 1),
+        lambda: dh.dsmem_grouped_matmul_wgrad(wide(), h[:0], off),
+        lambda: dh.dsmem_grouped_matmul_wgrad(h[:0], wide(), off),
+        lambda: dh.dsmem_combine(wide(), no),
+        lambda: dh.dsmem_combine_backward(wide(), wide(), no, i[:0], real),
+    ]:
+        with pytest.raises(ValueError):
+            call()
