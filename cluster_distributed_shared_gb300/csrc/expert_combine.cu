@@ -2,6 +2,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "dtypes.cuh"
 #include "experts.h"
 
@@ -9,6 +11,7 @@ namespace dsmh {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMostPieces = 65535;  // a grid's second extent; wider rows take more launches
 
 // What one thread handles of a row at a time: 16 bytes, or (kWide false, where
 // addresses allow none) two elements kThreads apart.  Rows of z, the outputs
@@ -68,7 +71,7 @@ template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads, kCtas) combine_kernel(CombineArgs a) {
   using P = Piece<T, kWide>;
   const int64_t token = blockIdx.x;
-  const int col = P::column(blockIdx.y * kThreads * P::kEach), left = a.width - col;
+  const int col = P::column((a.first_piece + blockIdx.y) * kThreads * P::kEach), left = a.width - col;
   if (left <= 0) return;
   const T* z = static_cast<const T*>(a.z) + col;
   float2 acc[P::kPairs];
@@ -182,12 +185,19 @@ bool wide(const void* p, int64_t stride, int size) {
 template <typename T, bool kWide>
 cudaError_t launch(const CombineArgs& a, bool backward, cudaStream_t stream) {
   const unsigned tokens = static_cast<unsigned>(a.tokens);
-  const int columns = kThreads * Piece<T, kWide>::kEach;
-  if (backward)
+  if (backward) {
     combine_backward_kernel<T, kWide><<<tokens, kThreads, 0, stream>>>(a);
-  else
-    combine_kernel<T, kWide><<<dim3(tokens, (a.width + columns - 1) / columns), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+    return cudaGetLastError();
+  }
+  const int columns = kThreads * Piece<T, kWide>::kEach, pieces = (a.width + columns - 1) / columns;
+  cudaError_t e = cudaSuccess;
+  CombineArgs part = a;
+  for (; part.first_piece < pieces && e == cudaSuccess; part.first_piece += kMostPieces) {
+    const unsigned here = static_cast<unsigned>(std::min(pieces - part.first_piece, kMostPieces));
+    combine_kernel<T, kWide><<<dim3(tokens, here), kThreads, 0, stream>>>(part);
+    e = cudaGetLastError();
+  }
+  return e;
 }
 
 // 16 bytes at a time where every base and row allows it.

@@ -116,6 +116,7 @@ struct CombineArgs {
   const float* weights;  // may be null (forward)
   int64_t tokens;
   int top_k, width, dtype;
+  int first_piece;  // forward: the launch's first kThreads pieces of a row
   void* out;  // forward: [tokens, width]; backward: dz
   float* dweights;
 };

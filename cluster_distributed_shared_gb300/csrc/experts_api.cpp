@@ -189,6 +189,8 @@ int check_combine(int64_t tokens, int32_t top_k, int32_t width, int32_t dtype) {
   DSMH_REQUIRE(known_dtype(dtype), "dtype must be DSMEM_F32, DSMEM_F16 or DSMEM_BF16 (got %d)", dtype);
   DSMH_REQUIRE(tokens >= 0 && top_k >= 1 && width >= 1 && tokens <= kMaxRows / top_k,
                "tokens must be >= 0, top_k and width >= 1, and tokens * top_k < 2^31");
+  // Columns step past a row's end by less than the 2048 that a CTA takes at once.
+  DSMH_REQUIRE(width <= kMaxRows - 2048, "width must be < 2^31 - 2048 (got %d)", width);
   return DSMEM_HIST_OK;
 }
 

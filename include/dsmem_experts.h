@@ -127,7 +127,8 @@ DSMEM_HIST_API int dsmem_grouped_matmul_wgrad(const void* dy, int64_t dy_stride,
  * others (dropped) are not read, and a token without any is 0.
  *   weights  float [tokens, top_k], or NULL for 1
  *   dtype    of z and out: DSMEM_F32, DSMEM_F16 or DSMEM_BF16
- *   z        [z_rows, width], z_stride elements between rows; out contiguous */
+ *   z        [z_rows, width], z_stride elements between rows; out contiguous
+ *   width    1 .. 2^31 - 2049;  tokens * top_k < 2^31 */
 DSMEM_HIST_API int dsmem_combine(const void* z, int64_t z_rows, int64_t z_stride,
                                  const int32_t* position, const float* weights, int64_t tokens,
                                  int32_t top_k, int32_t width, int32_t dtype, void* out,

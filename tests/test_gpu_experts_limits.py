@@ -54,3 +54,18 @@ def test_sizes_past_32_bits_are_refused():
     ]:
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("width", [65535 * 512 + 515, 65535 * 2048 + 2056])
+def test_combine_of_rows_wider_than_one_grid(width):
+    """More pieces of a row than a grid's second extent, element by element
+    (an odd width) and in 16-byte vectors.  Products by 0.5 and the sums are exact."""
+    g = torch.Generator(device="cuda").manual_seed(width)
+    z = torch.randn(1, width, generator=g, device="cuda", dtype=torch.bfloat16)
+    position = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    half = torch.full((1, 1), 0.5, device="cuda")
+    assert torch.equal(dh.dsmem_combine(z, position, half), z * 0.5)
+    ones = torch.zeros_like(z)
+    ones[:, ::1024] = 1.0
+    dz, dw = dh.dsmem_combine_backward(ones, ones, position, position.view(1), half)
+    assert torch.equal(dz, ones * 0.5) and float(dw) == float(ones.sum(dtype=torch.float64))
