@@ -487,7 +487,7 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
       const uint32_t sa = base + stage * kStage, sb = sa + kABytes;
       if (!kBMn) {
         const int c = tid & 7, col = (t.block0 + k) * kDepth + c * 8;
-        const int left = max(0, min(16, (a.depth - col) * 2));
+        const int left = max(0, min(8, a.depth - col)) * 2;
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
           const int line = r * kLines + tid / 8;
@@ -501,7 +501,7 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
         const bool ragged = p0 + kDepth > t.end;
         if (a.order || ragged) {
           const int c = tid % kPieces, col = col0 + c * 8;
-          const int left = max(0, min(16, (a.width - col) * 2));
+          const int left = max(0, min(8, a.width - col)) * 2;
 #pragma unroll
           for (int r = 0; r < kDepth / kAtOnce; ++r) {
             const int line = r * kAtOnce + tid / kPieces;
@@ -513,7 +513,7 @@ __device__ __forceinline__ void gather_rows(const TileArgs& a, Schedule<kKind, k
         }
         if (ragged) {
           const int c = tid & 15, col = chan0 + c * 8;
-          const int left = max(0, min(16, (a.channels - col) * 2));
+          const int left = max(0, min(8, a.channels - col)) * 2;
 #pragma unroll
           for (int r = 0; r < kDepth * 16 / kShift; ++r) {
             const int line = r * (kShift / 16) + tid / 16;

@@ -116,7 +116,9 @@ int check_product(int64_t x_rows, int32_t groups, int32_t fan, int64_t n, int32_
                DSMEM_PRODUCT_MAX_GROUPS, groups);
   DSMH_REQUIRE(n >= 0 && n <= kMaxRows - 512 && x_rows >= 0 && x_rows <= kMaxRows - 512,
                "n and x_rows must be in [0, 2^31 - 512)");
-  DSMH_REQUIRE(outer >= 1 && inner >= 1, "outer and inner must be >= 1 (got %d and %d)", outer, inner);
+  // Tiles end at most 256 past these extents, in 32 bits.
+  DSMH_REQUIRE(outer >= 1 && inner >= 1 && outer <= kMaxRows - 512 && inner <= kMaxRows - 512,
+               "outer and inner must be in [1, 2^31 - 512) (got %d and %d)", outer, inner);
   DSMH_REQUIRE(fan >= 1, "fan must be >= 1 (got %d)", fan);
   return DSMEM_HIST_OK;
 }

@@ -99,7 +99,7 @@ DSMEM_HIST_API int dsmem_group(const int32_t* keys, int64_t n, int32_t num_group
  *   out_dtype   `dtype` or DSMEM_F32
  *   *_stride    elements between rows (weight_group_stride: between groups);
  *               rows themselves are contiguous, and out's rows too
- *   groups      1 .. 2048;  x_rows, n < 2^31 - 512
+ *   groups      1 .. 2048;  x_rows, n, outer, inner < 2^31 - 512
  * Any sizes, strides and alignments are right.  Sources whose base, row
  * stride and group stride are multiples of 16 bytes are read in place; others
  * are first laid out so in pool scratch (one more pass over them). */

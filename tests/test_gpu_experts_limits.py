@@ -69,3 +69,22 @@ def test_combine_of_rows_wider_than_one_grid(width):
     ones[:, ::1024] = 1.0
     dz, dw = dh.dsmem_combine_backward(ones, ones, position, position.view(1), half)
     assert torch.equal(dz, ones * 0.5) and float(dw) == float(ones.sum(dtype=torch.float64))
+
+
+def test_products_of_rows_longer_than_2_to_30():
+    """Gathered rows of more than 2^30 elements: all of a row is read, its
+    first elements and its last.  The products and sums are exact."""
+    long = 2 ** 30 + 72
+    x = torch.zeros(1, long, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(1, 1, long, dtype=torch.bfloat16, device="cuda")
+    x[0, :64], x[0, -8:] = 1.0, 2.0
+    w[0, 0, :64], w[0, 0, -8:] = 0.5, 1.0
+    off = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    order = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = dh.dsmem_grouped_matmul(x, w, off, order=order, out_dtype=torch.float32)
+    assert y.item() == 64 * 0.5 + 8 * 2.0
+    dy = torch.full((1, 1), 2.0, dtype=torch.bfloat16, device="cuda")
+    dw = dh.dsmem_grouped_matmul_wgrad(dy, x, off, order=order)
+    assert torch.equal(dw.view(-1), x.view(-1) * 2.0)
+    dw = dh.dsmem_grouped_matmul_wgrad(x, dy, off, order=order)
+    assert torch.equal(dw.view(-1), x.view(-1) * 2.0)
