@@ -179,8 +179,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
     }
     all = warp_sum(all);
     const float scale = all > 0.0f ? -s / all : 0.0f;
+    // Masked logits keep their 0 where s is no finite number.
 #pragma unroll
-    for (int r = 0; r < R; ++r) grad[r] *= scale;
+    for (int r = 0; r < R; ++r) grad[r] = v[r] > -INFINITY ? grad[r] * scale : 0.0f;
   }
   const int first = lane * R;
   for (int j = 0; j < a.top_k; ++j) {
