@@ -31,6 +31,7 @@
 
 #include <algorithm>
 
+#include "bounded_wait.h"
 #include "dtypes.cuh"
 #include "experts.h"
 #include "ptx.cuh"
@@ -133,11 +134,9 @@ __device__ __forceinline__ uint32_t flag_set(uint32_t addr) {
 // another wait of this CTA has given up.
 __device__ __noinline__ bool wait_slow(uint32_t mbar, uint32_t parity, uint32_t gave_up, long long limit,
                                        uint32_t* status) {
-  const long long deadline = clock64() + limit;
-  do {
-    if (mbar_try_wait(mbar, parity)) return true;
-    if (flag_set(gave_up)) return false;
-  } while (clock64() < deadline);
+  const Waited how = bounded_wait([&] { return mbar_try_wait(mbar, parity); },
+                                  [&] { return flag_set(gave_up) != 0u; }, [] { return clock64(); }, limit);
+  if (how != Waited::kGaveUp) return how == Waited::kArrived;
   asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(gave_up), "r"(1u) : "memory");
   atomicOr(&g_product_status, kStatusProduct);
   if (status) *reinterpret_cast<volatile uint32_t*>(status) = kStatusProduct;

@@ -1,0 +1,27 @@
+"""Host-side pieces of the expert-layer kernels, compiled and driven on the CPU."""
+from __future__ import annotations
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def check(name, tmp_path):
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no g++")
+    exe = str(tmp_path / name)
+    subprocess.run([gxx, "-std=c++17", "-O2", "-Wall", "-Wextra", "-Werror",
+                    "-I", os.path.join(ROOT, "cluster_distributed_shared_gb300", "csrc"),
+                    os.path.join(ROOT, "tests", name + ".cpp"), "-o", exe], check=True)
+    out = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert out.returncode == 0, out.stdout + out.stderr
+    assert out.stdout.strip() == "ok"
+
+
+def test_a_bounded_wait_looks_once_more_before_it_gives_up(tmp_path):
+    check("bounded_wait_check", tmp_path)
