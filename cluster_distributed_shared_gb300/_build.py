@@ -19,7 +19,8 @@ SOURCES = ["cluster_hist.cu", "cluster_ship.cu", "static_scratch.cu", "microbenc
            "api.cpp", "experts_api.cpp", "expert_route.cu", "expert_product.cu", "expert_combine.cu",
            "grad_clip.cu"]
 HEADERS = [os.path.join(CSRC, name) for name in ("internal.h", "ptx.cuh", "helper_split.h", "experts.h",
-                                                 "dtypes.cuh", "tcgen.cuh", "bounded_wait.h")] + \
+                                                 "dtypes.cuh", "tcgen.cuh", "bounded_wait.h",
+                                                 "launch_rules.h")] + \
           [os.path.join(INCLUDE, name) for name in ("dsmem_hist.h", "dsmem_experts.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

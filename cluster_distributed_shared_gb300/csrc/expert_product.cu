@@ -30,10 +30,12 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "bounded_wait.h"
 #include "dtypes.cuh"
 #include "experts.h"
+#include "launch_rules.h"
 #include "ptx.cuh"
 #include "tcgen.cuh"
 
@@ -1072,6 +1074,20 @@ int64_t tile_bound(const ProductArgs& p, int cols, int height) {
   return across * ((channels + height - 1) / height);
 }
 
+cudaLaunchAttribute cluster_of(int ctas) {
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = static_cast<unsigned>(ctas);
+  a.val.clusterDim.y = a.val.clusterDim.z = 1;
+  return a;
+}
+
+template <int kKind, int kCols, int kTeam>
+cudaError_t allow_smem(int device, int bytes) {
+  static SmemLimit limit;
+  return limit.need(reinterpret_cast<const void*>(product_kernel<kKind, kCols, kTeam>), device, bytes);
+}
+
 template <int kKind, int kCols, int kTeam>
 int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w, int split,
            cudaStream_t stream) {
@@ -1113,8 +1129,7 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
   if (kKind == kWeightGrad) a.by_group_tiles = Divisor(static_cast<uint32_t>(tiles / p.groups));
   const int smem = R::smem_bytes(p.groups, kTeam == kSplit ? split : 1);
   const auto kernel = product_kernel<kKind, kCols, kTeam>;
-  static SmemLimit limit;
-  cudaError_t e = limit.need(reinterpret_cast<const void*>(kernel), ctx.device, smem);
+  cudaError_t e = allow_smem<kKind, kCols, kTeam>(ctx.device, smem);
   if (e != cudaSuccess) return fail_with_cuda(e, "cudaFuncSetAttribute");
   const int per_unit = kTeam == kSplit ? split : (kTeam == kPair ? 2 : 1);
   cudaLaunchConfig_t cfg = {};
@@ -1122,34 +1137,50 @@ int launch(const ProductArgs& p, const CallContext& ctx, const Source& x, const 
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = per_unit;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
+  cudaLaunchAttribute attr = cluster_of(per_unit);
+  cfg.attrs = &attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kernel, m, a);
   return e == cudaSuccess ? DSMEM_HIST_OK : fail_with_cuda(e, "grouped product launch");
 }
 
-// CTAs to split a tile's depth over, where whole tiles leave SMs idle; each
-// keeps two stages or more.  Split / whole, us: one row of 4096 by 1024
-// channels 7.7 / 15.3, 64 rows 11.2 / 17.1, 16384 rows' weight gradient of
-// 512 x 512 22 / 57; no difference where little is idle (64 rows of 1024 by
-// 4096 channels 7.9 / 7.8).
-int split_for(int64_t tiles, int64_t depth_blocks, int most, int sm_count) {
-  int split = 1;
-  while (split < most && tiles * split * 2 <= sm_count && depth_blocks >= split * 4) split *= 2;
-  return split;
+// Clusters of `split` CTAs of a split kernel that are resident together, asked
+// of the runtime once.  (One CTA fills an SM, whatever the tables of the groups
+// take of its shared memory.)
+constexpr int kMostGroupsOf8 = 1024;  // beside longer tables the sums of 8 CTAs do not fit
+template <int kKind, int kCols>
+int resident_clusters(const CallContext& ctx, int split) {
+  static std::atomic<int> known[kMaxDevices][4] = {};  // one more than the count; 0: not asked yet
+  std::atomic<int>& mine = known[ctx.device][split == 8 ? 3 : split / 2];
+  int have = mine.load(std::memory_order_relaxed);
+  if (have > 0) return have - 1;
+  const int smem = Ring<kCols, kSplit>::smem_bytes(
+      split == 8 ? kMostGroupsOf8 : DSMEM_PRODUCT_MAX_GROUPS, split);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr = cluster_of(split);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int count = 0;
+  cudaError_t e = allow_smem<kKind, kCols, kSplit>(ctx.device, smem);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&count, product_kernel<kKind, kCols, kSplit>, &cfg);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return 0;  // whole tiles need no clusters
+  }
+  mine.store(count + 1, std::memory_order_relaxed);
+  return count;
 }
 
 template <int kKind, int kCols>
 int launch_narrow(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
                   cudaStream_t stream) {
   const int64_t depth = kKind == kForward ? p.inner : (kKind == kInputGrad ? p.outer : p.n / p.groups);
-  // The sums of 8 CTAs fit beside tables of up to 1024 groups.
-  const int most = std::min(Ring<kCols, kSplit>::kMaxSplit, p.groups > 1024 ? 4 : 8);
-  const int split = split_for(tile_bound(p, kCols, kChannels), depth / kDepth, most, ctx.sm_count);
+  const int most = std::min(Ring<kCols, kSplit>::kMaxSplit, p.groups > kMostGroupsOf8 ? 4 : 8);
+  const int split = split_for(tile_bound(p, kCols, kChannels), depth / kDepth, most,
+                              [&](int of) { return resident_clusters<kKind, kCols>(ctx, of); });
   if (split > 1) return launch<kKind, kCols, kSplit>(p, ctx, x, w, split, stream);
   return launch<kKind, kCols, kSolo>(p, ctx, x, w, 1, stream);
 }

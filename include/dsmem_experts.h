@@ -19,8 +19,9 @@
  * orders and positions that are out of range read and write nothing outside
  * the stated buffers.
  *
- * The same call gives the same bits: sums are taken in an order that sizes
- * alone decide, in 32 bits or more, and rounded once to the output's type.
+ * The same call gives the same bits: sums are taken in an order that sizes and
+ * the device alone decide, in 32 bits or more, and rounded once to the output's
+ * type.
  *
  * The product kernels wait for their own copies and matrix instructions with
  * bounded waits (about 50 ms each).  A wait that gives up makes the launch's

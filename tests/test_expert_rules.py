@@ -25,3 +25,7 @@ def check(name, tmp_path):
 
 def test_a_bounded_wait_looks_once_more_before_it_gives_up(tmp_path):
     check("bounded_wait_check", tmp_path)
+
+
+def test_launch_rules(tmp_path):
+    check("launch_rules_check", tmp_path)
