@@ -1179,7 +1179,7 @@ int launch_narrow(const ProductArgs& p, const CallContext& ctx, const Source& x,
                   cudaStream_t stream) {
   const int64_t depth = kKind == kForward ? p.inner : (kKind == kInputGrad ? p.outer : p.n / p.groups);
   const int most = std::min(Ring<kCols, kSplit>::kMaxSplit, p.groups > kMostGroupsOf8 ? 4 : 8);
-  const int split = split_for(tile_bound(p, kCols, kChannels), depth / kDepth, most,
+  const int split = split_for(tile_bound(p, kCols, kChannels), depth / kDepth, split_stages(kCols), most,
                               [&](int of) { return resident_clusters<kKind, kCols>(ctx, of); });
   if (split > 1) return launch<kKind, kCols, kSplit>(p, ctx, x, w, split, stream);
   return launch<kKind, kCols, kSolo>(p, ctx, x, w, 1, stream);
