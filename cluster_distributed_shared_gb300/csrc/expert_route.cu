@@ -5,6 +5,7 @@
 
 #include "dtypes.cuh"
 #include "experts.h"
+#include "launch_rules.h"
 #include "ptx.cuh"
 
 namespace dsmh {
@@ -259,16 +260,14 @@ cudaError_t dispatch_route(const RouteArgs& a, bool backward, cudaStream_t strea
 // needs no atomics whose order could matter (the counts of step 1 commute).
 // Bound by the latency of its steps: 4 keys 2.4 us, 131072 keys into 256
 // groups 10.4 us (16 CTAs).
-// More keys than a cluster's 16 SMs are good for (kClusterKeys) take three
-// launches over all SMs: every CTA's counts, their prefixes over the CTAs, and
-// the same kernel with these in place of the cluster's totals.  256 groups, one
-// cluster / all SMs, us: 2^18 keys 17.1 / 17.7, 2^20 55 / 23, 2^24 770 / 175,
-// 2^26 7009 / 1349 (bound by scattered 4-byte writes of the order).
+// More keys (group_shape) take three launches over all SMs: every CTA's counts,
+// their prefixes over the CTAs, and the same kernel with these in place of the
+// cluster's totals.
 struct GroupArgs {
   const int32_t* keys;
   int64_t n;
   int groups, warps, bits;
-  int shared_totals;  // one warp in one CTA: its row is the CTA's totals as well
+  int shared_totals;  // one warp: its row is the CTA's totals and bases as well
   int32_t* offsets;
   int32_t* order;
   int32_t* position;
@@ -423,9 +422,6 @@ __global__ void __launch_bounds__(1024) group_kernel(GroupArgs a) {
   if (P > 1) cluster_wait();
 }
 
-constexpr int kGroupSmemLimit = 200 * 1024;
-constexpr int64_t kClusterKeys = int64_t{1} << 18;
-
 // The CTAs' counts of their keys, [CTAs][groups]; CTAs and their keys are
 // those of group_kernel.
 __global__ void __launch_bounds__(1024) group_count_kernel(const int32_t* keys, int64_t n, int groups,
@@ -492,29 +488,17 @@ int run_group(const int32_t* keys, int64_t n, int num_groups, int32_t* offsets, 
   a.keys = keys, a.n = n, a.groups = num_groups;
   a.offsets = offsets, a.order = order, a.position = position;
   while ((int64_t{1} << a.bits) < num_groups) ++a.bits;
-  // Warps: as many counter rows as shared memory holds beside the totals, but
-  // no more than the keys fill with 32 each.
-  // Where a row, the totals and the bases do not fit (17,057 groups or more),
-  // one warp in one CTA keeps all in one row.
-  const int64_t fit = (kGroupSmemLimit / 4 - 32) / num_groups - 2;
-  a.shared_totals = fit < 1;
-  int64_t warps = (n + 31) / 32;
-  if (warps > fit) warps = fit;
-  a.warps = static_cast<int>(warps < 1 ? 1 : (warps > 32 ? 32 : warps));
-  const size_t smem = (static_cast<size_t>(a.warps + (a.shared_totals ? 0 : 2)) * num_groups + 32) * 4;
+  const GroupShape shape = group_shape(n, num_groups, ctx.sm_count);
+  a.shared_totals = shape.shared_totals;
+  a.warps = shape.warps;
+  const size_t smem = shape.smem_bytes;
 
   static SmemLimit limit, count_limit;
   cudaError_t e = limit.need(reinterpret_cast<const void*>(group_kernel), ctx.device, kGroupSmemLimit, true);
   if (e != cudaSuccess) return fail_with_cuda(e, "cudaFuncSetAttribute");
-  // CTAs: one cluster, doubled while every warp still has 128 keys or more,
-  // or two an SM (one where the rows take its shared memory).
-  int P = 1, ctas = 1;
   uint32_t* scratch = nullptr;
-  if (n <= kClusterKeys || a.shared_totals) {
-    while (P < 16 && !a.shared_totals && n >= int64_t{2} * P * a.warps * 128) P *= 2;
-    ctas = P;
-  } else {
-    ctas = ctx.sm_count * (smem <= 100 * 1024 ? 2 : 1);
+  const int ctas = shape.ctas;
+  if (!shape.one_cluster) {
     const size_t counts = static_cast<size_t>(ctas) * num_groups;
     int rc = pool_alloc(ctx, reinterpret_cast<void**>(&scratch), (counts + num_groups) * 4, stream);
     if (rc) return rc;
@@ -538,7 +522,7 @@ int run_group(const int32_t* keys, int64_t n, int num_groups, int32_t* offsets, 
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = P;
+    attr[0].val.clusterDim.x = shape.one_cluster ? ctas : 1;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

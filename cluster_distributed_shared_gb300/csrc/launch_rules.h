@@ -34,4 +34,42 @@ int split_for(int64_t tiles, int64_t depth_blocks, int stages, int most, Residen
   return split;
 }
 
+// How a call groups n keys: one cluster of CTAs, or three launches over all SMs.
+constexpr int kGroupSmemLimit = 200 * 1024;
+constexpr int64_t kClusterKeys = int64_t{1} << 18, kOneWarpKeys = 12288;
+struct GroupShape {
+  int warps;           // of a CTA, each with a row of counters
+  bool shared_totals;  // one warp, whose row is the CTA's totals and bases as well
+  bool one_cluster;
+  int ctas;
+  int smem_bytes;
+};
+// Warps: as many counter rows as shared memory holds beside the totals and the
+// bases, but no more than the keys fill with 32 each.  Where not even one row
+// fits beside them (17,057 groups or more) one warp keeps all in one row.
+// CTAs: one cluster, doubled while every warp still has 128 keys or more; with
+// more keys than a cluster's 16 SMs (or the one warp) are good for, two an SM (one
+// where the rows take its shared memory).  256 groups, one cluster / all SMs, us:
+// 2^18 keys 17.1 / 17.7, 2^20 55 / 23, 2^24 770 / 175, 2^26 7009 / 1349 (bound by
+// scattered 4-byte writes of the order).  17,057 groups, one warp / all SMs: 2^12
+// keys 194 / 317, 2^14 367 / 317, 2^18 3815 / 328, 2^20 14857 / 365, and 2^24 keys
+// 1278 (bound by each CTA's scan over the groups); 32,768 groups 313 / 476,
+// 487 / 477, 3937 / 498, 14974 / 570, and 2432.
+inline GroupShape group_shape(int64_t n, int groups, int sm_count) {
+  GroupShape s = {};
+  const int64_t fit = (kGroupSmemLimit / 4 - 32) / groups - 2;
+  s.shared_totals = fit < 1;
+  int64_t warps = (n + 31) / 32;
+  if (warps > fit) warps = fit;
+  s.warps = static_cast<int>(warps < 1 ? 1 : (warps > 32 ? 32 : warps));
+  s.smem_bytes = ((s.warps + (s.shared_totals ? 0 : 2)) * groups + 32) * 4;
+  s.one_cluster = n <= (s.shared_totals ? kOneWarpKeys : kClusterKeys);
+  s.ctas = 1;
+  if (!s.one_cluster)
+    s.ctas = sm_count * (s.smem_bytes <= 100 * 1024 ? 2 : 1);
+  else
+    while (s.ctas < 16 && !s.shared_totals && n >= int64_t{2} * s.ctas * s.warps * 128) s.ctas *= 2;
+  return s;
+}
+
 }  // namespace dsmh

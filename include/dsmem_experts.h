@@ -84,7 +84,8 @@ DSMEM_HIST_API int dsmem_route_backward(const void* logits, int32_t dtype, int64
  *   order[p]     = the i with position[i] == p;   -1 for p >= offsets[num_groups]
  *   num_groups  1 .. 32768
  *   offsets int32 [num_groups + 1], order and position int32 [n]
- * Takes scratch from the pool for more than 2^18 keys. */
+ * Takes scratch from the pool for more than 2^18 keys, and for more than 12,288
+ * into 17,057 groups or more. */
 DSMEM_HIST_API int dsmem_group(const int32_t* keys, int64_t n, int32_t num_groups, int32_t* offsets,
                                int32_t* order, int32_t* position, cudaStream_t stream);
 

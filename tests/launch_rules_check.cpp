@@ -3,6 +3,8 @@
 // exits 0 when every check holds.
 #include <stdio.h>
 
+#include <initializer_list>
+
 #include "launch_rules.h"
 
 using namespace dsmh;
@@ -50,6 +52,24 @@ int main() {
   CHECK(split_for(77, 64, 8, 4, resident) == 1);
   // A device without clusters, or of which none could be asked.
   CHECK(split_for(1, 1024, 4, 8, [](int) { return 0; }) == 1);
+  // Grouping: the counters fit, every warp of a cluster has work, and many keys
+  // use every SM, whatever the groups.
+  for (int groups = 1; groups <= 32768; groups += groups < 64 ? 1 : 61)
+    for (int64_t n : {int64_t{0}, int64_t{1}, int64_t{31}, int64_t{33}, int64_t{4097}, int64_t{12288}, int64_t{12289},
+                      int64_t{262144}, int64_t{262145}, int64_t{1} << 20, int64_t{1} << 24, int64_t{2147483647}}) {
+      const GroupShape s = group_shape(n, groups, 152);
+      const int rows = s.warps + (s.shared_totals ? 0 : 2);
+      CHECK(s.warps >= 1 && s.warps <= 32 && (s.warps == 1 || !s.shared_totals));
+      CHECK(s.smem_bytes <= kGroupSmemLimit && s.smem_bytes >= (rows * groups + 32) * 4);
+      CHECK(s.one_cluster ? (s.ctas >= 1 && s.ctas <= 16 && (s.ctas & (s.ctas - 1)) == 0) : s.ctas >= 152);
+      if (s.ctas > 1 && s.one_cluster) CHECK(n >= int64_t{s.ctas} * s.warps * 128);
+      if (n > 262144) CHECK(s.ctas >= 152);
+      CHECK(s.shared_totals == (groups > 17056));
+    }
+  CHECK(group_shape(12288, 17057, 152).ctas == 1);
+  CHECK(group_shape(12289, 17057, 152).ctas == 304);
+  CHECK(group_shape(1 << 20, 32768, 152).ctas == 152);
+  CHECK(group_shape(131072, 256, 152).ctas == 16);
   if (failures == 0) printf("ok\n");
   return failures != 0;
 }

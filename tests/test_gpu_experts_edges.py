@@ -10,7 +10,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import cluster_distributed_shared_gb300 as dh  # noqa: E402
-from test_gpu_experts import cuda_ready, generator  # noqa: E402,F401
+from test_gpu_experts import cuda_ready, generator, group_exact  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,21 @@ def test_masked_logits_have_no_gradient_beside_infinite_ones(experts, bad, renor
     masked = ~(logits > -math.inf)
     assert (got[masked] == 0).all()
     assert torch.isfinite(got[[0, 2, 3, 4]]).all() and not torch.isfinite(got[1]).all()
+
+
+# ------------------------------------------------------------------- group
+
+@pytest.mark.parametrize("n", [12288, 12289, 262145])
+@pytest.mark.parametrize("groups", [17056, 17057, 32768])
+@pytest.mark.parametrize("kind", ["uniform", "one", "dropped"])
+def test_group_into_very_many(n, groups, kind):
+    """Both sides of the counters' shared row and of the sizes that use all SMs."""
+    keys = torch.randint(0, groups, (n,), generator=generator(n + groups), dtype=torch.int32)
+    if kind == "one":
+        keys[:] = groups - 1
+    if kind == "dropped":
+        keys[::3] = -1
+        keys[1::7] = 2 ** 31 - 1
+    got = dh.dsmem_group(keys.cuda(), groups)
+    for a, b in zip(got, group_exact(keys, groups)):
+        assert torch.equal(a.cpu(), b)
