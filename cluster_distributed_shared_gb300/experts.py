@@ -8,6 +8,10 @@ Argument marshalling only, like the histogram's binding: ``dsmem_route`` and
 ``dsmem_combine`` and ``dsmem_combine_backward`` bring the rows back to their
 tokens, and ``dsmem_grad_clip`` clips gradients by their global norm.
 
+Rows of float inputs are contiguous and may be further apart than their length
+(slices of columns); views that repeat rows by a stride of 0, as ``expand``
+makes, are refused.
+
 Every call is asynchronous on ``stream`` (default: torch's current stream).
 With a ``stream`` given, new outputs belong to it, and inputs are recorded on
 it, so their memory is not reused before the call has run; work that produces
@@ -313,7 +317,7 @@ def dsmem_combine(z, position, weights=None, stream=None):
 
 def dsmem_combine_backward(dy, z, position, order, weights, stream=None):
     """Gradients (dz, dweights) of dsmem_combine; `position` and `order` are
-    one dsmem_group call's."""
+    one dsmem_group call's, `weights` ones for a combination without."""
     dtype, index = _float_tensor("dy", dy, 2)
     _like("z", z, 2, dtype, index)
     _int_tensor("position", position, None, index)
@@ -345,7 +349,8 @@ def dsmem_grad_clip(grads, max_norm: float, out=None, stream=None):
     """Global norm of `grads` (a list of contiguous CUDA tensors), returned as
     a float32 tensor without dimensions; the gradients times min(1, max_norm /
     (norm + 1e-6)) go to `out`, a list of tensors of their types and sizes, or
-    in place."""
+    in place.  max_norm is positive and finite; the largest float32 gives the
+    norm alone."""
     grads = list(grads)
     out = grads if out is None else list(out)
     if len(out) != len(grads):

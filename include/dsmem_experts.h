@@ -27,7 +27,8 @@
  * bounded waits (about 50 ms each).  A wait that gives up makes the launch's
  * output wrong and is reported as in dsmem_hist.h: the next call on the same
  * stream returns DSMEM_HIST_ETIMEOUT and enqueues nothing, and
- * dsmem_hist_device_status() shows bit 1.  The test hooks of dsmem_hist.h hold
+ * dsmem_hist_device_status() shows bit 1 (after the last product of a step, which
+ * no call follows, ask there once the stream has been synchronised).  The test hooks of dsmem_hist.h hold
  * here too: DSMEM_HIST_TEST_WAIT_CYCLES bounds these waits,
  * DSMEM_HIST_TEST_WITHHOLD_LAST_ROUND leaves out the copies of the last stage of
  * depth, so that the wait for them runs out with none of them in flight, and
@@ -99,10 +100,13 @@ DSMEM_HIST_API int dsmem_group(const int32_t* keys, int64_t n, int32_t num_group
  *   dtype       of x and weight: DSMEM_F16 or DSMEM_BF16; products are summed
  *               in 32 bits
  *   out_dtype   `dtype` or DSMEM_F32
- *   *_stride    elements between rows (weight_group_stride: between groups);
- *               rows themselves are contiguous, and out's rows too
+ *   *_stride    elements between rows, at least a row's length, and
+ *               weight_group_stride between groups, at least 1: views that repeat
+ *               a row or a matrix by a stride of 0 are refused.  Rows themselves
+ *               are contiguous, and out's rows too
  *   groups      1 .. 2048;  x_rows, n, outer, inner < 2^31 - 512
- * Any sizes, strides and alignments are right.  Sources whose base, row
+ * All such sizes and strides, and any alignment of the elements, are right.
+ * Sources whose base, row
  * stride and group stride are multiples of 16 bytes are read in place; others
  * are first laid out so in pool scratch (one more pass over them). */
 DSMEM_HIST_API int dsmem_grouped_matmul(const void* x, int64_t x_rows, int64_t x_stride,
@@ -129,7 +133,8 @@ DSMEM_HIST_API int dsmem_grouped_matmul_wgrad(const void* dy, int64_t dy_stride,
  * others (dropped) are not read, and a token without any is 0.
  *   weights  float [tokens, top_k], or NULL for 1
  *   dtype    of z and out: DSMEM_F32, DSMEM_F16 or DSMEM_BF16
- *   z        [z_rows, width], z_stride elements between rows; out contiguous
+ *   z        [z_rows, width], z_stride >= width elements between rows; out
+ *            contiguous
  *   width    1 .. 2^31 - 2049;  tokens * top_k < 2^31 */
 DSMEM_HIST_API int dsmem_combine(const void* z, int64_t z_rows, int64_t z_stride,
                                  const int32_t* position, const float* weights, int64_t tokens,
@@ -140,8 +145,9 @@ DSMEM_HIST_API int dsmem_combine(const void* z, int64_t z_rows, int64_t z_stride
  * and dweights[t, j] = <dy[t, :], z[position[t, j], :]> (0 where dropped).
  * `position` and `order` are one dsmem_group call's, with tokens * top_k
  * keys; rows p of dz with order[p] < 0 are 0.
- *   dy       [tokens, width], dy_stride elements between rows
- *   z        [tokens * top_k, width], z_stride elements between rows
+ *   dy       [tokens, width], dy_stride >= width elements between rows
+ *   z        [tokens * top_k, width], z_stride >= width elements between rows
+ *   weights  not NULL (ones for a combination without)
  *   dz       [tokens * top_k, width] contiguous;  dweights float [tokens, top_k] */
 DSMEM_HIST_API int dsmem_combine_backward(const void* dy, int64_t dy_stride, const void* z,
                                           int64_t z_stride, const int32_t* position,
@@ -160,9 +166,9 @@ typedef struct dsmem_grad {
 
 /* Global norm and clipping:  *norm = sqrt(sum of all squares), and every
  * out = grad * min(1, max_norm / (*norm + 1e-6)).  A norm that is infinite or
- * NaN goes through the formula.
+ * NaN goes through the formula.  No gradient overlaps another, nor another's out.
  *   grads     HOST array of num_grads entries (read before the call returns)
- *   max_norm  > 0
+ *   max_norm  positive and finite (FLT_MAX for the norm alone)
  *   norm      device, one float
  * Takes scratch from the pool. */
 DSMEM_HIST_API int dsmem_grad_clip(const dsmem_grad_t* grads, int32_t num_grads, float max_norm,

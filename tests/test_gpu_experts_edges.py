@@ -55,3 +55,29 @@ def test_group_into_very_many(n, groups, kind):
     got = dh.dsmem_group(keys.cuda(), groups)
     for a, b in zip(got, group_exact(keys, groups)):
         assert torch.equal(a.cpu(), b)
+
+
+# ---------------------------------------------------------------- refusals
+
+def test_repeated_rows_are_refused():
+    """Views that repeat rows or matrices by a stride of 0, and what a norm
+    alone is asked for with."""
+    h = torch.ones(1, 16, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(2, 8, 16, dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    i = torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    ones = torch.ones(2, 2, device="cuda")
+    z = torch.ones(4, 16, dtype=torch.bfloat16, device="cuda")
+    for call in [lambda: dh.dsmem_route(h.expand(4, 16), 2),
+                 lambda: dh.dsmem_grouped_matmul(h.expand(4, 16), w, off),
+                 lambda: dh.dsmem_grouped_matmul(z, w[:1].expand(2, 8, 16), off),
+                 lambda: dh.dsmem_grouped_matmul(z, w[:, :1].expand(2, 8, 16), off),
+                 lambda: dh.dsmem_grouped_matmul_wgrad(h.expand(4, 16), z, off),
+                 lambda: dh.dsmem_combine(h.expand(4, 16), i),
+                 lambda: dh.dsmem_combine_backward(h.expand(2, 16), z, i, i.view(-1), ones),
+                 lambda: dh.dsmem_grad_clip([ones], math.inf)]:
+        with pytest.raises(dh.DsmemHistError) as e:
+            call()
+        assert e.value.code == dh.DSMEM_HIST_EINVAL
+    most = torch.finfo(torch.float32).max
+    assert float(dh.dsmem_grad_clip([ones], most)) == 2.0 and (ones == 1).all()
