@@ -10,7 +10,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import cluster_distributed_shared_gb300 as dh  # noqa: E402
-from test_gpu_experts import cuda_ready, generator, group_exact  # noqa: E402,F401
+from test_gpu_experts import (  # noqa: E402,F401
+    FLOOR, UNIT, cuda_ready, generator, group_exact, route_exact)
 
 pytestmark = pytest.mark.gpu
 
@@ -37,6 +38,46 @@ def test_masked_logits_have_no_gradient_beside_infinite_ones(experts, bad, renor
     masked = ~(logits > -math.inf)
     assert (got[masked] == 0).all()
     assert torch.isfinite(got[[0, 2, 3, 4]]).all() and not torch.isfinite(got[1]).all()
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("pad", [0, 8])
+@pytest.mark.parametrize("tokens,experts,k", [(6, 8, 2), (300, 64, 8), (61, 120, 4), (515, 128, 8),
+                                              (1026, 256, 8), (7, 248, 32), (66, 384, 6), (35, 512, 10),
+                                              (40, 1024, 8)])
+def test_route_of_aligned_rows(tokens, experts, k, dtype, pad, renormalize):
+    """Rows that are read and written 16 bytes at a time where a lane holds as
+    much: whole rows side by side, and rows some aligned distance apart."""
+    g = generator(tokens + experts)
+    logits = (torch.randn(tokens, experts, generator=g) * 3).to(dtype)
+    logits[:, torch.rand(experts, generator=g) < 0.1] = -math.inf
+    logits[0, experts // 2] = math.nan
+    logits[1] = -math.inf
+    logits[2] = 0.25                   # all equal: the lowest indexes
+    logits[3, experts - 1] = math.inf
+    buf = torch.full((tokens, experts + pad), math.nan, dtype=dtype)
+    buf[:, :experts] = logits
+    dev = buf.cuda()[:, :experts]
+    assert dev.data_ptr() % 16 == 0 and dev.stride(0) * dev.element_size() % 16 == 0
+    ids, w = dh.dsmem_route(dev, k, renormalize=renormalize)
+    want_ids, want_w, p = route_exact(logits, k, renormalize)
+    assert torch.equal(ids.cpu(), want_ids)
+    # as test_route_and_gradient's bound, with the argument's rounding: |x - top|
+    # is below 32 here, so 16 units of 2^-24 of a weight of 1 at most
+    assert (w.cpu().double() - want_w).abs().max() <= (64 + 16) * 2.0 ** -24
+    dw = torch.randn(tokens, k, generator=g)
+    got = dh.dsmem_route_backward(dev, ids, w, dw.cuda(), renormalize=renormalize)
+    d = dw.double()
+    dot = torch.where(want_ids >= 0, want_w * d, 0.0).sum(1, keepdim=True)
+    full = torch.zeros(tokens, experts, dtype=torch.float64)
+    part = want_w * (d - dot) if renormalize else want_w * d
+    full.scatter_add_(1, want_ids.clamp(min=0).long(), torch.where(want_ids >= 0, part, 0.0))
+    if not renormalize:
+        full -= p * dot
+    # weights that are off by 80 units, times up to k gradients, and their sums
+    bound = UNIT[dtype] * full.abs() + (k + 2) * 96 * 2.0 ** -24 * (d.abs().max() + 1) + FLOOR[dtype]
+    assert ((got.cpu().double() - full).abs() <= bound).all()
 
 
 # ------------------------------------------------------------------- group
