@@ -11,7 +11,7 @@ torch = pytest.importorskip("torch")
 
 import cluster_distributed_shared_gb300 as dh  # noqa: E402
 from test_gpu_experts import (  # noqa: E402,F401
-    FLOOR, UNIT, cuda_ready, generator, group_exact, route_exact)
+    FLOOR, UNIT, close, cuda_ready, generator, group_exact, route_exact, spans)
 
 pytestmark = pytest.mark.gpu
 
@@ -96,6 +96,115 @@ def test_group_into_very_many(n, groups, kind):
     got = dh.dsmem_group(keys.cuda(), groups)
     for a, b in zip(got, group_exact(keys, groups)):
         assert torch.equal(a.cpu(), b)
+
+
+# ---------------------------------------------------------------- products
+
+def ragged(g, groups, n, empty, behind):
+    """Offsets of n places in `groups` groups, a share of them empty, the last
+    `behind` places of none."""
+    share = torch.rand(groups, generator=g).double()
+    share[torch.rand(groups, generator=g) < empty] = 0
+    if not share.any():
+        share[groups // 2] = 1
+    ends = ((share.cumsum(0) / share.sum()) * (n - behind)).round().int()
+    return torch.cat([torch.zeros(1, dtype=torch.int32), ends])
+
+
+def plain_products(x, w, dy, offsets, row):
+    """The three products in 64 bits, each with the sums of magnitudes."""
+    n, outer, inner = dy.shape[0], dy.shape[1], x.shape[1]
+    y, my = torch.zeros(2, n, outer, dtype=torch.float64)
+    dx, mdx = torch.zeros(2, n, inner, dtype=torch.float64)
+    dw, mdw = torch.zeros(2, *w.shape, dtype=torch.float64)
+    for e, a, b in spans(offsets):
+        xr, we, d = x[row[a:b]].double(), w[e].double(), dy[a:b].double()
+        y[a:b], my[a:b] = xr @ we.T, xr.abs() @ we.abs().T
+        dx[a:b], mdx[a:b] = d @ we, d.abs() @ we.abs()
+        dw[e], mdw[e] = d.T @ xr, d.abs().T @ xr.abs()
+    return (y, my), (dx, mdx), (dw, mdw)
+
+
+# Groups: either side of one round of the tables (480) and of the sizes up to
+# which the weight gradient's groups are sorted (512), beyond the split over 8
+# CTAs (1024), and the most there are, where the tables fill shared memory.
+@pytest.mark.parametrize("groups,n,inner,outer,empty", [
+    (480, 700, 64, 72, 0.0), (481, 700, 64, 72, 0.0), (481, 300, 64, 72, 0.9), (512, 2000, 72, 64, 0.3),
+    (513, 2000, 72, 64, 0.3), (961, 40, 136, 40, 0.0), (1024, 3, 2048, 8, 0.0), (1025, 3, 1024, 8, 0.0),
+    (1025, 5000, 40, 136, 0.5), (2048, 2, 1024, 8, 0.0), (2048, 1, 264, 72, 0.0), (2048, 60, 520, 24, 0.9),
+    (2048, 9000, 72, 136, 0.2), (2048, 140000, 64, 64, 0.9)])
+def test_products_of_many_groups(groups, n, inner, outer, empty):
+    g = generator(groups + n)
+    behind = n // 10
+    offsets = ragged(g, groups, n, empty, behind)
+    x = torch.randn(n, inner, generator=g).to(torch.bfloat16)
+    w = (torch.randn(groups, outer, inner, generator=g) / math.sqrt(inner)).to(torch.bfloat16)
+    dy = torch.randn(n, outer, generator=g).to(torch.bfloat16)
+    x[n - behind:], dy[n - behind:] = math.nan, math.nan     # of no group: not read
+    order = torch.randperm(n - behind, generator=g).int()
+    order = torch.cat([order, torch.full((behind,), -1, dtype=torch.int32)])
+    plain = torch.arange(n)
+    off, xd, wd, dyd = offsets.cuda(), x.cuda(), w.cuda(), dy.cuda()
+    for named in (None, order):
+        (y, my), (dx, mdx), (dw, mdw) = plain_products(x, w, dy, offsets, plain if named is None else
+                                                       named.clamp(min=0).long())
+        rows = {} if named is None else dict(order=named.cuda())
+        for out_dtype in (torch.bfloat16, torch.float32):
+            close(dh.dsmem_grouped_matmul(xd, wd, off, out_dtype=out_dtype, **rows), y, my, inner)
+            if named is None:
+                got = dh.dsmem_grouped_matmul(dyd, wd, off, transpose=True, out_dtype=out_dtype)
+                close(got, dx, mdx, outer)
+            close(dh.dsmem_grouped_matmul_wgrad(dyd, xd, off, out_dtype=out_dtype, **rows), dw, mdw, n)
+        del y, my, dx, mdx, dw, mdw
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("tokens,groups,fan,inner,outer", [(1, 4, 2, 136, 72), (3, 2, 1, 264, 4096),
+                                                           (40, 3, 2, 1003, 517), (300, 7, 3, 129, 65),
+                                                           (1300, 16, 1, 800, 520), (3000, 4, 1, 1304, 776)])
+def test_input_gradients_of_gathered_rows(tokens, groups, fan, inner, outer, dtype):
+    """`transpose` with an `order`: rows of dy by token, each for `fan` places."""
+    g = generator(tokens + outer)
+    ids = torch.randint(-1 if tokens > 8 else 0, groups, (tokens * fan,), generator=g, dtype=torch.int32)
+    offsets, order, _ = group_exact(ids, groups)
+    dy = torch.randn(tokens, outer, generator=g).to(dtype)
+    w = (torch.randn(groups, outer, inner, generator=g) / math.sqrt(inner)).to(dtype)
+    row = torch.where(order < 0, 0, order // fan).long()
+    want, size = torch.zeros(2, tokens * fan, inner, dtype=torch.float64)
+    for e, a, b in spans(offsets):
+        d, we = dy[row[a:b]].double(), w[e].double()
+        want[a:b], size[a:b] = d @ we, d.abs() @ we.abs()
+    for out_dtype in (dtype, torch.float32):
+        got = dh.dsmem_grouped_matmul(dy.cuda(), w.cuda(), offsets.cuda(), order=order.cuda(), fan=fan,
+                                      transpose=True, out_dtype=out_dtype)
+        close(got, want, size, outer)
+
+
+@pytest.mark.parametrize("inner", [64, 129])
+def test_products_with_permuted_weights(inner):
+    """Group strides that are smaller than the row stride, or no multiple of it."""
+    g = generator(inner)
+    groups, outer, n = 5, 136, 150
+    offsets = ragged(g, groups, n, 0.0, 7).cuda()
+    w = torch.randn(groups, outer, inner, generator=g).to(torch.bfloat16).cuda()
+    x = torch.randn(n, inner, generator=g).to(torch.bfloat16).cuda()
+    dy = torch.randn(n, outer, generator=g).to(torch.bfloat16).cuda()
+    want = (dh.dsmem_grouped_matmul(x, w, offsets), dh.dsmem_grouped_matmul(dy, w, offsets, transpose=True))
+    by_row = torch.empty(outer, groups, inner, dtype=w.dtype, device="cuda").permute(1, 0, 2)
+    by_row.copy_(w)
+    flat = torch.full((groups * (outer * inner + 24),), math.nan, dtype=w.dtype, device="cuda")
+    apart = flat.as_strided((groups, outer, inner), (outer * inner + 24, inner, 1))
+    apart.copy_(w)
+    lapping = torch.empty(groups - 1 + outer, inner, dtype=w.dtype, device="cuda").normal_()
+    lapping = lapping.as_strided((groups, outer, inner), (inner, inner, 1))    # matrices that share rows
+    assert by_row.stride(0) < by_row.stride(1) and apart.stride(0) % apart.stride(1) != 0
+    for view in (by_row, apart):
+        assert torch.equal(dh.dsmem_grouped_matmul(x, view, offsets), want[0])
+        assert torch.equal(dh.dsmem_grouped_matmul(dy, view, offsets, transpose=True), want[1])
+    whole = lapping.contiguous()
+    assert torch.equal(dh.dsmem_grouped_matmul(x, lapping, offsets), dh.dsmem_grouped_matmul(x, whole, offsets))
+    assert torch.equal(dh.dsmem_grouped_matmul(dy, lapping, offsets, transpose=True),
+                       dh.dsmem_grouped_matmul(dy, whole, offsets, transpose=True))
 
 
 # ---------------------------------------------------------------- refusals
