@@ -3,6 +3,7 @@ infinities and NaN, aligned and permuted sources, many groups, offsets out of
 range, threads and graphs.  Tolerances as in test_gpu_experts."""
 from __future__ import annotations
 
+import ctypes
 import math
 
 import pytest
@@ -10,6 +11,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import cluster_distributed_shared_gb300 as dh  # noqa: E402
+from cluster_distributed_shared_gb300 import experts  # noqa: E402
 from test_gpu_experts import (  # noqa: E402,F401
     FLOOR, UNIT, close, cuda_ready, generator, group_exact, route_exact, spans)
 
@@ -205,6 +207,61 @@ def test_products_with_permuted_weights(inner):
     assert torch.equal(dh.dsmem_grouped_matmul(x, lapping, offsets), dh.dsmem_grouped_matmul(x, whole, offsets))
     assert torch.equal(dh.dsmem_grouped_matmul(dy, lapping, offsets, transpose=True),
                        dh.dsmem_grouped_matmul(dy, whole, offsets, transpose=True))
+
+
+def guarded(shape, dtype):
+    """An output between two margins, and a check that they are untouched."""
+    count, margin = math.prod(shape), 4096
+    buf = torch.full((count + 2 * margin,), 7.0, dtype=dtype, device="cuda")
+
+    def untouched():
+        return bool((buf[:margin] == 7).all() and (buf[margin + count:] == 7).all())
+
+    return buf[margin:margin + count].view(shape), untouched
+
+
+def entry(name, *args):
+    fn = getattr(dh.lib(), name)
+    fn.argtypes, fn.restype = experts.SIGNATURES[name], ctypes.c_int
+    stream = torch.cuda.current_stream().cuda_stream
+    return fn(*[a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args], stream)
+
+
+@pytest.mark.parametrize("out", [torch.float16, torch.float32])
+@pytest.mark.parametrize("inner,outer", [(64, 128), (72, 136), (33, 65)])
+@pytest.mark.parametrize("off", [[0, -5, 2 ** 31 - 1, 7], [3, 30, 10, 20], [-1, -1, -1, -1], [0, 0, 0, 2 ** 31 - 1],
+                                 [-2 ** 31, 40, 40, 41], [17, 16, 15, 14]])
+def test_products_with_offsets_out_of_range(off, inner, outer, out):
+    """Ends are clamped to the rows there are and never fall; the first offset
+    counts as 0.  Every element is written, and nothing beside them."""
+    n, groups = 40, 3
+    g = generator(sum(off) + inner)
+    ends, last = [0], 0
+    for e in off[1:]:
+        last = max(last, min(max(e, 0), n))
+        ends.append(last)
+    x = torch.randn(n, inner, generator=g).to(torch.float16)
+    w = torch.randn(groups, outer, inner, generator=g).to(torch.float16)
+    dy = torch.randn(n, outer, generator=g).to(torch.float16)
+    (y, my), (dx, mdx), (dw, mdw) = plain_products(x, w, dy, torch.tensor(ends), torch.arange(n))
+    t = torch.tensor(off, dtype=torch.int32, device="cuda")
+    xd, wd, dyd = x.cuda(), w.cuda(), dy.cuda()
+    code = experts.F32 if out == torch.float32 else experts.F16
+    got, untouched = guarded((n, outer), out)
+    assert entry("dsmem_grouped_matmul", xd, n, inner, wd, inner, outer * inner, t, groups, None, 1, n, outer,
+                 inner, 0, experts.F16, got, code) == 0
+    close(got, y, my, inner)
+    assert untouched()
+    got, untouched = guarded((n, inner), out)
+    assert entry("dsmem_grouped_matmul", dyd, n, outer, wd, inner, outer * inner, t, groups, None, 1, n, outer,
+                 inner, 1, experts.F16, got, code) == 0
+    close(got, dx, mdx, outer)
+    assert untouched()
+    got, untouched = guarded((groups, outer, inner), out)
+    assert entry("dsmem_grouped_matmul_wgrad", dyd, outer, xd, n, inner, t, groups, None, 1, n, outer, inner,
+                 experts.F16, got, code) == 0
+    close(got, dw, mdw, n)
+    assert untouched()
 
 
 # ---------------------------------------------------------------- refusals
