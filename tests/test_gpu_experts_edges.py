@@ -264,6 +264,36 @@ def test_products_with_offsets_out_of_range(off, inner, outer, out):
     assert untouched()
 
 
+# ----------------------------------------------------------------- combine
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("width", [8, 129, 264, 2056])
+@pytest.mark.parametrize("pad,shift", [(8, 0), (16, 8), (5, 1)])
+def test_combine_gradients_of_strided_rows(width, dtype, pad, shift):
+    """dy and z as columns of wider tensors, aligned and not."""
+    g = generator(width + pad)
+    tokens, k = 33, 3
+    ids = torch.randint(-1, 5, (tokens, k), generator=g, dtype=torch.int32)
+    _, order, position = group_exact(ids.flatten(), 5)
+    position = position.view(tokens, k)
+
+    def view(rows):
+        buf = torch.full((rows, width + pad), math.nan, dtype=dtype, device="cuda")
+        buf[:, shift:shift + width] = torch.randn(rows, width, generator=g).to(dtype).cuda()
+        return buf[:, shift:shift + width]
+
+    dy, z, w = view(tokens), view(tokens * k), torch.rand(tokens, k, generator=g).cuda()
+    rest = (position.cuda(), order.cuda(), w)
+    dz, dw = dh.dsmem_combine_backward(dy, z, *rest)
+    ok = position >= 0
+    want = torch.zeros(tokens * k, width, dtype=torch.float64)
+    want[position[ok].long()] = (w.cpu().double()[..., None] * dy.cpu().double()[:, None, :])[ok]
+    close(dz, want, want.abs(), 1)
+    rows = torch.where(ok[..., None], z.cpu().double()[position.clamp(min=0).long()], 0.0)
+    prod = rows * dy.cpu().double()[:, None, :]
+    close(dw, prod.sum(-1), prod.abs().sum(-1), width)
+
+
 # ---------------------------------------------------------------- refusals
 
 def test_repeated_rows_are_refused():
