@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 
 import pytest
 
@@ -292,6 +293,88 @@ def test_combine_gradients_of_strided_rows(width, dtype, pad, shift):
     rows = torch.where(ok[..., None], z.cpu().double()[position.clamp(min=0).long()], 0.0)
     prod = rows * dy.cpu().double()[:, None, :]
     close(dw, prod.sum(-1), prod.abs().sum(-1), width)
+
+
+# ------------------------------------------------------- threads and graphs
+
+def layer_step(x, up, logits, k):
+    """All the operators, as a training step has them."""
+    ids, w = dh.dsmem_route(logits, k)
+    off, order, pos = dh.dsmem_group(ids, up.shape[0])
+    pos = pos.view(ids.shape)
+    h = dh.dsmem_grouped_matmul(x, up, off, order=order, fan=k)
+    y = dh.dsmem_combine(h, pos, w)
+    dz, dw = dh.dsmem_combine_backward(y, h, pos, order, w)
+    dx = dh.dsmem_combine(dh.dsmem_grouped_matmul(dz, up, off, transpose=True), pos)
+    dup = dh.dsmem_grouped_matmul_wgrad(dz, x, off, order=order, fan=k)
+    dl = dh.dsmem_route_backward(logits, ids, w, dw)
+    clipped = [torch.empty_like(dup), torch.empty_like(dl)]
+    norm = dh.dsmem_grad_clip([dup, dl], 1.0, out=clipped)
+    return [ids, w, off, order, pos, h, y, dz, dw, dx, dup, dl, norm, *clipped]
+
+
+def layer_inputs(seed, tokens=200, experts=24, inner=72, outer=136):
+    g = generator(seed)
+    return (torch.randn(tokens, inner, generator=g).to(torch.bfloat16).cuda(),
+            torch.randn(experts, outer, inner, generator=g).to(torch.bfloat16).cuda(),
+            torch.randn(tokens, experts, generator=g).cuda(), 3)
+
+
+def test_threads_on_their_own_streams():
+    """Calls of many shapes from several threads at once give what one gives."""
+    shapes = [dict(tokens=t, experts=e, inner=i, outer=o)
+              for t, e, i, o in [(1, 4, 64, 128), (200, 24, 72, 136), (900, 3, 129, 520), (60, 700, 64, 64),
+                                 (2500, 5, 264, 304)]]
+    inputs = [layer_inputs(7 + j, **s) for j, s in enumerate(shapes)]
+    want = [layer_step(*a) for a in inputs]
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(4)
+
+    def work(t):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                start.wait()
+                for r in range(10):
+                    j = (t + r) % len(inputs)
+                    got = layer_step(*inputs[j])
+                    stream.synchronize()
+                    for i, (a, b) in enumerate(zip(got, want[j])):
+                        if not torch.equal(a, b):
+                            wrong.append((t, r, i))
+        except Exception as e:  # noqa: BLE001
+            wrong.append((t, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not any(t.is_alive() for t in threads) and not wrong, wrong[:3]
+
+
+@pytest.mark.parametrize("shape", [dict(tokens=1, experts=4, inner=2048, outer=256), dict(),
+                                   dict(tokens=300, experts=7, inner=129, outer=65)])
+def test_a_step_in_a_graph(shape):
+    """A captured step, replayed on new contents of its inputs (the odd sizes
+    take scratch from the pool inside the graph)."""
+    x, up, logits, k = layer_inputs(1, **shape)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer_step(x, up, logits, k)               # sets the device up before the capture
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer_step(x, up, logits, k)
+    for seed in (2, 3):
+        new = layer_inputs(seed, **shape)
+        for a, b in zip((x, up, logits), new):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(out, layer_step(*new))):
+            assert torch.equal(a, b), i
 
 
 # ---------------------------------------------------------------- refusals
