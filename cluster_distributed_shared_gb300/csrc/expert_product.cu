@@ -21,7 +21,7 @@
 // (forward, gathered rows), 309 (input gradient) and 329 (weight gradient,
 // gathered rows) or 1.67 to 1.78 PFLOP/s, where one library product of that
 // size takes 288.  Few rows are bound by reading the weights: 32 tokens over
-// 128 experts (469 MB) 73 us, 95% of the copy rate.
+// 128 experts (469 MB) 73 to 76 us, 92 to 97% of the copy rate.
 //
 // The group sizes are on the device only: every CTA lays the groups' tiles
 // end to end from the offsets and takes every gridDim-th.
@@ -1214,6 +1214,9 @@ int launch_rows(const ProductArgs& p, const CallContext& ctx, const Source& x, c
 // 256 / 128 / 64: 4 groups of 1024 rows, 1024 x 1024 (64 tiles of 256)
 // 12.2 / 15.3 / 20.2; 7 of 333, 512 x 1024 (56) 8.7 / 9.7 / 10.8; 2 of 2048,
 // 512 x 1024 (16; 64 tiles of 128) 15.3 / 13.8 / 11.8.
+// A tile's whole depth is one unit's but for the split: 64 groups of 256 x 256
+// over 131072 rows take 28.7 us where they are equal and 283 where one has half
+// of the rows.
 int launch_weight_grad(const ProductArgs& p, const CallContext& ctx, const Source& x, const Source& w,
                        cudaStream_t stream) {
   const int64_t pairs = ctx.sm_count / 2;

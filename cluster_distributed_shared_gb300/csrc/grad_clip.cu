@@ -305,6 +305,8 @@ __device__ __forceinline__ void scale_chunks(const Table<kTensors>& tab, uint32_
 // pieces 505.  Shorter runs are mostly in L2 and gain nothing; without pieces /
 // with: 128 MiB (13 chunks) 69.7 / 74.4, 256 MiB (26) 134.1 / 135.7, 384 MiB
 // (40) 202.2 / 200.4, 512 MiB (53) 262.6 / 256.3.
+// At its limit of 64 registers (four CTAs an SM) the kernel spills 40 bytes a
+// thread, 44 read back.
 constexpr uint32_t kShared = 32, kPiece = 4;
 
 template <int kTensors>

@@ -19,6 +19,10 @@
  * orders and positions that are out of range read and write nothing outside
  * the stated buffers.
  *
+ * The calls can be captured into a CUDA graph once one has run on the device.
+ * Such a graph reports to the captured stream's status word, so it is not
+ * replayed after dsmem_hist_release().
+ *
  * The same call gives the same bits: sums are taken in an order that sizes and
  * the device alone decide, in 32 bits or more, and rounded once to the output's
  * type.
