@@ -119,6 +119,7 @@ EXPORTS = (
     "dsmem_hist_version",
     "dsmem_route", "dsmem_route_backward", "dsmem_group", "dsmem_grouped_matmul",
     "dsmem_grouped_matmul_wgrad", "dsmem_combine", "dsmem_combine_backward", "dsmem_grad_clip",
+    "dsmem_mx4_quantize", "dsmem_mx4_dequantize", "dsmem_expert_layer",
 )
 
 _lib = None
@@ -456,5 +457,6 @@ def strerror(code: int) -> str:
 
 
 from .experts import (  # noqa: E402
-    dsmem_combine, dsmem_combine_backward, dsmem_grad_clip, dsmem_group, dsmem_grouped_matmul,
-    dsmem_grouped_matmul_wgrad, dsmem_route, dsmem_route_backward)
+    dsmem_combine, dsmem_combine_backward, dsmem_expert_layer, dsmem_grad_clip, dsmem_group,
+    dsmem_grouped_matmul, dsmem_grouped_matmul_wgrad, dsmem_mx4_dequantize, dsmem_mx4_quantize,
+    dsmem_route, dsmem_route_backward)

@@ -77,6 +77,27 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return *reinterpret_cast<const float2*>(&r);
 }
 
+// Eight 16-bit elements of a row of `cols` from column c (a multiple of 8) on,
+// zeros behind its end.  Rows need no more alignment than their elements:
+// 32-bit words, joined where the row begins between two of them (`between`), and
+// single elements at a row's ends.
+__device__ __forceinline__ uint4 aligned_piece(const uint16_t* row, int c, int cols, bool between) {
+  if (!between && c + 8 <= cols) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(row + c);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (between && c > 0 && c + 8 < cols) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(row + c - 1);
+    const uint32_t w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3], w4 = w[4];
+    return make_uint4(__funnelshift_r(w0, w1, 16), __funnelshift_r(w1, w2, 16), __funnelshift_r(w2, w3, 16),
+                      __funnelshift_r(w3, w4, 16));
+  }
+  uint32_t e[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) e[k] = c + k < cols ? row[c + k] : 0u;
+  return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+}
+
 // V elements that move as one access of V * sizeof(T) bytes (up to 16).
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Pack {

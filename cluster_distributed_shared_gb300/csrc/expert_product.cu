@@ -33,6 +33,7 @@
 #include <atomic>
 
 #include "bounded_wait.h"
+#include "divisor.cuh"
 #include "dtypes.cuh"
 #include "experts.h"
 #include "launch_rules.h"
@@ -88,19 +89,6 @@ struct Ring {
 struct Maps {
   CUtensorMap a;  // weights (3-D), or dy
   CUtensorMap b;  // x
-};
-
-// Division of 31-bit values by a fixed divisor: with l = ceil(log2 d) and
-// m = floor(2^32 (2^l - d) / d) + 1, the quotient is (mulhi(m, v) + v) >> l.
-struct Divisor {
-  uint32_t m, l;
-  Divisor(uint32_t d = 1) : m(0), l(0) {
-    while ((uint64_t{1} << l) < d) ++l;
-    m = static_cast<uint32_t>((uint64_t{1} << 32) * ((uint64_t{1} << l) - d) / d + 1);
-  }
-  __device__ __forceinline__ int quotient(int v) const {
-    return static_cast<int>((__umulhi(m, static_cast<uint32_t>(v)) + static_cast<uint32_t>(v)) >> l);
-  }
 };
 
 struct TileArgs {
@@ -934,22 +922,6 @@ struct Layout {
 struct Layouts {
   Layout of[2];
 };
-__device__ __forceinline__ uint4 aligned_piece(const uint16_t* row, int c, int cols, bool between) {
-  if (!between && c + 8 <= cols) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(row + c);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  if (between && c > 0 && c + 8 < cols) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(row + c - 1);
-    const uint32_t w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3], w4 = w[4];
-    return make_uint4(__funnelshift_r(w0, w1, 16), __funnelshift_r(w1, w2, 16), __funnelshift_r(w2, w3, 16),
-                      __funnelshift_r(w3, w4, 16));
-  }
-  uint32_t e[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) e[k] = c + k < cols ? row[c + k] : 0u;
-  return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-}
 __global__ void __launch_bounds__(256) layout_kernel(const __grid_constant__ Layouts layouts) {
   const int cta = blockIdx.x;
   const bool second = cta >= layouts.of[0].ctas;

@@ -106,6 +106,46 @@ int run_product(const ProductArgs& a, const CallContext& ctx, cudaStream_t strea
 // Reads (synchronously) and clears the product kernels' device status word.
 cudaError_t read_and_clear_product_status(uint32_t* out);
 
+// Microscaled 4-bit rows are padded to a multiple of this many elements.
+constexpr int64_t kMx4Pad = 128;
+inline int64_t mx4_padded(int64_t columns) { return (columns + kMx4Pad - 1) / kMx4Pad * kMx4Pad; }
+
+struct Mx4Args {
+  const void* x;  // quantise: floats, `stride` elements between rows
+  int64_t rows, stride;
+  int columns, dtype;
+  uint8_t* values;
+  uint8_t* scales;
+  void* out;  // the way back: floats, contiguous
+};
+cudaError_t launch_quantize(const Mx4Args& a, cudaStream_t stream);
+cudaError_t launch_dequantize(const Mx4Args& a, cudaStream_t stream);
+
+// One of the expert layer's three sets of matrices.
+struct LayerMatrix {
+  const void* values;
+  const uint8_t* scales;  // 4-bit matrices only
+  int64_t row_stride, group_stride;  // of the values: 16-bit elements, or bytes of 4-bit rows
+  int rows, scale_stride;            // 4-bit matrices: of a group, and bytes of a row's scales
+};
+struct LayerArgs {
+  const void* x;
+  int64_t x_stride;
+  int tokens, width, hidden, dtype;
+  const void* logits;
+  int64_t logits_stride;
+  int logits_dtype, experts, top_k, renormalize;
+  LayerMatrix up, gate, down;
+  int mx4, gated, silu;
+  void* out;
+  // Set by run_expert_layer.
+  uint16_t* h;  // [rows][2][h_pitch], the two 16-bit parts of each value
+  int h_pitch;
+  int team;  // warps that split the depth of a tile of the up kernel
+};
+cudaError_t launch_layer_down(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream);
+int run_expert_layer(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream);
+
 struct CombineArgs {
   const void* z;
   int64_t z_rows, z_stride;

@@ -242,6 +242,97 @@ int run_combine_backward(const void* dy, int64_t dy_stride, const void* z, int64
   return finish(launch_combine_backward(a, stream), "combine_backward launch");
 }
 
+int check_mx4(int64_t rows, int32_t columns, int32_t dtype) {
+  DSMH_REQUIRE(known_dtype(dtype), "dtype must be DSMEM_F32, DSMEM_F16 or DSMEM_BF16 (got %d)", dtype);
+  DSMH_REQUIRE(rows >= 0 && rows <= kMaxRows, "rows must be in [0, 2^31) (got %lld)",
+               static_cast<long long>(rows));
+  DSMH_REQUIRE(columns >= 1 && columns <= kMaxRows - 512, "columns must be in [1, 2^31 - 512) (got %d)", columns);
+  return DSMEM_HIST_OK;
+}
+
+int run_quantize(const void* x, int32_t dtype, int64_t rows, int32_t columns, int64_t stride, uint8_t* values,
+                 uint8_t* scales, cudaStream_t stream) {
+  int rc = check_mx4(rows, columns, dtype);
+  if (rc) return rc;
+  DSMH_REQUIRE(stride >= columns, "stride must be >= columns");
+  if (rows == 0) return DSMEM_HIST_OK;
+  DSMH_POINTER(x, dtype_size(dtype));
+  DSMH_POINTER(values, 4);
+  DSMH_POINTER(scales, 1);
+  CallContext ctx;
+  if ((rc = begin_call(stream, &ctx))) return rc;
+  return finish(launch_quantize({x, rows, stride, columns, dtype, values, scales, nullptr}, stream),
+                "quantise launch");
+}
+
+int run_dequantize(const uint8_t* values, const uint8_t* scales, int64_t rows, int32_t columns, int32_t dtype,
+                   void* out, cudaStream_t stream) {
+  int rc = check_mx4(rows, columns, dtype);
+  if (rc) return rc;
+  if (rows == 0) return DSMEM_HIST_OK;
+  DSMH_POINTER(values, 4);
+  DSMH_POINTER(scales, 1);
+  DSMH_POINTER(out, dtype_size(dtype));
+  CallContext ctx;
+  if ((rc = begin_call(stream, &ctx))) return rc;
+  return finish(launch_dequantize({nullptr, rows, columns, columns, dtype, const_cast<uint8_t*>(values),
+                                   const_cast<uint8_t*>(scales), out}, stream), "dequantise launch");
+}
+
+// Takes one set of a layer's matrices, [experts, rows, columns], over.
+int take_matrices(const char* name, const dsmem_matrices_t& m, bool mx4, int64_t rows, int64_t columns,
+                  int32_t experts, LayerMatrix* out) {
+  DSMH_REQUIRE(m.values, "%s: values is NULL", name);
+  DSMH_REQUIRE((m.scales != nullptr) == mx4, "%s: matrices must be all in 16 or all in 4 bits", name);
+  out->values = m.values, out->scales = m.scales, out->rows = static_cast<int>(rows);
+  if (mx4) {
+    DSMH_REQUIRE(!misaligned(m.values, 16), "%s: 4-bit values must be 16-byte aligned", name);
+    out->row_stride = DSMEM_MX4_VALUES(columns);
+    out->group_stride = rows * out->row_stride;
+    out->scale_stride = static_cast<int>(DSMEM_MX4_SCALES(columns));
+    return DSMEM_HIST_OK;
+  }
+  DSMH_REQUIRE(!misaligned(m.values, 2), "%s: values must be aligned to their element size", name);
+  DSMH_REQUIRE(m.row_stride >= columns, "%s: row_stride must be >= %lld", name, static_cast<long long>(columns));
+  DSMH_REQUIRE(experts == 1 || m.group_stride >= 1, "%s: group_stride must be >= 1", name);
+  out->row_stride = m.row_stride;
+  out->group_stride = experts == 1 ? 0 : m.group_stride;
+  return DSMEM_HIST_OK;
+}
+
+int run_layer(const void* x, int64_t x_stride, int32_t dtype, int32_t tokens, int32_t width, int32_t hidden,
+              const void* logits, int32_t logits_dtype, int32_t experts, int64_t logits_stride, int32_t top_k,
+              int32_t renormalize, const dsmem_matrices_t* up, const dsmem_matrices_t* gate,
+              const dsmem_matrices_t* down, int32_t activation, void* out, cudaStream_t stream) {
+  int rc = check_route(logits_dtype, tokens, experts, logits_stride, top_k);
+  if (rc) return rc;
+  DSMH_REQUIRE(dtype == DSMEM_F16 || dtype == DSMEM_BF16, "dtype must be DSMEM_F16 or DSMEM_BF16 (got %d)", dtype);
+  DSMH_REQUIRE(tokens <= DSMEM_LAYER_MAX_TOKENS, "tokens must be in [0, %d] (got %d)", DSMEM_LAYER_MAX_TOKENS, tokens);
+  DSMH_REQUIRE(width >= 1 && hidden >= 1 && width <= DSMEM_LAYER_MAX_WIDTH && hidden <= DSMEM_LAYER_MAX_WIDTH,
+               "width and hidden must be in [1, %d] (got %d and %d)", DSMEM_LAYER_MAX_WIDTH, width, hidden);
+  DSMH_REQUIRE(x_stride >= width, "x_stride must be >= width");
+  DSMH_REQUIRE(activation == DSMEM_RELU || activation == DSMEM_SILU,
+               "activation must be DSMEM_RELU or DSMEM_SILU (got %d)", activation);
+  if (!up) return null_pointer("up");
+  if (!down) return null_pointer("down");
+  LayerArgs a{};
+  a.mx4 = up->scales != nullptr;
+  if ((rc = take_matrices("up", *up, a.mx4, hidden, width, experts, &a.up))) return rc;
+  if (gate && (rc = take_matrices("gate", *gate, a.mx4, hidden, width, experts, &a.gate))) return rc;
+  if ((rc = take_matrices("down", *down, a.mx4, width, hidden, experts, &a.down))) return rc;
+  if (tokens == 0) return DSMEM_HIST_OK;
+  DSMH_POINTER(x, 2);
+  DSMH_POINTER(logits, dtype_size(logits_dtype));
+  DSMH_POINTER(out, 2);
+  a.x = x, a.x_stride = x_stride, a.tokens = tokens, a.width = width, a.hidden = hidden, a.dtype = dtype;
+  a.logits = logits, a.logits_stride = logits_stride, a.logits_dtype = logits_dtype;
+  a.experts = experts, a.top_k = top_k, a.renormalize = renormalize != 0;
+  a.gated = gate != nullptr, a.silu = activation == DSMEM_SILU, a.out = out;
+  CallContext ctx;
+  if ((rc = begin_call(stream, &ctx))) return rc;
+  return run_expert_layer(a, ctx, stream);
+}
+
 int run_clip(const dsmem_grad_t* grads, int32_t num_grads, float max_norm, float* norm,
              cudaStream_t stream) {
   DSMH_REQUIRE(num_grads >= 0, "num_grads must be >= 0 (got %d)", num_grads);
@@ -333,6 +424,31 @@ int dsmem_combine_backward(const void* dy, int64_t dy_stride, const void* z, int
   return dsmh::guarded([&] {
     return dsmh::run_combine_backward(dy, dy_stride, z, z_stride, position, order, weights, tokens, top_k,
                                       width, dtype, dz, dweights, stream);
+  });
+}
+
+int dsmem_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int32_t columns, int64_t stride,
+                       uint8_t* values, uint8_t* scales, cudaStream_t stream) {
+  return dsmh::guarded([&] {
+    return dsmh::run_quantize(x, dtype, rows, columns, stride, values, scales, stream);
+  });
+}
+
+int dsmem_mx4_dequantize(const uint8_t* values, const uint8_t* scales, int64_t rows, int32_t columns,
+                         int32_t dtype, void* out, cudaStream_t stream) {
+  return dsmh::guarded([&] {
+    return dsmh::run_dequantize(values, scales, rows, columns, dtype, out, stream);
+  });
+}
+
+int dsmem_expert_layer(const void* x, int64_t x_stride, int32_t dtype, int32_t tokens, int32_t width,
+                       int32_t hidden, const void* logits, int32_t logits_dtype, int32_t experts,
+                       int64_t logits_stride, int32_t top_k, int32_t renormalize, const dsmem_matrices_t* up,
+                       const dsmem_matrices_t* gate, const dsmem_matrices_t* down, int32_t activation,
+                       void* out, cudaStream_t stream) {
+  return dsmh::guarded([&] {
+    return dsmh::run_layer(x, x_stride, dtype, tokens, width, hidden, logits, logits_dtype, experts,
+                           logits_stride, top_k, renormalize, up, gate, down, activation, out, stream);
   });
 }
 

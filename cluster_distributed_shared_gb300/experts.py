@@ -39,6 +39,10 @@ SIGNATURES = {
     "dsmem_combine": [_p, _i64, _i64, _p, _p, _i64, _i32, _i32, _i32, _p, _p],
     "dsmem_combine_backward": [_p, _i64, _p, _i64, _p, _p, _p, _i64, _i32, _i32, _i32, _p, _p, _p],
     "dsmem_grad_clip": [_p, _i32, _f32, _p, _p],
+    "dsmem_mx4_quantize": [_p, _i32, _i64, _i32, _i64, _p, _p, _p],
+    "dsmem_mx4_dequantize": [_p, _p, _i64, _i32, _i32, _p, _p],
+    "dsmem_expert_layer": [_p, _i64, _i32, _i32, _i32, _i32, _p, _i32, _i32, _i64, _i32, _i32, _p, _p, _p,
+                           _i32, _p, _p],
 }
 
 
@@ -55,7 +59,7 @@ class _Library:
             entry.restype = ctypes.c_int
             self.__dict__[fn] = entry
         self.torch, self.Tensor, self.empty = torch, torch.Tensor, torch.empty
-        self.int32, self.float32 = torch.int32, torch.float32
+        self.int32, self.float32, self.uint8 = torch.int32, torch.float32, torch.uint8
         self.device = torch._C._cuda_getDevice
         self.raw_stream = torch._C._cuda_getCurrentRawStream
         self.codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
@@ -136,7 +140,7 @@ def _elsewhere(call, device, stream, *args, **options):
         with torch.cuda.stream(stream):
             result = call(*args, **options)
     for t in (*args, *options.values()):
-        for each in t if isinstance(t, list) else (t,):
+        for each in t if isinstance(t, (list, tuple)) else (t,):
             if isinstance(each, torch.Tensor):
                 each.record_stream(stream)
     return result
@@ -343,6 +347,145 @@ def dsmem_combine_backward(dy, z, position, order, weights, stream=None):
         position.data_ptr(), order.data_ptr(), weights.data_ptr(), tokens, top_k, width, dtype,
         dz.data_ptr(), dweights.data_ptr(), s))
     return dz, dweights
+
+
+def _mx4_tensors(name, pair, dims, index=None):
+    """The device index of a pair (values, scales) of 4-bit rows, contiguous
+    CUDA uint8 tensors whose last dimensions belong together."""
+    if not isinstance(pair, (tuple, list)) or len(pair) != 2 or not all(
+            isinstance(t, _lib.Tensor) and t.dtype == _lib.uint8 and t.get_device() >= 0 for t in pair):
+        raise TypeError(f"{name} must be a pair (values, scales) of CUDA torch.uint8 tensors")
+    values, scales = pair
+    if dims is not None and values.dim() != dims or values.dim() < 1:
+        raise ValueError(f"{name}'s values must have {dims} dimensions (got {values.dim()})")
+    if values.shape[:-1] != scales.shape[:-1] or values.shape[-1] != 16 * scales.shape[-1] \
+            or values.shape[-1] % 64 or values.shape[-1] == 0:
+        raise ValueError(f"{name}'s values and scales must have rows of 64 and 4 bytes for each 128 elements")
+    if not values.is_contiguous() or not scales.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    got = values.get_device()
+    if scales.get_device() != got or index not in (None, got):
+        raise ValueError(f"{name} must be on one device" if index is None else f"{name} must be on device {index}")
+    return got
+
+
+def dsmem_mx4_quantize(x, stream=None):
+    """Rows of floats [..., columns] to microscaled 4-bit elements: e2m1 values
+    with a power-of-two scale of each 32.  Returns (values, scales), uint8 [...,
+    64 * q] and [..., 4 * q] for q = ceil(columns / 128); what is behind a row's
+    end is zero.  More than one leading dimension must be viewable as one."""
+    if isinstance(x, _lib.Tensor) and x.dim() != 2:
+        if x.dim() < 1 or x.shape[-1] < 1:
+            raise ValueError("x must have rows of one column or more")
+        flat = x.view(-1, x.shape[-1])
+    else:
+        flat = x
+    dtype, index = _float_tensor("x", flat, 2)
+    s = _current(index, stream)
+    if s is None:
+        return _elsewhere(dsmem_mx4_quantize, x.device, stream, x)
+    rows, columns = flat.shape
+    if columns > _MOST:
+        raise _out_of_range(columns=columns)
+    lead, quads = x.shape[:-1], (columns + 127) // 128
+    values = _lib.empty((*lead, 64 * quads), dtype=_lib.uint8, device=x.device)
+    scales = _lib.empty((*lead, 4 * quads), dtype=_lib.uint8, device=x.device)
+    _check(_lib.dsmem_mx4_quantize(
+        flat.data_ptr(), dtype, rows, columns, _row_stride(flat, columns), values.data_ptr(),
+        scales.data_ptr(), s))
+    return values, scales
+
+
+def dsmem_mx4_dequantize(values, scales, columns=None, dtype=None, stream=None):
+    """The floats that 4-bit rows stand for, [..., columns] (default: all, with
+    what pads them), in `dtype` (default torch.float32)."""
+    index = _mx4_tensors("values and scales", (values, scales), None)
+    most = 2 * values.shape[-1]
+    columns = most if columns is None else columns
+    if not most - 128 < columns <= most:
+        raise ValueError(f"columns must be in ({most - 128}, {most}] (got {columns})")
+    dtype = _lib.float32 if dtype is None else dtype
+    code = _lib.codes.get(dtype)
+    if code is None:
+        raise TypeError("dtype must be torch.float32, torch.float16 or torch.bfloat16")
+    if columns > _MOST:
+        raise _out_of_range(columns=columns)
+    s = _current(index, stream)
+    if s is None:
+        return _elsewhere(dsmem_mx4_dequantize, values.device, stream, values, scales, columns, dtype)
+    out = _lib.empty((*values.shape[:-1], columns), dtype=dtype, device=values.device)
+    _check(_lib.dsmem_mx4_dequantize(
+        values.data_ptr(), scales.data_ptr(), values.numel() // values.shape[-1], columns, code,
+        out.data_ptr(), s))
+    return out
+
+
+_ACTIVATIONS = {"relu": 0, "silu": 1}
+
+
+def _layer_matrices(name, m, shape, code, index):
+    """The words of a dsmem_matrices_t for matrices of `shape`, 16-bit ones of
+    the type `code` or a pair of 4-bit tensors."""
+    if not isinstance(m, (tuple, list)):
+        _like(name, m, 3, code, index)
+        if m.shape != shape:
+            raise ValueError(f"{name} must be of shape {tuple(shape)} (got {tuple(m.shape)})")
+        experts, rows, columns = shape
+        if m.is_contiguous():
+            return m.data_ptr(), 0, columns, rows * columns
+        return (m.data_ptr(), 0, m.stride(1) if rows > 1 else columns,
+                m.stride(0) if experts > 1 else rows * columns)
+    _mx4_tensors(name, m, 3, index)
+    values, scales = m
+    want = (*shape[:2], (shape[2] + 127) // 128 * 64)
+    if values.shape != want:
+        raise ValueError(f"{name}'s values must be of shape {want} (got {tuple(values.shape)})")
+    return values.data_ptr(), scales.data_ptr(), 0, 0
+
+
+def dsmem_expert_layer(x, logits, up, down, top_k: int, gate=None, activation: str = "relu",
+                       renormalize: bool = True, stream=None):
+    """A whole expert layer for up to 64 tokens x [tokens, width], as when
+    decoding: with ids and weights those of dsmem_route(logits, top_k,
+    renormalize), the sum over each token's experts e of weight * down[e] h, where
+    h = act(up[e] x), or act(gate[e] x) * (up[e] x) with a `gate`.
+
+    up and gate are [experts, hidden, width], down [experts, width, hidden]: all
+    three tensors of x's type (float16 or bfloat16), or all pairs (values,
+    scales) of dsmem_mx4_quantize.  `activation` is "relu" or "silu"."""
+    code, index = _float_tensor("x", x, 2)
+    if code == F32:
+        raise TypeError("x must be a CUDA float16 or bfloat16 tensor")
+    logits_code, _ = got = _float_tensor("logits", logits, 2)
+    if got[1] != index:
+        raise ValueError(f"logits must be on device {index}")
+    (tokens, width), experts = x.shape, logits.shape[1]
+    if logits.shape[0] != tokens:
+        raise ValueError(f"logits must have {tokens} rows (got {logits.shape[0]})")
+    kind = _ACTIVATIONS.get(activation)
+    if kind is None:
+        raise ValueError('activation must be "relu" or "silu"')
+    first = up[0] if isinstance(up, (tuple, list)) and up else up
+    if not isinstance(first, _lib.Tensor) or first.dim() != 3:
+        raise TypeError("up must be a tensor of 3 dimensions or a pair of such (values, scales)")
+    hidden = first.shape[1]
+    if max(tokens, width, hidden, experts) > _MOST or not 0 <= top_k <= _MOST:
+        raise _out_of_range(tokens=tokens, width=width, hidden=hidden, experts=experts, top_k=top_k)
+    s = _current(index, stream)
+    if s is None:
+        return _elsewhere(dsmem_expert_layer, x.device, stream, x, logits, up, down, top_k, gate,
+                          activation, renormalize)
+    words = array.array("Q", _layer_matrices("up", up, (experts, hidden, width), code, index)
+                        + _layer_matrices("down", down, (experts, width, hidden), code, index))
+    if gate is not None:
+        words.extend(_layer_matrices("gate", gate, (experts, hidden, width), code, index))
+    out = _lib.empty((tokens, width), dtype=x.dtype, device=x.device)
+    at = words.buffer_info()[0]
+    _check(_lib.dsmem_expert_layer(
+        x.data_ptr(), _row_stride(x, width), code, tokens, width, hidden, logits.data_ptr(), logits_code,
+        experts, _row_stride(logits, experts), int(top_k), int(renormalize), at,
+        None if gate is None else at + 64, at + 32, kind, out.data_ptr(), s))
+    return out
 
 
 def dsmem_grad_clip(grads, max_norm: float, out=None, stream=None):

@@ -159,6 +159,76 @@ DSMEM_HIST_API int dsmem_combine_backward(const void* dy, int64_t dy_stride, con
                                           int32_t top_k, int32_t width, int32_t dtype, void* dz,
                                           float* dweights, cudaStream_t stream);
 
+/* Microscaled 4-bit elements (e2m1 values with an e8m0 scale of each 32): a row
+ * of `columns` floats, padded with zeros to a multiple of 128, becomes
+ *   values  columns / 2 bytes, element 2i in the low and 2i + 1 in the high half
+ *           of byte i: sign, two exponent bits, one fraction bit, for 0, 0.5, 1,
+ *           1.5, 2, 3, 4 and 6
+ *   scales  columns / 32 bytes s, each for 2^(s - 127)
+ * where, with m the largest magnitude of a block of 32, s = max(floor(log2 m) -
+ * 2 + 127, 0) (0 for m = 0) and a value is x / 2^(s - 127) rounded to the
+ * nearest, ties to the even fraction, above 6 to 6; signs are kept.  A block with
+ * an infinity or NaN has the scale 255, which is NaN, and zeros for values.
+ * DSMEM_MX4_VALUES and DSMEM_MX4_SCALES give the bytes of a row. */
+#define DSMEM_MX4_VALUES(columns) (((int64_t)(columns) + 127) / 128 * 64)
+#define DSMEM_MX4_SCALES(columns) (((int64_t)(columns) + 127) / 128 * 4)
+
+/* Rows of floats [rows, columns] to 4 bits.
+ *   dtype   of x: DSMEM_F32, DSMEM_F16 or DSMEM_BF16
+ *   stride  elements between rows of x (>= columns)
+ *   values  [rows, DSMEM_MX4_VALUES(columns)], 4-byte aligned;  scales [rows,
+ *           DSMEM_MX4_SCALES(columns)];  both contiguous */
+DSMEM_HIST_API int dsmem_mx4_quantize(const void* x, int32_t dtype, int64_t rows, int32_t columns,
+                                      int64_t stride, uint8_t* values, uint8_t* scales,
+                                      cudaStream_t stream);
+
+/* The floats that 4-bit rows stand for, rounded once to `dtype`; out [rows,
+ * columns] is contiguous. */
+DSMEM_HIST_API int dsmem_mx4_dequantize(const uint8_t* values, const uint8_t* scales, int64_t rows,
+                                        int32_t columns, int32_t dtype, void* out,
+                                        cudaStream_t stream);
+
+#define DSMEM_LAYER_MAX_TOKENS 64
+#define DSMEM_LAYER_MAX_WIDTH 1048576
+
+/* One set of an expert layer's matrices, [experts, rows, columns].  16-bit
+ * matrices have x's type, `scales` NULL, rows of contiguous elements, row_stride
+ * (>= columns) elements apart, and group_stride (>= 1) elements between
+ * matrices.  4-bit matrices are dsmem_mx4_quantize's values and scales of all
+ * experts' rows, contiguous, values 16-byte aligned; the strides are not used. */
+typedef struct dsmem_matrices {
+  const void* values;
+  const uint8_t* scales;
+  int64_t row_stride;
+  int64_t group_stride;
+} dsmem_matrices_t;
+
+enum { DSMEM_RELU = 0, DSMEM_SILU = 1 };
+
+/* A whole expert layer for a few tokens:  with ids and weights those of
+ * dsmem_route(logits), and e = ids[t, j],
+ *   out[t] = sum over j of weights[t, j] * down[e] h
+ *   h = act(up[e] x[t]),  or with a gate  act(gate[e] x[t]) * (up[e] x[t])
+ * act(v) = max(v, 0) or v / (1 + exp(-v)).  A token without choices gives 0.
+ * Products are summed in 32 bits; h is held in two 16-bit numbers an element
+ * (f16: beyond 65504 infinite), and only the output is rounded to x's type.
+ *   dtype       of x and out: DSMEM_F16 or DSMEM_BF16
+ *   tokens      0 .. 64;  width, hidden 1 .. 1048576;  x_stride >= width
+ *   logits      [tokens, experts], logits_stride >= experts elements between
+ *               rows, of logits_dtype (F32, F16 or BF16);  experts 1 .. 1024,
+ *               top_k 1 .. min(experts, 32), renormalize as in dsmem_route
+ *   up, gate    [experts, hidden, width];  gate NULL for a layer without
+ *   down        [experts, width, hidden];  all three in 16 or all in 4 bits
+ *   out         [tokens, width], contiguous
+ * Matrices that no token chose are not read.  Takes scratch from the pool. */
+DSMEM_HIST_API int dsmem_expert_layer(const void* x, int64_t x_stride, int32_t dtype, int32_t tokens,
+                                      int32_t width, int32_t hidden, const void* logits,
+                                      int32_t logits_dtype, int32_t experts, int64_t logits_stride,
+                                      int32_t top_k, int32_t renormalize,
+                                      const dsmem_matrices_t* up, const dsmem_matrices_t* gate,
+                                      const dsmem_matrices_t* down, int32_t activation, void* out,
+                                      cudaStream_t stream);
+
 /* One gradient of dsmem_grad_clip. */
 typedef struct dsmem_grad {
   const void* grad; /* device, `count` elements, contiguous */
