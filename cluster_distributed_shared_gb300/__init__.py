@@ -119,7 +119,8 @@ EXPORTS = (
     "dsmem_hist_version",
     "dsmem_route", "dsmem_route_backward", "dsmem_group", "dsmem_grouped_matmul",
     "dsmem_grouped_matmul_wgrad", "dsmem_combine", "dsmem_combine_backward", "dsmem_grad_clip",
-    "dsmem_mx4_quantize", "dsmem_mx4_dequantize", "dsmem_expert_layer",
+    "dsmem_mx4_quantize", "dsmem_mx4_dequantize", "dsmem_mx4_grouped_matmul",
+    "dsmem_expert_layer",
 )
 
 _lib = None
@@ -458,5 +459,5 @@ def strerror(code: int) -> str:
 
 from .experts import (  # noqa: E402
     dsmem_combine, dsmem_combine_backward, dsmem_expert_layer, dsmem_grad_clip, dsmem_group,
-    dsmem_grouped_matmul, dsmem_grouped_matmul_wgrad, dsmem_mx4_dequantize, dsmem_mx4_quantize,
-    dsmem_route, dsmem_route_backward)
+    dsmem_grouped_matmul, dsmem_grouped_matmul_wgrad, dsmem_mx4_dequantize, dsmem_mx4_grouped_matmul,
+    dsmem_mx4_quantize, dsmem_route, dsmem_route_backward)

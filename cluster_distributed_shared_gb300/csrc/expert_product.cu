@@ -32,20 +32,17 @@
 #include <algorithm>
 #include <atomic>
 
-#include "bounded_wait.h"
 #include "divisor.cuh"
 #include "dtypes.cuh"
 #include "experts.h"
 #include "launch_rules.h"
-#include "ptx.cuh"
-#include "tcgen.cuh"
+#include "product.cuh"
 
 namespace dsmh {
 namespace {
 
 using namespace ptx;
 
-constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kChannels = 128;  // channels of a tile in one CTA
 constexpr int kDepth = 64;      // depth of a stage: 128 bytes of 16-bit elements
 constexpr int kGatherThreads = 256;
@@ -111,79 +108,6 @@ struct TileArgs {
   long long wait_cycles;
   int withhold;        // test hook: each unit's last stage is not copied
 };
-
-__device__ uint32_t g_product_status;  // kStatusProduct once a bounded wait gave up
-
-__device__ __forceinline__ uint32_t flag_set(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-
-// Waits for phase `parity` of an mbarrier, at most `limit` cycles or until
-// another wait of this CTA has given up.
-__device__ __noinline__ bool wait_slow(uint32_t mbar, uint32_t parity, uint32_t gave_up, long long limit,
-                                       uint32_t* status) {
-  const Waited how = bounded_wait([&] { return mbar_try_wait(mbar, parity); },
-                                  [&] { return flag_set(gave_up) != 0u; }, [] { return clock64(); }, limit);
-  if (how != Waited::kGaveUp) return how == Waited::kArrived;
-  asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(gave_up), "r"(1u) : "memory");
-  atomicOr(&g_product_status, kStatusProduct);
-  if (status) *reinterpret_cast<volatile uint32_t*>(status) = kStatusProduct;
-  return false;
-}
-__device__ __forceinline__ bool wait_for(uint32_t mbar, uint32_t parity, uint32_t gave_up,
-                                         long long limit, uint32_t* status) {
-  return mbar_try_wait(mbar, parity) || wait_slow(mbar, parity, gave_up, limit, status);
-}
-
-// Shared-memory matrix descriptors, 128-byte swizzle.  K-major: rows of 128
-// bytes, groups of 8 rows 1024 bytes apart.  MN-major: boxes of 64 elements by
-// 64 depth, 8192 bytes each, in them groups of 8 depth 1024 bytes apart.
-constexpr uint64_t kDescBase = (uint64_t{1} << 46) | (uint64_t{2} << 61) | (uint64_t{1024 >> 4} << 32);
-template <bool kMnMajor>
-__device__ __forceinline__ uint64_t descriptor(uint32_t addr) {
-  return kDescBase | (uint64_t{kMnMajor ? 8192 >> 4 : 1} << 16) | ((addr & 0x3ffffu) >> 4);
-}
-
-__device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-template <typename P>
-__device__ __forceinline__ void st_shared_16(uint32_t addr, const P& p) {
-  static_assert(sizeof(P) == 16, "one vector");
-  const uint4 v = *reinterpret_cast<const uint4*>(&p);
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-template <typename O>
-__device__ __forceinline__ void st_shared_value(uint32_t addr, O v) {
-  if constexpr (sizeof(O) == 2) {
-    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(*reinterpret_cast<const uint16_t*>(&v)) : "memory");
-  } else {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(static_cast<float>(v)) : "memory");
-  }
-}
-
-template <typename O>
-__device__ __forceinline__ O ld_shared_value(uint32_t addr) {
-  O v;
-  if constexpr (sizeof(O) == 2) {
-    uint16_t bits;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(bits) : "r"(addr) : "memory");
-    *reinterpret_cast<uint16_t*>(&v) = bits;
-  } else {
-    float bits;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(bits) : "r"(addr) : "memory");
-    v = static_cast<O>(bits);
-  }
-  return v;
-}
 
 struct Tile {
   int group;       // `groups`: the rows behind the last group
@@ -574,58 +498,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_map(&maps.a);
     prefetch_map(&maps.b);
   }
-  // begin[g + 1] := the group's end, clamped into [0, n]; then the ends are made
-  // monotone and the tiles laid end to end.
-  for (int g = threadIdx.x; g < a.groups; g += kThreads) {
-    const int64_t e = a.offsets[g + 1];
-    begin[g + 1] = static_cast<int32_t>(e < 0 ? 0 : (e > a.n ? a.n : e));
-  }
-  if (threadIdx.x == 0) {
-    begin[0] = 0;
-    if (kKind != kWeightGrad) first[0] = 0;
-    begin[a.groups + 1] = static_cast<int32_t>(a.n);
-  }
-  if (warp == 1) tmem_alloc<kTwo>(tmem_at, kTmemColumns);
-  __syncthreads();
-  // Each warp takes 32 groups of every kWarps * 32: the running maximum
-  // of their ends, then the running sum of their tiles.
-  constexpr int kWarps = kThreads / 32;
-  __shared__ int of_warp[2][32];
-  int end_before = 0, tiles_before = 0;
-  for (int g0 = 0; g0 < schedule.owners(); g0 += kWarps * 32) {
-    const int g = g0 + warp * 32 + lane;
-    const bool owner = g < schedule.owners();
-    int end = owner ? begin[g + 1] : 0;
-    const int most = __reduce_max_sync(kFull, end);
-    if (lane == 0) of_warp[0][warp] = most;
-    __syncthreads();
-    const int other = lane < kWarps ? of_warp[0][lane] : 0;
-    const int earlier = max(end_before, __reduce_max_sync(kFull, lane < warp ? other : 0));
-    end_before = max(end_before, __reduce_max_sync(kFull, other));
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(kFull, end, d);
-      if (lane >= d) end = max(end, up);
-    }
-    end = max(end, earlier);
-    int start = __shfl_up_sync(kFull, end, 1);
-    if (lane == 0) start = earlier;
-    int tiles = owner ? schedule.tiles_of(end - start) : 0;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(kFull, tiles, d);
-      if (lane >= d) tiles += up;
-    }
-    if (lane == 31) of_warp[1][warp] = tiles;
-    __syncthreads();
-    const int sum = lane < kWarps ? of_warp[1][lane] : 0;
-    tiles += tiles_before + __reduce_add_sync(kFull, lane < warp ? sum : 0);
-    tiles_before += __reduce_add_sync(kFull, sum);
-    if (owner) {
-      begin[g + 1] = end;
-      if (kKind != kWeightGrad) first[g + 1] = tiles;
-    }
-  }
+  lay_groups<kThreads>(a.offsets, a.n, a.groups, schedule.owners(), begin, kKind == kWeightGrad ? nullptr : first,
+                       [&](int rows) { return schedule.tiles_of(rows); }, [&] {
+                         if (warp == 1) tmem_alloc<kTwo>(tmem_at, kTmemColumns);
+                       });
   if (kKind == kWeightGrad) {
     // The groups by falling size (by number alone where counting the larger
     // ones of each would take longer than it saves).
@@ -943,21 +819,6 @@ __global__ void __launch_bounds__(256) layout_kernel(const __grid_constant__ Lay
   }
 }
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeFn encoder() {
-  static EncodeFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
-            cudaSuccess || found != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeFn>(p);
-  }();
-  return fn;
-}
-
 // A 16-bit tensor [groups, rows, cols] in boxes of box_rows x 64.
 int make_map(CUtensorMap* map, int dtype, const void* data, int64_t cols, int64_t rows, int64_t groups,
              int64_t row_stride, int64_t group_stride, int box_rows, bool three) {
@@ -1044,14 +905,6 @@ int64_t tile_bound(const ProductArgs& p, int cols, int height) {
   const int64_t across = p.kind == kWeightGrad ? static_cast<int64_t>(p.groups) * ((p.inner + cols - 1) / cols)
                                                : p.n / cols + std::min<int64_t>(p.groups + 1, p.n);
   return across * ((channels + height - 1) / height);
-}
-
-cudaLaunchAttribute cluster_of(int ctas) {
-  cudaLaunchAttribute a = {};
-  a.id = cudaLaunchAttributeClusterDimension;
-  a.val.clusterDim.x = static_cast<unsigned>(ctas);
-  a.val.clusterDim.y = a.val.clusterDim.z = 1;
-  return a;
 }
 
 template <int kKind, int kCols, int kTeam>
@@ -1220,10 +1073,11 @@ int run_product(const ProductArgs& p, const CallContext& ctx, cudaStream_t strea
 }
 
 cudaError_t read_and_clear_product_status(uint32_t* out) {
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_product_status, sizeof(uint32_t));
-  if (e != cudaSuccess) return e;
-  const uint32_t zero = 0;
-  return *out ? cudaMemcpyToSymbol(g_product_status, &zero, sizeof(uint32_t)) : cudaSuccess;
+  uint32_t of_mx4 = 0;
+  cudaError_t e = take_product_status(out);
+  if (e == cudaSuccess) e = read_and_clear_mx4_status(&of_mx4);
+  *out |= of_mx4;
+  return e;
 }
 
 }  // namespace dsmh

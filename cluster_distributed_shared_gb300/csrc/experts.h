@@ -121,6 +121,23 @@ struct Mx4Args {
 cudaError_t launch_quantize(const Mx4Args& a, cudaStream_t stream);
 cudaError_t launch_dequantize(const Mx4Args& a, cudaStream_t stream);
 
+struct Mx4ProductArgs {
+  const uint8_t* x_values;  // [x_rows, 64 quads]
+  const uint8_t* x_scales;  // [x_rows, 4 quads]
+  int64_t x_rows;
+  const uint8_t* w_values;  // [groups, outer, 64 quads]
+  const uint8_t* w_scales;
+  const int32_t* offsets;
+  const int32_t* order;  // may be null
+  int groups, fan;
+  int64_t n;
+  int outer, quads;  // of 128 elements
+  int out_dtype;
+  void* out;
+};
+int run_mx4_product(const Mx4ProductArgs& a, const CallContext& ctx, cudaStream_t stream);
+cudaError_t read_and_clear_mx4_status(uint32_t* out);
+
 // One of the expert layer's three sets of matrices.
 struct LayerMatrix {
   const void* values;

@@ -279,6 +279,31 @@ int run_dequantize(const uint8_t* values, const uint8_t* scales, int64_t rows, i
                                    const_cast<uint8_t*>(scales), out}, stream), "dequantise launch");
 }
 
+int run_mx4_matmul(const uint8_t* x_values, const uint8_t* x_scales, int64_t x_rows, const uint8_t* w_values,
+                   const uint8_t* w_scales, const int32_t* offsets, int32_t groups, const int32_t* order,
+                   int32_t fan, int64_t n, int32_t outer, int32_t inner, void* out, int32_t out_dtype,
+                   cudaStream_t stream) {
+  DSMH_REQUIRE(known_dtype(out_dtype), "out_dtype must be DSMEM_F32, DSMEM_F16 or DSMEM_BF16 (got %d)", out_dtype);
+  int rc = check_product(x_rows, groups, fan, n, outer, inner, DSMEM_F16, DSMEM_F16);
+  if (rc || n == 0) return rc;
+  if (x_rows > 0) {
+    DSMH_POINTER(x_values, 16);
+    DSMH_POINTER(x_scales, 4);
+  }
+  DSMH_POINTER(w_values, 16);
+  DSMH_POINTER(w_scales, 4);
+  DSMH_POINTER(offsets, 4);
+  DSMH_POINTER(out, dtype_size(out_dtype));
+  if (misaligned(order, 4)) return bad_alignment("order");
+  CallContext ctx;
+  if ((rc = begin_call(stream, &ctx))) return rc;
+  if (x_rows == 0)
+    return finish(cudaMemsetAsync(out, 0, static_cast<size_t>(n) * outer * dtype_size(out_dtype), stream),
+                  "cudaMemsetAsync");
+  return run_mx4_product({x_values, x_scales, x_rows, w_values, w_scales, offsets, order, groups, fan, n, outer,
+                          static_cast<int>(mx4_padded(inner) / kMx4Pad), out_dtype, out}, ctx, stream);
+}
+
 // Takes one set of a layer's matrices, [experts, rows, columns], over.
 int take_matrices(const char* name, const dsmem_matrices_t& m, bool mx4, int64_t rows, int64_t columns,
                   int32_t experts, LayerMatrix* out) {
@@ -438,6 +463,16 @@ int dsmem_mx4_dequantize(const uint8_t* values, const uint8_t* scales, int64_t r
                          int32_t dtype, void* out, cudaStream_t stream) {
   return dsmh::guarded([&] {
     return dsmh::run_dequantize(values, scales, rows, columns, dtype, out, stream);
+  });
+}
+
+int dsmem_mx4_grouped_matmul(const uint8_t* x_values, const uint8_t* x_scales, int64_t x_rows,
+                             const uint8_t* w_values, const uint8_t* w_scales, const int32_t* offsets,
+                             int32_t groups, const int32_t* order, int32_t fan, int64_t n, int32_t outer,
+                             int32_t inner, void* out, int32_t out_dtype, cudaStream_t stream) {
+  return dsmh::guarded([&] {
+    return dsmh::run_mx4_matmul(x_values, x_scales, x_rows, w_values, w_scales, offsets, groups, order, fan, n,
+                                outer, inner, out, out_dtype, stream);
   });
 }
 

@@ -69,6 +69,22 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
   }
 }
+// D[tmem] (+)= A[smem] B[smem] of 4-bit elements (e2m1) with scales (e8m0) of
+// each 32 along the depth, which lie in tensor memory; 64 depth, 32-bit sums.
+__device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t a_scales,
+                                        uint32_t b_scales, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+// 512 bytes of scales from shared to tensor memory: 32 rows of 16 bytes become
+// four columns of 32 lanes, repeated in all four quarters of the lanes.  In
+// order with this thread's matrix instructions behind it.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
 // Arrives on an mbarrier of this CTA (of a pair: at this offset in both) once
 // this thread's matrix instructions so far have completed.
 template <bool kPair>
@@ -166,6 +182,10 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 // rest zero.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// 4 bytes, likewise.
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // Arrives on an mbarrier of this CTA once this thread's copies so far have landed.
 __device__ __forceinline__ void copy_arrive(uint32_t mbar) {

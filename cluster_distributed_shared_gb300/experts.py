@@ -41,6 +41,7 @@ SIGNATURES = {
     "dsmem_grad_clip": [_p, _i32, _f32, _p, _p],
     "dsmem_mx4_quantize": [_p, _i32, _i64, _i32, _i64, _p, _p, _p],
     "dsmem_mx4_dequantize": [_p, _p, _i64, _i32, _i32, _p, _p],
+    "dsmem_mx4_grouped_matmul": [_p, _p, _i64, _p, _p, _p, _i32, _p, _i32, _i64, _i32, _i32, _p, _i32, _p],
     "dsmem_expert_layer": [_p, _i64, _i32, _i32, _i32, _i32, _p, _i32, _i32, _i64, _i32, _i32, _p, _p, _p,
                            _i32, _p, _p],
 }
@@ -60,6 +61,7 @@ class _Library:
             self.__dict__[fn] = entry
         self.torch, self.Tensor, self.empty = torch, torch.Tensor, torch.empty
         self.int32, self.float32, self.uint8 = torch.int32, torch.float32, torch.uint8
+        self.bfloat16 = torch.bfloat16
         self.device = torch._C._cuda_getDevice
         self.raw_stream = torch._C._cuda_getCurrentRawStream
         self.codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
@@ -417,6 +419,37 @@ def dsmem_mx4_dequantize(values, scales, columns=None, dtype=None, stream=None):
     _check(_lib.dsmem_mx4_dequantize(
         values.data_ptr(), scales.data_ptr(), values.numel() // values.shape[-1], columns, code,
         out.data_ptr(), s))
+    return out
+
+
+def dsmem_mx4_grouped_matmul(x, weight, offsets, order=None, fan: int = 1, out_dtype=None, stream=None):
+    """dsmem_grouped_matmul of 4-bit rows with 4-bit matrices: x and weight are
+    pairs (values, scales) of dsmem_mx4_quantize, of [rows, inner] and [groups,
+    outer, inner].  The result has `out_dtype` (default torch.bfloat16)."""
+    index = _mx4_tensors("x", x, 2)
+    _mx4_tensors("weight", weight, 3, index)
+    (x_values, x_scales), (w_values, w_scales) = x, weight
+    (rows, pitch), (groups, outer, w_pitch) = x_values.shape, w_values.shape
+    if pitch != w_pitch:
+        raise ValueError(f"x and weight must have rows of one length (got {pitch} and {w_pitch} bytes)")
+    if max(groups, outer, 2 * pitch) > _MOST or not -_MOST <= fan <= _MOST:
+        raise _out_of_range(groups=groups, outer=outer, inner=2 * pitch, fan=fan)
+    dtype = _lib.bfloat16 if out_dtype is None else out_dtype
+    code = _lib.codes.get(dtype)
+    if code is None:
+        raise TypeError("out_dtype must be torch.float32, torch.float16 or torch.bfloat16")
+    _int_tensor("offsets", offsets, groups + 1, index)
+    n, named = rows, None
+    if order is not None:
+        _int_tensor("order", order, None, index)
+        n, named = order.numel(), order.data_ptr()
+    s = _current(index, stream)
+    if s is None:
+        return _elsewhere(dsmem_mx4_grouped_matmul, x_values.device, stream, x, weight, offsets, order, fan, dtype)
+    out = _lib.empty((n, outer), dtype=dtype, device=x_values.device)
+    _check(_lib.dsmem_mx4_grouped_matmul(
+        x_values.data_ptr(), x_scales.data_ptr(), rows, w_values.data_ptr(), w_scales.data_ptr(),
+        offsets.data_ptr(), groups, named, int(fan), n, outer, 2 * pitch, out.data_ptr(), code, s))
     return out
 
 

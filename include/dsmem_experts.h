@@ -188,6 +188,22 @@ DSMEM_HIST_API int dsmem_mx4_dequantize(const uint8_t* values, const uint8_t* sc
                                         int32_t columns, int32_t dtype, void* out,
                                         cudaStream_t stream);
 
+/* Products grouped by key of 4-bit rows with 4-bit matrices: rows, groups,
+ * offsets, order and fan as in dsmem_grouped_matmul, and
+ *   out[p, :] = X[row(p), :] W[g]^T
+ * with X [x_rows, inner] and W [groups, outer, inner] what the 4-bit tensors
+ * stand for, summed in 32 bits.  Rows p of no group, and rows whose source lies
+ * outside x, are 0.
+ *   x_values, w_values  16-byte aligned, and with the scales contiguous
+ *   inner               1 .. 2^31 - 513, rows padded as above
+ *   out                 [n, outer] of out_dtype, any of the three */
+DSMEM_HIST_API int dsmem_mx4_grouped_matmul(const uint8_t* x_values, const uint8_t* x_scales,
+                                            int64_t x_rows, const uint8_t* w_values,
+                                            const uint8_t* w_scales, const int32_t* offsets,
+                                            int32_t groups, const int32_t* order, int32_t fan, int64_t n,
+                                            int32_t outer, int32_t inner, void* out, int32_t out_dtype,
+                                            cudaStream_t stream);
+
 #define DSMEM_LAYER_MAX_TOKENS 64
 #define DSMEM_LAYER_MAX_WIDTH 1048576
 
