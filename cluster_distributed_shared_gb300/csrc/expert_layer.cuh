@@ -207,43 +207,53 @@ struct Slot {
   uint32_t scale[2];
 };
 
-// Two rows of a matrix, as far as a lane reads them; null where there is none.
+// Where a lane's part of the next batch of steps lies in two rows of a matrix.
 struct TwoRows {
   const uint8_t* row[2];
   const uint8_t* scale[2];
 };
-// Row `row` of expert `e`.
+// Row `row` of expert `e`, at the batch that begins with step `step`.
 template <int kHeld>
-__device__ __forceinline__ void point_at(const LayerMatrix& m, int e, int row, bool there, TwoRows& to, int i) {
+__device__ __forceinline__ void point_at(const LayerMatrix& m, int e, int row, int step, TwoRows& to, int i) {
+  const int t = threadIdx.x & 3;
   const int64_t size = kIsMx4<kHeld> ? 1 : 2;
-  to.row[i] = there ? static_cast<const uint8_t*>(m.values) + (e * m.group_stride + row * m.row_stride) * size
-                    : nullptr;
+  to.row[i] = static_cast<const uint8_t*>(m.values) + (e * m.group_stride + row * m.row_stride) * size + step * 64 + t * 16;
   if (kIsMx4<kHeld>)
-    to.scale[i] = there ? m.scales + (static_cast<int64_t>(e) * m.rows + row) * m.scale_stride : nullptr;
+    to.scale[i] = m.scales + (static_cast<int64_t>(e) * m.rows + row) * m.scale_stride + step * 4 + t;
 }
 
-// kWide: rows of 16-bit matrices begin at 16-byte boundaries and are whole
-// vectors.  (4-bit rows always do and are.)
+// The part of a matrix's rows that a batch of kSteps steps takes.
+struct Batch {
+  int step;    // its first step
+  bool whole;  // all of its steps lie inside the rows
+};
+
+// Step d of a batch.  kWide: rows of 16-bit matrices begin at 16-byte boundaries
+// and are whole vectors.  (4-bit rows always do and are.)
 template <int kHeld, bool kWide>
-__device__ __forceinline__ void load_slot(Slot& s, const TwoRows& from, int step, int steps, int depth) {
-  const int t = threadIdx.x & 3;
+__device__ __forceinline__ void load_slot(Slot& s, const TwoRows& from, int d, const Batch& b, int steps, int depth) {
+  const int at = d * 64;
+  if constexpr (kIsMx4<kHeld>) {
+    if (b.whole || b.step + d < steps) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    s.row[i] = make_uint4(0, 0, 0, 0);
-    if constexpr (kIsMx4<kHeld>) {
-      s.scale[i] = 0;
-      if (from.row[i] && step < steps) {
-        s.row[i] = load_once(from.row[i] + step * 64 + t * 16);
-        s.scale[i] = __ldg(from.scale[i] + step * 4 + t);
+      for (int i = 0; i < 2; ++i) {
+        s.row[i] = load_once(from.row[i] + at);
+        s.scale[i] = __ldg(from.scale[i] + d * 4);
       }
-    } else {
-      const int c = step * 32 + t * 8;
-      if (from.row[i] && step < steps && c < depth) {
-        if constexpr (kWide)
-          s.row[i] = load_once(from.row[i] + 2 * static_cast<int64_t>(c));
-        else
-          s.row[i] = aligned_piece(reinterpret_cast<const uint16_t*>(from.row[i]), c, depth,
-                                   (reinterpret_cast<uintptr_t>(from.row[i]) & 2u) != 0);
+    }
+  } else if (kWide && b.whole) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s.row[i] = load_once(from.row[i] + at);
+  } else if (b.step + d < steps) {
+    const int t = threadIdx.x & 3, c = (b.step + d) * 32 + t * 8;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s.row[i] = make_uint4(0, 0, 0, 0);
+      if constexpr (kWide) {
+        if (c < depth) s.row[i] = load_once(from.row[i] + at);
+      } else {
+        const uint16_t* row = reinterpret_cast<const uint16_t*>(from.row[i] + at) - c;
+        s.row[i] = aligned_piece(row, c, depth, (reinterpret_cast<uintptr_t>(row) & 2u) != 0);
       }
     }
   }
@@ -293,35 +303,35 @@ struct Eight {
   uint32_t high[4], low[4];
 };
 
-// Where the rows' side comes from.  x: a token's vector, 16-bit, any alignment.
-// h: the up kernel's rows, two numbers an element, in the fragments' order.
-template <int kHeld, bool kWideX>
+// Where the rows' side comes from; `row` is an element's row there and c its
+// place.  x: a token's vector, 16-bit, any alignment, read again and again.
+template <int kHeld, bool kWide>
 struct FromX {
   static constexpr bool kTwo = kHeld == kMx4F16;  // f16 is the sum of two bf16
   const uint16_t* x;
   int64_t stride;
   int depth;
-  __device__ __forceinline__ void get(int token, int c, Eight& e) const {
-    const uint16_t* row = x + token * stride;
+  __device__ __forceinline__ void get(int row, int c, bool whole, Eight& e) const {
+    const uint16_t* p = x + row * stride;
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (c < depth) {
-      if constexpr (kWideX) v = __ldg(reinterpret_cast<const uint4*>(row + c));
-      else v = aligned_piece(row, c, depth, (reinterpret_cast<uintptr_t>(row) & 2u) != 0);
+    if constexpr (kWide) {
+      if (whole || c < depth) v = __ldg(reinterpret_cast<const uint4*>(p + c));
+    } else {
+      v = aligned_piece(p, c, depth, (reinterpret_cast<uintptr_t>(p) & 2u) != 0);
     }
     if constexpr (kIsMx4<kHeld>) {
-      uint32_t p[4] = {__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                       __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)};
+      const uint32_t w[4] = {__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                             __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        e.high[i] = w[i];
         if constexpr (kHeld == kMx4F16) {
-          const float2 f = pair_to_floats(p[i], __half());
+          const float2 f = pair_to_floats(w[i], __half());
           e.high[i] = floats_to_pair(f, __nv_bfloat16());
           const float2 h = pair_to_floats(e.high[i], __nv_bfloat16());
           // An infinity's rest is 0, not inf - inf.
           e.low[i] = floats_to_pair(make_float2(isinf(h.x) ? 0.0f : f.x - h.x, isinf(h.y) ? 0.0f : f.y - h.y),
                                     __nv_bfloat16());
-        } else {
-          e.high[i] = p[i];
         }
       }
     } else {
@@ -329,11 +339,13 @@ struct FromX {
     }
   }
 };
+// h: the up kernel's rows, two numbers an element, in the fragments' order, with
+// zeros up to whole steps; each row is read once by a CTA.
 struct FromH {
   static constexpr bool kTwo = true;
   const uint16_t* h;  // [rows][2][pitch]
   int pitch;
-  __device__ __forceinline__ void get(int row, int c, Eight& e) const {
+  __device__ __forceinline__ void get(int row, int c, bool, Eight& e) const {
     const uint16_t* p = h + static_cast<int64_t>(row) * 2 * pitch + c;
     const uint4 high = __ldcg(reinterpret_cast<const uint4*>(p));
     const uint4 low = __ldcg(reinterpret_cast<const uint4*>(p + pitch));
@@ -342,46 +354,75 @@ struct FromH {
   }
 };
 
-// One step: the slot's two rows by up to kTiles tiles of eight columns.
-// column[i] is the row of the other side that this lane brings into tile i, or
-// negative.
-template <int kHeld, int kTiles, typename From>
-__device__ __forceinline__ void multiply(const Slot& s, int step, int tiles, const int (&column)[kTiles],
-                                         const From& from, float (&sum)[kTiles][4]) {
+template <int kHeld, bool kTwo>
+__device__ __forceinline__ void mma_eight(float (&sum)[4], uint32_t a0, uint32_t b0, uint32_t a1, uint32_t b1,
+                                          uint32_t a2, uint32_t b2, uint32_t a3, uint32_t b3, const Eight& e) {
+  mma<kHeld>(sum, a0, b0, a1, b1, e.high[0], e.high[1]);
+  mma<kHeld>(sum, a2, b2, a3, b3, e.high[2], e.high[3]);
+  if (kTwo) {
+    mma<kHeld>(sum, a0, b0, a1, b1, e.low[0], e.low[1]);
+    mma<kHeld>(sum, a2, b2, a3, b3, e.low[2], e.low[3]);
+  }
+}
+
+// A batch: the slots' two rows by up to kTiles tiles of eight columns; column[n]
+// is the row of the other side that this lane brings into tile n.  reload(d)
+// fills slot d again as soon as it has been used.  The last tiles come first, so
+// that this is after tile 0 for any number of them.
+template <int kHeld, int kTiles, typename From, typename Reload>
+__device__ __forceinline__ void multiply(Slot (&slot)[kSteps], const Batch& b, int steps, int tiles,
+                                         const int (&column)[kTiles], const From& from, float (&sum)[kTiles][4],
+                                         Reload reload) {
   const int t = threadIdx.x & 3;
   if constexpr (kIsMx4<kHeld>) {
-    const bool twice = __any_sync(kFullWarp, max(s.scale[0], s.scale[1]) > 128u);
-    const uint32_t f0 = factor_of(s.scale[0], twice), f1 = factor_of(s.scale[1], twice);
-    const uint32_t g0 = again_of(s.scale[0]), g1 = again_of(s.scale[1]);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t a[4], b[4];
-      decode8(word_of(s.row[0], q), f0, twice, g0, a);
-      decode8(word_of(s.row[1], q), f1, twice, g1, b);
+    for (int d = 0; d < kSteps; ++d) {
+      if (b.whole || b.step + d < steps) {
+        const Slot& s = slot[d];
+        const bool twice = __any_sync(kFullWarp, max(s.scale[0], s.scale[1]) > 128u);
+        const uint32_t f0 = factor_of(s.scale[0], twice), f1 = factor_of(s.scale[1], twice);
+        const uint32_t g0 = again_of(s.scale[0]), g1 = again_of(s.scale[1]);
+        const int c = (b.step + d) * 128 + t * 32;
+        Eight first[4];
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) {
-        if (kTiles > 1 && n >= tiles) break;
-        Eight e = {};
-        if (column[n] >= 0) from.get(column[n], step * 128 + t * 32 + q * 8, e);
-        mma<kHeld>(sum[n], a[0], b[0], a[1], b[1], e.high[0], e.high[1]);
-        mma<kHeld>(sum[n], a[2], b[2], a[3], b[3], e.high[2], e.high[3]);
-        if (From::kTwo) {
-          mma<kHeld>(sum[n], a[0], b[0], a[1], b[1], e.low[0], e.low[1]);
-          mma<kHeld>(sum[n], a[2], b[2], a[3], b[3], e.low[2], e.low[3]);
+        for (int q = 0; q < 4; ++q) from.get(column[0], c + q * 8, b.whole, first[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[4], w[4];
+          decode8(word_of(s.row[0], q), f0, twice, g0, v);
+          decode8(word_of(s.row[1], q), f1, twice, g1, w);
+          mma_eight<kHeld, From::kTwo>(sum[0], v[0], w[0], v[1], w[1], v[2], w[2], v[3], w[3], first[q]);
+#pragma unroll
+          for (int n = 1; n < kTiles; ++n) {
+            if (n >= tiles) break;
+            Eight e;
+            from.get(column[n], c + q * 8, b.whole, e);
+            mma_eight<kHeld, From::kTwo>(sum[n], v[0], w[0], v[1], w[1], v[2], w[2], v[3], w[3], e);
+          }
         }
       }
+      reload(d);
     }
   } else {
+    constexpr int kAtOnce = From::kTwo ? 2 : 4;  // steps whose columns are loaded together
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n) {
-      if (kTiles > 1 && n >= tiles) break;
-      Eight e = {};
-      if (column[n] >= 0) from.get(column[n], step * 32 + t * 8, e);
-      mma<kHeld>(sum[n], s.row[0].x, s.row[1].x, s.row[0].y, s.row[1].y, e.high[0], e.high[1]);
-      mma<kHeld>(sum[n], s.row[0].z, s.row[1].z, s.row[0].w, s.row[1].w, e.high[2], e.high[3]);
-      if (From::kTwo) {
-        mma<kHeld>(sum[n], s.row[0].x, s.row[1].x, s.row[0].y, s.row[1].y, e.low[0], e.low[1]);
-        mma<kHeld>(sum[n], s.row[0].z, s.row[1].z, s.row[0].w, s.row[1].w, e.low[2], e.low[3]);
+    for (int n = kTiles - 1; n >= 0; --n) {
+      if (n > 0 && n >= tiles) continue;
+#pragma unroll
+      for (int d0 = 0; d0 < kSteps; d0 += kAtOnce) {
+        Eight e[kAtOnce];
+#pragma unroll
+        for (int d = 0; d < kAtOnce; ++d)
+          if (b.whole || b.step + d0 + d < steps)
+            from.get(column[n], (b.step + d0 + d) * 32 + t * 8, b.whole, e[d]);
+#pragma unroll
+        for (int d = 0; d < kAtOnce; ++d) {
+          const Slot& s = slot[d0 + d];
+          if (b.whole || b.step + d0 + d < steps)
+            mma_eight<kHeld, From::kTwo>(sum[n], s.row[0].x, s.row[1].x, s.row[0].y, s.row[1].y, s.row[0].z,
+                                         s.row[1].z, s.row[0].w, s.row[1].w, e[d]);
+          if (n == 0) reload(d0 + d);
+        }
       }
     }
   }
@@ -394,11 +435,6 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 inline bool whole_vectors(const LayerMatrix& m, int columns) {
   return reinterpret_cast<uintptr_t>(m.values) % 16 == 0 && m.row_stride % 8 == 0 && m.group_stride % 8 == 0 &&
          columns % 8 == 0;
-}
-
-// Barrier of the 32 * warps threads of one team.
-__device__ __forceinline__ void team_barrier(int team, int warps) {
-  asm volatile("barrier.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
 }
 
 }  // namespace layer

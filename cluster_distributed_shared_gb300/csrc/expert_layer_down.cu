@@ -28,55 +28,57 @@ __global__ void __launch_bounds__(kLayerThreads, 1) down_kernel(const __grid_con
   const int last = static_cast<int>(width * (blockIdx.x + 1) / gridDim.x);
   const FromH from{a.h, a.h_pitch};
   float* mine = sums + warp * a.tokens * 16;
-  bool waited = false;
 
   for (int channel = first; channel < last; channel += 16) {
     const int count = min(16, last - channel);
     for (int i = lane; i < a.tokens * 16; i += 32) mine[i] = 0.0f;
     __syncwarp();
-    TwoRows rows = {};
-    int ahead = begin / batches, ahead_batch = begin % batches;  // of the next loads
+    int ahead = begin / batches, ahead_batch = begin % batches, left = end - begin;
+    TwoRows at;
+    // Channels beyond the tile's are read as its last one and left out of y.
     const auto point = [&] {
-      const int e = routing.active[ahead];
-      point_at<kHeld>(a.down, e, channel + g, g < count, rows, 0);
-      point_at<kHeld>(a.down, e, channel + 8 + g, g + 8 < count, rows, 1);
+      const int e = routing.active[ahead], last_channel = channel + count - 1;
+      point_at<kHeld>(a.down, e, min(channel + g, last_channel), ahead_batch * kSteps, at, 0);
+      point_at<kHeld>(a.down, e, min(channel + 8 + g, last_channel), ahead_batch * kSteps, at, 1);
     };
+    const auto batch_at = [&](int b) { return Batch{b * kSteps, (b + 1) * kSteps * kDepth<kHeld> <= a.hidden}; };
+    Batch next = batch_at(ahead_batch);
     Slot slot[kSteps];
-    if (begin < end) {
+    if (left > 0) {
       point();
 #pragma unroll
-      for (int d = 0; d < kSteps; ++d)
-        load_slot<kHeld, kWide>(slot[d], rows, ahead_batch * kSteps + d, steps, a.hidden);
+      for (int d = 0; d < kSteps; ++d) load_slot<kHeld, kWide>(slot[d], at, d, next, steps, a.hidden);
     }
-    if (!waited) wait_for_previous();
-    waited = true;
-    for (int i = begin; i < end;) {
+    if (channel == first) wait_for_previous();
+    while (left > 0) {
       const int expert = ahead, columns = routing.rows_of[expert], first_row = routing.start[expert];
       const int tiles = (columns + 7) >> 3;
       int column[kTiles];
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) column[n] = n * 8 + g < columns ? first_row + n * 8 + g : -1;
+      for (int n = 0; n < kTiles; ++n) column[n] = first_row + min(n * 8 + g, columns - 1);
       float sum[kTiles][4];
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = 0.0f;
       do {
-        const int batch = ahead_batch;
-        if (++i < end) {
-          if (++ahead_batch == batches) {
+        const Batch now = next;
+        if (--left > 0) {
+          if (++ahead_batch < batches) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              at.row[i] += kSteps * 64;
+              if (kIsMx4<kHeld>) at.scale[i] += kSteps * 4;
+            }
+          } else {
             ahead_batch = 0;
             ++ahead;
             point();
           }
-        } else {
-          rows = TwoRows{};
+          next = batch_at(ahead_batch);
         }
-#pragma unroll
-        for (int d = 0; d < kSteps; ++d) {
-          const int step = batch * kSteps + d;
-          if (step < steps) multiply<kHeld, kTiles>(slot[d], step, tiles, column, from, sum);
-          load_slot<kHeld, kWide>(slot[d], rows, ahead_batch * kSteps + d, steps, a.hidden);
-        }
-      } while (i < end && ahead == expert);
+        multiply<kHeld, kTiles>(slot, now, steps, tiles, column, from, sum, [&](int d) {
+          if (left > 0) load_slot<kHeld, kWide>(slot[d], at, d, next, steps, a.hidden);
+        });
+      } while (left > 0 && ahead == expert);
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
         if (kTiles > 1 && n >= tiles) break;
@@ -104,7 +106,6 @@ __global__ void __launch_bounds__(kLayerThreads, 1) down_kernel(const __grid_con
     }
     __syncthreads();
   }
-  if (!waited) wait_for_previous();
 }
 
 template <int kHeld, int kTiles, bool kWide>
@@ -133,6 +134,7 @@ cudaError_t launch_held(const LayerArgs& a, const CallContext& ctx, cudaStream_t
     if (!whole_vectors(a.down, a.hidden)) return launch<kHeld, kMaxTokens / 8, false>(a, ctx, stream);
   }
   if (a.tokens <= 8) return launch<kHeld, 1, true>(a, ctx, stream);
+  if (a.tokens <= 32) return launch<kHeld, 4, true>(a, ctx, stream);
   return launch<kHeld, kMaxTokens / 8, true>(a, ctx, stream);
 }
 

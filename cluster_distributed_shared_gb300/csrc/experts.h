@@ -158,7 +158,6 @@ struct LayerArgs {
   // Set by run_expert_layer.
   uint16_t* h;  // [rows][2][h_pitch], the two 16-bit parts of each value
   int h_pitch;
-  int team;  // warps that split the depth of a tile of the up kernel
 };
 cudaError_t launch_layer_down(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream);
 int run_expert_layer(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream);
