@@ -17,11 +17,12 @@ LIB_PATH = os.path.join(PKG, "libdsmemhist.so")
 
 SOURCES = ["cluster_hist.cu", "cluster_ship.cu", "static_scratch.cu", "microbench.cu", "planner.cpp",
            "api.cpp", "experts_api.cpp", "expert_route.cu", "expert_product.cu", "expert_combine.cu",
-           "grad_clip.cu", "mx4_quantize.cu", "expert_layer_up.cu",
-           "expert_layer_down.cu", "mx4_product.cu"]
+           "grad_clip.cu", "mx4_quantize.cu", "expert_layer.cu",
+           "expert_layer_mx4.cu", "mx4_product.cu"]
 HEADERS = [os.path.join(CSRC, name) for name in ("internal.h", "ptx.cuh", "helper_split.h", "experts.h",
                                                  "dtypes.cuh", "tcgen.cuh", "bounded_wait.h",
-                                                 "launch_rules.h", "divisor.cuh", "route.cuh", "mx4.cuh", "expert_layer.cuh", "product.cuh")] + \
+                                                 "launch_rules.h", "divisor.h", "route.cuh", "mx4.cuh", "product.cuh",
+                                                 "expert_layer.cuh")] + \
           [os.path.join(INCLUDE, name) for name in ("dsmem_hist.h", "dsmem_experts.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -13,9 +13,11 @@ struct Divisor {
     while ((uint64_t{1} << l) < d) ++l;
     m = static_cast<uint32_t>((uint64_t{1} << 32) * ((uint64_t{1} << l) - d) / d + 1);
   }
+#ifdef __CUDACC__
   __device__ __forceinline__ int quotient(int v) const {
     return static_cast<int>((__umulhi(m, static_cast<uint32_t>(v)) + static_cast<uint32_t>(v)) >> l);
   }
+#endif
 };
 
 }  // namespace dsmh

@@ -7,18 +7,20 @@
 // by reading the chosen experts' matrices once, and everything follows from
 // keeping loads of them in flight:
 //   * Rows of the matrices go from global memory straight to the registers of
-//     mma.sync fragments.  The depth may be summed in any order, so lane
-//     (g, t) = (lane / 4, lane % 4) takes 16 consecutive bytes of rows g and
-//     g + 8 and the same elements of the rows' side: no shared memory, no
-//     transposition, one load for two (16-bit) or eight (4-bit) instructions.
-//     (A tcgen05 tile would be 128 rows high, of which one token's share of an
-//     SM fills 27, and would pass every byte through shared memory.)
+//     mma.sync fragments, kSteps steps ahead.  The depth may be summed in any
+//     order, so lane (g, t) = (lane / 4, lane % 4) takes 16 consecutive bytes of
+//     rows g and g + 8 and the same elements of the rows' side: no shared memory,
+//     no exchange between lanes, one load for two (16-bit) or eight (4-bit)
+//     instructions.  (A tcgen05 tile would be 128 rows high, of which one token's
+//     share of an SM fills 27, and would pass every byte through shared memory.)
 //   * Every SM reads the same number of rows, every warp the same number of
-//     steps of depth, kSteps of them in flight.
-//   * Each CTA routes all tokens for itself instead of waiting for a launch
-//     that does; the down kernel is launched while the up kernel runs
-//     (programmatic dependent launch) and waits for it only after its own
-//     routing and first loads of weights.
+//     batches of kSteps steps.
+//   * Each CTA routes all tokens for itself instead of waiting for a launch that
+//     does.  The down kernel is launched while the up kernel runs (programmatic
+//     dependent launch), and waits for it only after its own routing and first
+//     loads of weights; for up to 8 tokens both fit an SM together.
+//   * Code that runs once costs about 10 cycles an instruction, for its fetch:
+//     hence loops where unrolled code would do less work.
 // Sums are 32-bit: in the fragments along a warp's part of the depth, then over
 // the warps through shared memory in their order.  Nothing is added atomically.
 #pragma once
@@ -28,147 +30,185 @@
 
 #include <algorithm>
 
+#include "divisor.h"
 #include "dtypes.cuh"
 #include "experts.h"
 #include "mx4.cuh"
+#include "ptx.cuh"
 #include "route.cuh"
 
 namespace dsmh {
-namespace layer {
+namespace {
 
-constexpr int kLayerWarps = 16;
-constexpr int kLayerThreads = kLayerWarps * 32;
-constexpr int kSteps = 4;  // steps of depth a warp has in flight
 constexpr int kMaxTokens = DSMEM_LAYER_MAX_TOKENS;
 constexpr int kMaxRows = kMaxTokens * DSMEM_ROUTE_MAX_TOP_K;
-
 // How the matrices are held, and with them the type of the fragments: 16-bit
 // matrices have x's type; 4-bit ones become bf16, which holds every value they
 // stand for exactly.
 enum Held { kBf16, kF16, kMx4Bf16, kMx4F16 };
 template <int kHeld>
 constexpr bool kIsMx4 = kHeld == kMx4Bf16 || kHeld == kMx4F16;
+// Warps of a CTA whose experts have up to kTiles tiles of eight rows: of the 16
+// that registers allow an SM, the few tokens' kernels of 16-bit matrices take half
+// each.  (Those of 4-bit ones are bound by instructions, and need them all.)
+template <int kHeld, int kTiles>
+constexpr int kWarps = kTiles == 1 && !kIsMx4<kHeld> ? 8 : 16;
+// Steps of depth that a warp has in flight, a batch: as registers allow.
+template <int kHeld>
+constexpr int kSteps = kIsMx4<kHeld> ? 2 : 4;
+// Whether both kernels' CTAs fit an SM together.
+template <int kHeld, int kTiles>
+constexpr bool kShared = kWarps<kHeld, kTiles> == 8;
 template <int kHeld>
 constexpr int kDepth = kIsMx4<kHeld> ? 128 : 32;  // elements of a step
 
 // Everything a CTA knows about the routing.  Rows are (token, expert) pairs,
 // expert after expert, an expert's rows by token.
-struct Routing {
+struct alignas(16) Routing {
   unsigned long long tokens_of[DSMEM_ROUTE_MAX_EXPERTS];  // a bit for each token
-  uint16_t start[DSMEM_ROUTE_MAX_EXPERTS + 1];            // of active experts: first row
-  uint16_t active[DSMEM_ROUTE_MAX_EXPERTS + 1];           // experts that any token chose, by number
+  uint16_t place_of[DSMEM_ROUTE_MAX_EXPERTS];             // among the active experts
+  uint16_t active[DSMEM_ROUTE_MAX_EXPERTS];               // experts that any token chose, by number
+  uint16_t start[DSMEM_ROUTE_MAX_EXPERTS];                // of active experts: first row
   uint16_t rows_of[DSMEM_ROUTE_MAX_EXPERTS];              // of active experts
   float weight[kMaxRows];                                 // of each row
   uint8_t token[kMaxRows];
-  float chosen_weight[kMaxRows];                          // of each token's choices
-  int16_t chosen[kMaxRows];
-  int count;                                              // active experts
+  uint32_t of_warp[16];
+  int count;  // of active experts
 };
 
-// One token's choices by one warp; experts in lane l are l, l + 32, ...
+// What a token's warp hands from its choices to its rows.
+struct Choice {
+  float weight;
+  int id;
+};
+
+// The choices of two tokens, `between` apart (the second may lie behind the last),
+// by one warp, the j-th in lane j, as in routing.
 template <int R>
-__device__ __forceinline__ void choose(const LayerArgs& a, int token, Routing& r) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = token * a.logits_stride;
-  uint32_t key[R];
+__device__ __forceinline__ void choose(const LayerArgs& a, int token, int between, Choice (&choice)[2]) {
+  const int first = (threadIdx.x & 31) * R;
+  uint32_t key[2][R];
+  float v[2][R];
+  const auto load = [&](auto* logits) {
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int e = i * 32 + lane;
-    float v = -INFINITY;
-    if (e < a.experts) {
-      if (a.logits_dtype == DSMEM_F32) v = static_cast<const float*>(a.logits)[row + e];
-      else if (a.logits_dtype == DSMEM_F16) v = to_float(static_cast<const __half*>(a.logits)[row + e]);
-      else v = to_float(static_cast<const __nv_bfloat16*>(a.logits)[row + e]);
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        v[i][r] = first + r < a.experts && token + i * between < a.tokens
+                      ? to_float(logits[(token + i * between) * a.logits_stride + first + r])
+                      : -INFINITY;
+  };
+  if (a.logits_dtype == DSMEM_F32) load(static_cast<const float*>(a.logits));
+  else if (a.logits_dtype == DSMEM_F16) load(static_cast<const __half*>(a.logits));
+  else load(static_cast<const __nv_bfloat16*>(a.logits));
+  Best best[2];
+  float top[2], all[2] = {};
+  int id[2] = {-1, -1};
+  uint32_t chosen[2] = {};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) key[i][r] = rank_key(v[i][r]);
+    best[i] = two_best(key[i], 0u);
+    top[i] = rank_value(__reduce_max_sync(kFullWarp, best[i].key));
+    if (!a.renormalize) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (key[i][r]) all[i] += raised(rank_value(key[i][r]), top[i]);
     }
-    key[i] = rank_key(v);
   }
-  uint32_t best = 0;
+  pick(key, best, a.top_k, id, chosen);
 #pragma unroll
-  for (int i = 0; i < R; ++i) best = max(best, key[i]);
-  const float top = rank_value(__reduce_max_sync(kFullWarp, best));
-  float all = 0.0f;
-  if (!a.renormalize) {
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (key[i]) all += raised(rank_value(key[i]), top);
-    all = warp_sum(all);
-  }
-  int my_id = -1;
-  uint32_t my_key = 0;
-  for (int j = 0; j < a.top_k; ++j) {
-    best = 0;
-#pragma unroll
-    for (int i = 0; i < R; ++i) best = max(best, key[i]);
-    const uint32_t m = __reduce_max_sync(kFullWarp, best);
-    if (m == 0u) break;
-    uint32_t id = 0xffffffffu;
-#pragma unroll
-    for (int i = R - 1; i >= 0; --i)
-      if (key[i] == m) id = i * 32 + lane;
-    id = __reduce_min_sync(kFullWarp, id);
-    if (lane == j) my_id = static_cast<int>(id), my_key = m;
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (i * 32 + lane == static_cast<int>(id)) key[i] = 0u;
-  }
-  const float mine = my_id >= 0 ? raised(rank_value(my_key), top) : 0.0f;
-  if (a.renormalize) all = warp_sum(mine);
-  if (lane < a.top_k) {
-    r.chosen[token * a.top_k + lane] = static_cast<int16_t>(my_id);
-    r.chosen_weight[token * a.top_k + lane] = my_id >= 0 ? mine / all : 0.0f;
-    if (my_id >= 0) atomicOr(&r.tokens_of[my_id], 1ull << token);
+  for (int i = 0; i < 2; ++i) {
+    const float mine = id[i] >= 0 ? raised(rank_value(chosen[i]), top[i]) : 0.0f;
+    const float sum = warp_sum(a.renormalize ? mine : all[i]);
+    choice[i] = Choice{id[i] >= 0 ? mine / sum : 0.0f, id[i]};
   }
 }
 
-// Fills `r`; all threads of the CTA.
-__device__ __forceinline__ void route_all(const LayerArgs& a, Routing& r) {
+// Fills `r` and returns the number of active experts; all threads of the CTA.
+// choices: shared memory for tokens * top_k of them.
+template <int kWarps>
+__device__ __forceinline__ int route_all(const LayerArgs& a, Routing& r, Choice* choices) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < a.experts; e += kLayerThreads) r.tokens_of[e] = 0ull;
+  constexpr int kEach = DSMEM_ROUTE_MAX_EXPERTS / (kWarps * 32);  // experts of a lane
+  for (int e = threadIdx.x; e < a.experts; e += kWarps * 32) r.tokens_of[e] = 0ull;
   __syncthreads();
-  for (int token = warp; token < a.tokens; token += kLayerWarps) {
-    if (a.experts <= 128) choose<4>(a, token, r);
-    else choose<DSMEM_ROUTE_MAX_EXPERTS / 32>(a, token, r);
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int count = 0, rows = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 32) {
-      const int e = e0 + lane;
-      const int mine = e < a.experts ? __popcll(r.tokens_of[e]) : 0;
-      const uint32_t some = __ballot_sync(kFullWarp, mine > 0);
-      int before = mine;
+#pragma unroll 1
+  for (int token = warp; token < a.tokens; token += 2 * kWarps) {
+    Choice c[2];
+    if (a.experts <= 64) choose<2>(a, token, kWarps, c);
+    else if (a.experts <= 128) choose<4>(a, token, kWarps, c);
+    else if (a.experts <= 256) choose<8>(a, token, kWarps, c);
+    else choose<DSMEM_ROUTE_MAX_EXPERTS / 32>(a, token, kWarps, c);
+    if (lane < a.top_k) {
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int up = __shfl_up_sync(kFullWarp, before, d);
-        if (lane >= d) before += up;
+      for (int i = 0; i < 2; ++i) {
+        const int of = token + i * kWarps;
+        if (of >= a.tokens) break;
+        choices[of * a.top_k + lane] = c[i];
+        if (c[i].id >= 0) atomicOr(&r.tokens_of[c[i].id], 1ull << of);
       }
-      if (mine > 0) {
-        const int i = count + __popc(some & ((1u << lane) - 1u));
-        r.active[i] = static_cast<uint16_t>(e);
-        r.start[i] = static_cast<uint16_t>(rows + before - mine);
-        r.rows_of[i] = static_cast<uint16_t>(mine);
-      }
-      count += __popc(some);
-      rows += __shfl_sync(kFullWarp, before, 31);
     }
-    if (lane == 0) r.count = count;
   }
   __syncthreads();
-  // Each choice to its row.  An active expert's place is found by bisection.
-  for (int i = threadIdx.x; i < a.tokens * a.top_k; i += kLayerThreads) {
-    const int e = r.chosen[i];
-    if (e < 0) continue;
-    int low = 0, high = r.count - 1;
-    while (low < high) {
-      const int mid = (low + high) >> 1;
-      if (r.active[mid] < e) low = mid + 1;
-      else high = mid;
-    }
-    const int token = i / a.top_k;
-    const int row = r.start[low] + __popcll(r.tokens_of[e] & ((1ull << token) - 1ull));
-    r.token[row] = static_cast<uint8_t>(token);
-    r.weight[row] = r.chosen_weight[i];
+  // Places among the active experts in the upper half of a word, rows in the lower.
+  const int first = (warp * 32 + lane) * kEach;
+  uint32_t mine = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int rows = first + i < a.experts ? __popcll(r.tokens_of[first + i]) : 0;
+    mine += rows + ((rows > 0) << 16);
   }
+  uint32_t before = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t up = __shfl_up_sync(kFullWarp, before, d);
+    if (lane >= d) before += up;
+  }
+  if (lane == 31) r.of_warp[warp] = before;
+  __syncthreads();
+  const uint32_t other = lane < kWarps ? r.of_warp[lane] : 0u;
+  before += __reduce_add_sync(kFullWarp, lane < warp ? other : 0u) - mine;
+  const int count = static_cast<int>(__reduce_add_sync(kFullWarp, other) >> 16);
+  if (threadIdx.x == 0) r.count = count;
+  if (mine > 0) {
+    int place = static_cast<int>(before >> 16), row = static_cast<int>(before & 0xffffu);
+#pragma unroll 1
+    for (int e = first; e < min(first + kEach, a.experts); ++e) {
+      const int rows = __popcll(r.tokens_of[e]);
+      if (rows == 0) continue;
+      r.place_of[e] = static_cast<uint16_t>(place);
+      r.active[place] = static_cast<uint16_t>(e);
+      r.start[place] = static_cast<uint16_t>(row);
+      r.rows_of[place] = static_cast<uint16_t>(rows);
+      ++place;
+      row += rows;
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int token = warp; token < a.tokens; token += kWarps) {
+    const Choice c = lane < a.top_k ? choices[token * a.top_k + lane] : Choice{0.0f, -1};
+    if (c.id < 0) continue;
+    const int to = r.start[r.place_of[c.id]] + __popcll(r.tokens_of[c.id] & ((1ull << token) - 1ull));
+    r.token[to] = static_cast<uint8_t>(token);
+    r.weight[to] = c.weight;
+  }
+  __syncthreads();
+  return count;
+}
+
+// The routing to the down kernel and there, by all threads, where that does not
+// route for itself while the up kernel runs.
+__device__ __forceinline__ void pass_on(void* to, const Routing& r) {
+  static_assert(sizeof(Routing) % 16 == 0, "whole vectors");
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(Routing) / 16); i += blockDim.x)
+    static_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(&r)[i];
+}
+__device__ __forceinline__ void take_over(Routing& r, const void* from) {
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(Routing) / 16); i += blockDim.x)
+    reinterpret_cast<uint4*>(&r)[i] = __ldcg(static_cast<const uint4*>(from) + i);
   __syncthreads();
 }
 
@@ -200,29 +240,50 @@ __device__ __forceinline__ uint4 load_once(const void* p) {
   return v;
 }
 
-// A lane's part of a step: 16 bytes of two rows, and for 4-bit elements (32 of
-// them, one block) their scales.
+// Eight elements of the rows' side as fragments' words: pairs in the order of
+// the matrices', and for values that one 16-bit number does not hold a second
+// one, the rest.
+struct Eight {
+  uint32_t high[4], low[4];
+};
+
+// A lane's part of a step: 16 bytes of two rows; for 4-bit elements (32 of them,
+// one block) their scales, else its part of the first column tile too.
 struct Slot {
   uint4 row[2];
   uint32_t scale[2];
+  Eight column;
 };
 
-// Where a lane's part of the next batch of steps lies in two rows of a matrix.
-struct TwoRows {
+// Where a lane's part of the next batch of steps lies: in two rows of a matrix,
+// and in its row of the first column tile.
+struct Ahead {
   const uint8_t* row[2];
   const uint8_t* scale[2];
+  const uint16_t* column;
 };
+
 // Row `row` of expert `e`, at the batch that begins with step `step`.
 template <int kHeld>
-__device__ __forceinline__ void point_at(const LayerMatrix& m, int e, int row, int step, TwoRows& to, int i) {
+__device__ __forceinline__ void point_at(const LayerMatrix& m, int e, int row, int step, Ahead& to, int i) {
   const int t = threadIdx.x & 3;
   const int64_t size = kIsMx4<kHeld> ? 1 : 2;
   to.row[i] = static_cast<const uint8_t*>(m.values) + (e * m.group_stride + row * m.row_stride) * size + step * 64 + t * 16;
   if (kIsMx4<kHeld>)
     to.scale[i] = m.scales + (static_cast<int64_t>(e) * m.rows + row) * m.scale_stride + step * 4 + t;
 }
+// On to the next batch of the same rows.
+template <int kHeld>
+__device__ __forceinline__ void move_on(Ahead& at) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    at.row[i] += kSteps<kHeld> * 64;
+    if (kIsMx4<kHeld>) at.scale[i] += kSteps<kHeld> * 4;
+  }
+  if (!kIsMx4<kHeld>) at.column += kSteps<kHeld> * kDepth<kHeld>;
+}
 
-// The part of a matrix's rows that a batch of kSteps steps takes.
+// The part of a matrix's rows that a batch takes.
 struct Batch {
   int step;    // its first step
   bool whole;  // all of its steps lie inside the rows
@@ -231,45 +292,49 @@ struct Batch {
 // Step d of a batch.  kWide: rows of 16-bit matrices begin at 16-byte boundaries
 // and are whole vectors.  (4-bit rows always do and are.)
 template <int kHeld, bool kWide>
-__device__ __forceinline__ void load_slot(Slot& s, const TwoRows& from, int d, const Batch& b, int steps, int depth) {
-  const int at = d * 64;
+__device__ __forceinline__ void load_rows(Slot& s, const Ahead& at, int d, const Batch& b, int steps, int depth) {
+  if (!b.whole && b.step + d >= steps) return;
   if constexpr (kIsMx4<kHeld>) {
-    if (b.whole || b.step + d < steps) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        s.row[i] = load_once(from.row[i] + at);
-        s.scale[i] = __ldg(from.scale[i] + d * 4);
-      }
+    for (int i = 0; i < 2; ++i) {
+      s.row[i] = load_once(at.row[i] + d * 64);
+      s.scale[i] = __ldg(at.scale[i] + d * 4);
     }
   } else if (kWide && b.whole) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) s.row[i] = load_once(from.row[i] + at);
-  } else if (b.step + d < steps) {
+    for (int i = 0; i < 2; ++i) s.row[i] = load_once(at.row[i] + d * 64);
+  } else {
     const int t = threadIdx.x & 3, c = (b.step + d) * 32 + t * 8;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       s.row[i] = make_uint4(0, 0, 0, 0);
       if constexpr (kWide) {
-        if (c < depth) s.row[i] = load_once(from.row[i] + at);
+        if (c < depth) s.row[i] = load_once(at.row[i] + d * 64);
       } else {
-        const uint16_t* row = reinterpret_cast<const uint16_t*>(from.row[i] + at) - c;
+        const uint16_t* row = reinterpret_cast<const uint16_t*>(at.row[i] + d * 64) - c;
         s.row[i] = aligned_piece(row, c, depth, (reinterpret_cast<uintptr_t>(row) & 2u) != 0);
       }
     }
   }
 }
+template <int kHeld, typename From>
+__device__ __forceinline__ void load_column(Slot& s, const Ahead& at, int d, const Batch& b, int steps,
+                                            const From& from) {
+  if (kIsMx4<kHeld> || (!b.whole && b.step + d >= steps)) return;
+  from.fetch(at.column + d * 32, (b.step + d) * 32 + (threadIdx.x & 3) * 8, b.whole, s.column);
+}
 
 // Eight 4-bit elements as bf16 pairs (0,4), (1,5), (2,6), (3,7), scaled.  An
 // element's sign, exponent and fraction bits at those of a bf16 make its value
-// times 2^-126; `factor` (twice, in a pair) makes up for it with the scale.
-// Both products are exact.  `again` is the second factor where one bf16 cannot
-// hold both, which a whole warp takes together.
+// times 2^-126; `factor` (twice, in a pair) makes up for it with the scale, an
+// exact product.  A warp that has a scale for which no bf16 does both multiplies
+// twice (again_of).
 __device__ __forceinline__ uint32_t times_bf16(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t factor, bool twice, uint32_t again, uint32_t (&r)[4]) {
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t factor, uint32_t (&r)[4]) {
   constexpr uint32_t kSign = 0x80008000u, kRest = 0x01c001c0u;
   r[0] = ((w << 6) & kRest) | ((w << 12) & kSign);
   r[1] = ((w << 2) & kRest) | ((w << 8) & kSign);
@@ -277,10 +342,6 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t factor, bool twice,
   r[3] = ((w >> 6) & kRest) | (w & kSign);
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] = times_bf16(r[i], factor);
-  if (twice) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = times_bf16(r[i], again);
-  }
 }
 // 2^(byte - 1) = 2^126 2^(byte - 127) as a bf16 pair where it is one, else
 // 2^126, with 2^(byte - 127) (or NaN) for `again`.
@@ -296,28 +357,21 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
   return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }
 
-// Eight elements of the rows' side as fragments' words: pairs in the order of
-// the matrices', and for values that one 16-bit number does not hold a second
-// one, the rest.
-struct Eight {
-  uint32_t high[4], low[4];
-};
-
-// Where the rows' side comes from; `row` is an element's row there and c its
-// place.  x: a token's vector, 16-bit, any alignment, read again and again.
+// Where the rows' side comes from.  fetch() takes eight elements at p, c of its
+// row.  x: a token's vector, 16-bit, any alignment, read again and again.
 template <int kHeld, bool kWide>
 struct FromX {
   static constexpr bool kTwo = kHeld == kMx4F16;  // f16 is the sum of two bf16
   const uint16_t* x;
   int64_t stride;
   int depth;
-  __device__ __forceinline__ void get(int row, int c, bool whole, Eight& e) const {
-    const uint16_t* p = x + row * stride;
+  __device__ __forceinline__ const uint16_t* row(int r) const { return x + r * stride; }
+  __device__ __forceinline__ void fetch(const uint16_t* p, int c, bool whole, Eight& e) const {
     uint4 v = make_uint4(0, 0, 0, 0);
     if constexpr (kWide) {
-      if (whole || c < depth) v = __ldg(reinterpret_cast<const uint4*>(p + c));
+      if (whole || c < depth) v = __ldg(reinterpret_cast<const uint4*>(p));
     } else {
-      v = aligned_piece(p, c, depth, (reinterpret_cast<uintptr_t>(p) & 2u) != 0);
+      v = aligned_piece(p - c, c, depth, (reinterpret_cast<uintptr_t>(p) & 2u) != 0);
     }
     if constexpr (kIsMx4<kHeld>) {
       const uint32_t w[4] = {__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
@@ -345,8 +399,8 @@ struct FromH {
   static constexpr bool kTwo = true;
   const uint16_t* h;  // [rows][2][pitch]
   int pitch;
-  __device__ __forceinline__ void get(int row, int c, bool, Eight& e) const {
-    const uint16_t* p = h + static_cast<int64_t>(row) * 2 * pitch + c;
+  __device__ __forceinline__ const uint16_t* row(int r) const { return h + static_cast<int64_t>(r) * 2 * pitch; }
+  __device__ __forceinline__ void fetch(const uint16_t* p, int, bool, Eight& e) const {
     const uint4 high = __ldcg(reinterpret_cast<const uint4*>(p));
     const uint4 low = __ldcg(reinterpret_cast<const uint4*>(p + pitch));
     e.high[0] = high.x, e.high[1] = high.y, e.high[2] = high.z, e.high[3] = high.w;
@@ -370,72 +424,437 @@ __device__ __forceinline__ void mma_eight(float (&sum)[4], uint32_t a0, uint32_t
 // fills slot d again as soon as it has been used.  The last tiles come first, so
 // that this is after tile 0 for any number of them.
 template <int kHeld, int kTiles, typename From, typename Reload>
-__device__ __forceinline__ void multiply(Slot (&slot)[kSteps], const Batch& b, int steps, int tiles,
+__device__ __forceinline__ void multiply(Slot (&slot)[kSteps<kHeld>], const Batch& b, int steps, int tiles,
                                          const int (&column)[kTiles], const From& from, float (&sum)[kTiles][4],
                                          Reload reload) {
   const int t = threadIdx.x & 3;
   if constexpr (kIsMx4<kHeld>) {
 #pragma unroll
-    for (int d = 0; d < kSteps; ++d) {
-      if (b.whole || b.step + d < steps) {
+    for (int d = 0; d < kSteps<kHeld>; ++d) {
+      if (!b.whole && b.step + d >= steps) {
+        reload(d);
+        continue;
+      }
+      // The columns' way from the caches passes behind the decoding.
+      const int c = (b.step + d) * 128 + t * 32;
+      Eight first[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) from.fetch(from.row(column[0]) + c + q * 8, c + q * 8, b.whole, first[q]);
+      uint32_t v[4][4], w[4][4];
+      {
         const Slot& s = slot[d];
         const bool twice = __any_sync(kFullWarp, max(s.scale[0], s.scale[1]) > 128u);
         const uint32_t f0 = factor_of(s.scale[0], twice), f1 = factor_of(s.scale[1], twice);
-        const uint32_t g0 = again_of(s.scale[0]), g1 = again_of(s.scale[1]);
-        const int c = (b.step + d) * 128 + t * 32;
-        Eight first[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) from.get(column[0], c + q * 8, b.whole, first[q]);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t v[4], w[4];
-          decode8(word_of(s.row[0], q), f0, twice, g0, v);
-          decode8(word_of(s.row[1], q), f1, twice, g1, w);
-          mma_eight<kHeld, From::kTwo>(sum[0], v[0], w[0], v[1], w[1], v[2], w[2], v[3], w[3], first[q]);
+          decode8(word_of(s.row[0], q), f0, v[q]);
+          decode8(word_of(s.row[1], q), f1, w[q]);
+        }
+        if (twice) {
+          const uint32_t g0 = again_of(s.scale[0]), g1 = again_of(s.scale[1]);
 #pragma unroll
-          for (int n = 1; n < kTiles; ++n) {
-            if (n >= tiles) break;
-            Eight e;
-            from.get(column[n], c + q * 8, b.whole, e);
-            mma_eight<kHeld, From::kTwo>(sum[n], v[0], w[0], v[1], w[1], v[2], w[2], v[3], w[3], e);
+          for (int i = 0; i < 16; ++i) {
+            v[i / 4][i % 4] = times_bf16(v[i / 4][i % 4], g0);
+            w[i / 4][i % 4] = times_bf16(w[i / 4][i % 4], g1);
           }
         }
       }
       reload(d);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        mma_eight<kHeld, From::kTwo>(sum[0], v[q][0], w[q][0], v[q][1], w[q][1], v[q][2], w[q][2], v[q][3], w[q][3],
+                                     first[q]);
+#pragma unroll
+      for (int n = 1; n < kTiles; ++n) {
+        if (n >= tiles) break;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          Eight e;
+          from.fetch(from.row(column[n]) + c + q * 8, c + q * 8, b.whole, e);
+          mma_eight<kHeld, From::kTwo>(sum[n], v[q][0], w[q][0], v[q][1], w[q][1], v[q][2], w[q][2], v[q][3], w[q][3],
+                                       e);
+        }
+      }
     }
   } else {
-    constexpr int kAtOnce = From::kTwo ? 2 : 4;  // steps whose columns are loaded together
 #pragma unroll
-    for (int n = kTiles - 1; n >= 0; --n) {
-      if (n > 0 && n >= tiles) continue;
+    for (int n = kTiles - 1; n >= 1; --n) {
+      if (n >= tiles) continue;
 #pragma unroll
-      for (int d0 = 0; d0 < kSteps; d0 += kAtOnce) {
-        Eight e[kAtOnce];
+      for (int d0 = 0; d0 < kSteps<kHeld>; d0 += 2) {  // the columns of two steps are loaded together
+        Eight e[2];
 #pragma unroll
-        for (int d = 0; d < kAtOnce; ++d)
-          if (b.whole || b.step + d0 + d < steps)
-            from.get(column[n], (b.step + d0 + d) * 32 + t * 8, b.whole, e[d]);
+        for (int d = 0; d < 2; ++d) {
+          const int c = (b.step + d0 + d) * 32 + t * 8;
+          if (b.whole || b.step + d0 + d < steps) from.fetch(from.row(column[n]) + c, c, b.whole, e[d]);
+        }
 #pragma unroll
-        for (int d = 0; d < kAtOnce; ++d) {
+        for (int d = 0; d < 2; ++d) {
           const Slot& s = slot[d0 + d];
           if (b.whole || b.step + d0 + d < steps)
             mma_eight<kHeld, From::kTwo>(sum[n], s.row[0].x, s.row[1].x, s.row[0].y, s.row[1].y, s.row[0].z,
                                          s.row[1].z, s.row[0].w, s.row[1].w, e[d]);
-          if (n == 0) reload(d0 + d);
         }
       }
     }
+#pragma unroll
+    for (int d = 0; d < kSteps<kHeld>; ++d) {
+      const Slot& s = slot[d];
+      if (b.whole || b.step + d < steps)
+        mma_eight<kHeld, From::kTwo>(sum[0], s.row[0].x, s.row[1].x, s.row[0].y, s.row[1].y, s.row[0].z, s.row[1].z,
+                                     s.row[0].w, s.row[1].w, s.column);
+      reload(d);
+    }
+  }
+}
+
+// A warp's way through the batches [begin, end) of tiles of `batches` batches each.
+//   point(tile, step, at)      where the lane's part of the batch at a tile's step lies
+//   look(tile, column)         column[] of a tile; returns how many column tiles it has
+//   before_columns()           runs before anything of the rows' side is read
+//   finish(tile, first, last, tiles, sum)  takes the sums of a tile's batches [first, last)
+template <int kHeld, int kTiles, bool kWide, typename From, typename Point, typename Look, typename Before,
+          typename Finish>
+__device__ __forceinline__ void stream(int begin, int end, int steps, const Divisor& by_batches, int depth,
+                                       const From& from, Point point, Look look, Before before_columns,
+                                       Finish finish) {
+  const int batches = (steps + kSteps<kHeld> - 1) / kSteps<kHeld>;
+  int tile = by_batches.quotient(begin), batch = begin - tile * batches, left = end - begin;
+  const auto batch_at = [&](int b) { return Batch{b * kSteps<kHeld>, (b + 1) * kSteps<kHeld> * kDepth<kHeld> <= depth}; };
+  Ahead at = {};
+  Batch next = batch_at(batch);
+  Slot slot[kSteps<kHeld>];
+  if (left > 0) {
+    point(tile, next.step, at);
+#pragma unroll
+    for (int d = 0; d < kSteps<kHeld>; ++d) load_rows<kHeld, kWide>(slot[d], at, d, next, steps, depth);
+  }
+  before_columns();
+  if (left > 0) {
+#pragma unroll
+    for (int d = 0; d < kSteps<kHeld>; ++d) load_column<kHeld>(slot[d], at, d, next, steps, from);
+  }
+#pragma unroll 1
+  while (left > 0) {
+    const int here = tile, first = batch;
+    int column[kTiles];
+    const int tiles = look(here, column);
+    float sum[kTiles][4];
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = 0.0f;
+    bool more;
+#pragma unroll 1
+    do {
+      const Batch now = next;
+      more = ++batch < batches;
+      if (--left > 0) {
+        next = batch_at(more ? batch : 0);
+        if (more) move_on<kHeld>(at);
+        else point(++tile, 0, at);
+      }
+      multiply<kHeld, kTiles>(slot, now, steps, tiles, column, from, sum, [&](int d) {
+        if (left == 0) return;
+        load_rows<kHeld, kWide>(slot[d], at, d, next, steps, depth);
+        load_column<kHeld>(slot[d], at, d, next, steps, from);
+      });
+    } while (more && left > 0);
+    finish(here, first, batch, tiles, sum);
+    batch = 0;
   }
 }
 
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A tile of h: the active expert, the tile's first row, its rows.
+struct Place {
+  int expert, row, count;
+};
+
+// A tile's sums to h.  v holds columns 2t and 2t + 1 of column tile n, rows g and g
+// + 8 of the weights (with a gate: of the gate and of up).
+template <int kHeld>
+__device__ __noinline__ void to_h(const LayerArgs& a, const Routing& routing, Place p, int n, float4 v) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int first_row = routing.start[p.expert], columns = routing.rows_of[p.expert];
+#pragma unroll 1
+  for (int j = 0; j < 2; ++j, v.x = v.y, v.z = v.w) {
+    const int col = n * 8 + t * 2 + j;
+    if (col >= columns) continue;
+    const int row = first_row + col;
+    uint16_t* h = a.h + static_cast<int64_t>(row) * 2 * a.h_pitch;
+#pragma unroll 1
+    for (int k = 0; k < (a.gated ? 1 : 2); ++k) {
+      const float f = k ? v.z : v.x;
+      const float act = a.silu ? f / (1.0f + expf(-f)) : (f > 0.0f || f != f ? f : 0.0f);
+      const float value = routing.weight[row] * (a.gated ? act * v.z : act);
+      const int at = g + 8 * k;
+      if (at >= p.count) continue;
+      // Two 16-bit numbers hold h to 16 bits or more: what they leave out is far
+      // below the output's rounding.  4-bit fragments pair elements 4 apart.
+      const int c = p.row + at, to = kIsMx4<kHeld> ? (c & ~7) | ((c & 3) << 1) | ((c >> 2) & 1) : c;
+      if constexpr (kHeld == kF16) {
+        const __half b = __float2half_rn(value);
+        h[to] = __half_as_ushort(b);
+        h[a.h_pitch + to] = __half_as_ushort(__float2half_rn(__hisinf(b) ? 0.0f : value - __half2float(b)));
+      } else {
+        const __nv_bfloat16 b = __float2bfloat16_rn(value);
+        h[to] = __bfloat16_as_ushort(b);
+        h[a.h_pitch + to] = __bfloat16_as_ushort(__float2bfloat16_rn(__hisinf(b) ? 0.0f : value - __bfloat162float(b)));
+      }
+    }
+    // Zeros behind the end of each row, up to a whole step.
+    if (p.row + p.count == a.hidden)
+      for (int c = a.hidden + g; c < a.h_pitch; c += 8) {
+        const int to = kIsMx4<kHeld> ? (c & ~7) | ((c & 3) << 1) | ((c >> 2) & 1) : c;
+        h[to] = h[a.h_pitch + to] = 0;
+      }
+  }
+}
+
+// The rows of h of all active experts laid end to end, each CTA an equal share
+// of them.  A tile is 16 rows of weights: 8 rows of h with a gate (rows g of the
+// gate beside rows g of up, so one lane ends up with both), 16 without.  The
+// tiles' batches are again laid end to end, and each warp takes an equal share of
+// these.  Parts of tiles go to shared memory and are joined in order when all
+// warps are done.
+template <int kHeld, int kTiles, bool kWide>
+__global__ void __launch_bounds__(kWarps<kHeld, kTiles> * 32, 16 / kWarps<kHeld, kTiles>)
+    up_kernel(const __grid_constant__ LayerArgs a) {
+  __shared__ Routing routing;
+  extern __shared__ float4 parts[];  // [warp][first, last][tile of columns][lane]
+  launch_dependents();
+  const int active = route_all<kWarps<kHeld, kTiles>>(a, routing, reinterpret_cast<Choice*>(parts));
+  if (a.passes_on && blockIdx.x == 0) pass_on(a.routing, routing);
+
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
+  const int high = a.gated ? 8 : 16;  // rows of h of a tile
+  const int steps = (a.width + kDepth<kHeld> - 1) / kDepth<kHeld>, batches = (steps + kSteps<kHeld> - 1) / kSteps<kHeld>;
+  const int rows = active * a.hidden, each = a.by_ctas.quotient(rows), over = rows - each * gridDim.x;
+  const int begin = each * blockIdx.x + min(static_cast<int>(blockIdx.x), over);
+  const int here = each + (static_cast<int>(blockIdx.x) < over);
+  if (here == 0) return;
+
+  // Tiles do not reach over the end of an expert: those of the first expert
+  // here, then as many of each other one.
+  const int expert0 = a.by_hidden.quotient(begin), row0 = begin - expert0 * a.hidden;
+  const int per_expert = (a.hidden + high - 1) / high;
+  const int rows_first = min(a.hidden - row0, here), in_first = (rows_first + high - 1) / high;
+  const int experts_whole = a.by_hidden.quotient(here - rows_first);
+  const int rows_last = here - rows_first - experts_whole * a.hidden;
+  const int total = (in_first + experts_whole * per_expert + (rows_last + high - 1) / high) * batches;
+  const auto place = [&](int tile) {
+    Place p{expert0, row0 + tile * high, 0};
+    if (tile >= in_first) {
+      const int other = a.by_tiles.quotient(tile - in_first);
+      p.expert = expert0 + 1 + other;
+      p.row = (tile - in_first - other * per_expert) * high;
+    }
+    p.count = min(min(high, a.hidden - p.row), begin + here - (p.expert * a.hidden + p.row));
+    return p;
+  };
+  const auto share = [&](int w) { return static_cast<int>(static_cast<int64_t>(total) * w / kWarps<kHeld, kTiles>); };
+  const int mine = share(warp), my_end = share(warp + 1);
+  const FromX<kHeld, kWide> from{static_cast<const uint16_t*>(a.x), a.x_stride, a.width};
+  // A warp's part of the tile that it ends in, or else begins in.
+  const auto part = [&](int w, bool last) { return parts + (w * 2 + last) * (kTiles * 32) + lane; };
+  // Rows and columns beyond the tile's are read as its last ones and left out of h.
+  const auto point = [&](int tile, int step, Ahead& at) {
+    const Place p = place(tile);
+    const int e = routing.active[p.expert], last = p.row + p.count - 1;
+    point_at<kHeld>(a.gated ? a.gate : a.up, e, min(p.row + g, last), step, at, 0);
+    point_at<kHeld>(a.up, e, min(p.row + (a.gated ? g : 8 + g), last), step, at, 1);
+    if (!kIsMx4<kHeld>) {
+      const int column = min(g, routing.rows_of[p.expert] - 1);
+      at.column = from.row(routing.token[routing.start[p.expert] + column]) + step * 32 + t * 8;
+    }
+  };
+  const auto look = [&](int tile, int (&column)[kTiles]) {
+    const int expert = place(tile).expert, first_row = routing.start[expert], columns = routing.rows_of[expert];
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) column[n] = routing.token[first_row + min(n * 8 + g, columns - 1)];
+    return (columns + 7) >> 3;
+  };
+  const auto finish = [&](int tile, int first, int last, int tiles, const float (&sum)[kTiles][4]) {
+    const bool whole = first == 0 && last == batches;
+    const Place p = place(tile);
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) {
+      if (kTiles > 1 && n >= tiles) break;
+      const float4 v = make_float4(sum[n][0], sum[n][1], sum[n][2], sum[n][3]);
+      if (whole) to_h<kHeld>(a, routing, p, n, v);
+      else part(warp, first == 0)[n * 32] = v;
+    }
+  };
+  stream<kHeld, kTiles, kWide>(mine, my_end, steps, a.by_up_batches, a.width, from, point, look, [] {}, finish);
+  __syncthreads();
+  // Each warp joins the tile that ends in its share having begun before it.
+  const int tile = a.by_up_batches.quotient(mine), tile_begin = tile * batches;
+  if (mine == my_end || tile_begin == mine || tile_begin + batches > my_end) return;
+  int from_warp = warp;
+  while (share(from_warp) > tile_begin) --from_warp;
+  const Place p = place(tile);
+#pragma unroll 1
+  for (int n = 0; n * 8 < routing.rows_of[p.expert]; ++n) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+    for (int w = from_warp; w <= warp; ++w) {
+      if (share(w) == share(w + 1)) continue;
+      const float4 o = part(w, share(w) <= tile_begin)[n * 32];
+      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    }
+    to_h<kHeld>(a, routing, p, n, v);
+  }
+}
+
+// Each CTA an equal share of y's channels, 16 at a time, over all active
+// experts: with their rows of h end to end the layer's second half is one
+// product of great depth, so no two CTAs add to one sum.  The warps split that
+// depth evenly; each adds an expert's columns to its tokens' sums in shared
+// memory when it has passed the expert, and at the end the warps' sums are
+// added in order.
+template <int kHeld, int kTiles, bool kWide>
+__global__ void __launch_bounds__(kWarps<kHeld, kTiles> * 32, 16 / kWarps<kHeld, kTiles>)
+    down_kernel(const __grid_constant__ LayerArgs a) {
+  __shared__ Routing routing;
+  extern __shared__ float sums[];  // [warp][token][16]
+  int active;
+  if (kShared<kHeld, kTiles>) {
+    active = route_all<kWarps<kHeld, kTiles>>(a, routing, reinterpret_cast<Choice*>(sums));
+  } else {
+    wait_for_previous();
+    take_over(routing, a.routing);
+    active = routing.count;
+  }
+
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
+  const int steps = (a.hidden + kDepth<kHeld> - 1) / kDepth<kHeld>, batches = (steps + kSteps<kHeld> - 1) / kSteps<kHeld>;
+  const int total = active * batches;
+  const int begin = total * warp / kWarps<kHeld, kTiles>, end = total * (warp + 1) / kWarps<kHeld, kTiles>;
+  const int each = a.by_ctas.quotient(a.width), over = a.width - each * gridDim.x;
+  const int first = each * blockIdx.x + min(static_cast<int>(blockIdx.x), over);
+  const int last = first + each + (static_cast<int>(blockIdx.x) < over);
+  const FromH from{a.h, a.h_pitch};
+  float* mine = sums + warp * a.tokens * 16;
+
+  for (int channel = first, turn = 0; channel < last; channel += 16, ++turn) {
+    const int count = min(16, last - channel);
+    for (int i = lane; i < a.tokens * 16; i += 32) mine[i] = 0.0f;
+    __syncwarp();
+    // Channels and columns beyond the tile's are read as its last ones and left out of y.
+    const auto point = [&](int tile, int step, Ahead& at) {
+      const int e = routing.active[tile], last_channel = channel + count - 1;
+      point_at<kHeld>(a.down, e, min(channel + g, last_channel), step, at, 0);
+      point_at<kHeld>(a.down, e, min(channel + 8 + g, last_channel), step, at, 1);
+      if (!kIsMx4<kHeld>)
+        at.column = from.row(routing.start[tile] + min(g, routing.rows_of[tile] - 1)) + step * 32 + t * 8;
+    };
+    const auto look = [&](int tile, int (&column)[kTiles]) {
+      const int first_row = routing.start[tile], columns = routing.rows_of[tile];
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) column[n] = first_row + min(n * 8 + g, columns - 1);
+      return (columns + 7) >> 3;
+    };
+    const auto finish = [&](int tile, int, int, int tiles, const float (&sum)[kTiles][4]) {
+      const int first_row = routing.start[tile], columns = routing.rows_of[tile];
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) {
+        if (kTiles > 1 && n >= tiles) break;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int col = n * 8 + t * 2 + j;
+          if (col < columns) {
+            float* p = mine + routing.token[first_row + col] * 16 + g;
+            p[0] += sum[n][j];
+            p[8] += sum[n][j + 2];
+          }
+        }
+      }
+      __syncwarp();
+    };
+    stream<kHeld, kTiles, kWide>(begin, end, steps, a.by_down_batches, a.hidden, from, point, look,
+                                 [&] { if (kShared<kHeld, kTiles> && turn == 0) wait_for_previous(); }, finish);
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.tokens * 16; i += kWarps<kHeld, kTiles> * 32) {
+      float v = sums[i];
+#pragma unroll 4
+      for (int w = 1; w < kWarps<kHeld, kTiles>; ++w) v += sums[w * a.tokens * 16 + i];
+      const int token = i >> 4, c = i & 15;
+      if (c >= count) continue;
+      const int64_t at = static_cast<int64_t>(token) * a.width + channel + c;
+      if (a.dtype == DSMEM_F16) static_cast<__half*>(a.out)[at] = from_float<__half>(v);
+      else static_cast<__nv_bfloat16*>(a.out)[at] = from_float<__nv_bfloat16>(v);
+    }
+    __syncthreads();
+  }
+}
+
+template <int kHeld, int kTiles, bool kWide>
+cudaError_t launch_up(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
+  static SmemLimit limit;
+  const auto kernel = up_kernel<kHeld, kTiles, kWide>;
+  constexpr int bytes = kWarps<kHeld, kTiles> * 2 * kTiles * 32 * static_cast<int>(sizeof(float4));
+  const cudaError_t e = limit.need(reinterpret_cast<const void*>(kernel), ctx.device, bytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<ctx.sm_count, kWarps<kHeld, kTiles> * 32, bytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int kHeld, int kTiles, bool kWide>
+cudaError_t launch_down(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
+  static SmemLimit limit;
+  const auto kernel = down_kernel<kHeld, kTiles, kWide>;
+  // The warps' sums, or while routing the choices.
+  const int bytes = std::max(kWarps<kHeld, kTiles> * a.tokens * 16 * static_cast<int>(sizeof(float)),
+                             a.tokens * a.top_k * static_cast<int>(sizeof(Choice)));
+  const cudaError_t e = limit.need(reinterpret_cast<const void*>(kernel), ctx.device, bytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctx.sm_count));
+  cfg.blockDim = dim3(kWarps<kHeld, kTiles> * 32);
+  cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 // Whether rows of a 16-bit matrix are whole 16-byte vectors.
-inline bool whole_vectors(const LayerMatrix& m, int columns) {
+bool whole_vectors(const LayerMatrix& m, int columns) {
   return reinterpret_cast<uintptr_t>(m.values) % 16 == 0 && m.row_stride % 8 == 0 && m.group_stride % 8 == 0 &&
          columns % 8 == 0;
 }
 
-}  // namespace layer
+template <int kHeld>
+cudaError_t launch_ups(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
+  const bool wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_stride % 8 == 0 && a.width % 8 == 0 &&
+                    (kIsMx4<kHeld> || (whole_vectors(a.up, a.width) && (!a.gated || whole_vectors(a.gate, a.width))));
+  if (!wide) return launch_up<kHeld, kMaxTokens / 8, false>(a, ctx, stream);
+  if (a.tokens <= 8) return launch_up<kHeld, 1, true>(a, ctx, stream);
+  if (a.tokens <= 32) return launch_up<kHeld, 4, true>(a, ctx, stream);
+  return launch_up<kHeld, kMaxTokens / 8, true>(a, ctx, stream);
+}
+
+// Both launches; the down kernel's tiles say whether it routes for itself.
+template <int kHeldUp, int kHeldDown, int kTiles, bool kWide>
+cudaError_t launch_with(LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
+  a.passes_on = !kShared<kHeldDown, kTiles>;
+  const cudaError_t e = launch_ups<kHeldUp>(a, ctx, stream);
+  return e == cudaSuccess ? launch_down<kHeldDown, kTiles, kWide>(a, ctx, stream) : e;
+}
+template <int kHeldUp, int kHeldDown>
+cudaError_t launch_both(LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
+  if constexpr (!kIsMx4<kHeldDown>) {
+    if (!whole_vectors(a.down, a.hidden))
+      return launch_with<kHeldUp, kHeldDown, kMaxTokens / 8, false>(a, ctx, stream);
+  }
+  if (a.tokens <= 8) return launch_with<kHeldUp, kHeldDown, 1, true>(a, ctx, stream);
+  if (a.tokens <= 32) return launch_with<kHeldUp, kHeldDown, 4, true>(a, ctx, stream);
+  return launch_with<kHeldUp, kHeldDown, kMaxTokens / 8, true>(a, ctx, stream);
+}
+
+}  // namespace
 }  // namespace dsmh

@@ -32,7 +32,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "divisor.cuh"
+#include "divisor.h"
 #include "dtypes.cuh"
 #include "experts.h"
 #include "launch_rules.h"

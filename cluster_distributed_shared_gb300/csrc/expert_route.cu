@@ -41,33 +41,7 @@ __device__ __forceinline__ void load_row(const T* row, int experts, float (&v)[R
   }
 }
 
-// A lane's two largest rank keys that have not been picked, and their places.
-// Equal keys come by rising place.
-struct Best {
-  uint32_t key = 0, next = 0;
-  int at = 0, next_at = 0;
-};
-template <int R>
-__device__ __forceinline__ Best two_best(const uint32_t (&key)[R], uint32_t picked) {
-  Best b;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const uint32_t k = (picked >> r & 1u) ? 0u : key[r];
-    if (k > b.key) {
-      b.next = b.key, b.next_at = b.at;
-      b.key = k, b.at = r;
-    } else if (k > b.next) {
-      b.next = k, b.next_at = r;
-    }
-  }
-  return b;
-}
-
-// One warp per token, the row in registers.  Each lane keeps the two largest
-// of its rank keys; a pick is a warp maximum, the lowest lane that holds it,
-// and that lane's next key, for which it looks through its keys again only
-// after two picks.  Lanes hold contiguous runs, so the lowest lane and the
-// first place in it are the lowest index.  Softmax statistics are 32-bit.
+// One warp per token, the row in registers.  Softmax statistics are 32-bit.
 // Bound by instructions: 16384 tokens, 256 experts, 8 picks in 10.5 us; with 32
 // logits a lane, some lanes empty below 1024 experts, 384 take 32 us, 1024 27.
 template <typename T, int R, bool kVector>
@@ -75,17 +49,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
   const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   if (token >= a.tokens) return;
   const int lane = threadIdx.x & 31;
-  uint32_t key[R];
+  uint32_t keys[1][R];
+  const uint32_t(&key)[R] = keys[0];
   {
     float v[R];
     load_row<T, R, kVector>(static_cast<const T*>(a.logits) + token * a.row_stride, a.experts, v);
 #pragma unroll
-    for (int r = 0; r < R; ++r) key[r] = rank_key(v[r]);
+    for (int r = 0; r < R; ++r) keys[0][r] = rank_key(v[r]);
   }
-  static_assert(R <= 32, "a lane's picked keys are bits of a word");
-  uint32_t picked = 0;
-  Best best = two_best(key, 0u);
-  const float top = rank_value(__reduce_max_sync(kFull, best.key));
+  Best best[1] = {two_best(key, 0u)};
+  const float top = rank_value(__reduce_max_sync(kFull, best[0].key));
   float all = 0.0f;
   if (!a.renormalize) {
 #pragma unroll
@@ -93,25 +66,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
       if (key[r]) all += raised(rank_value(key[r]), top);
     all = warp_sum(all);
   }
-  int my_id = -1;
-  uint32_t my_key = 0;
-  for (int j = 0; j < a.top_k; ++j) {
-    const uint32_t m = __reduce_max_sync(kFull, best.key);
-    if (m == 0u) break;
-    const int holder = __ffs(__ballot_sync(kFull, best.key == m)) - 1;
-    const int id = __shfl_sync(kFull, lane * R + best.at, holder);
-    if (lane == j) my_id = id, my_key = m;
-    if (lane == holder) {
-      picked |= 1u << best.at;
-      if (best.next != 0u) {
-        best.key = best.next, best.at = best.next_at;
-        best.next = 0u;
-      } else {
-        best = two_best(key, picked);
-      }
-    }
-    __syncwarp();
-  }
+  int my_ids[1] = {-1};
+  uint32_t my_keys[1] = {};
+  pick(keys, best, a.top_k, my_ids, my_keys);
+  const int my_id = my_ids[0];
+  const uint32_t my_key = my_keys[0];
   const float mine = my_id >= 0 ? raised(rank_value(my_key), top) : 0.0f;
   if (a.renormalize) all = warp_sum(mine);
   if (lane < a.top_k) {

@@ -9,6 +9,7 @@
 
 #include <cuda_runtime_api.h>
 
+#include "divisor.h"
 #include "dsmem_experts.h"
 #include "internal.h"
 
@@ -156,10 +157,13 @@ struct LayerArgs {
   int mx4, gated, silu;
   void* out;
   // Set by run_expert_layer.
+  void* routing;  // for the down kernel, where passes_on says so
+  int passes_on;
   uint16_t* h;  // [rows][2][h_pitch], the two 16-bit parts of each value
   int h_pitch;
+  Divisor by_ctas, by_hidden, by_tiles, by_up_batches, by_down_batches;
 };
-cudaError_t launch_layer_down(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream);
+cudaError_t launch_layer_mx4(LayerArgs& a, const CallContext& ctx, cudaStream_t stream);
 int run_expert_layer(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream);
 
 struct CombineArgs {

@@ -17,7 +17,7 @@
 
 #include <algorithm>
 
-#include "divisor.cuh"
+#include "divisor.h"
 #include "dtypes.cuh"
 #include "experts.h"
 #include "product.cuh"

@@ -4,7 +4,7 @@
 
 #include <algorithm>
 
-#include "divisor.cuh"
+#include "divisor.h"
 #include "dtypes.cuh"
 #include "experts.h"
 #include "mx4.cuh"

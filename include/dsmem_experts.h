@@ -205,7 +205,7 @@ DSMEM_HIST_API int dsmem_mx4_grouped_matmul(const uint8_t* x_values, const uint8
                                             cudaStream_t stream);
 
 #define DSMEM_LAYER_MAX_TOKENS 64
-#define DSMEM_LAYER_MAX_WIDTH 1048576
+#define DSMEM_LAYER_MAX_WIDTH 65536
 
 /* One set of an expert layer's matrices, [experts, rows, columns].  16-bit
  * matrices have x's type, `scales` NULL, rows of contiguous elements, row_stride
@@ -229,7 +229,7 @@ enum { DSMEM_RELU = 0, DSMEM_SILU = 1 };
  * Products are summed in 32 bits; h is held in two 16-bit numbers an element
  * (f16: beyond 65504 infinite), and only the output is rounded to x's type.
  *   dtype       of x and out: DSMEM_F16 or DSMEM_BF16
- *   tokens      0 .. 64;  width, hidden 1 .. 1048576;  x_stride >= width
+ *   tokens      0 .. 64;  width, hidden 1 .. 65536;  x_stride >= width
  *   logits      [tokens, experts], logits_stride >= experts elements between
  *               rows, of logits_dtype (F32, F16 or BF16);  experts 1 .. 1024,
  *               top_k 1 .. min(experts, 32), renormalize as in dsmem_route
