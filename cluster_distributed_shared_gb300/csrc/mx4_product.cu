@@ -4,18 +4,17 @@
 // D[rows, channels] = x W[g]^T: 128 rows high, kCols channels wide, so that a
 // lane of the accumulators is a row of the output.  One persistent CTA per SM.
 // Warp 0 copies the matrices' values by TMA (256 elements of depth a stage: 128
-// bytes a row, swizzled), warp 1 issues the matrix instructions, warps 2..5 write
-// finished accumulators out, the next eight copy the rows that the order names,
-// 16 bytes a copy, and the last four bring both sides' scales, four stages at a
-// time.  Scales are kept row by row, as quantisation writes them; shared memory
-// has them in the order that tensor memory wants: chunks of 128 rows by 4 scales,
-// row r at 16 (r % 32) + 4 (r / 32).
+// bytes a row, swizzled), warp 1 issues the matrix instructions, the next eight
+// write finished sums out, eight copy the rows that the order names, 16 bytes a
+// copy, and the last two bring both sides' scales.  Scales are kept row by row, as
+// quantisation writes them; shared memory has them in the order that tensor memory
+// wants: chunks of 128 rows by 4 scales, row r at 16 (r % 32) + 4 (r / 32).
 //
 // 4-bit operands are multiplied so fast that a tile is bound by what it takes in:
 // 128 x 256 tiles take in three quarters of the bytes of 128 x 128 ones.  Their
 // sums fill half of tensor memory, beside the scales, so there is no second
 // accumulator; the first stage of a tile is multiplied by halves instead, each
-// of which begins when the last tile's half has been written out.
+// of which begins when the last tile's half is in its warps' registers.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -34,32 +33,31 @@ constexpr int kHigh = 128;        // rows of a tile
 constexpr int kStageBytes = 128;  // of a row in a stage: 256 elements
 constexpr int kShifts = 2;        // groups of copying warps that take stages in turn
 constexpr int kShift = 128;       // threads of one
-constexpr int kFirstCopy = 6;     // TMA, matrix instructions, 4 warps of output
-constexpr int kRelayWarp = kFirstCopy + kShifts * kShift / 32;
-constexpr int kFirstScale = kRelayWarp + 1;
-constexpr int kScaleThreads = 128;
+constexpr int kOutWarps = 8;      // four for either half of a tile's columns
+constexpr int kFirstCopy = 2 + kOutWarps;  // behind TMA, matrix instructions and output
+constexpr int kFirstScale = kFirstCopy + kShifts * kShift / 32;
+constexpr int kScaleThreads = 64;
 constexpr int kThreads = kFirstScale * 32 + kScaleThreads;
-constexpr int kLine = 64;               // bytes of an output row that a warp writes at a time
-constexpr int kStageOut = 32 * kLine;   // output staging of a warp
+constexpr int kStageOut = 2048;         // output staging of a warp
 constexpr int kBarrierBytes = 320;
 constexpr int kChunk = 512;             // scales of 128 rows by 128 elements
-constexpr int kBlock = 4;               // stages whose scales are brought together
 
 template <int kCols>
 struct Ring {
   static constexpr int kA = kHigh * kStageBytes, kB = kCols * kStageBytes;
-  static constexpr int kStage = kA + kB;
-  static constexpr int kMostStages = kCols == 256 ? 4 : 8;
-  static constexpr int kChunksB = (kCols + 127) / 128;             // of 128 elements' scales
-  static constexpr int kScales = 2 * kBlock * (1 + kChunksB) * kChunk;  // of a block
-  // Tensor memory: the sums of one tile in two halves, or of two tiles, then each
-  // stage's scales.
+  static constexpr int kChunksB = (kCols + 127) / 128;  // of 128 elements' scales
+  static constexpr int kStage = kA + kB + 2 * (1 + kChunksB) * kChunk;
+  static constexpr int kMostStages = kCols == 256 ? 4 : (kCols == 128 ? 6 : 8);
+  // Tensor memory: the sums of one tile in two halves, or of two tiles, then the
+  // scales of each stage's rows, and those of kKept parts of the channels.
   static constexpr int kBuffers = kCols == 256 ? 1 : 2, kHalves = kCols == 256 ? 2 : 1;
-  static constexpr int kScaleColumns = 8 * (1 + kChunksB);
+  static constexpr int kKept = 8;
+  static constexpr int kMine = kCols / 2;  // columns of an output warp
+  static constexpr int kRowScales = kBuffers * kCols, kChannelScales = kRowScales + 8 * kMostStages;
   static constexpr uint32_t kColumns = 512;
-  static_assert(kBuffers * kCols + kMostStages * kScaleColumns <= 512, "tensor memory");
+  static_assert(kMostStages <= kKept && kChannelScales + 8 * kChunksB * kKept <= 512, "tensor memory");
   static int smem_bytes(int groups, int stages) {
-    return 1024 + stages * kStage + 2 * kScales + 4 * kStageOut + kBarrierBytes + 2 * 4 * (groups + 2);
+    return 1024 + stages * kStage + kOutWarps * kStageOut + kBarrierBytes + 2 * 4 * (groups + 2);
   }
   // As many stages as fit.
   static int stages(int groups) {
@@ -69,12 +67,17 @@ struct Ring {
   }
 };
 
+struct Maps {
+  CUtensorMap weights;
+  CUtensorMap out;  // where rows are whole 16-byte vectors
+};
+
 struct Args {
   const int32_t* offsets;
   const int32_t* order;
   int64_t n;
   int x_rows, groups, outer, quads, stages;
-  Divisor fan, by_chan_tiles;
+  Divisor fan;
   const uint8_t* x_values;
   const uint8_t* x_scales;
   const uint8_t* w_scales;
@@ -89,17 +92,16 @@ struct Tile {
   int group;  // `groups`: the rows behind the last group
   int row0, end, chan0;
   int blocks;  // stages of depth
+  bool fresh;  // the first of its channels in this CTA
 };
 
 template <int kCols>
 struct Schedule {
   const int32_t* begin;  // [groups + 2] first row of each group, in shared memory
   const int32_t* first;  // [groups + 2] first tile
-  Divisor by_chan_tiles;
-  int groups, chan_tiles, blocks, group;
+  int groups, chan_tiles, blocks, group, mine;
   __device__ __forceinline__ Schedule(const int32_t* b, const int32_t* f, const Args& a)
-      : begin(b), first(f), by_chan_tiles(a.by_chan_tiles), groups(a.groups),
-        chan_tiles((a.outer + kCols - 1) / kCols), blocks((a.quads + 1) / 2), group(0) {}
+      : begin(b), first(f), groups(a.groups), chan_tiles((a.outer + kCols - 1) / kCols), blocks((a.quads + 1) / 2), group(0), mine(0) {}
   __device__ __forceinline__ int tiles_of(int rows) const { return (rows + kHigh - 1) / kHigh * chan_tiles; }
   // Tile t; t only grows from call to call.  Many groups may be empty.
   __device__ __forceinline__ Tile at(int t) {
@@ -112,55 +114,74 @@ struct Schedule {
       }
       group = low;
     }
-    const int i = t - first[group], across = by_chan_tiles.quotient(i);
+    const int i = t - first[group], high = (begin[group + 1] - begin[group] + kHigh - 1) / kHigh;
     Tile r;
     r.group = group;
-    r.row0 = begin[group] + across * kHigh;
+    r.row0 = begin[group] + i % high * kHigh;
     r.end = begin[group + 1];
-    r.chan0 = (i - across * chan_tiles) * kCols;
+    r.chan0 = i / high * kCols;
     r.blocks = group < groups ? blocks : 0;
+    r.fresh = t == mine || i % high == 0;
     return r;
   }
 };
+
+// The first of all tiles that is a CTA's.
+__device__ __forceinline__ int share(int all, int cta) {
+  return static_cast<int>(static_cast<int64_t>(all) * cta / static_cast<int>(gridDim.x));
+}
 
 // Descriptor of a chunk of scales: not swizzled, groups of 8 rows of 16 bytes.
 __device__ __forceinline__ uint64_t scale_descriptor(uint32_t addr) {
   return (uint64_t{1} << 46) | (uint64_t{128 >> 4} << 32) | ((addr & 0x3ffffu) >> 4);
 }
 
-// kN columns of a warp's 32 rows, through its staging memory: 16-byte pieces of
-// a row, exchanged so that neighbouring rows meet other banks.
-template <int kN, typename O>
-__device__ __forceinline__ void store_columns(const Args& a, int row0, int end, int chan, const uint32_t (&r)[kN],
-                                              uint32_t staging) {
-  const int lane = threadIdx.x & 31;
-  constexpr int V = 16 / sizeof(O), kPieces = kN / V;
+// kLine bytes of each of a warp's 32 rows, in lane l row l, as channels [chan, limit)
+// to the output through its staging memory: 16-byte pieces of a row, exchanged so
+// that neighbouring rows meet other banks, as a map with a swizzle of 64 bytes has
+// them.  Where all rows are there, and whole 64 bytes, one TMA store takes them, and
+// costs the warp a quarter of the instructions.  (Rows written sector by sector
+// from the lanes that hold them took twice as long as this path without TMA.)
+template <typename O, int kLine>
+__device__ __forceinline__ void store_lines(const Args& a, const CUtensorMap* out_map, int row0, int end, int chan, int limit,
+                                            const uint32_t (&r)[kLine / 4], uint32_t staging) {
+  const int lane = threadIdx.x & 31, rows = min(32, end - row0);
+  constexpr int V = 16 / sizeof(O), kPieces = kLine / 16;
   const auto piece_at = [&](int row, int q) {
-    return staging + row * (kN * sizeof(O)) + ((q ^ (row * kPieces / 8 & (kPieces - 1))) << 4);
+    return staging + row * kLine + ((q ^ (row * kPieces / 8 & (kPieces - 1))) << 4);
   };
+  if (lane == 0) store_wait_read();
+  __syncwarp();
 #pragma unroll
-  for (int q = 0; q < kPieces; ++q) {
-    Pack<O, V> p;
-#pragma unroll
-    for (int v = 0; v < V; ++v) p.v[v] = from_float<O>(__uint_as_float(r[q * V + v]));
-    st_shared_16(piece_at(lane, q), p);
+  for (int q = 0; q < kPieces; ++q)
+    st_shared_16(piece_at(lane, q), make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]));
+  if (kLine == 64 && a.wide_out && rows == 32) {
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) tma_store_2d(out_map, staging, chan, row0);
+    return;
   }
   __syncwarp();
   O* out = static_cast<O*>(a.out) + static_cast<int64_t>(row0) * a.outer + chan;
-  const int rows = min(32, end - row0);
   if (a.wide_out) {
+    const int q = lane % kPieces;
+    uint4* to = reinterpret_cast<uint4*>(out + static_cast<int64_t>(lane / kPieces) * a.outer + q * V);
+    const int64_t step = static_cast<int64_t>(32 / kPieces) * a.outer / V;
+    if (chan + q * V < limit) {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int row = (i * 32 + lane) / kPieces, q = lane & (kPieces - 1);
-      const uint4 p = ld_shared_16(piece_at(row, q));
-      if (row < rows && chan + q * V < a.outer)
-        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(row) * a.outer + q * V) = p;
+      for (int i = 0; i < kPieces; ++i, to += step) {
+        const int row = i * (32 / kPieces) + lane / kPieces;
+        if (row < rows) *to = ld_shared_16(piece_at(row, q));
+      }
     }
   } else {
-    for (int row = 0; row < rows; ++row, out += a.outer)
-#pragma unroll
-      for (int j = lane; j < kN; j += 32)
-        if (chan + j < a.outer) out[j] = ld_shared_value<O>(piece_at(row, j / V) + j % V * sizeof(O));
+    constexpr int kEach = kLine / static_cast<int>(sizeof(O));  // values of a line
+    const int j = lane % kEach;
+    if (chan + j < limit) {
+#pragma unroll 1
+      for (int row = lane / kEach; row < rows; row += 32 / kEach)
+        out[static_cast<int64_t>(row) * a.outer + j] = ld_shared_value<O>(piece_at(row, j / V) + j % V * sizeof(O));
+    }
   }
   __syncwarp();
 }
@@ -175,23 +196,61 @@ __device__ __forceinline__ void store_zeros(const Args& a, int row0, int end, in
     if (a.wide_out) {
       for (int c = lane * V; c < cols; c += 32 * V) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
     } else {
-      for (int c = lane; c < cols; c += 32) out[c] = from_float<O>(0.0f);
+      for (int c = lane; c < cols; c += 32) out[c] = O(0);
     }
   }
 }
 
-// A warp's 32 rows of a tile's columns [first, last) from tensor memory to the output.
-template <typename O>
-__device__ __forceinline__ void store_tile(const Args& a, const Tile& t, int row0, int first, int last, uint32_t tmem,
-                                           uint32_t staging) {
-  constexpr int kN = kLine / static_cast<int>(sizeof(O));
+// A pair of values (bits of floats) rounded to bf16 or f16 here and now, in one
+// place for both: left to the compiler, roundings move behind the next loads, whose
+// values then do not fit registers.
+__device__ __forceinline__ uint32_t pair_now(uint32_t low, uint32_t high, bool bf16) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t@p cvt.rn.bf16x2.f32 %0, %1, %2;\n\t"
+      "@!p cvt.rn.f16x2.f32 %0, %1, %2;\n\t}"
+      : "=r"(r)
+      : "f"(__uint_as_float(high)), "f"(__uint_as_float(low)), "r"(static_cast<uint32_t>(bf16)));
+  return r;
+}
+
+// A warp's 32 rows by kMine columns from tensor memory to the output, up to 64 bytes
+// of a row at a time; free() is called when they have left tensor memory.  16-bit
+// values are first all brought to registers, as pairs, so that this is soon.
+template <int kMine, typename O, typename Free>
+__device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap* out_map, const Tile& t, int row0, int chan,
+                                           uint32_t tmem, uint32_t staging, Free free) {
+  constexpr int kLine = kMine * static_cast<int>(sizeof(O)) < 64 ? kMine * static_cast<int>(sizeof(O)) : 64;
+  constexpr int kN = kLine / static_cast<int>(sizeof(O)), kWords = kLine / 4;
+  const int limit = min(a.outer, chan + kMine);
+  const bool bf16 = a.out_dtype == DSMEM_BF16;
+  if constexpr (sizeof(O) == 2) {
+    uint32_t line[kMine / kN][kWords];
+    if (row0 < t.end) {
+#pragma unroll
+      for (int c = 0; c < kMine; c += 16) {
+        uint32_t r[16];
+        tmem_load16(tmem + c, r);
+        tmem_wait_load();
+#pragma unroll
+        for (int l = 0; l < 8; ++l)
+          line[c / kN][c % kN / 2 + l] = pair_now(r[2 * l], r[2 * l + 1], bf16);
+      }
+    }
+    free();
+#pragma unroll
+    for (int c = 0; c < kMine; c += kN)
+      if (row0 < t.end && chan + c < limit)
+        store_lines<O, kLine>(a, out_map, row0, t.end, chan + c, limit, line[c / kN], staging);
+  } else {
 #pragma unroll 1
-  for (int c = first; c < last && t.chan0 + c < a.outer; c += kN) {
-    uint32_t r[kN];
-    if constexpr (kN == 32) tmem_load32(tmem + c, r);
-    else tmem_load16(tmem + c, r);
-    tmem_wait_load();
-    store_columns<kN, O>(a, row0, t.end, t.chan0 + c, r, staging);
+    for (int c = 0; c < kMine && row0 < t.end && chan + c < limit; c += kN) {
+      uint32_t r[kN];
+      tmem_load16(tmem + c, r);
+      tmem_wait_load();
+      store_lines<O, kLine>(a, out_map, row0, t.end, chan + c, limit, r, staging);
+    }
+    free();
   }
 }
 
@@ -209,10 +268,9 @@ __device__ __forceinline__ int row_named(const Args& a, int o) {
 
 // The copying warps.  A thread copies one of the eight pieces of every 16th row.
 // Rows at and behind the tile's end are left as they are: what they hold reaches
-// no other row.  Each thread's copies of a stage arrive on `landed` by themselves;
-// the relay warp passes a landed stage on.
+// no other row.  Each thread's copies of a stage arrive on `landed` by themselves.
 template <int kCols>
-__device__ __forceinline__ void copy_rows(const Args& a, Schedule<kCols>& schedule, int total, uint32_t base,
+__device__ __forceinline__ void copy_rows(const Args& a, Schedule<kCols>& schedule, int i, int total, uint32_t base,
                                           uint32_t landed, uint32_t empty, uint32_t gave_up) {
   using R = Ring<kCols>;
   constexpr int kRows = kHigh * 8 / kShift, kLines = kShift / 8;
@@ -228,7 +286,6 @@ __device__ __forceinline__ void copy_rows(const Args& a, Schedule<kCols>& schedu
   uint32_t phase = 0;
   bool ok = true;
   Tile next;
-  int i = blockIdx.x;
   if (i < total) {
     next = schedule.at(i);
     ask(next);
@@ -238,8 +295,7 @@ __device__ __forceinline__ void copy_rows(const Args& a, Schedule<kCols>& schedu
     int row[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) row[r] = row_named(a, ahead[r]);
-    i += gridDim.x;
-    if (i < total) {
+    if (++i < total) {
       next = schedule.at(i);
       ask(next);
     }
@@ -270,82 +326,139 @@ __device__ __forceinline__ void copy_rows(const Args& a, Schedule<kCols>& schedu
   copy_wait_all();
 }
 
-// Eight times four scales (of a block's 1024 elements) of a row, from element
-// 1024 * block on, to their chunks; zeros behind the row's end, and for no row.
-__device__ __forceinline__ void put_scales(uint32_t chunks, int apart, int line, const uint8_t* row, int block,
-                                           const Args& a) {
-  uint32_t s[2 * kBlock];
-  const int first = block * 2 * kBlock;
-  if (row && a.wide_scales && first + 2 * kBlock <= a.quads) {
-#pragma unroll
-    for (int q = 0; q < 2 * kBlock; q += 4) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + (first + q) * 4));
-      s[q] = v.x, s[q + 1] = v.y, s[q + 2] = v.z, s[q + 3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 2 * kBlock; ++q)
-      s[q] = row && first + q < a.quads ? __ldg(reinterpret_cast<const uint32_t*>(row) + first + q) : 0u;
-  }
-  const uint32_t to = chunks + (line & 31) * 16 + (line >> 5 & 3) * 4 + (line >> 7) * kChunk;
-#pragma unroll
-  for (int q = 0; q < 2 * kBlock; ++q) st_shared_u32(to + q * apart, s[q]);
-}
-
-// The scales' warps: a thread brings one row's of x, and kCols / 128 channels' (or
-// one's, of the first kCols).
+// The scales' warps.  A thread brings those of every kScaleThreads-th row and
+// channel, two stages' at a time, which are asked for four stages ahead.
 template <int kCols>
-__device__ __forceinline__ void bring_scales(const Args& a, Schedule<kCols>& schedule, int of_groups, uint32_t scales,
-                                             uint32_t full, uint32_t empty, uint32_t gave_up) {
+__device__ __forceinline__ void bring_scales(const Args& a, Schedule<kCols>& schedule, int i, int total, bool keep, uint32_t base,
+                                             uint32_t landed, uint32_t empty, uint32_t gave_up) {
   using R = Ring<kCols>;
-  const int tid = threadIdx.x - kFirstScale * 32;
+  constexpr int kRows = kHigh / kScaleThreads, kLines = kRows + (kCols + kScaleThreads - 1) / kScaleThreads;
+  const int tid = threadIdx.x - kFirstScale * 32, blocks = schedule.blocks;
   const int64_t pitch = int64_t{4} * a.quads;
-  uint32_t buffer = 0, phase = 0;
-  bool ok = true;
-  for (int i = blockIdx.x; i < of_groups && ok; i += gridDim.x) {
-    const Tile t = schedule.at(i);
-    const int row = row_named(a, place_at(a, t.row0 + tid, t.end));
-    const uint8_t* x = row >= 0 ? a.x_scales + row * pitch : nullptr;
-    for (int b = 0; b * kBlock < t.blocks; ++b) {
-      ok = wait_for(empty + 8 * buffer, phase ^ 1, gave_up, a.wait_cycles, a.status);
-      ok = __all_sync(kFull, ok);
-      if (!ok) break;
-      const uint32_t to = scales + buffer * R::kScales;
-      put_scales(to, kChunk, tid, x, b, a);
+  // What comes next to ask for: a tile's lines (null for none) and the stage; the
+  // order's entry of the tile behind.
+  const uint8_t* line[kLines];
+  int tile = i, stage_ahead = 0, entry[kRows], chan0 = 0, group = 0;
+  bool fresh = true, fresh_ahead = true;  // whether its channels' scales are wanted, and the tile behind's
+  const auto look = [&] {
+    if (tile >= total) return;
+    const Tile t = schedule.at(tile);
 #pragma unroll
-      for (int c = 0; c < kCols; c += kScaleThreads) {
-        const int channel = t.chan0 + c + tid;
-        if (c + tid < kCols)
-          put_scales(to + 2 * kBlock * kChunk, R::kChunksB * kChunk, c + tid,
-                     channel < a.outer ? a.w_scales + (static_cast<int64_t>(t.group) * a.outer + channel) * pitch : nullptr,
-                     b, a);
+    for (int r = 0; r < kRows; ++r) entry[r] = place_at(a, t.row0 + r * kScaleThreads + tid, t.end);
+    chan0 = t.chan0, group = t.group;
+    fresh_ahead = t.fresh || !keep;
+  };
+  const auto enter = [&] {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int row = row_named(a, entry[r]);
+      line[r] = row >= 0 ? a.x_scales + row * pitch : nullptr;
+    }
+#pragma unroll
+    for (int l = kRows; l < kLines; ++l) {
+      const int c = (l - kRows) * kScaleThreads + tid;
+      line[l] = chan0 + c < a.outer && c < kCols
+                    ? a.w_scales + (static_cast<int64_t>(group) * a.outer + chan0 + c) * pitch
+                    : nullptr;
+    }
+    fresh = fresh_ahead;
+    ++tile;
+    look();
+  };
+  // Four quads of each line; zeros behind a line's end, and for none.
+  struct Pair {
+    uint4 of[kLines];
+    bool fresh;
+  };
+  int left = (total - i) * ((blocks + 1) / 2);  // pairs to ask for
+  const auto ask = [&](Pair& p) {
+    if (--left < 0) return;
+    if (stage_ahead >= blocks) {
+      stage_ahead = 0;
+      enter();
+    }
+    const int first = 2 * stage_ahead;
+    stage_ahead += 2;
+    p.fresh = fresh;
+#pragma unroll
+    for (int l = 0; l < kLines; ++l) {
+      if (l >= kRows && !fresh) break;
+      p.of[l] = make_uint4(0, 0, 0, 0);
+      if (!line[l]) continue;
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(line[l]) + first;
+      if (a.wide_scales) {
+        p.of[l] = __ldg(reinterpret_cast<const uint4*>(q));
+      } else {
+        p.of[l].x = __ldg(q);
+        if (first + 1 < a.quads) p.of[l].y = __ldg(q + 1);
+        if (first + 2 < a.quads) p.of[l].z = __ldg(q + 2);
+        if (first + 3 < a.quads) p.of[l].w = __ldg(q + 3);
       }
-      fence_async_shared();
-      mbar_arrive_local(full + 8 * buffer);
-      if (++buffer == 2) {
-        buffer = 0;
+    }
+  };
+  uint32_t stage = 0, phase = 0;
+  int k = 0;
+  bool ok = true;
+  const auto put = [&](const Pair& p) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (half == 1 && k == 0) break;  // a tile's last stage had no second
+      ok = ok && wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
+      ok = __all_sync(kFull, ok);
+      if (!ok) return;
+      const uint32_t to = base + stage * R::kStage + R::kA + R::kB;
+#pragma unroll
+      for (int l = 0; l < kLines; ++l) {
+        const bool row = l < kRows;
+        if (!row && !p.fresh) break;
+        const int c = (row ? l : l - kRows) * kScaleThreads + tid;
+        if (!row && kCols % kScaleThreads != 0 && c >= kCols) break;
+        const uint32_t at = to + (c & 31) * 16 + (c >> 5 & 3) * 4 + (row ? 0 : 2 * kChunk + (c >> 7) * kChunk);
+        st_shared_u32(at, half ? p.of[l].z : p.of[l].x);
+        st_shared_u32(at + (row ? 1 : R::kChunksB) * kChunk, half ? p.of[l].w : p.of[l].y);
+      }
+      __syncwarp();
+      if (tid % 32 == 0) mbar_arrive_local(landed + 8 * stage);
+      if (++stage == static_cast<uint32_t>(a.stages)) {
+        stage = 0;
         phase ^= 1;
       }
+      if (++k == blocks) k = 0;
     }
+  };
+  int pairs = left;
+  Pair first, second;
+  if (pairs > 0) {
+    look();
+    enter();
+  }
+  ask(first);
+  ask(second);
+  while (pairs > 0 && ok) {
+    put(first);
+    if (--pairs == 0 || !ok) break;
+    ask(first);
+    put(second);
+    --pairs;
+    ask(second);
   }
 }
 
 template <int kCols>
 __global__ void __launch_bounds__(kThreads, 1)
-    mx4_product_kernel(const __grid_constant__ CUtensorMap weights, const __grid_constant__ Args a) {
+    mx4_product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
   using R = Ring<kCols>;
   constexpr int kStage = R::kStage;
   const int kStages = a.stages;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* base_ptr = raw + (base - smem_u32(raw));
-  const uint32_t scales = base + kStages * kStage, out_staging = scales + 2 * R::kScales;
-  const uint32_t bars = out_staging + 4 * kStageOut;
+  const uint32_t out_staging = base + kStages * kStage;
+  const uint32_t bars = out_staging + kOutWarps * kStageOut;
   const uint32_t full = bars, empty = full + 8 * R::kMostStages, landed = empty + 8 * R::kMostStages;
-  const uint32_t acc_full = landed + 8 * R::kMostStages, acc_empty = acc_full + 16, scales_full = acc_empty + 16;
-  const uint32_t scales_empty = scales_full + 16, drained = scales_empty + 16;
+  const uint32_t acc_full = landed + 8 * R::kMostStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
   const uint32_t tmem_at = drained + 8, gave_up = tmem_at + 4;
-  static_assert(8 * (3 * R::kMostStages + 9) + 8 <= kBarrierBytes, "barriers");
+  static_assert(8 * (3 * R::kMostStages + 5) + 8 <= kBarrierBytes, "barriers");
   int32_t* begin = reinterpret_cast<int32_t*>(base_ptr + (bars - base) + kBarrierBytes);
   int32_t* first = begin + a.groups + 2;
 
@@ -353,20 +466,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   Schedule<kCols> schedule(begin, first, a);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + 8 * s, 2);  // the TMA thread and the relay
-      mbar_init(landed + 8 * s, kShift);
+      mbar_init(full + 8 * s, 1);
+      mbar_init(landed + 8 * s, kShift + kScaleThreads / 32);
       mbar_init(empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + 8 * i, 1);
-      mbar_init(acc_empty + 8 * i, 4);
-      mbar_init(scales_full + 8 * i, kScaleThreads);
-      mbar_init(scales_empty + 8 * i, 1);
+      mbar_init(acc_empty + 8 * i, kOutWarps / R::kHalves);
     }
     mbar_init(drained, 1);
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(gave_up), "r"(0u) : "memory");
     fence_mbar_init();
-    prefetch_map(&weights);
+    prefetch_map(&maps.weights);
+    if (a.wide_out) prefetch_map(&maps.out);
   }
   lay_groups<kThreads>(a.offsets, a.n, a.groups, a.groups + 1, begin, first,
                        [&](int rows) { return schedule.tiles_of(rows); },
@@ -376,20 +488,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   tcgen_fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_at));
-  const int total = first[a.groups + 1], step = gridDim.x;
-  const int of_groups = first[a.groups];  // tiles of real groups
+  // A CTA's tiles are neighbours, row tiles of the same channels first: CTAs that
+  // took every gridDim-th tile met in the same matrices, and waited together for
+  // memory where one began.
+  const int all = first[a.groups + 1], of_groups = first[a.groups];  // all, and those of real groups
+  const int mine = share(all, blockIdx.x), total = share(all, blockIdx.x + 1);
+  const int of_mine = min(of_groups, total);
+  schedule.mine = mine;
+  // The scales of a tile's channels stay in tensor memory for the next row tiles,
+  // where the ring is short enough for the instructions that read a part of them
+  // to have completed when the part is written again.
+  const bool keep = schedule.blocks >= kStages && schedule.blocks <= R::kKept;
 
   if (warp == 0) {
     uint32_t stage = 0, phase = 0, issued = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < total && ok; i += step) {
+    for (int i = mine; i < of_mine && ok; ++i) {
       const Tile t = schedule.at(i);
       for (int k = 0; k < t.blocks; ++k) {
         ok = __all_sync(kFull, wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status));
-        if (!ok || (a.withhold && i + step >= of_groups && k + 1 == t.blocks)) break;
+        if (!ok || (a.withhold && i + 1 == of_mine && k + 1 == t.blocks)) break;
         if (elect_one()) {
           mbar_expect_tx(full + 8 * stage, R::kB);
-          tma_load_3d<false>(base + stage * kStage + R::kA, &weights, k * kStageBytes, t.chan0, t.group,
+          tma_load_3d<false>(base + stage * kStage + R::kA, &maps.weights, k * kStageBytes, t.chan0, t.group,
                              full + 8 * stage);
         }
         __syncwarp();
@@ -410,29 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kRelayWarp) {
-    // Copied stages, once landed, on to the matrix instructions.
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0;
-      bool ok = true;
-      for (int i = blockIdx.x; i < of_groups && ok; i += step) {
-        for (int k = 0; k < schedule.blocks; ++k) {
-          ok = wait_for(landed + 8 * stage, phase, gave_up, a.wait_cycles, a.status);
-          if (!ok) break;
-          fence_async_shared();
-          mbar_arrive_local(full + 8 * stage);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
-      }
-    }
-    __syncwarp();
   } else if (warp >= kFirstScale) {
-    bring_scales<kCols>(a, schedule, of_groups, scales, scales_full, scales_empty, gave_up);
+    bring_scales<kCols>(a, schedule, mine, of_mine, keep, base, landed, empty, gave_up);
   } else if (warp >= kFirstCopy) {
-    copy_rows<kCols>(a, schedule, of_groups, base, landed, empty, gave_up);
+    copy_rows<kCols>(a, schedule, mine, of_mine, base, landed, empty, gave_up);
   } else if (warp == 1) {
     // A and B e2m1, K-major, scales e8m0.  Bits 4 and 29 choose the first or the
     // third of a row's four scales, of which an instruction takes two.
@@ -440,29 +542,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kDesc = (1u << 7) | (1u << 10) | (1u << 23) | (uint32_t{kHigh >> 7} << 27);
     constexpr uint32_t kWhole = kDesc | (uint32_t{kCols >> 3} << 17), kPart = kDesc | (uint32_t{kHalf >> 3} << 17);
     constexpr uint32_t kSecond = (2u << 4) | (2u << 29);
-    uint32_t stage = 0, phase = 0, done = 0, buffer = 0, scale_phase = 0;
+    uint32_t stage = 0, phase = 0, done = 0;
     bool ok = true;
     const auto await = [&](uint32_t bar, uint32_t parity) {
       ok = __all_sync(kFull, wait_for(bar, parity, gave_up, a.wait_cycles, a.status));
       tcgen_fence_after();
       return ok;
     };
-    for (int i = blockIdx.x; i < of_groups && ok; i += step) {
+    for (int i = mine; i < of_mine && ok; ++i) {
       // Sums: a tile's own place of two, or the halves of the only one.
       const uint32_t place = R::kBuffers == 2 ? done & 1 : 0, d = tmem + place * kCols;
       const uint32_t turn = R::kBuffers == 2 ? done >> 1 & 1 : done & 1;
+      const bool fresh = !keep || schedule.at(i).fresh;
       if (!await(acc_empty + 8 * place, turn ^ 1)) break;
       for (int k = 0; k < schedule.blocks; ++k) {
-        if (k % kBlock == 0 && !await(scales_full + 8 * buffer, scale_phase)) break;
+        // Rows and scales come by plain copies, which this warp passes on to the
+        // matrix instructions.  (A fence of the scales' warps waited for their loads
+        // ahead too: 1400 cycles a stage.)
+        if (!await(landed + 8 * stage, phase)) break;
+        fence_async_shared();
         if (!await(full + 8 * stage, phase)) break;
         const uint32_t sa = base + stage * kStage;
         const uint64_t da = descriptor<false>(sa), db = descriptor<false>(sa + R::kA);
-        const uint32_t chunks = scales + buffer * R::kScales + k % kBlock * 2 * kChunk;
-        const uint64_t dsa = scale_descriptor(chunks);
-        const uint64_t dsb = scale_descriptor(chunks + 2 * kBlock * kChunk + k % kBlock * 2 * (R::kChunksB - 1) * kChunk);
+        const uint64_t ds = scale_descriptor(sa + R::kA + R::kB);
         // Each stage has columns of its own: the stage is handed back only when
         // the instructions that read them have completed.
-        const uint32_t sfa = tmem + R::kBuffers * kCols + stage * R::kScaleColumns, sfb = sfa + 8;
+        const uint32_t sfa = tmem + R::kRowScales + stage * 8;
+        const uint32_t sfb = tmem + R::kChannelScales + (keep ? k : stage) * (8 * R::kChunksB);
         const auto multiply = [&](int half, uint32_t desc) {
 #pragma unroll
           for (int s = 0; s < 4; ++s)
@@ -473,10 +579,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            copy_scales(sfa + 4 * q, dsa + q * (kChunk >> 4));
+            copy_scales(sfa + 4 * q, ds + q * (kChunk >> 4));
+            if (fresh) {
 #pragma unroll
-            for (int c = 0; c < R::kChunksB; ++c)
-              copy_scales(sfb + 4 * (R::kChunksB * q + c), dsb + (R::kChunksB * q + c) * (kChunk >> 4));
+              for (int c = 0; c < R::kChunksB; ++c)
+                copy_scales(sfb + 4 * (R::kChunksB * q + c), ds + (2 + R::kChunksB * q + c) * (kChunk >> 4));
+            }
           }
           if (R::kHalves == 1 || k > 0) multiply(0, kWhole);
           else multiply(0, kPart);
@@ -490,14 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool last = k + 1 == schedule.blocks;
         if (elect_one()) {
           mma_commit<false>(empty + 8 * stage);
-          if (last || k % kBlock == kBlock - 1) mma_commit<false>(scales_empty + 8 * buffer);
           if (last) mma_commit<false>(acc_full + 8 * place);
         }
         __syncwarp();
-        if (last || k % kBlock == kBlock - 1) {
-          buffer ^= 1;
-          scale_phase ^= buffer == 0;
-        }
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
@@ -515,15 +618,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // Output: warp w may read lanes 32 (w % 4) .. of tensor memory.
-    const int quadrant = warp & 3;
-    const uint32_t staging = out_staging + quadrant * kStageOut;
+    const int quadrant = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t staging = out_staging + (warp - 2) * kStageOut;
     uint32_t done = 0;
-    for (int i = blockIdx.x; i < total; i += step) {
+    for (int i = mine; i < total; ++i) {
       const Tile t = schedule.at(i);
-      const int row0 = t.row0 + quadrant * 32;
+      const int row0 = t.row0 + quadrant * 32, chan = t.chan0 + half * R::kMine;
       if (t.blocks == 0) {
-        if (a.out_dtype == DSMEM_F32) store_zeros<kCols, float>(a, row0, t.end, t.chan0);
-        else store_zeros<kCols, __half>(a, row0, t.end, t.chan0);
+        if (a.out_dtype == DSMEM_F32) store_zeros<R::kMine, float>(a, row0, t.end, chan);
+        else store_zeros<R::kMine, uint16_t>(a, row0, t.end, chan);
         continue;
       }
       const uint32_t place = R::kBuffers == 2 ? done & 1 : 0;
@@ -532,22 +635,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool ok = wait_for(acc_full + 8 * place, turn, gave_up, a.wait_cycles + 4096ll * t.blocks, a.status);
       if (!__all_sync(kFull, ok)) break;
       tcgen_fence_after();
-      const uint32_t d = tmem + place * kCols + (static_cast<uint32_t>(quadrant * 32) << 16);
-#pragma unroll 1
-      for (int half = 0; half < R::kHalves; ++half) {
-        constexpr int kHalf = kCols / R::kHalves;
-        const int from = half * kHalf, to = from + kHalf;
-        if (row0 < t.end) {
-          if (a.out_dtype == DSMEM_F32) store_tile<float>(a, t, row0, from, to, d, staging);
-          else if (a.out_dtype == DSMEM_F16) store_tile<__half>(a, t, row0, from, to, d, staging);
-          else store_tile<__nv_bfloat16>(a, t, row0, from, to, d, staging);
-        }
+      const uint32_t d = tmem + place * kCols + half * R::kMine + (static_cast<uint32_t>(quadrant * 32) << 16);
+      const auto free = [&] {
         tcgen_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_local(acc_empty + 8 * (R::kHalves == 2 ? half : place));
-      }
+      };
+      if (a.out_dtype == DSMEM_F32) store_tile<R::kMine, float>(a, &maps.out, t, row0, chan, d, staging, free);
+      else store_tile<R::kMine, uint16_t>(a, &maps.out, t, row0, chan, d, staging, free);
       ++done;
     }
+    if (lane == 0) store_wait();
     __syncwarp();
   }
   tcgen_fence_before();
@@ -574,6 +672,24 @@ int make_map(CUtensorMap* map, const Mx4ProductArgs& p, int cols) {
   return DSMEM_HIST_OK;
 }
 
+// The output in boxes of 32 rows by 64 bytes.
+int make_out_map(CUtensorMap* map, const Mx4ProductArgs& p) {
+  const int size = dtype_size(p.out_dtype);
+  const CUtensorMapDataType type = p.out_dtype == DSMEM_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : p.out_dtype == DSMEM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.outer), static_cast<cuuint64_t>(p.n)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.outer) * size};
+  const cuuint32_t box[2] = {64u / size, 32}, unit[2] = {1, 1};
+  const CUresult r = encoder()(map, type, 2, p.out, dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                               CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail_with(DSMEM_HIST_ECUDA, "cuTensorMapEncodeTiled: error %d (4-bit product's output, %lld x %d)",
+                     static_cast<int>(r), static_cast<long long>(p.n), p.outer);
+  return DSMEM_HIST_OK;
+}
+
 // Upper bound of a product's tiles: the group sizes are not known here.
 int64_t tile_bound(const Mx4ProductArgs& p, int cols) {
   return (p.n / kHigh + std::min<int64_t>(p.groups + 1, p.n)) * ((p.outer + cols - 1) / cols);
@@ -586,7 +702,6 @@ int launch(const Mx4ProductArgs& p, const CallContext& ctx, cudaStream_t stream)
   a.offsets = p.offsets, a.order = p.order, a.n = p.n;
   a.x_rows = static_cast<int>(p.x_rows), a.groups = p.groups, a.outer = p.outer, a.quads = p.quads;
   a.fan = Divisor(static_cast<uint32_t>(p.fan));
-  a.by_chan_tiles = Divisor(static_cast<uint32_t>((p.outer + kCols - 1) / kCols));
   a.x_values = p.x_values, a.x_scales = p.x_scales, a.w_scales = p.w_scales;
   a.out = p.out, a.out_dtype = p.out_dtype;
   a.wide_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
@@ -596,8 +711,9 @@ int launch(const Mx4ProductArgs& p, const CallContext& ctx, cudaStream_t stream)
   a.status = ctx.status;
   a.wait_cycles = call_wait_cycles();
   a.withhold = call_withholds();
-  CUtensorMap map;
-  const int rc = make_map(&map, p, kCols);
+  Maps maps;
+  int rc = make_map(&maps.weights, p, kCols);
+  if (!rc && a.wide_out) rc = make_out_map(&maps.out, p);
   if (rc) return rc;
   const int64_t tiles = tile_bound(p, kCols);
   if (tiles > INT32_MAX - 1024)  // tile counters step past the last tile
@@ -607,7 +723,7 @@ int launch(const Mx4ProductArgs& p, const CallContext& ctx, cudaStream_t stream)
   const auto kernel = mx4_product_kernel<kCols>;
   cudaError_t e = limit.need(reinterpret_cast<const void*>(kernel), ctx.device, smem);
   if (e != cudaSuccess) return fail_with_cuda(e, "cudaFuncSetAttribute");
-  kernel<<<static_cast<unsigned>(std::min<int64_t>(tiles, ctx.sm_count)), kThreads, smem, stream>>>(map, a);
+  kernel<<<static_cast<unsigned>(std::min<int64_t>(tiles, ctx.sm_count)), kThreads, smem, stream>>>(maps, a);
   e = cudaGetLastError();
   return e == cudaSuccess ? DSMEM_HIST_OK : fail_with_cuda(e, "4-bit grouped product launch");
 }

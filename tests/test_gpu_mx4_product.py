@@ -64,7 +64,9 @@ CASES = [  # group sizes, rows behind the last group, inner, outer
     ([127, 129, 1], 3, 300, 130), ([0, 0, 0], 5, 64, 33), ([200, 0, 57, 300], 0, 1003, 517),
     ([64] * 20, 11, 640, 264), ([1, 0, 2, 1] * 16, 0, 2048, 96), ([700], 0, 384, 1100), ([33] * 5, 0, 4096, 48),
     # enough tiles for 256 channels each: several a CTA, ragged ones, many groups without rows
-    ([1, 129, 0, 40, 128] * 10, 7, 300, 2050), ([5] * 300, 0, 1100, 520), ([2, 0] * 300 + [1], 3, 96, 300)]
+    ([1, 129, 0, 40, 128] * 10, 7, 300, 2050), ([5] * 300, 0, 1100, 520), ([2, 0] * 300 + [1], 3, 96, 300),
+    # several row tiles of the same channels, at each width of tile
+    ([600, 129, 0, 333] * 6, 0, 1100, 2050), ([700, 300] * 3, 5, 1600, 2050), ([700, 300], 0, 2048, 1100)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
