@@ -324,35 +324,6 @@ __device__ __forceinline__ void load_column(Slot& s, const Ahead& at, int d, con
   from.fetch(at.column + d * 32, (b.step + d) * 32 + (threadIdx.x & 3) * 8, b.whole, s.column);
 }
 
-// Eight 4-bit elements as bf16 pairs (0,4), (1,5), (2,6), (3,7), scaled.  An
-// element's sign, exponent and fraction bits at those of a bf16 make its value
-// times 2^-126; `factor` (twice, in a pair) makes up for it with the scale, an
-// exact product.  A warp that has a scale for which no bf16 does both multiplies
-// twice (again_of).
-__device__ __forceinline__ uint32_t times_bf16(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ void decode8(uint32_t w, uint32_t factor, uint32_t (&r)[4]) {
-  constexpr uint32_t kSign = 0x80008000u, kRest = 0x01c001c0u;
-  r[0] = ((w << 6) & kRest) | ((w << 12) & kSign);
-  r[1] = ((w << 2) & kRest) | ((w << 8) & kSign);
-  r[2] = ((w >> 2) & kRest) | ((w << 4) & kSign);
-  r[3] = ((w >> 6) & kRest) | (w & kSign);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = times_bf16(r[i], factor);
-}
-// 2^(byte - 1) = 2^126 2^(byte - 127) as a bf16 pair where it is one, else
-// 2^126, with 2^(byte - 127) (or NaN) for `again`.
-__device__ __forceinline__ uint32_t factor_of(uint32_t byte, bool twice) {
-  return (twice ? 253u : byte + 126u) * 0x00800080u;
-}
-__device__ __forceinline__ uint32_t again_of(uint32_t byte) {
-  const uint32_t bits = byte == 0u ? 0x0040u : (byte == 255u ? 0x7fc0u : byte << 7);
-  return bits | bits << 16;
-}
-
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
   return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }

@@ -8,12 +8,6 @@
 
 namespace dsmh {
 
-// 2^(byte - 127).  2^-127 lies below the normal 32-bit floats.
-__device__ __forceinline__ float mx_scale(uint32_t byte) {
-  if (byte == 0u) return __uint_as_float(0x00400000u);
-  return byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
-}
-
 // The scale byte of 32 elements of which the largest magnitude has these bits:
 // 2^(floor(log2 max) - 2), so that the largest lies in [4, 8) scaled, at least
 // 2^-127; NaN where one element is infinite or NaN.
@@ -27,22 +21,46 @@ __device__ __forceinline__ float mx_inverse(uint32_t byte) {
   return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
 }
 
-// Two floats to e2m1, to the nearest, ties to the even code, saturating at 6:
-// `low` in the low half of the byte.
-__device__ __forceinline__ uint32_t e2m1_pair(float low, float high) {
+// Eight floats to e2m1, to the nearest, ties to the even code, saturating at 6: two a
+// byte, the first in the low half of the lowest.
+__device__ __forceinline__ uint32_t e2m1_word(const float2 (&v)[4]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 p, z;\n\tcvt.rn.satfinite.e2m1x2.f32 p, %1, %2;\n\tmov.b32 %0, {p, z, z, z};\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(high), "f"(low));
-  return r & 0xffu;
+      : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
+  return r;
 }
-// Element i (0..7) of a word of eight, as a float.  Its bits at a float's
-// exponent and fraction make the value times 2^-126, an exact product.
-__device__ __forceinline__ float e2m1_value(uint32_t word, int i) {
-  const uint32_t sign = (i < 7 ? word << (28 - 4 * i) : word) & 0x80000000u;
-  const int up = 22 - 4 * i;
-  const uint32_t rest = (up >= 0 ? word << up : word >> -up) & 0x01c00000u;
-  return __uint_as_float(sign | rest) * 0x1p126f;
+
+// Eight 4-bit elements as bf16 pairs (0,4), (1,5), (2,6), (3,7), scaled.  An
+// element's sign, exponent and fraction bits at those of a bf16 make its value
+// times 2^-126; `factor` (twice, in a pair) makes up for it with the scale, an
+// exact product.  A warp that has a scale for which no bf16 does both multiplies
+// twice (again_of).
+__device__ __forceinline__ uint32_t times_bf16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t factor, uint32_t (&r)[4]) {
+  constexpr uint32_t kSign = 0x80008000u, kRest = 0x01c001c0u;
+  r[0] = ((w << 6) & kRest) | ((w << 12) & kSign);
+  r[1] = ((w << 2) & kRest) | ((w << 8) & kSign);
+  r[2] = ((w >> 2) & kRest) | ((w << 4) & kSign);
+  r[3] = ((w >> 6) & kRest) | (w & kSign);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = times_bf16(r[i], factor);
+}
+// 2^(byte - 1) = 2^126 2^(byte - 127) as a bf16 pair where it is one, else
+// 2^126, with 2^(byte - 127) (or NaN) for `again`.
+__device__ __forceinline__ uint32_t factor_of(uint32_t byte, bool twice) {
+  return (twice ? 253u : byte + 126u) * 0x00800080u;
+}
+__device__ __forceinline__ uint32_t again_of(uint32_t byte) {
+  const uint32_t bits = byte == 0u ? 0x0040u : (byte == 255u ? 0x7fc0u : byte << 7);
+  return bits | bits << 16;
 }
 
 }  // namespace dsmh
