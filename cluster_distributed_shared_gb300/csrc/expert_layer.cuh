@@ -64,7 +64,7 @@ constexpr int kDepth = kIsMx4<kHeld> ? 128 : 32;  // elements of a step
 
 // Everything a CTA knows about the routing.  Rows are (token, expert) pairs,
 // expert after expert, an expert's rows by token.
-struct alignas(16) Routing {
+struct alignas(32) Routing {
   unsigned long long tokens_of[DSMEM_ROUTE_MAX_EXPERTS];  // a bit for each token
   uint16_t place_of[DSMEM_ROUTE_MAX_EXPERTS];             // among the active experts
   uint16_t active[DSMEM_ROUTE_MAX_EXPERTS];               // experts that any token chose, by number
@@ -273,14 +273,14 @@ __device__ __forceinline__ void point_at(const LayerMatrix& m, int e, int row, i
     to.scale[i] = m.scales + (static_cast<int64_t>(e) * m.rows + row) * m.scale_stride + step * 4 + t;
 }
 // On to the next batch of the same rows.
-template <int kHeld>
+template <int kHeld, typename From>
 __device__ __forceinline__ void move_on(Ahead& at) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     at.row[i] += kSteps<kHeld> * 64;
     if (kIsMx4<kHeld>) at.scale[i] += kSteps<kHeld> * 4;
   }
-  if (!kIsMx4<kHeld>) at.column += kSteps<kHeld> * kDepth<kHeld>;
+  if (!kIsMx4<kHeld>) at.column += kSteps<kHeld> * From::kStep;
 }
 
 // The part of a matrix's rows that a batch takes.
@@ -321,26 +321,32 @@ template <int kHeld, typename From>
 __device__ __forceinline__ void load_column(Slot& s, const Ahead& at, int d, const Batch& b, int steps,
                                             const From& from) {
   if (kIsMx4<kHeld> || (!b.whole && b.step + d >= steps)) return;
-  from.fetch(at.column + d * 32, (b.step + d) * 32 + (threadIdx.x & 3) * 8, b.whole, s.column);
+  from.fetch(at.column + d * From::kStep, (b.step + d) * 32 + (threadIdx.x & 3) * 8, s.column);
 }
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
   return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }
 
-// Where the rows' side comes from.  fetch() takes eight elements at p, c of its
-// row.  x: a token's vector, 16-bit, any alignment, read again and again.
+// Where the rows' side comes from.  at() is where a lane's piece q of eight
+// elements of a step lies in its row (4-bit: of four, else the only one), and
+// fetch() takes one, c of its row.  x: a token's
+// vector, 16-bit, any alignment, read again and again.
 template <int kHeld, bool kWide>
 struct FromX {
   static constexpr bool kTwo = kHeld == kMx4F16;  // f16 is the sum of two bf16
+  static constexpr int kStep = kDepth<kHeld>;
   const uint16_t* x;
   int64_t stride;
   int depth;
   __device__ __forceinline__ const uint16_t* row(int r) const { return x + r * stride; }
-  __device__ __forceinline__ void fetch(const uint16_t* p, int c, bool whole, Eight& e) const {
+  __device__ __forceinline__ static int at(int step, int q) {
+    return step * kStep + (threadIdx.x & 3) * (kStep / 4) + q * 8;
+  }
+  __device__ __forceinline__ void fetch(const uint16_t* p, int c, Eight& e) const {
     uint4 v = make_uint4(0, 0, 0, 0);
     if constexpr (kWide) {
-      if (whole || c < depth) v = __ldg(reinterpret_cast<const uint4*>(p));
+      if (c < depth) v = __ldg(reinterpret_cast<const uint4*>(p));
     } else {
       v = aligned_piece(p - c, c, depth, (reinterpret_cast<uintptr_t>(p) & 2u) != 0);
     }
@@ -364,18 +370,28 @@ struct FromX {
     }
   }
 };
-// h: the up kernel's rows, two numbers an element, in the fragments' order, with
-// zeros up to whole steps; each row is read once by a CTA.
+// h: the up kernel's rows, each element as two numbers, with zeros up to whole
+// steps; each row is read once by a CTA.  A piece is eight first numbers and eight
+// second ones, a sector, in the fragments' order, and the pieces that the four
+// lanes of a row take together lie side by side.
+template <int kHeld>
 struct FromH {
   static constexpr bool kTwo = true;
-  const uint16_t* h;  // [rows][2][pitch]
-  int pitch;
+  static constexpr int kStep = 2 * kDepth<kHeld>;
+  const uint16_t* h;
+  int pitch;  // elements of a row
   __device__ __forceinline__ const uint16_t* row(int r) const { return h + static_cast<int64_t>(r) * 2 * pitch; }
-  __device__ __forceinline__ void fetch(const uint16_t* p, int, bool, Eight& e) const {
-    const uint4 high = __ldcg(reinterpret_cast<const uint4*>(p));
-    const uint4 low = __ldcg(reinterpret_cast<const uint4*>(p + pitch));
-    e.high[0] = high.x, e.high[1] = high.y, e.high[2] = high.z, e.high[3] = high.w;
-    e.low[0] = low.x, e.low[1] = low.y, e.low[2] = low.z, e.low[3] = low.w;
+  __device__ __forceinline__ static int at(int step, int q) { return step * kStep + (q * 4 + (threadIdx.x & 3)) * 16; }
+  // Where the first number of element c lies in its row; the second is 8 further on.
+  __device__ __forceinline__ static int place_of(int c) {
+    if constexpr (!kIsMx4<kHeld>) return (c >> 3) * 16 + (c & 7);
+    return (c >> 7) * kStep + ((c >> 3 & 3) * 4 + (c >> 5 & 3)) * 16 + ((c & 3) << 1) + (c >> 2 & 1);
+  }
+  __device__ __forceinline__ void fetch(const uint16_t* p, int, Eight& e) const {
+    asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(e.high[0]), "=r"(e.high[1]), "=r"(e.high[2]), "=r"(e.high[3]), "=r"(e.low[0]), "=r"(e.low[1]),
+                   "=r"(e.low[2]), "=r"(e.low[3])
+                 : "l"(p));
   }
 };
 
@@ -406,45 +422,41 @@ __device__ __forceinline__ void multiply(Slot (&slot)[kSteps<kHeld>], const Batc
         reload(d);
         continue;
       }
+      const Slot& s = slot[d];
+      const bool twice = __any_sync(kFullWarp, max(s.scale[0], s.scale[1]) > 128u);
+      const auto fetch = [&](int n, Eight (&e)[4]) {
+        const uint16_t* p = from.row(column[n]) + From::at(b.step + d, 0);
+        const int c = (b.step + d) * 128 + t * 32;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) from.fetch(p + (From::at(0, q) - From::at(0, 0)), c + q * 8, e[q]);
+      };
       // The columns' way from the caches passes behind the decoding.
-      const int c = (b.step + d) * 128 + t * 32;
-      Eight first[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) from.fetch(from.row(column[0]) + c + q * 8, c + q * 8, b.whole, first[q]);
+      Eight columns[4];
+      fetch(0, columns);
       uint32_t v[4][4], w[4][4];
-      {
-        const Slot& s = slot[d];
-        const bool twice = __any_sync(kFullWarp, max(s.scale[0], s.scale[1]) > 128u);
-        const uint32_t f0 = factor_of(s.scale[0], twice), f1 = factor_of(s.scale[1], twice);
+      const uint32_t f0 = factor_of(s.scale[0], twice), f1 = factor_of(s.scale[1], twice);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          decode8(word_of(s.row[0], q), f0, v[q]);
-          decode8(word_of(s.row[1], q), f1, w[q]);
-        }
-        if (twice) {
-          const uint32_t g0 = again_of(s.scale[0]), g1 = again_of(s.scale[1]);
+      for (int q = 0; q < 4; ++q) {
+        decode8(word_of(s.row[0], q), f0, v[q]);
+        decode8(word_of(s.row[1], q), f1, w[q]);
+      }
+      if (twice) {
+        const uint32_t g0 = again_of(s.scale[0]), g1 = again_of(s.scale[1]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            v[i / 4][i % 4] = times_bf16(v[i / 4][i % 4], g0);
-            w[i / 4][i % 4] = times_bf16(w[i / 4][i % 4], g1);
-          }
+        for (int i = 0; i < 16; ++i) {
+          v[i / 4][i % 4] = times_bf16(v[i / 4][i % 4], g0);
+          w[i / 4][i % 4] = times_bf16(w[i / 4][i % 4], g1);
         }
       }
       reload(d);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        mma_eight<kHeld, From::kTwo>(sum[0], v[q][0], w[q][0], v[q][1], w[q][1], v[q][2], w[q][2], v[q][3], w[q][3],
-                                     first[q]);
-#pragma unroll
-      for (int n = 1; n < kTiles; ++n) {
+      for (int n = 0; n < kTiles; ++n) {
         if (n >= tiles) break;
+        if (n > 0) fetch(n, columns);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          Eight e;
-          from.fetch(from.row(column[n]) + c + q * 8, c + q * 8, b.whole, e);
+        for (int q = 0; q < 4; ++q)
           mma_eight<kHeld, From::kTwo>(sum[n], v[q][0], w[q][0], v[q][1], w[q][1], v[q][2], w[q][2], v[q][3], w[q][3],
-                                       e);
-        }
+                                       columns[q]);
       }
     }
   } else {
@@ -456,8 +468,9 @@ __device__ __forceinline__ void multiply(Slot (&slot)[kSteps<kHeld>], const Batc
         Eight e[2];
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
-          const int c = (b.step + d0 + d) * 32 + t * 8;
-          if (b.whole || b.step + d0 + d < steps) from.fetch(from.row(column[n]) + c, c, b.whole, e[d]);
+          const int step = b.step + d0 + d;
+          const uint16_t* p = from.row(column[n]) + From::at(step, 0);
+          if (b.whole || step < steps) from.fetch(p, step * 32 + t * 8, e[d]);
         }
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
@@ -520,7 +533,7 @@ __device__ __forceinline__ void stream(int begin, int end, int steps, const Divi
       more = ++batch < batches;
       if (--left > 0) {
         next = batch_at(more ? batch : 0);
-        if (more) move_on<kHeld>(at);
+        if (more) move_on<kHeld, From>(at);
         else point(++tile, 0, at);
       }
       multiply<kHeld, kTiles>(slot, now, steps, tiles, column, from, sum, [&](int d) {
@@ -562,23 +575,23 @@ __device__ __noinline__ void to_h(const LayerArgs& a, const Routing& routing, Pl
       const int at = g + 8 * k;
       if (at >= p.count) continue;
       // Two 16-bit numbers hold h to 16 bits or more: what they leave out is far
-      // below the output's rounding.  4-bit fragments pair elements 4 apart.
-      const int c = p.row + at, to = kIsMx4<kHeld> ? (c & ~7) | ((c & 3) << 1) | ((c >> 2) & 1) : c;
+      // below the output's rounding.
+      const int to = FromH<kHeld>::place_of(p.row + at);
       if constexpr (kHeld == kF16) {
         const __half b = __float2half_rn(value);
         h[to] = __half_as_ushort(b);
-        h[a.h_pitch + to] = __half_as_ushort(__float2half_rn(__hisinf(b) ? 0.0f : value - __half2float(b)));
+        h[to + 8] = __half_as_ushort(__float2half_rn(__hisinf(b) ? 0.0f : value - __half2float(b)));
       } else {
         const __nv_bfloat16 b = __float2bfloat16_rn(value);
         h[to] = __bfloat16_as_ushort(b);
-        h[a.h_pitch + to] = __bfloat16_as_ushort(__float2bfloat16_rn(__hisinf(b) ? 0.0f : value - __bfloat162float(b)));
+        h[to + 8] = __bfloat16_as_ushort(__float2bfloat16_rn(__hisinf(b) ? 0.0f : value - __bfloat162float(b)));
       }
     }
     // Zeros behind the end of each row, up to a whole step.
     if (p.row + p.count == a.hidden)
       for (int c = a.hidden + g; c < a.h_pitch; c += 8) {
-        const int to = kIsMx4<kHeld> ? (c & ~7) | ((c & 3) << 1) | ((c >> 2) & 1) : c;
-        h[to] = h[a.h_pitch + to] = 0;
+        const int to = FromH<kHeld>::place_of(c);
+        h[to] = h[to + 8] = 0;
       }
   }
 }
@@ -598,7 +611,7 @@ __global__ void __launch_bounds__(kWarps<kHeld, kTiles> * 32, 16 / kWarps<kHeld,
   const int active = route_all<kWarps<kHeld, kTiles>>(a, routing, reinterpret_cast<Choice*>(parts));
   if (a.passes_on && blockIdx.x == 0) pass_on(a.routing, routing);
 
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, g = lane >> 2, warp = threadIdx.x >> 5;
   const int high = a.gated ? 8 : 16;  // rows of h of a tile
   const int steps = (a.width + kDepth<kHeld> - 1) / kDepth<kHeld>, batches = (steps + kSteps<kHeld> - 1) / kSteps<kHeld>;
   const int rows = active * a.hidden, each = a.by_ctas.quotient(rows), over = rows - each * gridDim.x;
@@ -637,7 +650,7 @@ __global__ void __launch_bounds__(kWarps<kHeld, kTiles> * 32, 16 / kWarps<kHeld,
     point_at<kHeld>(a.up, e, min(p.row + (a.gated ? g : 8 + g), last), step, at, 1);
     if (!kIsMx4<kHeld>) {
       const int column = min(g, routing.rows_of[p.expert] - 1);
-      at.column = from.row(routing.token[routing.start[p.expert] + column]) + step * 32 + t * 8;
+      at.column = from.row(routing.token[routing.start[p.expert] + column]) + from.at(step, 0);
     }
   };
   const auto look = [&](int tile, int (&column)[kTiles]) {
@@ -705,7 +718,7 @@ __global__ void __launch_bounds__(kWarps<kHeld, kTiles> * 32, 16 / kWarps<kHeld,
   const int each = a.by_ctas.quotient(a.width), over = a.width - each * gridDim.x;
   const int first = each * blockIdx.x + min(static_cast<int>(blockIdx.x), over);
   const int last = first + each + (static_cast<int>(blockIdx.x) < over);
-  const FromH from{a.h, a.h_pitch};
+  const FromH<kHeld> from{a.h, a.h_pitch};
   float* mine = sums + warp * a.tokens * 16;
 
   for (int channel = first, turn = 0; channel < last; channel += 16, ++turn) {
@@ -718,7 +731,7 @@ __global__ void __launch_bounds__(kWarps<kHeld, kTiles> * 32, 16 / kWarps<kHeld,
       point_at<kHeld>(a.down, e, min(channel + g, last_channel), step, at, 0);
       point_at<kHeld>(a.down, e, min(channel + 8 + g, last_channel), step, at, 1);
       if (!kIsMx4<kHeld>)
-        at.column = from.row(routing.start[tile] + min(g, routing.rows_of[tile] - 1)) + step * 32 + t * 8;
+        at.column = from.row(routing.start[tile] + min(g, routing.rows_of[tile] - 1)) + from.at(step, 0);
     };
     const auto look = [&](int tile, int (&column)[kTiles]) {
       const int first_row = routing.start[tile], columns = routing.rows_of[tile];
@@ -799,32 +812,29 @@ bool whole_vectors(const LayerMatrix& m, int columns) {
          columns % 8 == 0;
 }
 
-template <int kHeld>
+template <int kHeld, int kTiles>
 cudaError_t launch_ups(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
   const bool wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_stride % 8 == 0 && a.width % 8 == 0 &&
                     (kIsMx4<kHeld> || (whole_vectors(a.up, a.width) && (!a.gated || whole_vectors(a.gate, a.width))));
-  if (!wide) return launch_up<kHeld, kMaxTokens / 8, false>(a, ctx, stream);
-  if (a.tokens <= 8) return launch_up<kHeld, 1, true>(a, ctx, stream);
-  if (a.tokens <= 32) return launch_up<kHeld, 4, true>(a, ctx, stream);
-  return launch_up<kHeld, kMaxTokens / 8, true>(a, ctx, stream);
+  return wide ? launch_up<kHeld, kTiles, true>(a, ctx, stream) : launch_up<kHeld, kTiles, false>(a, ctx, stream);
 }
 
 // Both launches; the down kernel's tiles say whether it routes for itself.
-template <int kHeldUp, int kHeldDown, int kTiles, bool kWide>
+template <int kHeldUp, int kHeldDown, int kTiles>
 cudaError_t launch_with(LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
   a.passes_on = !kShared<kHeldDown, kTiles>;
-  const cudaError_t e = launch_ups<kHeldUp>(a, ctx, stream);
-  return e == cudaSuccess ? launch_down<kHeldDown, kTiles, kWide>(a, ctx, stream) : e;
+  const cudaError_t e = launch_ups<kHeldUp, kTiles>(a, ctx, stream);
+  if (e != cudaSuccess) return e;
+  if constexpr (!kIsMx4<kHeldDown>) {
+    if (!whole_vectors(a.down, a.hidden)) return launch_down<kHeldDown, kTiles, false>(a, ctx, stream);
+  }
+  return launch_down<kHeldDown, kTiles, true>(a, ctx, stream);
 }
 template <int kHeldUp, int kHeldDown>
 cudaError_t launch_both(LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
-  if constexpr (!kIsMx4<kHeldDown>) {
-    if (!whole_vectors(a.down, a.hidden))
-      return launch_with<kHeldUp, kHeldDown, kMaxTokens / 8, false>(a, ctx, stream);
-  }
-  if (a.tokens <= 8) return launch_with<kHeldUp, kHeldDown, 1, true>(a, ctx, stream);
-  if (a.tokens <= 32) return launch_with<kHeldUp, kHeldDown, 4, true>(a, ctx, stream);
-  return launch_with<kHeldUp, kHeldDown, kMaxTokens / 8, true>(a, ctx, stream);
+  if (a.tokens <= 8) return launch_with<kHeldUp, kHeldDown, 1>(a, ctx, stream);
+  if (a.tokens <= 32) return launch_with<kHeldUp, kHeldDown, 4>(a, ctx, stream);
+  return launch_with<kHeldUp, kHeldDown, kMaxTokens / 8>(a, ctx, stream);
 }
 
 }  // namespace

@@ -159,7 +159,7 @@ struct LayerArgs {
   // Set by run_expert_layer.
   void* routing;  // for the down kernel, where passes_on says so
   int passes_on;
-  uint16_t* h;  // [rows][2][h_pitch], the two 16-bit parts of each value
+  uint16_t* h;  // [rows][h_pitch], each value as two 16-bit numbers
   int h_pitch;
   Divisor by_ctas, by_hidden, by_tiles, by_up_batches, by_down_batches;
 };

@@ -45,11 +45,14 @@ __device__ __forceinline__ uint32_t times_bf16(uint32_t a, uint32_t b) {
   return r;
 }
 __device__ __forceinline__ void decode8(uint32_t w, uint32_t factor, uint32_t (&r)[4]) {
-  constexpr uint32_t kSign = 0x80008000u, kRest = 0x01c001c0u;
-  r[0] = ((w << 6) & kRest) | ((w << 12) & kSign);
-  r[1] = ((w << 2) & kRest) | ((w << 8) & kSign);
-  r[2] = ((w >> 2) & kRest) | ((w << 4) & kSign);
-  r[3] = ((w >> 6) & kRest) | (w & kSign);
+  // One product moves an element's four bits twice, which the logic pipe, half as
+  // wide as the others, need not do.
+  constexpr uint32_t kBits = 0x81c081c0u, kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+  const uint32_t rest = w >> 8;
+  r[0] = ((w & kLow) * 0x1040u) & kBits;
+  r[1] = ((w & kHigh) * 0x0104u) & kBits;
+  r[2] = ((rest & kLow) * 0x1040u) & kBits;
+  r[3] = ((rest & kHigh) * 0x0104u) & kBits;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] = times_bf16(r[i], factor);
 }
