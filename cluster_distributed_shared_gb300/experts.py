@@ -354,19 +354,23 @@ def dsmem_combine_backward(dy, z, position, order, weights, stream=None):
 def _mx4_tensors(name, pair, dims, index=None):
     """The device index of a pair (values, scales) of 4-bit rows, contiguous
     CUDA uint8 tensors whose last dimensions belong together."""
-    if not isinstance(pair, (tuple, list)) or len(pair) != 2 or not all(
-            isinstance(t, _lib.Tensor) and t.dtype == _lib.uint8 and t.get_device() >= 0 for t in pair):
+    got = other = -1
+    if isinstance(pair, (tuple, list)) and len(pair) == 2:
+        values, scales = pair
+        if isinstance(values, _lib.Tensor) and isinstance(scales, _lib.Tensor) \
+                and values.dtype is scales.dtype is _lib.uint8:
+            got, other = values.get_device(), scales.get_device()
+    if got < 0 or other < 0:
         raise TypeError(f"{name} must be a pair (values, scales) of CUDA torch.uint8 tensors")
-    values, scales = pair
-    if dims is not None and values.dim() != dims or values.dim() < 1:
-        raise ValueError(f"{name}'s values must have {dims} dimensions (got {values.dim()})")
-    if values.shape[:-1] != scales.shape[:-1] or values.shape[-1] != 16 * scales.shape[-1] \
-            or values.shape[-1] % 64 or values.shape[-1] == 0:
+    shape, of_scales = values.shape, scales.shape
+    if dims is not None and len(shape) != dims or len(shape) < 1:
+        raise ValueError(f"{name}'s values must have {dims or 'some'} dimensions (got {len(shape)})")
+    if len(of_scales) != len(shape) or shape[-1] != 16 * of_scales[-1] or shape[-1] % 64 or shape[-1] == 0 \
+            or shape[:-1] != of_scales[:-1]:
         raise ValueError(f"{name}'s values and scales must have rows of 64 and 4 bytes for each 128 elements")
     if not values.is_contiguous() or not scales.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    got = values.get_device()
-    if scales.get_device() != got or index not in (None, got):
+    if other != got or index is not None and index != got:
         raise ValueError(f"{name} must be on one device" if index is None else f"{name} must be on device {index}")
     return got
 
@@ -376,12 +380,11 @@ def dsmem_mx4_quantize(x, stream=None):
     with a power-of-two scale of each 32.  Returns (values, scales), uint8 [...,
     64 * q] and [..., 4 * q] for q = ceil(columns / 128); what is behind a row's
     end is zero.  More than one leading dimension must be viewable as one."""
+    flat = x
     if isinstance(x, _lib.Tensor) and x.dim() != 2:
         if x.dim() < 1 or x.shape[-1] < 1:
             raise ValueError("x must have rows of one column or more")
         flat = x.view(-1, x.shape[-1])
-    else:
-        flat = x
     dtype, index = _float_tensor("x", flat, 2)
     s = _current(index, stream)
     if s is None:
@@ -389,9 +392,10 @@ def dsmem_mx4_quantize(x, stream=None):
     rows, columns = flat.shape
     if columns > _MOST:
         raise _out_of_range(columns=columns)
-    lead, quads = x.shape[:-1], (columns + 127) // 128
-    values = _lib.empty((*lead, 64 * quads), dtype=_lib.uint8, device=x.device)
-    scales = _lib.empty((*lead, 4 * quads), dtype=_lib.uint8, device=x.device)
+    quads, device = (columns + 127) // 128, x.device
+    lead = (rows,) if flat is x else x.shape[:-1]
+    values = _lib.empty((*lead, 64 * quads), dtype=_lib.uint8, device=device)
+    scales = _lib.empty((*lead, 4 * quads), dtype=_lib.uint8, device=device)
     _check(_lib.dsmem_mx4_quantize(
         flat.data_ptr(), dtype, rows, columns, _row_stride(flat, columns), values.data_ptr(),
         scales.data_ptr(), s))
