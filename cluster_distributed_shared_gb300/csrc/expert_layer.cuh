@@ -48,17 +48,10 @@ constexpr int kMaxRows = kMaxTokens * DSMEM_ROUTE_MAX_TOP_K;
 enum Held { kBf16, kF16, kMx4Bf16, kMx4F16 };
 template <int kHeld>
 constexpr bool kIsMx4 = kHeld == kMx4Bf16 || kHeld == kMx4F16;
-// Warps of a CTA whose experts have up to kTiles tiles of eight rows: of the 16
-// that registers allow an SM, the few tokens' kernels of 16-bit matrices take half
-// each.  (Those of 4-bit ones are bound by instructions, and need them all.)
-template <int kHeld, int kTiles>
-constexpr int kWarps = kTiles == 1 && !kIsMx4<kHeld> ? 8 : 16;
+constexpr int kWarps = 16;  // of a CTA: as many as 128 registers a thread allow
 // Steps of depth that a warp has in flight, a batch: as registers allow.
 template <int kHeld>
 constexpr int kSteps = kIsMx4<kHeld> ? 2 : 4;
-// Whether both kernels' CTAs fit an SM together.
-template <int kHeld, int kTiles>
-constexpr bool kShared = kWarps<kHeld, kTiles> == 8;
 template <int kHeld>
 constexpr int kDepth = kIsMx4<kHeld> ? 128 : 32;  // elements of a step
 
@@ -128,7 +121,6 @@ __device__ __forceinline__ void choose(const LayerArgs& a, int token, int betwee
 
 // Fills `r` and returns the number of active experts; all threads of the CTA.
 // choices: shared memory for tokens * top_k of them.
-template <int kWarps>
 __device__ __forceinline__ int route_all(const LayerArgs& a, Routing& r, Choice* choices) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kEach = DSMEM_ROUTE_MAX_EXPERTS / (kWarps * 32);  // experts of a lane
@@ -493,57 +485,68 @@ __device__ __forceinline__ void multiply(Slot (&slot)[kSteps<kHeld>], const Batc
 }
 
 // A warp's way through the batches [begin, end) of tiles of `batches` batches each.
-//   point(tile, step, at)      where the lane's part of the batch at a tile's step lies
-//   look(tile, column)         column[] of a tile; returns how many column tiles it has
-//   before_columns()           runs before anything of the rows' side is read
-//   finish(tile, first, last, tiles, sum)  takes the sums of a tile's batches [first, last)
-template <int kHeld, int kTiles, bool kWide, typename From, typename Point, typename Look, typename Before,
-          typename Finish>
+// Experts of more than kTiles column tiles have their rows passed by again for each
+// kTiles of them (from the cache: they have just been read).
+//   point(tile, from, step, at)  where the lane's part of the batch at a tile's step
+//                                lies, and its row of column tile `from`
+//   look(tile, from, column)     column[] of column tiles `from` on; returns how many
+//                                there are
+//   finish(tile, first, last, from, tiles, sum)  takes the sums of a tile's batches
+//                                [first, last) by column tiles `from` on
+template <int kHeld, int kTiles, bool kWide, typename From, typename Point, typename Look, typename Finish>
 __device__ __forceinline__ void stream(int begin, int end, int steps, const Divisor& by_batches, int depth,
-                                       const From& from, Point point, Look look, Before before_columns,
-                                       Finish finish) {
+                                       const From& from, Point point, Look look, Finish finish) {
   const int batches = (steps + kSteps<kHeld> - 1) / kSteps<kHeld>;
-  int tile = by_batches.quotient(begin), batch = begin - tile * batches, left = end - begin;
+  int tile = by_batches.quotient(begin), first = begin - tile * batches, left = end - begin;
+  if (left <= 0) return;
   const auto batch_at = [&](int b) { return Batch{b * kSteps<kHeld>, (b + 1) * kSteps<kHeld> * kDepth<kHeld> <= depth}; };
   Ahead at = {};
-  Batch next = batch_at(batch);
+  Batch next = batch_at(first);
   Slot slot[kSteps<kHeld>];
-  if (left > 0) {
-    point(tile, next.step, at);
+  point(tile, 0, next.step, at);
 #pragma unroll
-    for (int d = 0; d < kSteps<kHeld>; ++d) load_rows<kHeld, kWide>(slot[d], at, d, next, steps, depth);
+  for (int d = 0; d < kSteps<kHeld>; ++d) {
+    load_rows<kHeld, kWide>(slot[d], at, d, next, steps, depth);
+    load_column<kHeld>(slot[d], at, d, next, steps, from);
   }
-  before_columns();
-  if (left > 0) {
-#pragma unroll
-    for (int d = 0; d < kSteps<kHeld>; ++d) load_column<kHeld>(slot[d], at, d, next, steps, from);
-  }
+  int column_tile = 0;
 #pragma unroll 1
   while (left > 0) {
-    const int here = tile, first = batch;
+    const int last = min(batches, first + left);
     int column[kTiles];
-    const int tiles = look(here, column);
+    const int tiles = look(tile, column_tile, column);
+    const bool again = kTiles > 1 && tiles > kTiles;
     float sum[kTiles][4];
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) sum[n][0] = sum[n][1] = sum[n][2] = sum[n][3] = 0.0f;
     bool more;
+    int batch = first;
 #pragma unroll 1
     do {
       const Batch now = next;
-      more = ++batch < batches;
-      if (--left > 0) {
-        next = batch_at(more ? batch : 0);
-        if (more) move_on<kHeld, From>(at);
-        else point(++tile, 0, at);
+      more = ++batch < last;
+      const bool any = more || again || left > last - first;
+      if (more) {
+        next = batch_at(batch);
+        move_on<kHeld, From>(at);
+      } else if (any) {
+        next = batch_at(again ? first : 0);
+        point(again ? tile : tile + 1, again ? column_tile + kTiles : 0, next.step, at);
       }
       multiply<kHeld, kTiles>(slot, now, steps, tiles, column, from, sum, [&](int d) {
-        if (left == 0) return;
+        if (!any) return;
         load_rows<kHeld, kWide>(slot[d], at, d, next, steps, depth);
         load_column<kHeld>(slot[d], at, d, next, steps, from);
       });
-    } while (more && left > 0);
-    finish(here, first, batch, tiles, sum);
-    batch = 0;
+    } while (more);
+    finish(tile, first, last, column_tile, min(tiles, kTiles), sum);
+    if (again) {
+      column_tile += kTiles;
+      continue;
+    }
+    left -= last - first;
+    first = column_tile = 0;
+    ++tile;
   }
 }
 
@@ -603,13 +606,14 @@ __device__ __noinline__ void to_h(const LayerArgs& a, const Routing& routing, Pl
 // these.  Parts of tiles go to shared memory and are joined in order when all
 // warps are done.
 template <int kHeld, int kTiles, bool kWide>
-__global__ void __launch_bounds__(kWarps<kHeld, kTiles> * 32, 16 / kWarps<kHeld, kTiles>)
+__global__ void __launch_bounds__(kWarps * 32, 1)
     up_kernel(const __grid_constant__ LayerArgs a) {
   __shared__ Routing routing;
   extern __shared__ float4 parts[];  // [warp][first, last][tile of columns][lane]
+  const int most_tiles = (a.tokens + 7) >> 3;
   launch_dependents();
-  const int active = route_all<kWarps<kHeld, kTiles>>(a, routing, reinterpret_cast<Choice*>(parts));
-  if (a.passes_on && blockIdx.x == 0) pass_on(a.routing, routing);
+  const int active = route_all(a, routing, reinterpret_cast<Choice*>(parts));
+  if (blockIdx.x == 0) pass_on(a.routing, routing);
 
   const int lane = threadIdx.x & 31, g = lane >> 2, warp = threadIdx.x >> 5;
   const int high = a.gated ? 8 : 16;  // rows of h of a tile
@@ -637,40 +641,40 @@ __global__ void __launch_bounds__(kWarps<kHeld, kTiles> * 32, 16 / kWarps<kHeld,
     p.count = min(min(high, a.hidden - p.row), begin + here - (p.expert * a.hidden + p.row));
     return p;
   };
-  const auto share = [&](int w) { return static_cast<int>(static_cast<int64_t>(total) * w / kWarps<kHeld, kTiles>); };
+  const auto share = [&](int w) { return static_cast<int>(static_cast<int64_t>(total) * w / kWarps); };
   const int mine = share(warp), my_end = share(warp + 1);
   const FromX<kHeld, kWide> from{static_cast<const uint16_t*>(a.x), a.x_stride, a.width};
   // A warp's part of the tile that it ends in, or else begins in.
-  const auto part = [&](int w, bool last) { return parts + (w * 2 + last) * (kTiles * 32) + lane; };
+  const auto part = [&](int w, bool last) { return parts + (w * 2 + last) * (most_tiles * 32) + lane; };
   // Rows and columns beyond the tile's are read as its last ones and left out of h.
-  const auto point = [&](int tile, int step, Ahead& at) {
+  const auto point = [&](int tile, int column_tile, int step, Ahead& at) {
     const Place p = place(tile);
     const int e = routing.active[p.expert], last = p.row + p.count - 1;
     point_at<kHeld>(a.gated ? a.gate : a.up, e, min(p.row + g, last), step, at, 0);
     point_at<kHeld>(a.up, e, min(p.row + (a.gated ? g : 8 + g), last), step, at, 1);
     if (!kIsMx4<kHeld>) {
-      const int column = min(g, routing.rows_of[p.expert] - 1);
+      const int column = min(column_tile * 8 + g, routing.rows_of[p.expert] - 1);
       at.column = from.row(routing.token[routing.start[p.expert] + column]) + from.at(step, 0);
     }
   };
-  const auto look = [&](int tile, int (&column)[kTiles]) {
+  const auto look = [&](int tile, int column_tile, int (&column)[kTiles]) {
     const int expert = place(tile).expert, first_row = routing.start[expert], columns = routing.rows_of[expert];
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n) column[n] = routing.token[first_row + min(n * 8 + g, columns - 1)];
-    return (columns + 7) >> 3;
+    for (int n = 0; n < kTiles; ++n) column[n] = routing.token[first_row + min((column_tile + n) * 8 + g, columns - 1)];
+    return ((columns + 7) >> 3) - column_tile;
   };
-  const auto finish = [&](int tile, int first, int last, int tiles, const float (&sum)[kTiles][4]) {
+  const auto finish = [&](int tile, int first, int last, int column_tile, int tiles, const float (&sum)[kTiles][4]) {
     const bool whole = first == 0 && last == batches;
     const Place p = place(tile);
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
       if (kTiles > 1 && n >= tiles) break;
       const float4 v = make_float4(sum[n][0], sum[n][1], sum[n][2], sum[n][3]);
-      if (whole) to_h<kHeld>(a, routing, p, n, v);
-      else part(warp, first == 0)[n * 32] = v;
+      if (whole) to_h<kHeld>(a, routing, p, column_tile + n, v);
+      else part(warp, first == 0)[(column_tile + n) * 32] = v;
     }
   };
-  stream<kHeld, kTiles, kWide>(mine, my_end, steps, a.by_up_batches, a.width, from, point, look, [] {}, finish);
+  stream<kHeld, kTiles, kWide>(mine, my_end, steps, a.by_up_batches, a.width, from, point, look, finish);
   __syncthreads();
   // Each warp joins the tile that ends in its share having begun before it.
   const int tile = a.by_up_batches.quotient(mine), tile_begin = tile * batches;
@@ -698,55 +702,50 @@ __global__ void __launch_bounds__(kWarps<kHeld, kTiles> * 32, 16 / kWarps<kHeld,
 // memory when it has passed the expert, and at the end the warps' sums are
 // added in order.
 template <int kHeld, int kTiles, bool kWide>
-__global__ void __launch_bounds__(kWarps<kHeld, kTiles> * 32, 16 / kWarps<kHeld, kTiles>)
+__global__ void __launch_bounds__(kWarps * 32, 1)
     down_kernel(const __grid_constant__ LayerArgs a) {
   __shared__ Routing routing;
   extern __shared__ float sums[];  // [warp][token][16]
-  int active;
-  if (kShared<kHeld, kTiles>) {
-    active = route_all<kWarps<kHeld, kTiles>>(a, routing, reinterpret_cast<Choice*>(sums));
-  } else {
-    wait_for_previous();
-    take_over(routing, a.routing);
-    active = routing.count;
-  }
+  wait_for_previous();
+  take_over(routing, a.routing);
+  const int active = routing.count;
 
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
   const int steps = (a.hidden + kDepth<kHeld> - 1) / kDepth<kHeld>, batches = (steps + kSteps<kHeld> - 1) / kSteps<kHeld>;
   const int total = active * batches;
-  const int begin = total * warp / kWarps<kHeld, kTiles>, end = total * (warp + 1) / kWarps<kHeld, kTiles>;
+  const int begin = total * warp / kWarps, end = total * (warp + 1) / kWarps;
   const int each = a.by_ctas.quotient(a.width), over = a.width - each * gridDim.x;
   const int first = each * blockIdx.x + min(static_cast<int>(blockIdx.x), over);
   const int last = first + each + (static_cast<int>(blockIdx.x) < over);
   const FromH<kHeld> from{a.h, a.h_pitch};
   float* mine = sums + warp * a.tokens * 16;
 
-  for (int channel = first, turn = 0; channel < last; channel += 16, ++turn) {
+  for (int channel = first; channel < last; channel += 16) {
     const int count = min(16, last - channel);
     for (int i = lane; i < a.tokens * 16; i += 32) mine[i] = 0.0f;
     __syncwarp();
     // Channels and columns beyond the tile's are read as its last ones and left out of y.
-    const auto point = [&](int tile, int step, Ahead& at) {
+    const auto point = [&](int tile, int column_tile, int step, Ahead& at) {
       const int e = routing.active[tile], last_channel = channel + count - 1;
       point_at<kHeld>(a.down, e, min(channel + g, last_channel), step, at, 0);
       point_at<kHeld>(a.down, e, min(channel + 8 + g, last_channel), step, at, 1);
       if (!kIsMx4<kHeld>)
-        at.column = from.row(routing.start[tile] + min(g, routing.rows_of[tile] - 1)) + from.at(step, 0);
+        at.column = from.row(routing.start[tile] + min(column_tile * 8 + g, routing.rows_of[tile] - 1)) + from.at(step, 0);
     };
-    const auto look = [&](int tile, int (&column)[kTiles]) {
+    const auto look = [&](int tile, int column_tile, int (&column)[kTiles]) {
       const int first_row = routing.start[tile], columns = routing.rows_of[tile];
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) column[n] = first_row + min(n * 8 + g, columns - 1);
-      return (columns + 7) >> 3;
+      for (int n = 0; n < kTiles; ++n) column[n] = first_row + min((column_tile + n) * 8 + g, columns - 1);
+      return ((columns + 7) >> 3) - column_tile;
     };
-    const auto finish = [&](int tile, int, int, int tiles, const float (&sum)[kTiles][4]) {
+    const auto finish = [&](int tile, int, int, int column_tile, int tiles, const float (&sum)[kTiles][4]) {
       const int first_row = routing.start[tile], columns = routing.rows_of[tile];
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
         if (kTiles > 1 && n >= tiles) break;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int col = n * 8 + t * 2 + j;
+          const int col = (column_tile + n) * 8 + t * 2 + j;
           if (col < columns) {
             float* p = mine + routing.token[first_row + col] * 16 + g;
             p[0] += sum[n][j];
@@ -756,13 +755,12 @@ __global__ void __launch_bounds__(kWarps<kHeld, kTiles> * 32, 16 / kWarps<kHeld,
       }
       __syncwarp();
     };
-    stream<kHeld, kTiles, kWide>(begin, end, steps, a.by_down_batches, a.hidden, from, point, look,
-                                 [&] { if (kShared<kHeld, kTiles> && turn == 0) wait_for_previous(); }, finish);
+    stream<kHeld, kTiles, kWide>(begin, end, steps, a.by_down_batches, a.hidden, from, point, look, finish);
     __syncthreads();
-    for (int i = threadIdx.x; i < a.tokens * 16; i += kWarps<kHeld, kTiles> * 32) {
+    for (int i = threadIdx.x; i < a.tokens * 16; i += kWarps * 32) {
       float v = sums[i];
 #pragma unroll 4
-      for (int w = 1; w < kWarps<kHeld, kTiles>; ++w) v += sums[w * a.tokens * 16 + i];
+      for (int w = 1; w < kWarps; ++w) v += sums[w * a.tokens * 16 + i];
       const int token = i >> 4, c = i & 15;
       if (c >= count) continue;
       const int64_t at = static_cast<int64_t>(token) * a.width + channel + c;
@@ -777,10 +775,10 @@ template <int kHeld, int kTiles, bool kWide>
 cudaError_t launch_up(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
   static SmemLimit limit;
   const auto kernel = up_kernel<kHeld, kTiles, kWide>;
-  constexpr int bytes = kWarps<kHeld, kTiles> * 2 * kTiles * 32 * static_cast<int>(sizeof(float4));
+  const int bytes = kWarps * 2 * ((a.tokens + 7) / 8) * 32 * static_cast<int>(sizeof(float4));
   const cudaError_t e = limit.need(reinterpret_cast<const void*>(kernel), ctx.device, bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<ctx.sm_count, kWarps<kHeld, kTiles> * 32, bytes, stream>>>(a);
+  kernel<<<ctx.sm_count, kWarps * 32, bytes, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -788,14 +786,12 @@ template <int kHeld, int kTiles, bool kWide>
 cudaError_t launch_down(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
   static SmemLimit limit;
   const auto kernel = down_kernel<kHeld, kTiles, kWide>;
-  // The warps' sums, or while routing the choices.
-  const int bytes = std::max(kWarps<kHeld, kTiles> * a.tokens * 16 * static_cast<int>(sizeof(float)),
-                             a.tokens * a.top_k * static_cast<int>(sizeof(Choice)));
+  const int bytes = kWarps * a.tokens * 16 * static_cast<int>(sizeof(float));
   const cudaError_t e = limit.need(reinterpret_cast<const void*>(kernel), ctx.device, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctx.sm_count));
-  cfg.blockDim = dim3(kWarps<kHeld, kTiles> * 32);
+  cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
@@ -819,10 +815,8 @@ cudaError_t launch_ups(const LayerArgs& a, const CallContext& ctx, cudaStream_t 
   return wide ? launch_up<kHeld, kTiles, true>(a, ctx, stream) : launch_up<kHeld, kTiles, false>(a, ctx, stream);
 }
 
-// Both launches; the down kernel's tiles say whether it routes for itself.
 template <int kHeldUp, int kHeldDown, int kTiles>
-cudaError_t launch_with(LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
-  a.passes_on = !kShared<kHeldDown, kTiles>;
+cudaError_t launch_with(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
   const cudaError_t e = launch_ups<kHeldUp, kTiles>(a, ctx, stream);
   if (e != cudaSuccess) return e;
   if constexpr (!kIsMx4<kHeldDown>) {
@@ -831,10 +825,9 @@ cudaError_t launch_with(LayerArgs& a, const CallContext& ctx, cudaStream_t strea
   return launch_down<kHeldDown, kTiles, true>(a, ctx, stream);
 }
 template <int kHeldUp, int kHeldDown>
-cudaError_t launch_both(LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
+cudaError_t launch_both(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
   if (a.tokens <= 8) return launch_with<kHeldUp, kHeldDown, 1>(a, ctx, stream);
-  if (a.tokens <= 32) return launch_with<kHeldUp, kHeldDown, 4>(a, ctx, stream);
-  return launch_with<kHeldUp, kHeldDown, kMaxTokens / 8>(a, ctx, stream);
+  return launch_with<kHeldUp, kHeldDown, 4>(a, ctx, stream);
 }
 
 }  // namespace

@@ -157,13 +157,12 @@ struct LayerArgs {
   int mx4, gated, silu;
   void* out;
   // Set by run_expert_layer.
-  void* routing;  // for the down kernel, where passes_on says so
-  int passes_on;
+  void* routing;  // the up kernel's, for the down kernel
   uint16_t* h;  // [rows][h_pitch], each value as two 16-bit numbers
   int h_pitch;
   Divisor by_ctas, by_hidden, by_tiles, by_up_batches, by_down_batches;
 };
-cudaError_t launch_layer_mx4(LayerArgs& a, const CallContext& ctx, cudaStream_t stream);
+cudaError_t launch_layer_mx4(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream);
 int run_expert_layer(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream);
 
 struct CombineArgs {

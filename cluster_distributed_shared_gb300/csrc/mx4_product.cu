@@ -732,7 +732,7 @@ int launch(const Mx4ProductArgs& p, const CallContext& ctx, cudaStream_t stream)
 
 // Narrow tiles where wide ones would not give every SM one.
 int run_mx4_product(const Mx4ProductArgs& p, const CallContext& ctx, cudaStream_t stream) {
-  if (tile_bound(p, 128) < ctx.sm_count) return launch<32>(p, ctx, stream);
+  if (tile_bound(p, 32) <= ctx.sm_count) return launch<32>(p, ctx, stream);
   if (tile_bound(p, 256) < 2 * ctx.sm_count) return launch<128>(p, ctx, stream);
   return launch<256>(p, ctx, stream);
 }
