@@ -51,7 +51,7 @@ constexpr bool kIsMx4 = kHeld == kMx4Bf16 || kHeld == kMx4F16;
 constexpr int kWarps = 16;  // of a CTA: as many as 128 registers a thread allow
 // Steps of depth that a warp has in flight, a batch: as registers allow.
 template <int kHeld>
-constexpr int kSteps = kIsMx4<kHeld> ? 2 : 4;
+constexpr int kSteps = kIsMx4<kHeld> ? 1 : 4;
 template <int kHeld>
 constexpr int kDepth = kIsMx4<kHeld> ? 128 : 32;  // elements of a step
 
