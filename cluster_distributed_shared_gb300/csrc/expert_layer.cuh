@@ -15,14 +15,20 @@
 //     share of an SM fills 27, and would pass every byte through shared memory.)
 //   * Every SM reads the same number of rows, every warp the same number of
 //     batches of kSteps steps.
-//   * Each CTA routes all tokens for itself instead of waiting for a launch that
-//     does.  The down kernel is launched while the up kernel runs (programmatic
-//     dependent launch), and waits for it only after its own routing and first
-//     loads of weights; for up to 8 tokens both fit an SM together.
+//   * Each CTA of the up kernel routes all tokens for itself instead of waiting for
+//     a launch that does, and the first passes the routing on.  The down kernel is
+//     launched while the up kernel runs (programmatic dependent launch), so that
+//     its CTAs wait where the up kernel's leave.
 //   * Code that runs once costs about 10 cycles an instruction, for its fetch:
 //     hence loops where unrolled code would do less work.
 // Sums are 32-bit: in the fragments along a warp's part of the depth, then over
 // the warps through shared memory in their order.  Nothing is added atomically.
+//
+// Measured with 128 experts of 2048 x 1024, 8 a token, gated, 32 tokens (210 us of
+// reading): 16-bit 229 us, 6.1 TB/s; 4-bit 179 us, bound by instructions (17 for 8
+// elements of decoding, 280 a step in all; 55% of issue slots and of the logic pipe).
+// One token, 4 experts: 20.5 and 18.9 us, of which 7.5 and 2 are reading, the rest
+// launches, routing and first touches of code.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -48,8 +54,14 @@ constexpr int kMaxRows = kMaxTokens * DSMEM_ROUTE_MAX_TOP_K;
 enum Held { kBf16, kF16, kMx4Bf16, kMx4F16 };
 template <int kHeld>
 constexpr bool kIsMx4 = kHeld == kMx4Bf16 || kHeld == kMx4F16;
-constexpr int kWarps = 16;  // of a CTA: as many as 128 registers a thread allow
-// Steps of depth that a warp has in flight, a batch: as registers allow.
+// Warps of a CTA: as many as 128 registers a thread allow.  (With 8 a CTA, and both
+// kernels' CTAs on an SM together, 4 tokens of 64 experts of 2048 x 768, 4 a token,
+// took 40.0 us, not 34.9, and 1 token 19.1, not 18.8.)
+constexpr int kWarps = 16;
+// Steps of depth that a warp has in flight, a batch: as registers allow.  (16-bit: 2
+// instead of 4 took 108 us, not 97, at 32 tokens of 64 experts of 2048 x 768.  4-bit,
+// whose decoding hides a load's way: 2 instead of 1 spilled, 184 us and not 179 in
+// the case above.)
 template <int kHeld>
 constexpr int kSteps = kIsMx4<kHeld> ? 1 : 4;
 template <int kHeld>
@@ -191,8 +203,7 @@ __device__ __forceinline__ int route_all(const LayerArgs& a, Routing& r, Choice*
   return count;
 }
 
-// The routing to the down kernel and there, by all threads, where that does not
-// route for itself while the up kernel runs.
+// The routing to the down kernel and there, by all threads.
 __device__ __forceinline__ void pass_on(void* to, const Routing& r) {
   static_assert(sizeof(Routing) % 16 == 0, "whole vectors");
   for (int i = threadIdx.x; i < static_cast<int>(sizeof(Routing) / 16); i += blockDim.x)
@@ -260,7 +271,8 @@ template <int kHeld>
 __device__ __forceinline__ void point_at(const LayerMatrix& m, int e, int row, int step, Ahead& to, int i) {
   const int t = threadIdx.x & 3;
   const int64_t size = kIsMx4<kHeld> ? 1 : 2;
-  to.row[i] = static_cast<const uint8_t*>(m.values) + (e * m.group_stride + row * m.row_stride) * size + step * 64 + t * 16;
+  to.row[i] = static_cast<const uint8_t*>(m.values) + (e * m.group_stride + row * m.row_stride) * size + step * 64 +
+              t * 16;
   if (kIsMx4<kHeld>)
     to.scale[i] = m.scales + (static_cast<int64_t>(e) * m.rows + row) * m.scale_stride + step * 4 + t;
 }
@@ -373,7 +385,9 @@ struct FromH {
   const uint16_t* h;
   int pitch;  // elements of a row
   __device__ __forceinline__ const uint16_t* row(int r) const { return h + static_cast<int64_t>(r) * 2 * pitch; }
-  __device__ __forceinline__ static int at(int step, int q) { return step * kStep + (q * 4 + (threadIdx.x & 3)) * 16; }
+  __device__ __forceinline__ static int at(int step, int q) {
+    return step * kStep + (q * 4 + (threadIdx.x & 3)) * 16;
+  }
   // Where the first number of element c lies in its row; the second is 8 further on.
   __device__ __forceinline__ static int place_of(int c) {
     if constexpr (!kIsMx4<kHeld>) return (c >> 3) * 16 + (c & 7);
@@ -499,7 +513,9 @@ __device__ __forceinline__ void stream(int begin, int end, int steps, const Divi
   const int batches = (steps + kSteps<kHeld> - 1) / kSteps<kHeld>;
   int tile = by_batches.quotient(begin), first = begin - tile * batches, left = end - begin;
   if (left <= 0) return;
-  const auto batch_at = [&](int b) { return Batch{b * kSteps<kHeld>, (b + 1) * kSteps<kHeld> * kDepth<kHeld> <= depth}; };
+  const auto batch_at = [&](int b) {
+    return Batch{b * kSteps<kHeld>, (b + 1) * kSteps<kHeld> * kDepth<kHeld> <= depth};
+  };
   Ahead at = {};
   Batch next = batch_at(first);
   Slot slot[kSteps<kHeld>];
@@ -617,7 +633,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
   const int lane = threadIdx.x & 31, g = lane >> 2, warp = threadIdx.x >> 5;
   const int high = a.gated ? 8 : 16;  // rows of h of a tile
-  const int steps = (a.width + kDepth<kHeld> - 1) / kDepth<kHeld>, batches = (steps + kSteps<kHeld> - 1) / kSteps<kHeld>;
+  const int steps = (a.width + kDepth<kHeld> - 1) / kDepth<kHeld>;
+  const int batches = (steps + kSteps<kHeld> - 1) / kSteps<kHeld>;
   const int rows = active * a.hidden, each = a.by_ctas.quotient(rows), over = rows - each * gridDim.x;
   const int begin = each * blockIdx.x + min(static_cast<int>(blockIdx.x), over);
   const int here = each + (static_cast<int>(blockIdx.x) < over);
@@ -660,10 +677,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const auto look = [&](int tile, int column_tile, int (&column)[kTiles]) {
     const int expert = place(tile).expert, first_row = routing.start[expert], columns = routing.rows_of[expert];
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n) column[n] = routing.token[first_row + min((column_tile + n) * 8 + g, columns - 1)];
+    for (int n = 0; n < kTiles; ++n)
+      column[n] = routing.token[first_row + min((column_tile + n) * 8 + g, columns - 1)];
     return ((columns + 7) >> 3) - column_tile;
   };
-  const auto finish = [&](int tile, int first, int last, int column_tile, int tiles, const float (&sum)[kTiles][4]) {
+  const auto finish = [&](int tile, int first, int last, int column_tile, int tiles,
+                          const float (&sum)[kTiles][4]) {
     const bool whole = first == 0 && last == batches;
     const Place p = place(tile);
 #pragma unroll
@@ -711,7 +730,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int active = routing.count;
 
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
-  const int steps = (a.hidden + kDepth<kHeld> - 1) / kDepth<kHeld>, batches = (steps + kSteps<kHeld> - 1) / kSteps<kHeld>;
+  const int steps = (a.hidden + kDepth<kHeld> - 1) / kDepth<kHeld>;
+  const int batches = (steps + kSteps<kHeld> - 1) / kSteps<kHeld>;
   const int total = active * batches;
   const int begin = total * warp / kWarps, end = total * (warp + 1) / kWarps;
   const int each = a.by_ctas.quotient(a.width), over = a.width - each * gridDim.x;
@@ -730,7 +750,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       point_at<kHeld>(a.down, e, min(channel + g, last_channel), step, at, 0);
       point_at<kHeld>(a.down, e, min(channel + 8 + g, last_channel), step, at, 1);
       if (!kIsMx4<kHeld>)
-        at.column = from.row(routing.start[tile] + min(column_tile * 8 + g, routing.rows_of[tile] - 1)) + from.at(step, 0);
+        at.column =
+            from.row(routing.start[tile] + min(column_tile * 8 + g, routing.rows_of[tile] - 1)) + from.at(step, 0);
     };
     const auto look = [&](int tile, int column_tile, int (&column)[kTiles]) {
       const int first_row = routing.start[tile], columns = routing.rows_of[tile];
@@ -802,7 +823,8 @@ cudaError_t launch_down(const LayerArgs& a, const CallContext& ctx, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// Whether rows of a 16-bit matrix are whole 16-byte vectors.
+// Whether rows of a 16-bit matrix are whole 16-byte vectors.  Others are loaded by
+// words and shifted: 16 tokens, 16 experts of 1023 x 511 in 43 us, of 1024 x 512 in 21.
 bool whole_vectors(const LayerMatrix& m, int columns) {
   return reinterpret_cast<uintptr_t>(m.values) % 16 == 0 && m.row_stride % 8 == 0 && m.group_stride % 8 == 0 &&
          columns % 8 == 0;
@@ -824,6 +846,10 @@ cudaError_t launch_with(const LayerArgs& a, const CallContext& ctx, cudaStream_t
   }
   return launch_down<kHeldDown, kTiles, true>(a, ctx, stream);
 }
+// Up to 8 tokens have one column tile.  (With 4 tiles for any number, 8 tokens took
+// 54.0 us, not 51.1, and in 4 bits 44.6, not 43.0; 64 experts of 2048 x 768.)  For
+// more the kernels hold the sums of 4, which 32 tokens have at most; 8, for 64, spilled
+// registers: 33 tokens took 122 us, not 102, and in 4 bits 112, not 82.
 template <int kHeldUp, int kHeldDown>
 cudaError_t launch_both(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
   if (a.tokens <= 8) return launch_with<kHeldUp, kHeldDown, 1>(a, ctx, stream);

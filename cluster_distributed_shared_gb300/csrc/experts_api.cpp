@@ -332,7 +332,8 @@ int run_layer(const void* x, int64_t x_stride, int32_t dtype, int32_t tokens, in
   int rc = check_route(logits_dtype, tokens, experts, logits_stride, top_k);
   if (rc) return rc;
   DSMH_REQUIRE(dtype == DSMEM_F16 || dtype == DSMEM_BF16, "dtype must be DSMEM_F16 or DSMEM_BF16 (got %d)", dtype);
-  DSMH_REQUIRE(tokens <= DSMEM_LAYER_MAX_TOKENS, "tokens must be in [0, %d] (got %d)", DSMEM_LAYER_MAX_TOKENS, tokens);
+  DSMH_REQUIRE(tokens <= DSMEM_LAYER_MAX_TOKENS, "tokens must be in [0, %d] (got %d)", DSMEM_LAYER_MAX_TOKENS,
+               tokens);
   DSMH_REQUIRE(width >= 1 && hidden >= 1 && width <= DSMEM_LAYER_MAX_WIDTH && hidden <= DSMEM_LAYER_MAX_WIDTH,
                "width and hidden must be in [1, %d] (got %d and %d)", DSMEM_LAYER_MAX_WIDTH, width, hidden);
   DSMH_REQUIRE(x_stride >= width, "x_stride must be >= width");

@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const Rows r) {
   for (int u = 0; u < kPieces; ++u) {
     const int i = min(first + u * kThreads, r.total - 1);
     const int row = r.by_pieces.quotient(i);
-    piece[u].template load<kWide>(static_cast<const T*>(r.in) + row * r.stride, (i - row * r.pieces) * kEach, r.columns);
+    piece[u].template load<kWide>(static_cast<const T*>(r.in) + row * r.stride, (i - row * r.pieces) * kEach,
+                                  r.columns);
   }
 #pragma unroll
   for (int u = 0; u < kPieces; ++u) {

@@ -7,7 +7,8 @@ two-matrix network, and sums their answers with the router's weights:
 
     python examples/expert_layer.py
 
-trains it for a few steps on synthetic tokens and then answers single tokens.
+trains it for a few steps on synthetic tokens, then answers single tokens, and
+the same with its matrices in 4 bits.
 """
 from __future__ import annotations
 
@@ -76,9 +77,32 @@ class ExpertLayer:
             weight.sub_(grad, alpha=rate)
         return loss, norm
 
-    def decode(self, token):
-        """The answer for one token [width]."""
-        return self.forward(token.unsqueeze(0))[0][0]
+    def decode(self, tokens):
+        """The answers for a few tokens [up to 64, width], or one [width]."""
+        x = tokens.view(-1, tokens.shape[-1])
+        y = dh.dsmem_expert_layer(x, x.float() @ self.router.t(), self.up, self.down, self.top_k)
+        return y.view_as(tokens)
+
+
+class FourBitLayer:
+    """A trained layer for answering only, with its matrices as microscaled 4-bit
+    elements: a quarter of the memory, and of the reading when decoding."""
+
+    def __init__(self, layer: ExpertLayer):
+        self.experts, self.top_k, self.router = layer.experts, layer.top_k, layer.router
+        self.up, self.down = dh.dsmem_mx4_quantize(layer.up), dh.dsmem_mx4_quantize(layer.down)
+
+    def forward(self, x):
+        """Many tokens x [tokens, width], whose rows are multiplied in 4 bits too."""
+        ids, weights = dh.dsmem_route(x.float() @ self.router.t(), self.top_k)
+        offsets, order, position = dh.dsmem_group(ids, self.experts)
+        hidden = dh.dsmem_mx4_grouped_matmul(dh.dsmem_mx4_quantize(x), self.up, offsets, order=order,
+                                             fan=self.top_k, out_dtype=x.dtype)
+        active = dh.dsmem_mx4_quantize(torch.relu(hidden))
+        answers = dh.dsmem_mx4_grouped_matmul(active, self.down, offsets, out_dtype=x.dtype)
+        return dh.dsmem_combine(answers, position.view_as(ids), weights)
+
+    decode = ExpertLayer.decode
 
 
 def main(tokens=4096, width=1024, hidden=512, experts=32, top_k=4, steps=20):
@@ -91,6 +115,10 @@ def main(tokens=4096, width=1024, hidden=512, experts=32, top_k=4, steps=20):
         loss, norm = layer.train_step(x, teacher.forward(x)[0], rate=2.0)
         if step % 5 == 0 or step == steps - 1:
             print(f"step {step:3d}  loss {float(loss):.5f}  gradient norm {float(norm):.4f}")
+    four = FourBitLayer(layer)
+    whole, few, many = (t.float() for t in (layer.forward(x)[0][:32], four.decode(x[:32]), four.forward(x)[:32]))
+    print(f"4-bit matrices: answers off by {float((few - whole).norm() / whole.norm()):.3f}, with 4-bit rows by "
+          f"{float((many - whole).norm() / whole.norm()):.3f}")
     answers = [layer.decode(x[i]) for i in range(4)]
     batch = layer.forward(x[:4])[0]
     print("largest difference of 4 decoded tokens from their batch:",

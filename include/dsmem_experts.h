@@ -1,14 +1,18 @@
 /*
  * dsmem_experts -- an expert layer's operators for NVIDIA GB300 (sm_103a):
  * routing, grouping by key, products grouped by key, the weighted way back,
- * and the gradients' global norm with clipping.
+ * the gradients' global norm with clipping, microscaled 4-bit rows with their
+ * products, and a whole layer for a few tokens.
  *
  * dsmem_hist counts how many keys each owner has.  These calls go on from
  * there: they put rows in the order of their keys (dsmem_group), multiply
  * each group's rows with the group's own matrix (dsmem_grouped_matmul, and
  * its two gradients), bring the rows back to the tokens they came from
  * (dsmem_combine), choose the keys from a router's scores (dsmem_route), and
- * clip the gradients that come out (dsmem_grad_clip).
+ * clip the gradients that come out (dsmem_grad_clip).  Matrices and rows can be
+ * kept in 4 bits (dsmem_mx4_quantize) and multiplied so
+ * (dsmem_mx4_grouped_matmul); when decoding, dsmem_expert_layer goes the whole way
+ * from scores to answers in one call.
  *
  * Conventions are those of dsmem_hist.h: 0 or a negative DSMEM_HIST_E* code,
  * dsmem_hist_last_error() for the message, device pointers on the current
@@ -24,8 +28,8 @@
  * replayed after dsmem_hist_release().
  *
  * The same call gives the same bits: sums are taken in an order that sizes and
- * the device alone decide, in 32 bits or more, and rounded once to the output's
- * type.
+ * the device alone decide (in dsmem_expert_layer also which experts the batch's
+ * tokens chose), in 32 bits or more, and rounded once to the output's type.
  *
  * The product kernels wait for their own copies and matrix instructions with
  * bounded waits (about 50 ms each).  A wait that gives up makes the launch's

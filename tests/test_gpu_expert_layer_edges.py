@@ -178,8 +178,9 @@ def guarded(shape, dtype):
     that the rest still holds it."""
     n = math.prod(shape)
     raw = torch.full(((n + 512) * dtype.itemsize,), 0x5a, dtype=torch.uint8, device="cuda").view(dtype)
-    return raw[256:256 + n].view(shape), lambda: bool((raw.view(torch.uint8)[:256 * dtype.itemsize] == 0x5a).all() and (
-        raw.view(torch.uint8)[(256 + n) * dtype.itemsize:] == 0x5a).all())
+    around, size = raw.view(torch.uint8), dtype.itemsize
+    return raw[256:256 + n].view(shape), lambda: bool((around[:256 * size] == 0x5a).all() and (
+        around[(256 + n) * size:] == 0x5a).all())
 
 
 @pytest.mark.parametrize("tokens,width,hidden", [(1, 33, 20), (7, 1000, 70), (33, 129, 8)])
