@@ -17,7 +17,7 @@
 // of which begins when the last tile's half is in its warps' registers.
 //
 // Measured, 16384 tokens x 8 of 64 experts of 1024 x 2048, groups of unequal size, rows
-// named by the order: 155 to 160 us, 3.5 PFLOP/s, where the bytes alone would take 53
+// named by the order: 162 us, 3.4 PFLOP/s, where the bytes alone would take 53
 // (matrices and rows once, bf16 results once).  The matrix warp is busy 700 cycles a
 // stage of 384 of arithmetic: 48 KB a stage go into shared memory and out of it
 // again, and the scales' way to tensor memory comes on top.  32 tokens x 8 of 128
@@ -209,29 +209,43 @@ __device__ __forceinline__ void store_zeros(const Args& a, int row0, int end, in
   }
 }
 
-// A pair of values (bits of floats) rounded to bf16 or f16 here and now, in one
-// place for both: left to the compiler, roundings move behind the next loads, whose
+// A pair of values (bits of floats) rounded to bf16 or f16, of which the bits `kept`
+// remain, here and now, in one place for both: left to the compiler, roundings move behind the next loads, whose
 // values then do not fit registers.
-__device__ __forceinline__ uint32_t pair_now(uint32_t low, uint32_t high, bool bf16) {
+__device__ __forceinline__ uint32_t pair_now(uint32_t low, uint32_t high, bool bf16, uint32_t kept) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t@p cvt.rn.bf16x2.f32 %0, %1, %2;\n\t"
-      "@!p cvt.rn.f16x2.f32 %0, %1, %2;\n\t}"
+      "@!p cvt.rn.f16x2.f32 %0, %1, %2;\n\tand.b32 %0, %0, %4;\n\t}"
       : "=r"(r)
-      : "f"(__uint_as_float(high)), "f"(__uint_as_float(low)), "r"(static_cast<uint32_t>(bf16)));
+      : "f"(__uint_as_float(high)), "f"(__uint_as_float(low)), "r"(static_cast<uint32_t>(bf16)), "r"(kept));
   return r;
+}
+
+// The order's entry of a place, kBehind behind the tile's end, and the row of x
+// that it names, -1 for none.
+constexpr int kBehind = -2;
+__device__ __forceinline__ int place_at(const Args& a, int p, int end) {
+  return p < end ? (a.order ? max(a.order[p], -1) : p) : kBehind;
+}
+__device__ __forceinline__ int row_named(const Args& a, int o) {
+  if (o < 0) return o;
+  const int row = a.order ? a.fan.quotient(o) : o;
+  return row < a.x_rows ? row : -1;
 }
 
 // A warp's 32 rows by kMine columns from tensor memory to the output, up to 64 bytes
 // of a row at a time; free() is called when they have left tensor memory.  16-bit
-// values are first all brought to registers, as pairs, so that this is soon.
+// values are first all brought to registers, as pairs, so that this is soon.  A row
+// without a source was multiplied as zeros, which a matrix's NaN makes NaN.
 template <int kMine, typename O, typename Free>
 __device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap* out_map, const Tile& t, int row0,
-                                           int chan, uint32_t tmem, uint32_t staging, Free free) {
+                                           int chan, uint32_t tmem, uint32_t staging, bool none, Free free) {
   constexpr int kLine = kMine * static_cast<int>(sizeof(O)) < 64 ? kMine * static_cast<int>(sizeof(O)) : 64;
   constexpr int kN = kLine / static_cast<int>(sizeof(O)), kWords = kLine / 4;
   const int limit = min(a.outer, chan + kMine);
   const bool bf16 = a.out_dtype == DSMEM_BF16;
+  const uint32_t kept = none ? 0u : ~0u;
   if constexpr (sizeof(O) == 2) {
     uint32_t line[kMine / kN][kWords];
     if (row0 < t.end) {
@@ -242,7 +256,7 @@ __device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap* out
         tmem_wait_load();
 #pragma unroll
         for (int l = 0; l < 8; ++l)
-          line[c / kN][c % kN / 2 + l] = pair_now(r[2 * l], r[2 * l + 1], bf16);
+          line[c / kN][c % kN / 2 + l] = pair_now(r[2 * l], r[2 * l + 1], bf16, kept);
       }
     }
     free();
@@ -256,22 +270,12 @@ __device__ __forceinline__ void store_tile(const Args& a, const CUtensorMap* out
       uint32_t r[kN];
       tmem_load16(tmem + c, r);
       tmem_wait_load();
+#pragma unroll
+      for (int l = 0; l < kN; ++l) r[l] &= kept;
       store_lines<O, kLine>(a, out_map, row0, t.end, chan + c, limit, r, staging);
     }
     free();
   }
-}
-
-// The order's entry of a place, kBehind behind the tile's end, and the row of x
-// that it names, -1 for none.
-constexpr int kBehind = -2;
-__device__ __forceinline__ int place_at(const Args& a, int p, int end) {
-  return p < end ? (a.order ? max(a.order[p], -1) : p) : kBehind;
-}
-__device__ __forceinline__ int row_named(const Args& a, int o) {
-  if (o < 0) return o;
-  const int row = a.order ? a.fan.quotient(o) : o;
-  return row < a.x_rows ? row : -1;
 }
 
 // The copying warps.  A thread copies one of the eight pieces of every 16th row.
@@ -640,6 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t place = R::kBuffers == 2 ? done & 1 : 0;
       const uint32_t turn = R::kBuffers == 2 ? done >> 1 & 1 : done & 1;
+      const bool none = row_named(a, place_at(a, row0 + lane, t.end)) == -1;
       // A long contraction may take longer than one bounded wait of a copy.
       const bool ok = wait_for(acc_full + 8 * place, turn, gave_up, a.wait_cycles + 4096ll * t.blocks, a.status);
       if (!__all_sync(kFull, ok)) break;
@@ -650,8 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_local(acc_empty + 8 * (R::kHalves == 2 ? half : place));
       };
-      if (a.out_dtype == DSMEM_F32) store_tile<R::kMine, float>(a, &maps.out, t, row0, chan, d, staging, free);
-      else store_tile<R::kMine, uint16_t>(a, &maps.out, t, row0, chan, d, staging, free);
+      if (a.out_dtype == DSMEM_F32) store_tile<R::kMine, float>(a, &maps.out, t, row0, chan, d, staging, none, free);
+      else store_tile<R::kMine, uint16_t>(a, &maps.out, t, row0, chan, d, staging, none, free);
       ++done;
     }
     if (lane == 0) store_wait();

@@ -198,7 +198,7 @@ DSMEM_HIST_API int dsmem_mx4_dequantize(const uint8_t* values, const uint8_t* sc
  * with X [x_rows, inner] and W [groups, outer, inner] what the 4-bit tensors
  * stand for, summed in 32 bits.  Rows p of no group, and rows whose source lies
  * outside x, are 0.
- *   x_values, w_values  16-byte aligned, and with the scales contiguous
+ *   x_values, w_values  16-byte aligned; the scales 4-byte aligned; all contiguous
  *   inner               1 .. 2^31 - 513, rows padded as above
  *   out                 [n, outer] of out_dtype, any of the three */
 DSMEM_HIST_API int dsmem_mx4_grouped_matmul(const uint8_t* x_values, const uint8_t* x_scales,

@@ -199,6 +199,45 @@ def test_nothing_around_the_answer_is_written(tokens, width, hidden):
     assert torch.equal(out, want) and untouched()
 
 
+@pytest.mark.parametrize("tokens", [1, 9, 64])
+def test_tokens_that_choose_nothing(tokens):
+    for mx4 in (False, True):
+        layer = Layer(4, 72, 40, torch.float16, mx4, True, 27)
+        x, logits = tokens_of(tokens, 4, 72, torch.float16, 28)
+        assert (layer.run(x, torch.full_like(logits, -math.inf), 2) == 0).all()
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_infinite_logits_are_weighted_as_dsmem_route_does(renormalize):
+    layer = Layer(6, 64, 48, torch.bfloat16, False, False, 29)
+    x, logits = tokens_of(5, 6, 64, torch.bfloat16, 30)
+    want = layer.run(x, logits, 2, renormalize=renormalize)
+    logits[1, 3] = math.inf
+    logits[2, 1] = logits[2, 4] = math.inf
+    ids, weights = dh.dsmem_route(logits, 2, renormalize=renormalize)
+    got = layer.run(x, logits, 2, renormalize=renormalize)
+    exact = few.choices
+    try:
+        few.choices = lambda *_: (ids.cpu(), weights.cpu())
+        y, off = layer.exact(x, logits, 2, renormalize=renormalize)
+    finally:
+        few.choices = exact
+    assert torch.equal(got.isnan().cpu(), y.isnan())
+    rest = [t for t in range(5) if not y[t].isnan().any()]
+    layer.dtype = got.dtype
+    layer.check(got[rest], (y[rest], off[rest]))
+    assert torch.equal(got[[0, 3, 4]].isnan(), want[[0, 3, 4]].isnan())
+
+
+def test_all_of_one_expert():
+    """64 tokens of one expert among many: its matrices are passed again."""
+    for mx4 in (False, True):
+        layer = Layer(9, 136, 200, torch.bfloat16, mx4, True, 31)
+        x, logits = tokens_of(64, 9, 136, torch.bfloat16, 32)
+        logits[:, 4] = 9.0
+        layer.check(layer.run(x, logits, 2), layer.exact(x, logits, 2))
+
+
 def test_no_tokens():
     layer = Layer(4, 64, 40, torch.bfloat16, False, True, 25)
     x, logits = tokens_of(3, 4, 64, torch.bfloat16, 26)
@@ -255,6 +294,23 @@ def test_products_with_no_rows_to_name():
     assert dh.dsmem_mx4_grouped_matmul(none, w, offsets).shape == (0, 40)
 
 
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,outer", [(60, 40), (900, 2600), (9000, 2600)])
+def test_rows_without_a_source_are_zero_beside_what_is_not_a_number(n, outer, out):
+    """Tiles of each width, with NaN in the matrices."""
+    g = generator(35)
+    x, x64 = four_bit(g, 50, 300)
+    w = torch.randn(2, outer, 300, generator=g)
+    w[0, ::3, 7] = math.nan
+    pair = dh.dsmem_mx4_quantize(w.cuda())
+    order = torch.randint(-20, 70, (n,), generator=g).to(torch.int32)
+    offsets = torch.tensor([0, n // 2, n - 2], dtype=torch.int32)
+    got = dh.dsmem_mx4_grouped_matmul(x, pair, offsets.cuda(), order=order.cuda(), out_dtype=out).cpu()
+    there = (order >= 0) & (order < 50) & (torch.arange(n) < n - 2)
+    assert (got[~there] == 0).all()
+    assert got[: n // 2][there[: n // 2]][:, ::3].isnan().all() and not got[n // 2:].isnan().any()
+
+
 def test_products_past_32_bits_of_outputs():
     g = generator(33)
     x, x64 = four_bit(g, 64, 32)
@@ -291,6 +347,27 @@ def test_a_wait_that_gives_up_is_reported_by_the_next_call(monkeypatch, n, outer
     assert e.value.code == dh.DSMEM_HIST_ETIMEOUT and "grouped product" in str(e.value)
     assert dh.dsmem_hist_device_status() == 2 and dh.dsmem_hist_device_status() == 0
     assert torch.equal(dh.dsmem_mx4_grouped_matmul(x, w, dev), want)
+
+
+# ---------------------------------------------------------------- quantisation
+
+def test_the_longest_row():
+    from test_gpu_mx4 import quantized
+    columns = 2 ** 31 - 513
+    x = torch.zeros(1, columns, dtype=torch.bfloat16, device="cuda")
+    mark = torch.randn(1, 127, generator=generator(36)).to(torch.bfloat16)
+    x[:, -127:] = mark.cuda()
+    x[0, 2 ** 30] = -3.0
+    values, scales = dh.dsmem_mx4_quantize(x)
+    last = columns - columns % 128
+    tail = quantized(x[:, last - 128:].cpu())
+    assert torch.equal(values[:, last // 2 - 64:].cpu(), tail[0]) and torch.equal(scales[:, last // 32 - 4:].cpu(),
+                                                                                 tail[1])
+    assert int((scales != 0).sum()) == int((tail[1] != 0).sum()) + 1 and int(scales[0, 2 ** 25]) == 126
+    back = dh.dsmem_mx4_dequantize(values, scales, columns, dtype=torch.bfloat16)
+    assert float(back[0, 2 ** 30]) == -3.0 and int((back != 0).sum()) <= 128
+    want = stood_for(*tail, 128 + columns % 128).to(torch.bfloat16)
+    assert torch.equal(back[:, last - 128:].cpu(), want)
 
 
 # ------------------------------------------------- together, streams, graphs
