@@ -55,14 +55,13 @@ struct Ring {
   static constexpr int kChunksB = (kCols + 127) / 128;  // of 128 elements' scales
   static constexpr int kStage = kA + kB + 2 * (1 + kChunksB) * kChunk;
   static constexpr int kMostStages = kCols == 256 ? 4 : (kCols == 128 ? 6 : 8);
-  // Tensor memory: the sums of one tile in two halves, or of two tiles, then the
-  // scales of each stage's rows, and those of kKept parts of the channels.
+  // Tensor memory: the sums of one tile in two halves, or of two tiles, then each
+  // stage's scales of the rows, and of the channels.
   static constexpr int kBuffers = kCols == 256 ? 1 : 2, kHalves = kCols == 256 ? 2 : 1;
-  static constexpr int kKept = 8;
   static constexpr int kMine = kCols / 2;  // columns of an output warp
   static constexpr int kRowScales = kBuffers * kCols, kChannelScales = kRowScales + 8 * kMostStages;
   static constexpr uint32_t kColumns = 512;
-  static_assert(kMostStages <= kKept && kChannelScales + 8 * kChunksB * kKept <= 512, "tensor memory");
+  static_assert(kChannelScales + 8 * kChunksB * kMostStages <= 512, "tensor memory");
   static int smem_bytes(int groups, int stages) {
     return 1024 + stages * kStage + kOutWarps * kStageOut + kBarrierBytes + 2 * 4 * (groups + 2);
   }
@@ -99,17 +98,16 @@ struct Tile {
   int group;  // `groups`: the rows behind the last group
   int row0, end, chan0;
   int blocks;  // stages of depth
-  bool fresh;  // the first of its channels in this CTA
 };
 
 template <int kCols>
 struct Schedule {
   const int32_t* begin;  // [groups + 2] first row of each group, in shared memory
   const int32_t* first;  // [groups + 2] first tile
-  int groups, chan_tiles, blocks, group, mine;
+  int groups, chan_tiles, blocks, group;
   __device__ __forceinline__ Schedule(const int32_t* b, const int32_t* f, const Args& a)
       : begin(b), first(f), groups(a.groups), chan_tiles((a.outer + kCols - 1) / kCols), blocks((a.quads + 1) / 2),
-        group(0), mine(0) {}
+        group(0) {}
   __device__ __forceinline__ int tiles_of(int rows) const { return (rows + kHigh - 1) / kHigh * chan_tiles; }
   // Tile t; t only grows from call to call.  Many groups may be empty.
   __device__ __forceinline__ Tile at(int t) {
@@ -129,7 +127,6 @@ struct Schedule {
     r.end = begin[group + 1];
     r.chan0 = i / high * kCols;
     r.blocks = group < groups ? blocks : 0;
-    r.fresh = t == mine || i % high == 0;
     return r;
   }
 };
@@ -150,6 +147,8 @@ __device__ __forceinline__ uint64_t scale_descriptor(uint32_t addr) {
 // them.  Where all rows are there, and whole 64 bytes, one TMA store takes them, and
 // costs the warp a quarter of the instructions.  (Rows written sector by sector
 // from the lanes that hold them took twice as long as this path without TMA.)
+// Other rows are written value by value: 131072 rows of 1028 bf16 channels in 333 us,
+// of 1032 in 204; by words, which begin elsewhere in each row, in 406.
 template <typename O, int kLine>
 __device__ __forceinline__ void store_lines(const Args& a, const CUtensorMap* out_map, int row0, int end, int chan,
                                             int limit, const uint32_t (&r)[kLine / 4], uint32_t staging) {
@@ -342,8 +341,8 @@ __device__ __forceinline__ void copy_rows(const Args& a, Schedule<kCols>& schedu
 // The scales' warps.  A thread brings those of every kScaleThreads-th row and
 // channel, two stages' at a time, which are asked for four stages ahead.
 template <int kCols>
-__device__ __forceinline__ void bring_scales(const Args& a, Schedule<kCols>& schedule, int i, int total, bool keep,
-                                             uint32_t base, uint32_t landed, uint32_t empty, uint32_t gave_up) {
+__device__ __forceinline__ void bring_scales(const Args& a, Schedule<kCols>& schedule, int i, int total, uint32_t base,
+                                             uint32_t landed, uint32_t empty, uint32_t gave_up) {
   using R = Ring<kCols>;
   constexpr int kRows = kHigh / kScaleThreads, kLines = kRows + (kCols + kScaleThreads - 1) / kScaleThreads;
   const int tid = threadIdx.x - kFirstScale * 32, blocks = schedule.blocks;
@@ -352,14 +351,12 @@ __device__ __forceinline__ void bring_scales(const Args& a, Schedule<kCols>& sch
   // order's entry of the tile behind.
   const uint8_t* line[kLines];
   int tile = i, stage_ahead = 0, entry[kRows], chan0 = 0, group = 0;
-  bool fresh = true, fresh_ahead = true;  // whether its channels' scales are wanted, and the tile behind's
   const auto look = [&] {
     if (tile >= total) return;
     const Tile t = schedule.at(tile);
 #pragma unroll
     for (int r = 0; r < kRows; ++r) entry[r] = place_at(a, t.row0 + r * kScaleThreads + tid, t.end);
     chan0 = t.chan0, group = t.group;
-    fresh_ahead = t.fresh || !keep;
   };
   const auto enter = [&] {
 #pragma unroll
@@ -374,14 +371,12 @@ __device__ __forceinline__ void bring_scales(const Args& a, Schedule<kCols>& sch
                     ? a.w_scales + (static_cast<int64_t>(group) * a.outer + chan0 + c) * pitch
                     : nullptr;
     }
-    fresh = fresh_ahead;
     ++tile;
     look();
   };
   // Four quads of each line; zeros behind a line's end, and for none.
   struct Pair {
     uint4 of[kLines];
-    bool fresh;
   };
   int64_t left = static_cast<int64_t>(total - i) * ((blocks + 1) / 2);  // pairs to ask for
   const auto ask = [&](Pair& p) {
@@ -392,10 +387,8 @@ __device__ __forceinline__ void bring_scales(const Args& a, Schedule<kCols>& sch
     }
     const int first = 2 * stage_ahead;
     stage_ahead += 2;
-    p.fresh = fresh;
 #pragma unroll
     for (int l = 0; l < kLines; ++l) {
-      if (l >= kRows && !fresh) break;
       p.of[l] = make_uint4(0, 0, 0, 0);
       if (!line[l]) continue;
       const uint32_t* q = reinterpret_cast<const uint32_t*>(line[l]) + first;
@@ -423,7 +416,6 @@ __device__ __forceinline__ void bring_scales(const Args& a, Schedule<kCols>& sch
 #pragma unroll
       for (int l = 0; l < kLines; ++l) {
         const bool row = l < kRows;
-        if (!row && !p.fresh) break;
         const int c = (row ? l : l - kRows) * kScaleThreads + tid;
         if (!row && kCols % kScaleThreads != 0 && c >= kCols) break;
         const uint32_t at = to + (c & 31) * 16 + (c >> 5 & 3) * 4 + (row ? 0 : 2 * kChunk + (c >> 7) * kChunk);
@@ -507,11 +499,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int all = first[a.groups + 1], of_groups = first[a.groups];  // all, and those of real groups
   const int mine = share(all, blockIdx.x), total = share(all, blockIdx.x + 1);
   const int of_mine = min(of_groups, total);
-  schedule.mine = mine;
-  // The scales of a tile's channels stay in tensor memory for the next row tiles,
-  // where the ring is short enough for the instructions that read a part of them
-  // to have completed when the part is written again.
-  const bool keep = schedule.blocks >= kStages && schedule.blocks <= R::kKept;
 
   if (warp == 0) {
     uint32_t stage = 0, phase = 0, issued = 0;
@@ -545,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp >= kFirstScale) {
-    bring_scales<kCols>(a, schedule, mine, of_mine, keep, base, landed, empty, gave_up);
+    bring_scales<kCols>(a, schedule, mine, of_mine, base, landed, empty, gave_up);
   } else if (warp >= kFirstCopy) {
     copy_rows<kCols>(a, schedule, mine, of_mine, base, landed, empty, gave_up);
   } else if (warp == 1) {
@@ -566,7 +553,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Sums: a tile's own place of two, or the halves of the only one.
       const uint32_t place = R::kBuffers == 2 ? done & 1 : 0, d = tmem + place * kCols;
       const uint32_t turn = R::kBuffers == 2 ? done >> 1 & 1 : done & 1;
-      const bool fresh = !keep || schedule.at(i).fresh;
       if (!await(acc_empty + 8 * place, turn ^ 1)) break;
       for (int k = 0; k < schedule.blocks; ++k) {
         // Rows and scales come by plain copies, which this warp passes on to the
@@ -581,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Each stage has columns of its own: the stage is handed back only when
         // the instructions that read them have completed.
         const uint32_t sfa = tmem + R::kRowScales + stage * 8;
-        const uint32_t sfb = tmem + R::kChannelScales + (keep ? k : stage) * (8 * R::kChunksB);
+        const uint32_t sfb = tmem + R::kChannelScales + stage * (8 * R::kChunksB);
         const auto multiply = [&](int half, uint32_t desc) {
 #pragma unroll
           for (int s = 0; s < 4; ++s)
@@ -593,11 +579,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             copy_scales(sfa + 4 * q, ds + q * (kChunk >> 4));
-            if (fresh) {
 #pragma unroll
-              for (int c = 0; c < R::kChunksB; ++c)
-                copy_scales(sfb + 4 * (R::kChunksB * q + c), ds + (2 + R::kChunksB * q + c) * (kChunk >> 4));
-            }
+            for (int c = 0; c < R::kChunksB; ++c)
+              copy_scales(sfb + 4 * (R::kChunksB * q + c), ds + (2 + R::kChunksB * q + c) * (kChunk >> 4));
           }
           if (R::kHalves == 1 || k > 0) multiply(0, kWhole);
           else multiply(0, kPart);
@@ -720,6 +704,8 @@ int launch(const Mx4ProductArgs& p, const CallContext& ctx, cudaStream_t stream)
   a.out = p.out, a.out_dtype = p.out_dtype;
   a.wide_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
                static_cast<int64_t>(p.outer) * dtype_size(p.out_dtype) % 16 == 0;
+  // 16 bytes of scales at a time, where rows begin so: depth 2048 in 171 us, 2176 in
+  // 214, by words (131072 rows, 64 matrices of 1024 channels; 1792 in 167).
   a.wide_scales = p.quads % 4 == 0 && reinterpret_cast<uintptr_t>(p.x_scales) % 16 == 0 &&
                   reinterpret_cast<uintptr_t>(p.w_scales) % 16 == 0;
   a.status = ctx.status;

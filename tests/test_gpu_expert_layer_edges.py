@@ -132,6 +132,18 @@ def test_strides_and_odd_bases(tokens, width, hidden, pad, shift):
     layer.check(dh.dsmem_expert_layer(x, logits, mixed[0], mixed[2], 3, gate=mixed[1]), want)
 
 
+@pytest.mark.parametrize("tokens", [1, 12, 40])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("width,pad,shift", [(128, 3, 0), (128, 0, 1), (101, 2, 1), (256, 8, 8)])
+def test_4_bit_matrices_and_tokens_with_odd_bases(width, pad, shift, dtype, tokens):
+    layer = Layer(4, width, 72, dtype, True, True, 18)
+    x, logits = tokens_of(tokens, 4, width, dtype, 19)
+    base = torch.full((tokens * (width + pad) + shift + 8,), math.nan, dtype=dtype, device="cuda")
+    view = base[shift:shift + tokens * (width + pad)].view(tokens, -1)[:, :width]
+    view.copy_(x)
+    layer.check(layer.run(view, logits, 2), layer.exact(x, logits, 2))
+
+
 @pytest.mark.parametrize("mx4", [False, True])
 def test_gate_and_up_may_be_one(mx4):
     layer = Layer(3, 96, 64, torch.bfloat16, mx4, True, 20)

@@ -120,7 +120,8 @@ def tokens_of(tokens, experts, width, dtype, seed):
 SHAPES = [  # tokens, experts, top_k, width, hidden
     (1, 1, 1, 1, 1), (1, 64, 4, 256, 128), (1, 8, 8, 2048, 96), (2, 3, 2, 33, 17), (5, 33, 32, 64, 40),
     (8, 16, 3, 136, 72), (9, 7, 3, 100, 51), (13, 7, 3, 1003, 517), (33, 200, 5, 264, 130), (64, 4, 2, 640, 200),
-    (64, 1, 1, 129, 260), (3, 1024, 6, 40, 24), (1, 16, 2, 24, 1100)]
+    (64, 1, 1, 129, 260), (3, 1024, 6, 40, 24), (1, 16, 2, 24, 1100), (64, 32, 32, 72, 40),
+    (2, 3, 1, 1, 65536), (2, 3, 2, 65536, 1)]
 
 
 @pytest.mark.parametrize("gated,activation", [(True, "silu"), (False, "relu"), (True, "relu"), (False, "silu")])
