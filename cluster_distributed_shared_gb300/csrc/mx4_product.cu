@@ -5,8 +5,9 @@
 // lane of the accumulators is a row of the output.  One persistent CTA per SM.
 // Warp 0 copies the matrices' values by TMA (256 elements of depth a stage: 128
 // bytes a row, swizzled), warp 1 issues the matrix instructions, the next eight
-// write finished sums out, eight copy the rows that the order names, 16 bytes a
-// copy, and the last two bring both sides' scales.  Scales are kept row by row, as
+// write finished sums out, four copy the rows that the order names, 16 bytes a
+// copy, and the last two bring both sides' scales.  (Four more copying warps left the
+// writing ones 96 registers instead of 128: 177 us, not 162, in the case below.)  Scales are kept row by row, as
 // quantisation writes them; shared memory has them in the order that tensor memory
 // wants: chunks of 128 rows by 4 scales, row r at 16 (r % 32) + 4 (r / 32).
 //
@@ -38,11 +39,10 @@ namespace {
 
 constexpr int kHigh = 128;        // rows of a tile
 constexpr int kStageBytes = 128;  // of a row in a stage: 256 elements
-constexpr int kShifts = 2;        // groups of copying warps that take stages in turn
-constexpr int kShift = 128;       // threads of one
+constexpr int kCopyThreads = 128;
 constexpr int kOutWarps = 8;      // four for either half of a tile's columns
 constexpr int kFirstCopy = 2 + kOutWarps;  // behind TMA, matrix instructions and output
-constexpr int kFirstScale = kFirstCopy + kShifts * kShift / 32;
+constexpr int kFirstScale = kFirstCopy + kCopyThreads / 32;
 constexpr int kScaleThreads = 64;
 constexpr int kThreads = kFirstScale * 32 + kScaleThreads;
 constexpr int kStageOut = 2048;         // output staging of a warp
@@ -284,8 +284,8 @@ template <int kCols>
 __device__ __forceinline__ void copy_rows(const Args& a, Schedule<kCols>& schedule, int i, int total, uint32_t base,
                                           uint32_t landed, uint32_t empty, uint32_t gave_up) {
   using R = Ring<kCols>;
-  constexpr int kRows = kHigh * 8 / kShift, kLines = kShift / 8;
-  const int shift = (threadIdx.x - kFirstCopy * 32) / kShift, tid = (threadIdx.x - kFirstCopy * 32) % kShift;
+  constexpr int kRows = kHigh * 8 / kCopyThreads, kLines = kCopyThreads / 8;
+  const int tid = threadIdx.x - kFirstCopy * 32;
   const int64_t pitch = int64_t{64} * a.quads;
   // A tile's entries of the order are asked for while the tile before is copied.
   int ahead[kRows];
@@ -293,7 +293,7 @@ __device__ __forceinline__ void copy_rows(const Args& a, Schedule<kCols>& schedu
 #pragma unroll
     for (int r = 0; r < kRows; ++r) ahead[r] = place_at(a, t.row0 + r * kLines + tid / 8, t.end);
   };
-  int stage = shift, skip = shift;  // skip: stages until this shift's next
+  int stage = 0;
   uint32_t phase = 0;
   bool ok = true;
   Tile next;
@@ -310,8 +310,7 @@ __device__ __forceinline__ void copy_rows(const Args& a, Schedule<kCols>& schedu
       next = schedule.at(i);
       ask(next);
     }
-    int k = skip;
-    for (; k < t.blocks; k += kShifts) {
+    for (int k = 0; k < t.blocks; ++k) {
       ok = wait_for(empty + 8 * stage, phase ^ 1, gave_up, a.wait_cycles, a.status);
       ok = __all_sync(kFull, ok);
       if (!ok) break;
@@ -327,13 +326,11 @@ __device__ __forceinline__ void copy_rows(const Args& a, Schedule<kCols>& schedu
                  read ? 16 : 0);
       }
       copy_arrive(landed + 8 * stage);
-      stage += kShifts;
-      if (stage >= a.stages) {
-        stage -= a.stages;
+      if (++stage == a.stages) {
+        stage = 0;
         phase ^= 1;
       }
     }
-    skip = k - t.blocks;
   }
   copy_wait_all();
 }
@@ -472,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full + 8 * s, 1);
-      mbar_init(landed + 8 * s, kShift + kScaleThreads / 32);
+      mbar_init(landed + 8 * s, kCopyThreads + kScaleThreads / 32);
       mbar_init(empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
