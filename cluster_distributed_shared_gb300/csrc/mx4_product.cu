@@ -7,7 +7,8 @@
 // bytes a row, swizzled), warp 1 issues the matrix instructions, the next eight
 // write finished sums out, four copy the rows that the order names, 16 bytes a
 // copy, and the last two bring both sides' scales.  (Four more copying warps left the
-// writing ones 96 registers instead of 128: 177 us, not 162, in the case below.)  Scales are kept row by row, as
+// writing ones 96 registers instead of 128: 177 us, not 161, with the quantisation
+// before it, in the case below.)  Scales are kept row by row, as
 // quantisation writes them; shared memory has them in the order that tensor memory
 // wants: chunks of 128 rows by 4 scales, row r at 16 (r % 32) + 4 (r / 32).
 //
@@ -18,11 +19,10 @@
 // of which begins when the last tile's half is in its warps' registers.
 //
 // Measured, 16384 tokens x 8 of 64 experts of 1024 x 2048, groups of unequal size, rows
-// named by the order: 162 us, 3.4 PFLOP/s, where the bytes alone would take 53
-// (matrices and rows once, bf16 results once).  The matrix warp is busy 700 cycles a
-// stage of 384 of arithmetic: 48 KB a stage go into shared memory and out of it
-// again, and the scales' way to tensor memory comes on top.  32 tokens x 8 of 128
-// experts: 28 us for 127 MB, 4.5 TB/s; every SM has two or three tiles of 2.5.
+// named by the order: 142 us, 3.9 PFLOP/s, where the bytes alone would take 53
+// (matrices and rows once, bf16 results once) and the arithmetic 71.  48 KB a stage
+// go into shared memory and out of it again, about 700 cycles of 384 of arithmetic.
+// 32 tokens x 8 of 128 experts: 26 us for 127 MB, 4.9 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -147,8 +147,9 @@ __device__ __forceinline__ uint64_t scale_descriptor(uint32_t addr) {
 // them.  Where all rows are there, and whole 64 bytes, one TMA store takes them, and
 // costs the warp a quarter of the instructions.  (Rows written sector by sector
 // from the lanes that hold them took twice as long as this path without TMA.)
-// Other rows are written value by value: 131072 rows of 1028 bf16 channels in 333 us,
-// of 1032 in 204; by words, which begin elsewhere in each row, in 406.
+// Other rows are written value by value: 131072 rows of 1028 bf16 channels in 275 us,
+// of 1032 in 183.  (By words, which begin elsewhere in each row: 406, not the 333 of
+// that step.)
 template <typename O, int kLine>
 __device__ __forceinline__ void store_lines(const Args& a, const CUtensorMap* out_map, int row0, int end, int chan,
                                             int limit, const uint32_t (&r)[kLine / 4], uint32_t staging) {
@@ -701,8 +702,8 @@ int launch(const Mx4ProductArgs& p, const CallContext& ctx, cudaStream_t stream)
   a.out = p.out, a.out_dtype = p.out_dtype;
   a.wide_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
                static_cast<int64_t>(p.outer) * dtype_size(p.out_dtype) % 16 == 0;
-  // 16 bytes of scales at a time, where rows begin so: depth 2048 in 171 us, 2176 in
-  // 214, by words (131072 rows, 64 matrices of 1024 channels; 1792 in 167).
+  // 16 bytes of scales at a time, where rows begin so (by words 16384 tokens take 190
+  // us, not 161).
   a.wide_scales = p.quads % 4 == 0 && reinterpret_cast<uintptr_t>(p.x_scales) % 16 == 0 &&
                   reinterpret_cast<uintptr_t>(p.w_scales) % 16 == 0;
   a.status = ctx.status;
@@ -727,14 +728,14 @@ int launch(const Mx4ProductArgs& p, const CallContext& ctx, cudaStream_t stream)
 
 }  // namespace
 
-// The widest tiles that give the SMs enough of them.  32 channels pay only where no
-// SM gets a second tile: one row of 64 experts of 1536 x 2048 took 7.7 us, with 128
-// channels 8.2; eight rows (384 tiles of 32) 13.9 and 9.1.  256 channels pay from two
-// tiles an SM on: 4096 rows of 8 experts of 4096 x 2048 took 27.8 us, with 128 32.3;
-// 1024 rows (272 tiles of 256) 18.6 and 17.6.
+// The narrowest tiles of which no SM gets a second one, for a tile's time is that of
+// its share of the matrices: one row of 64 experts of 1536 x 2048 takes 7.4 us with 32
+// channels, 8.0 with 128 and 9.4 with 256; eight rows (384 tiles of 32, 96 of 128)
+// 13.3, 9.1 and 10.1.  Otherwise the widest, which take in the least: 16 rows (192
+// tiles of 128) 15.9, 12.1 and 10.8; 16384 rows 53.1 with 128 and 45.9 with 256.
 int run_mx4_product(const Mx4ProductArgs& p, const CallContext& ctx, cudaStream_t stream) {
   if (tile_bound(p, 32) <= ctx.sm_count) return launch<32>(p, ctx, stream);
-  if (tile_bound(p, 256) < 2 * ctx.sm_count) return launch<128>(p, ctx, stream);
+  if (tile_bound(p, 128) <= ctx.sm_count) return launch<128>(p, ctx, stream);
   return launch<256>(p, ctx, stream);
 }
 
