@@ -847,13 +847,16 @@ cudaError_t launch_with(const LayerArgs& a, const CallContext& ctx, cudaStream_t
   return launch_down<kHeldDown, kTiles, true>(a, ctx, stream);
 }
 // Up to 8 tokens have one column tile.  (With 4 tiles for any number, 8 tokens took
-// 54.0 us, not 51.1, and in 4 bits 44.6, not 43.0; 64 experts of 2048 x 768.)  For
-// more the kernels hold the sums of 4, which 32 tokens have at most; 8, for 64, spilled
-// registers: 33 tokens took 122 us, not 102, and in 4 bits 112, not 82.
+// 54.0 us, not 51.1, and in 4 bits 44.6, not 43.0; 64 experts of 2048 x 768, 4 a token.)
+// For more the kernels hold the sums of 2, or of 4 where the matrices would have to be
+// decoded again for each 2: with 4 the 16-bit ones, whose columns of a step wait in
+// registers too, took 100 us, not 96, for 32 tokens and 139, not 128, for 64; with 2
+// the 4-bit ones 38, not 33, for 32 tokens of 8 experts (80 and 78 of 64).  8 tiles, for
+// 64 tokens, spilled registers: 33 tokens took 122 us and in 4 bits 112, not 82.
 template <int kHeldUp, int kHeldDown>
 cudaError_t launch_both(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
   if (a.tokens <= 8) return launch_with<kHeldUp, kHeldDown, 1>(a, ctx, stream);
-  return launch_with<kHeldUp, kHeldDown, 4>(a, ctx, stream);
+  return launch_with<kHeldUp, kHeldDown, kIsMx4<kHeldDown> ? 4 : 2>(a, ctx, stream);
 }
 
 }  // namespace
