@@ -20,8 +20,9 @@
 //
 // Measured, 16384 tokens x 8 of 64 experts of 1024 x 2048, groups of unequal size, rows
 // named by the order: 142 us, 3.9 PFLOP/s, where the bytes alone would take 53
-// (matrices and rows once, bf16 results once) and the arithmetic 71.  48 KB a stage
-// go into shared memory and out of it again, about 700 cycles of 384 of arithmetic.
+// (matrices and rows once, bf16 results once) and the arithmetic 71.  The tiles take
+// in 1.7 GB from L2, 12 TB/s; without rows, scales and results the matrices' 1.1 GB
+// and the arithmetic still took 120.
 // 32 tokens x 8 of 128 experts: 26 us for 127 MB, 4.9 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
