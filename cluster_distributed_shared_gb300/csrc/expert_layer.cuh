@@ -1,8 +1,9 @@
-// A whole expert layer for a few tokens, in two kernels.
+// A whole expert layer for a few tokens, in two kernels (f16 matrices: three).
 //
 // With e = ids[t, j] and w = weights[t, j] of a token's routing,
 //   up kernel    h[t, j] = w act(up[e] x[t]),  or  w act(gate[e] x[t]) * (up[e] x[t])
 //   down kernel  y[t]    = sum over j of down[e] h[t, j]
+// and between them, beside f16 matrices, a scale of each row of h.
 // A few tokens do little arithmetic on many weights, so both kernels are bound
 // by reading the chosen experts' matrices once, and everything follows from
 // keeping loads of them in flight:
@@ -75,7 +76,7 @@ struct alignas(32) Routing {
   uint16_t active[DSMEM_ROUTE_MAX_EXPERTS];               // experts that any token chose, by number
   uint16_t start[DSMEM_ROUTE_MAX_EXPERTS];                // of active experts: first row
   uint16_t rows_of[DSMEM_ROUTE_MAX_EXPERTS];              // of active experts
-  float weight[kMaxRows];                                 // of each row
+  float weight[kMaxRows];                                 // of each row; behind scale_kernel, the row's scale
   uint8_t token[kMaxRows];
   uint32_t of_warp[16];
   int count;  // of active experts
@@ -375,9 +376,9 @@ struct FromX {
   }
 };
 // h: the up kernel's rows, each element as two numbers, with zeros up to whole
-// steps; each row is read once by a CTA.  A piece is eight first numbers and eight
-// second ones, a sector, in the fragments' order, and the pieces that the four
-// lanes of a row take together lie side by side.
+// steps; each row is read once by a CTA for every 16 of its channels.  A piece is
+// eight first numbers and eight second ones, a sector, in the fragments' order, and
+// the pieces that the four lanes of a row take together lie side by side.
 template <int kHeld>
 struct FromH {
   static constexpr bool kTwo = true;
@@ -388,10 +389,22 @@ struct FromH {
   __device__ __forceinline__ static int at(int step, int q) {
     return step * kStep + (q * 4 + (threadIdx.x & 3)) * 16;
   }
-  // Where the first number of element c lies in its row; the second is 8 further on.
-  __device__ __forceinline__ static int place_of(int c) {
-    if constexpr (!kIsMx4<kHeld>) return (c >> 3) * 16 + (c & 7);
-    return (c >> 7) * kStep + ((c >> 3 & 3) * 4 + (c >> 5 & 3)) * 16 + ((c & 3) << 1) + (c >> 2 & 1);
+  // Element c of a row.  Two bf16 numbers hold 16 bits of it, whatever its size.  Two
+  // f16 numbers would hold less below 2^-9 and nothing below 2^-25 or above 65504,
+  // which a small x or a small routing weight passes, so that beside f16 matrices a
+  // piece is at first eight floats, and scale_kernel makes the numbers of them.
+  __device__ __forceinline__ static void put(uint16_t* row, int c, float value) {
+    if constexpr (kHeld == kF16) {
+      reinterpret_cast<float*>(row)[c] = value;
+    } else {
+      // Where the first number lies; the second is 8 further on.
+      uint16_t* to = row + (kIsMx4<kHeld> ? (c >> 7) * kStep + ((c >> 3 & 3) * 4 + (c >> 5 & 3)) * 16 +
+                                                ((c & 3) << 1) + (c >> 2 & 1)
+                                          : (c >> 3) * 16 + (c & 7));
+      const __nv_bfloat16 b = __float2bfloat16_rn(value);
+      to[0] = __bfloat16_as_ushort(b);
+      to[8] = __bfloat16_as_ushort(__float2bfloat16_rn(__hisinf(b) ? 0.0f : value - __bfloat162float(b)));
+    }
   }
   __device__ __forceinline__ void fetch(const uint16_t* p, int, Eight& e) const {
     asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -593,25 +606,11 @@ __device__ __noinline__ void to_h(const LayerArgs& a, const Routing& routing, Pl
       const float value = routing.weight[row] * (a.gated ? act * v.z : act);
       const int at = g + 8 * k;
       if (at >= p.count) continue;
-      // Two 16-bit numbers hold h to 16 bits or more: what they leave out is far
-      // below the output's rounding.
-      const int to = FromH<kHeld>::place_of(p.row + at);
-      if constexpr (kHeld == kF16) {
-        const __half b = __float2half_rn(value);
-        h[to] = __half_as_ushort(b);
-        h[to + 8] = __half_as_ushort(__float2half_rn(__hisinf(b) ? 0.0f : value - __half2float(b)));
-      } else {
-        const __nv_bfloat16 b = __float2bfloat16_rn(value);
-        h[to] = __bfloat16_as_ushort(b);
-        h[to + 8] = __bfloat16_as_ushort(__float2bfloat16_rn(__hisinf(b) ? 0.0f : value - __bfloat162float(b)));
-      }
+      FromH<kHeld>::put(h, p.row + at, value);
     }
     // Zeros behind the end of each row, up to a whole step.
     if (p.row + p.count == a.hidden)
-      for (int c = a.hidden + g; c < a.h_pitch; c += 8) {
-        const int to = FromH<kHeld>::place_of(c);
-        h[to] = h[to + 8] = 0;
-      }
+      for (int c = a.hidden + g; c < a.h_pitch; c += 8) FromH<kHeld>::put(h, c, 0.0f);
   }
 }
 
@@ -714,6 +713,62 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
 }
 
+// h beside f16 matrices, a CTA to a row: from floats to two f16 numbers an element,
+// times the power of two that brings the row's largest finite magnitude into [2^14,
+// 2^15).  So an element is held to 22 bits, or to 2^-39 of its row's largest, whatever
+// the row's size; the down kernel takes the power back out of its 32-bit sums.  Eight
+// elements keep their 32 bytes.
+// A launch of its own costs 2 us for one token and 4 of 230 for 32 of 128 experts of
+// 2048 x 1024.  (With both sides as tf32 none is needed, but what is worked on between
+// its load and the matrix instruction is waited for early: 277 us.)
+constexpr int kScaleThreads = 256;
+template <int kHeld>
+__global__ void __launch_bounds__(kScaleThreads) scale_kernel(const __grid_constant__ LayerArgs a) {
+  static_assert(kHeld == kF16, "others need none");
+  __shared__ uint32_t of_warp[kScaleThreads / 32];
+  launch_dependents();
+  wait_for_previous();
+  Routing& routing = *static_cast<Routing*>(a.routing);
+  const int row = blockIdx.x, last = routing.count - 1;
+  if (last < 0 || row >= routing.start[last] + routing.rows_of[last]) return;
+  uint4* h = reinterpret_cast<uint4*>(a.h + static_cast<int64_t>(row) * 2 * a.h_pitch);
+  const int pieces = a.h_pitch / 8;
+  uint32_t most = 0;
+  const auto look = [&](uint32_t bits) {
+    bits &= 0x7fffffffu;
+    if (bits < 0x7f800000u) most = max(most, bits);
+  };
+  for (int i = threadIdx.x; i < 2 * pieces; i += kScaleThreads) {
+    const uint4 v = h[i];
+    look(v.x), look(v.y), look(v.z), look(v.w);
+  }
+  most = __reduce_max_sync(kFullWarp, most);
+  if (threadIdx.x % 32 == 0) of_warp[threadIdx.x / 32] = most;
+  __syncthreads();
+  most = __reduce_max_sync(kFullWarp, of_warp[threadIdx.x % (kScaleThreads / 32)]);
+  // Both powers are normal floats.
+  const uint32_t exponent = max(most >> 23, 15u);
+  const float factor = __uint_as_float((268u - exponent) << 23);
+  for (int i = threadIdx.x; i < pieces; i += kScaleThreads) {
+    const uint4 v[2] = {h[2 * i], h[2 * i + 1]};
+    uint32_t high[4], low[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4& w = v[j / 2];
+      const float2 f = mul2(make_float2(__uint_as_float(j % 2 ? w.z : w.x), __uint_as_float(j % 2 ? w.w : w.y)),
+                            make_float2(factor, factor));
+      high[j] = floats_to_pair(f, __half());
+      const float2 first = pair_to_floats(high[j], __half());
+      // An infinity's rest is 0, not inf - inf.
+      low[j] = floats_to_pair(make_float2(isinf(first.x) ? 0.0f : f.x - first.x,
+                                          isinf(first.y) ? 0.0f : f.y - first.y), __half());
+    }
+    h[2 * i] = make_uint4(high[0], high[1], high[2], high[3]);
+    h[2 * i + 1] = make_uint4(low[0], low[1], low[2], low[3]);
+  }
+  if (threadIdx.x == 0) routing.weight[row] = __uint_as_float((exponent - 14u) << 23);
+}
+
 // Each CTA an equal share of y's channels, 16 at a time, over all active
 // experts: with their rows of h end to end the layer's second half is one
 // product of great depth, so no two CTAs add to one sum.  The warps split that
@@ -769,8 +824,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           const int col = (column_tile + n) * 8 + t * 2 + j;
           if (col < columns) {
             float* p = mine + routing.token[first_row + col] * 16 + g;
-            p[0] += sum[n][j];
-            p[8] += sum[n][j + 2];
+            // scale_kernel's power of two, back out of the sum
+            const float scale = kHeld == kF16 ? routing.weight[first_row + col] : 1.0f;
+            p[0] += scale * sum[n][j];
+            p[8] += scale * sum[n][j + 2];
           }
         }
       }
@@ -803,16 +860,12 @@ cudaError_t launch_up(const LayerArgs& a, const CallContext& ctx, cudaStream_t s
   return cudaGetLastError();
 }
 
-template <int kHeld, int kTiles, bool kWide>
-cudaError_t launch_down(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
-  static SmemLimit limit;
-  const auto kernel = down_kernel<kHeld, kTiles, kWide>;
-  const int bytes = kWarps * a.tokens * 16 * static_cast<int>(sizeof(float));
-  const cudaError_t e = limit.need(reinterpret_cast<const void*>(kernel), ctx.device, bytes);
-  if (e != cudaSuccess) return e;
+// A launch that begins while the one before it runs, and waits for it itself.
+template <typename Kernel>
+cudaError_t launch_behind(Kernel kernel, int ctas, int threads, int bytes, const LayerArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctx.sm_count));
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
@@ -821,6 +874,18 @@ cudaError_t launch_down(const LayerArgs& a, const CallContext& ctx, cudaStream_t
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int kHeld, int kTiles, bool kWide>
+cudaError_t launch_down(const LayerArgs& a, const CallContext& ctx, cudaStream_t stream) {
+  static SmemLimit limit;
+  const auto kernel = down_kernel<kHeld, kTiles, kWide>;
+  const int bytes = kWarps * a.tokens * 16 * static_cast<int>(sizeof(float));
+  cudaError_t e = limit.need(reinterpret_cast<const void*>(kernel), ctx.device, bytes);
+  if constexpr (kHeld == kF16) {
+    if (e == cudaSuccess) e = launch_behind(scale_kernel<kHeld>, a.tokens * a.top_k, kScaleThreads, 0, a, stream);
+  }
+  return e == cudaSuccess ? launch_behind(kernel, ctx.sm_count, kWarps * 32, bytes, a, stream) : e;
 }
 
 // Whether rows of a 16-bit matrix are whole 16-byte vectors.  Others are loaded by

@@ -158,7 +158,7 @@ struct LayerArgs {
   void* out;
   // Set by run_expert_layer.
   void* routing;  // the up kernel's, for the down kernel
-  uint16_t* h;  // [rows][h_pitch], each value as two 16-bit numbers
+  uint16_t* h;  // [rows][h_pitch], each value as two 16-bit numbers (for scale_kernel as a float)
   int h_pitch;
   Divisor by_ctas, by_hidden, by_tiles, by_up_batches, by_down_batches;
 };

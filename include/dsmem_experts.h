@@ -230,8 +230,10 @@ enum { DSMEM_RELU = 0, DSMEM_SILU = 1 };
  *   out[t] = sum over j of weights[t, j] * down[e] h
  *   h = act(up[e] x[t]),  or with a gate  act(gate[e] x[t]) * (up[e] x[t])
  * act(v) = max(v, 0) or v / (1 + exp(-v)).  A token without choices gives 0.
- * Products are summed in 32 bits; h is held in two 16-bit numbers an element
- * (f16: beyond 65504 infinite), and only the output is rounded to x's type.
+ * Products are summed in 32 bits, and only the output is rounded to x's type;
+ * weights[t, j] * h is held in two 16-bit numbers an element, together 16 bits of
+ * it (f16 matrices: 22, or 2^-39 of the largest element of that token and expert),
+ * whatever its size.  (An infinite element of down gives an infinity or NaN.)
  *   dtype       of x and out: DSMEM_F16 or DSMEM_BF16
  *   tokens      0 .. 64;  width, hidden 1 .. 65536;  x_stride >= width
  *   logits      [tokens, experts], logits_stride >= experts elements between
