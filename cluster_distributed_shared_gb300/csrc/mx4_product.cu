@@ -69,7 +69,7 @@ struct Ring {
   // As many stages as fit.
   static int stages(int groups) {
     int n = kMostStages;
-    while (smem_bytes(groups, n) > 227 * 1024) --n;
+    while (smem_bytes(groups, n) > kMostShared) --n;
     return n;
   }
 };

@@ -99,6 +99,10 @@ __device__ __forceinline__ O ld_shared_value(uint32_t addr) {
   return v;
 }
 
+// A CTA's shared memory (227 KB) but for what lay_groups takes of it: a kernel's
+// limit is on the sum.
+constexpr int kMostShared = 227 * 1024 - 2 * 32 * static_cast<int>(sizeof(int));
+
 // The groups' tables in shared memory, by all kThreads threads: begin[g], the
 // first row of group g (begin[groups + 1] = n), from the offsets clamped into
 // [0, n] and made monotone, and (where asked for) first[g], the first tile of
@@ -122,7 +126,7 @@ __device__ __forceinline__ void lay_groups(const int32_t* offsets, int64_t n, in
   // Each warp takes 32 groups of every kWarps * 32: the running maximum
   // of their ends, then the running sum of their tiles.
   constexpr int kWarps = kThreads / 32;
-  __shared__ int of_warp[2][32];
+  __shared__ int of_warp[2][32];  // counted in kMostShared
   int end_before = 0, tiles_before = 0;
   for (int g0 = 0; g0 < owners; g0 += kWarps * 32) {
     const int g = g0 + warp * 32 + lane;
