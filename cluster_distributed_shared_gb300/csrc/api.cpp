@@ -38,7 +38,10 @@ int fail(int code, const char* fmt, ...) {
   return code;
 }
 
+// The runtime keeps the error for the next cudaGetLastError, which would report it for
+// a later call's launch: it is reported here and cleared.
 int fail_cuda(cudaError_t e, const char* what) {
+  cudaGetLastError();
   return fail(DSMEM_HIST_ECUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
 
@@ -1174,7 +1177,7 @@ int dsmem_hist_device_status(uint32_t* status) {
   if (e == cudaSuccess) e = read_and_clear_product_status(&product);
   word |= product;
   if (status) *status = word;
-  if (e != cudaSuccess) return fail(DSMEM_HIST_ECUDA, "device_status: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return fail_cuda(e, "device_status");
   if (word) return fail(DSMEM_HIST_ETIMEOUT, "device_status: a bounded wait gave up (word 0x%x)", word);
   return DSMEM_HIST_OK;
 }

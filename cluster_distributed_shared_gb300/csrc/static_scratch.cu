@@ -38,15 +38,20 @@ uint32_t* g_static_ptr[kMaxDevices] = {};
 int static_scratch(uint32_t** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return record_error(DSMEM_HIST_ECUDA, "cudaGetDevice failed");
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return record_error(DSMEM_HIST_ECUDA, "cudaGetDevice failed");
+  }
   if (dev < 0 || dev >= kMaxDevices)
     return record_error(DSMEM_HIST_EUNSUPPORTED, "device ordinal beyond the static scratch table");
   std::lock_guard<std::mutex> g(g_static_mutex);
   if (!g_static_ptr[dev]) {
     void* p = nullptr;
     e = cudaGetSymbolAddress(&p, g_static_partials);
-    if (e != cudaSuccess || !p)
+    if (e != cudaSuccess || !p) {
+      cudaGetLastError();
       return record_error(DSMEM_HIST_ECUDA, "cudaGetSymbolAddress of the static scratch failed");
+    }
     g_static_ptr[dev] = static_cast<uint32_t*>(p);
   }
   *out = g_static_ptr[dev];
