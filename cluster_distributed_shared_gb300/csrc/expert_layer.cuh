@@ -13,7 +13,8 @@
 //     rows g and g + 8 and the same elements of the rows' side: no shared memory,
 //     no exchange between lanes, one load for two (16-bit) or eight (4-bit)
 //     instructions.  (A tcgen05 tile would be 128 rows high, of which one token's
-//     share of an SM fills 27, and would pass every byte through shared memory.)
+//     share of an SM fills 27, and would pass every byte through shared memory.  A
+//     batch of 32 fills it; tiles for those have not been tried.)
 //   * Every SM reads the same number of rows, every warp the same number of
 //     batches of kSteps steps.
 //   * Each CTA of the up kernel routes all tokens for itself instead of waiting for
@@ -61,8 +62,9 @@ constexpr bool kIsMx4 = kHeld == kMx4Bf16 || kHeld == kMx4F16;
 constexpr int kWarps = 16;
 // Steps of depth that a warp has in flight, a batch: as registers allow.  (16-bit: 2
 // instead of 4 took 108 us, not 97, at 32 tokens of 64 experts of 2048 x 768.  4-bit,
-// whose decoding hides a load's way: 2 instead of 1 spilled, 184 us and not 179 in
-// the case above.)
+// whose decoding hides a load's way: 2 instead of 1 took 184 us, not 179, in the case
+// above; with four column tiles its down kernel spills 88 bytes, not 32, and the up
+// kernel of f16 tokens 70, not none.)
 template <int kHeld>
 constexpr int kSteps = kIsMx4<kHeld> ? 1 : 4;
 template <int kHeld>
@@ -513,7 +515,10 @@ __device__ __forceinline__ void multiply(Slot (&slot)[kSteps<kHeld>], const Batc
 
 // A warp's way through the batches [begin, end) of tiles of `batches` batches each.
 // Experts of more than kTiles column tiles have their rows passed by again for each
-// kTiles of them (from the cache: they have just been read).
+// kTiles of them, a warp's share of a tile at a time.  Between its passes all warps read
+// so much that the rows come from the cache only where the kernel's matrices fit it:
+// 64 tokens of 8 experts, 4 a token, two passes, read 1.0 times up and gate and 1.0
+// times down from memory with 1024 x 2048, and 1.7 and 2.0 times with 4096 x 2048.
 //   point(tile, from, step, at)  where the lane's part of the batch at a tile's step
 //                                lies, and its row of column tile `from`
 //   look(tile, from, column)     column[] of column tiles `from` on; returns how many
@@ -774,7 +779,10 @@ __global__ void __launch_bounds__(kScaleThreads) scale_kernel(const __grid_const
 // product of great depth, so no two CTAs add to one sum.  The warps split that
 // depth evenly; each adds an expert's columns to its tokens' sums in shared
 // memory when it has passed the expert, and at the end the warps' sums are
-// added in order.
+// added in order.  More than 16 channels a CTA are more passes, each over all of the
+// depth and of h, the last for what is left: on 152 SMs 8 tokens of 32 experts of width
+// x 768, 4 a token, take 75 us at a width of 2432 and 87 at 2560 (in 4 bits 62 and 74),
+// 132 at 4864 and 189 at 7168 (102 and 141).
 template <int kHeld, int kTiles, bool kWide>
 __global__ void __launch_bounds__(kWarps * 32, 1)
     down_kernel(const __grid_constant__ LayerArgs a) {
